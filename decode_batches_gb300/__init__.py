@@ -23,6 +23,8 @@ from .build import LIB as LIB_PATH
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_NOT_READY = 0, 1, 2, 3
 MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE, MOE_ERR_TIMEOUT = 4, 5, 6, 7
 MOE_W_BF16, MOE_W_MXFP4 = 0, 1
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # moe_dtype
+FP8_BLOCK = 128  # elements (of a row), or rows and columns (of a weight), that share a scale
 PATHS = {"auto": 0, "simt": 1, "tc": 2}
 DEVERR_EXPERT_RANGE, DEVERR_NONFINITE, DEVERR_TIMEOUT, DEVERR_SEGMENT, DEVERR_RANGE = 0x1, 0x2, 0x4, 0x8, 0x10
 
@@ -32,7 +34,9 @@ EXPORTED = (
     "moe_route", "moe_route_logits", "moe_permute", "moe_experts", "moe_combine",
     "moe_plan_get_device_error", "moe_plan_enable_timing", "moe_plan_timing_report",
     "moe_plan_last_launch_count", "moe_compose_prefill", "moe_permute_static", "moe_selftest_wait_expiry",
-    "moe_plan_resolved_path",
+    "moe_plan_resolved_path", "moe_quantize_rows", "moe_quantize_blocks", "moe_linear_create", "moe_linear_destroy",
+    "moe_linear_set_weights", "moe_linear_workspace_bytes", "moe_linear_set_workspace", "moe_linear_forward",
+    "moe_linear_forward_quantized", "moe_linear_get_device_error",
 )
 
 _lib = None
@@ -59,6 +63,7 @@ def load_library(path: str = LIB_PATH):
                           "(there is no CPU or eager fallback)")
     lib = ctypes.CDLL(path)
     vp, i32, sz, u32p = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.POINTER(ctypes.c_uint32)
+    i64 = ctypes.c_int64
     sig = {
         "moe_plan_create": ([i32, i32, i32, i32, i32, i32], vp),
         "moe_plan_destroy": ([vp], None),
@@ -82,6 +87,18 @@ def load_library(path: str = LIB_PATH):
         "moe_compose_prefill": ([ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                  ctypes.POINTER(PrefillCall), ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)], i32),
     }
+    sig.update({
+        "moe_quantize_rows": ([vp, i32, i64, i32, i32, vp, i64, vp, i64, vp], i32),
+        "moe_quantize_blocks": ([vp, i32, i32, i32, vp, vp, vp], i32),
+        "moe_linear_create": ([i32, i32], vp),
+        "moe_linear_destroy": ([vp], None),
+        "moe_linear_set_weights": ([vp, vp, vp], i32),
+        "moe_linear_workspace_bytes": ([vp, i32], sz),
+        "moe_linear_set_workspace": ([vp, vp, sz, i32], i32),
+        "moe_linear_forward": ([vp, vp, i32, i64, i32, vp, i32, i64, vp], i32),
+        "moe_linear_forward_quantized": ([vp, vp, i64, vp, i64, i32, vp, i32, i64, vp], i32),
+        "moe_linear_get_device_error": ([vp, u32p], i32),
+    })
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -133,6 +150,146 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, width: int):
+    """(pointer, row pitch in elements) of a 2-D CUDA tensor [rows][width] whose rows are dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != width:
+        raise ValueError(f"{name} must have shape (rows, {width}), got {tuple(t.shape)}")
+    if t.shape[0] and width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows")
+    # with one row (or none) the pitch is never used to step; keep it valid
+    pitch = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+    return ctypes.c_void_p(t.data_ptr()), pitch
+
+
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def quantize_fp8(x: torch.Tensor, stream=None):
+    """Rows x [T][K] (bf16, fp16 or fp32, any row pitch) as e4m3 codes [T][K] and fp32 scales
+    [T][ceil(K/128)] of 1 x 128 blocks (moe_quantize_rows).  Both are views of padded rows, as
+    ``Fp8Linear.forward_quantized`` takes them."""
+    lib = load_library()
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
+    T, K = x.shape
+    if K < 1:
+        raise ValueError("x must have at least one column")
+    px, ldx = _rows(x, "x", DTYPES, K)
+    nb = _blocks(K)
+    q = torch.empty((T, nb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
+    s = torch.empty((T, (nb + 3) // 4 * 4), dtype=torch.float32, device=x.device)
+    _check(lib.moe_quantize_rows(px, DTYPES[x.dtype], ldx, T, K, _ptr(q), q.shape[1], _ptr(s), s.shape[1],
+                                 _stream(stream)))
+    return q[:, :K], s[:, :nb]
+
+
+def quantize_fp8_weight(w: torch.Tensor, stream=None):
+    """A weight [..., rows, K] as e4m3 codes of the same shape and fp32 scales
+    [..., ceil(rows/128), ceil(K/128)] of 128 x 128 blocks (moe_quantize_blocks, a call per matrix)."""
+    lib = load_library()
+    if w.dim() < 2 or w.shape[-1] < 1:
+        raise ValueError(f"w must be a matrix or a batch of matrices, got {tuple(w.shape)}")
+    if not w.is_cuda or w.dtype not in DTYPES:
+        raise ValueError("w must be a CUDA tensor of bf16, fp16 or fp32")
+    rows, K = w.shape[-2:]
+    w = w.contiguous()
+    q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
+    s = torch.empty((*w.shape[:-2], _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
+    for wm, qm, sm in zip(w.view(-1, rows, K), q.view(-1, rows, K), s.view(-1, s.shape[-2], s.shape[-1])):
+        _check(lib.moe_quantize_blocks(_ptr(wm), DTYPES[w.dtype], rows, K, _ptr(qm), _ptr(sm), _stream(stream)))
+    return q, s
+
+
+class Fp8Linear:
+    """A projection with e4m3 weights and a scale for each block of 128 x 128 (C ABI ``moe_linear``).
+
+        lin = Fp8Linear(N, K)
+        lin.set_weights(*quantize_fp8_weight(w))     # w [N][K]
+        lin.allocate_workspace(T_max)
+        out = lin.forward(x)                         # x [T][K] -> [T][N]
+    """
+
+    def __init__(self, N: int, K: int):
+        self.lib = load_library()
+        self.N, self.K = N, K
+        h = self.lib.moe_linear_create(N, K)
+        if not h:
+            raise MoeError(MOE_ERR_INVALID_ARG, self.lib.moe_last_error().decode())
+        self._h = ctypes.c_void_p(h)
+        self._ws = None
+        self.T_max = 0
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value:
+            self.lib.moe_linear_destroy(h)
+            self._h = None
+
+    close = __del__
+
+    def set_weights(self, q: torch.Tensor, s: torch.Tensor):
+        _check(self.lib.moe_linear_set_weights(
+            self._h, _dev(q, "q", torch.float8_e4m3fn, (self.N, self.K)),
+            _dev(s, "s", torch.float32, (_blocks(self.N), _blocks(self.K)))))
+
+    def workspace_bytes(self, T_max: int) -> int:
+        return int(self.lib.moe_linear_workspace_bytes(self._h, T_max))
+
+    def set_workspace(self, buf: torch.Tensor, T_max: int):
+        _check(self.lib.moe_linear_set_workspace(self._h, _dev(buf, "workspace"), buf.numel() * buf.element_size(), T_max))
+        self._ws = buf
+        self.T_max = T_max
+
+    def allocate_workspace(self, T_max: int, device=None) -> torch.Tensor:
+        buf = torch.empty(self.workspace_bytes(T_max), dtype=torch.uint8, device=device or "cuda")
+        self.set_workspace(buf, T_max)
+        return buf
+
+    def _out(self, T, out, out_dtype, device):
+        if out is None:
+            out = torch.empty((T, self.N), dtype=out_dtype, device=device)
+        return out, *_rows(out, "out", (torch.bfloat16, torch.float32), self.N)
+
+    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None):
+        """x [T][K] (bf16, fp16 or fp32; rows may have a pitch) -> [T][N] in bf16 or fp32."""
+        px, ldx = _rows(x, "x", DTYPES, self.K)
+        T = x.shape[0]
+        out, po, ldo = self._out(T, out, out_dtype, x.device)
+        if out.shape[0] != T:
+            raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
+        _check(self.lib.moe_linear_forward(self._h, px, DTYPES[x.dtype], ldx, T, po, DTYPES[out.dtype], ldo, _stream(stream)))
+        return out
+
+    def forward_quantized(self, q: torch.Tensor, s: torch.Tensor, out: Optional[torch.Tensor] = None,
+                          out_dtype=torch.bfloat16, stream=None):
+        """The same for rows that ``quantize_fp8`` already quantised (several projections of one x)."""
+        pq, ldq = _rows(q, "q", (torch.float8_e4m3fn,), self.K)
+        ps, lds = _rows(s, "s", (torch.float32,), _blocks(self.K))
+        T = q.shape[0]
+        if s.shape[0] != T:
+            raise ValueError(f"s must have {T} rows, got {s.shape[0]}")
+        if T == 1:  # a single row: its pitch may be anything; only its padding to the vector width matters
+            ldq, lds = (ldq + 15) // 16 * 16, (lds + 3) // 4 * 4
+        out, po, ldo = self._out(T, out, out_dtype, q.device)
+        if out.shape[0] != T:
+            raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
+        _check(self.lib.moe_linear_forward_quantized(self._h, pq, ldq, ps, lds, T, po, DTYPES[out.dtype], ldo,
+                                                     _stream(stream)))
+        return out
+
+    def device_error(self) -> int:
+        code = ctypes.c_uint32(0)
+        st = self.lib.moe_linear_get_device_error(self._h, ctypes.byref(code))
+        if st not in (MOE_OK, MOE_ERR_DEVICE):
+            _check(st)
+        return int(code.value)
 
 
 class MoePlan:

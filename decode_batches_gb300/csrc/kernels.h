@@ -11,6 +11,9 @@ namespace moe {
 
 // Sets the thread's moe_last_error() message and returns s (api.cu).
 moe_status fail_message(moe_status s, const char* msg);
+// 2-D byte tensor [rows][inner] (row pitch ld bytes, a multiple of 16), box {128, 32}, 128-byte swizzle:
+// 8-bit rows as a GEMM operand.  Bytes beyond the extents read as zero (api.cu).
+moe_status make_map_f8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld);
 
 // A conversion x (bf16) -> x16 (fp16) of n8 * 8 elements that a kernel performs on the side with
 // every thread of its grid (the 4-bit path's activation copy; convert_x16 in common.cuh);
@@ -183,6 +186,61 @@ cudaError_t launch_mx_down(const TcArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_h_to_mx(const uint16_t* h, uint8_t* hq, uint8_t* hs, int R, int f, cudaStream_t st);
 // scale bytes per quantised row of K elements (K / 32 rounded up to a multiple of 4)
 int mx_scale_bytes(int K);
+
+// ---- 8-bit block-scaled path (quant_fp8.cu, gemm_fp8.cu) ---------------------------------------
+// One stage tile of 8-bit weights: 128 rows x 128 K elements, stored as the 128-byte-swizzled K-major
+// shared-memory image ((r, 16-byte chunk c) at r * 128 + ((c ^ (r & 7)) << 4)).  A GEMM tile is 256
+// weight rows, two such halves, adjacent at each K block (a lone last half stands alone):
+//   linear / down: half h = rows 128 h .. 128 h + 127 of the matrix;
+//   gate/up: half h = gate rows 64 h .. 64 h + 63, then the up rows of the same features; always
+//     whole tiles (128 features, the block that shares one activation scale of h).
+// Scales [matrix][tile][K block][2]: the two 128-row blocks', or gate's and up's.
+constexpr int kF8TileBytes = 128 * 128;
+__host__ __device__ inline int f8_halves(int rows, bool gate_up) {
+  return gate_up ? 2 * ((rows + 127) / 128) : (rows + 127) / 128;
+}
+__host__ __device__ inline int64_t f8_half_offset(int h, int kb, int halves, int nk) {
+  const int t = h >> 1, np = halves - 2 * t < 2 ? 1 : 2;
+  return (static_cast<int64_t>(t) * 2 * nk + static_cast<int64_t>(kb) * np + (h & 1)) * kF8TileBytes;
+}
+// Row pitch of an activation's block scales: 16-byte groups of four K blocks.
+__host__ __device__ inline int f8_scale_ld(int nk) { return (nk + 3) & ~3; }
+
+cudaError_t launch_quant_rows(const void* x, moe_dtype dt, int64_t ldx, int rows, int K, uint8_t* q, int64_t ldq,
+                              float* s, int64_t lds, int num_sms, cudaStream_t st);
+cudaError_t launch_quant_blocks(const void* w, moe_dtype dt, int64_t ldw, int rows, int K, uint8_t* q, int64_t ldq,
+                                float* s, int64_t lds, cudaStream_t st);
+// n matrices [rows][K] of codes (b != nullptr: gate = a and up = b) and their scales
+// [n][ceil(rows/128)][ceil(K/128)] into the layout above.
+cudaError_t launch_tile_fp8(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, uint8_t* dst,
+                            float* sdst, int n, int rows, int K, cudaStream_t st);
+
+struct F8Args {
+  const uint8_t* w = nullptr;   // tiled weights; matrix stride w_stride bytes
+  const float* ws = nullptr;    // tiled scales; matrix stride tiles * nk * 2
+  int64_t w_stride = 0;
+  const uint8_t* a = nullptr;   // gate/up: e4m3 rows of x (gathered by perm), pitch lda bytes
+  int64_t lda = 0;
+  const float* as = nullptr;    // activation scales, pitch lds floats (a multiple of 4)
+  int64_t lds = 0;
+  const Seg* segs = nullptr;    // routed rows; linear: the T rows split evenly
+  const int32_t* n_segs = nullptr;
+  const int32_t* perm = nullptr;
+  uint8_t* hq = nullptr;        // gate/up out: e4m3 rows [grouped rows][ldh], scales [.][ldhs]
+  float* hs = nullptr;
+  int64_t ldh = 0, ldhs = 0;
+  void* out = nullptr;          // linear / down out [rows][ldo] of out_type, columns < N
+  int64_t ldo = 0;
+  int out_type = MOE_FP16;      // fp16 (the layer's y: clamped, flags MOE_DEVERR_RANGE), bf16 or fp32
+  int out_vec = 0;              // 32-byte stores are aligned
+  int N = 0, halves = 0, nk = 0;
+  int T = 0, k = 0;
+  uint32_t* err = nullptr;
+};
+// amap: the activation rows [rows][K] as bytes, box {128, 32}, 128-byte swizzle (not gate/up).
+cudaError_t launch_f8_gateup(const F8Args& a, int num_sms, cudaStream_t st);
+cudaError_t launch_f8_down(const CUtensorMap* amap, const F8Args& a, int num_sms, cudaStream_t st);
+cudaError_t launch_f8_linear(const CUtensorMap* amap, const F8Args& a, int num_sms, cudaStream_t st);
 
 // ---- one-launch layer of a small step (layer_small.cu) ------------------------------------------
 constexpr int kLsTMax = 8;                  // tokens per step

@@ -67,10 +67,16 @@ typedef enum {
 
 typedef enum {
   MOE_W_BF16 = 0,  /* routed expert weights in bf16 */
-  MOE_W_MXFP4 = 1  /* routed expert weights block-scaled 4-bit: e2m1 codes, two per byte
+  MOE_W_MXFP4 = 1, /* routed expert weights block-scaled 4-bit: e2m1 codes, two per byte
                       (even element in the low nibble, bit 3 = sign), one e8m0 scale byte
                       2^(s-127) per 32 consecutive K elements (OCP MX v1.0) */
+  MOE_W_FP8 = 3    /* routed expert weights in e4m3 with one fp32 scale per 128 x 128 block
+                      (rows and columns counted from 0, partial blocks at the edges); the
+                      activations are quantised on the fly, see moe_quantize_rows */
 } moe_wdtype;
+
+/* Element types of tensors whose type is an argument. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
 
 /* Which kernels run the expert FFN (gate/up + SwiGLU + down). */
 typedef enum {
@@ -331,6 +337,61 @@ typedef struct {
 moe_status moe_compose_prefill(int64_t start_pos, int64_t n_tokens, int32_t quantum,
                                int32_t generation_active, int32_t prefill_cap,
                                moe_prefill_call* calls, int64_t max_calls, int64_t* n_calls);
+
+/*
+ * 8-bit blocks.  Source: "moe-prefill-quantum", hardware-check paragraph (a quantised weight read
+ * is unpack, times scale, accumulate) and the DSpark paragraph of "DeepSeek V4.1F Q4 with native
+ * DSpark MTP on M3 Ultra" (8-bit projections of a 6-row verify block); the format is this
+ * library's choice.  A block of values with largest magnitude amax is stored as e4m3 codes q
+ * (sign, 4 exponent bits, 3 mantissa bits, largest value 448, 0x7F / 0xFF NaN) and one fp32 scale s:
+ *   s = max(amax / 448, 2^-126),  q = e4m3(v * (1 / s)),  v ~ q * s,
+ * the quotients and the product in fp32, q rounded to nearest even.  A NaN element keeps the code
+ * of NaN; an infinite element makes its block's scale infinite and the block NaN.
+ *
+ * moe_quantize_rows: rows [T][K] of x_dtype (row pitch ldx elements) in blocks of 1 x 128 along K
+ *   (the last one partial): codes uint8 [T][ldq] (ldq >= K rounded up to 128, a multiple of 16; the
+ *   columns from K to the end of the last block are zeroed), scales fp32 [T][lds], lds >= ceil(K / 128).
+ * moe_quantize_blocks: a matrix [rows][K] in blocks of 128 x 128: codes [rows][K] without
+ *   padding, scales [ceil(rows / 128)][ceil(K / 128)].
+ * Both only enqueue work; codes must be 16-byte aligned.  T == 0 or rows == 0 enqueues nothing.
+ */
+moe_status moe_quantize_rows(const void* x, moe_dtype x_dtype, int64_t ldx, int T, int K, uint8_t* q, int64_t ldq,
+                            float* s, int64_t lds, moe_stream_t stream);
+moe_status moe_quantize_blocks(const void* w, moe_dtype w_dtype, int rows, int K, uint8_t* q, float* s,
+                                   moe_stream_t stream);
+
+/*
+ * A projection with 8-bit weights: out[t][n] = sum_b sa[t][b] sw[n / 128][b] (sum over block b of
+ * a[t][k] w[n][k]).  Source: the 8-bit projections of the DSpark paragraph (above); the pages have
+ * no counterpart to the 8-bit activations.  The sums of one block of 128 are formed by the tensor
+ * core and added up in fp32.
+ *   moe_linear_create       N output features, K input features, both >= 1 (<= 2^20).  Host only.
+ *   moe_linear_set_weights  codes [N][K] and scales [ceil(N/128)][ceil(K/128)] (device), copied into
+ *                               memory of the handle in the kernel's layout; synchronous.
+ *   ..._workspace_bytes / set_workspace   caller-owned memory for the quantised rows of up to T_max rows,
+ *                               256-byte aligned; one call at a time uses it (order them on a stream).
+ *   moe_linear_forward      x [T][K] of x_dtype (pitch ldx) is quantised (moe_quantize_rows) and
+ *                               multiplied; out [T][N] (pitch ldo) in out_dtype, MOE_BF16 or MOE_FP32.
+ *   moe_linear_forward_quantized   the same for rows that are already codes (pitch ldq, a multiple
+ *                               of 16, 16-byte aligned) with their scales (pitch lds, a multiple of 4,
+ *                               16-byte aligned); columns beyond K are not read; needs no workspace.
+ *   moe_linear_get_device_error    as moe_plan_get_device_error, for the handle's calls.
+ * The forward calls only enqueue work, and a NULL or not-ready handle, T < 0 or T > T_max, a pitch
+ * below the width or an unknown type is an error before any launch.
+ */
+typedef struct moe_linear moe_linear; /* opaque */
+
+moe_linear* moe_linear_create(int N, int K);
+void moe_linear_destroy(moe_linear* lin);
+moe_status moe_linear_set_weights(moe_linear* lin, const uint8_t* q, const float* s);
+size_t moe_linear_workspace_bytes(const moe_linear* lin, int T_max);
+moe_status moe_linear_set_workspace(moe_linear* lin, void* dev_ptr, size_t bytes, int T_max);
+moe_status moe_linear_forward(moe_linear* lin, const void* x, moe_dtype x_dtype, int64_t ldx, int T, void* out,
+                                  moe_dtype out_dtype, int64_t ldo, moe_stream_t stream);
+moe_status moe_linear_forward_quantized(moe_linear* lin, const uint8_t* q, int64_t ldq, const float* s,
+                                            int64_t lds, int T, void* out, moe_dtype out_dtype, int64_t ldo,
+                                            moe_stream_t stream);
+moe_status moe_linear_get_device_error(moe_linear* lin, uint32_t* code);
 
 #ifdef __cplusplus
 }
