@@ -22,7 +22,7 @@ from .build import LIB as LIB_PATH
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_NOT_READY = 0, 1, 2, 3
 MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE, MOE_ERR_TIMEOUT = 4, 5, 6, 7
-MOE_W_BF16, MOE_W_MXFP4 = 0, 1
+MOE_W_BF16, MOE_W_MXFP4, MOE_W_FP8 = 0, 1, 3
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # moe_dtype
 FP8_BLOCK = 128  # elements (of a row), or rows and columns (of a weight), that share a scale
 PATHS = {"auto": 0, "simt": 1, "tc": 2}
@@ -36,7 +36,7 @@ EXPORTED = (
     "moe_plan_last_launch_count", "moe_compose_prefill", "moe_permute_static", "moe_selftest_wait_expiry",
     "moe_plan_resolved_path", "moe_quantize_rows", "moe_quantize_blocks", "moe_linear_create", "moe_linear_destroy",
     "moe_linear_set_weights", "moe_linear_workspace_bytes", "moe_linear_set_workspace", "moe_linear_forward",
-    "moe_linear_forward_quantized", "moe_linear_get_device_error",
+    "moe_linear_forward_quantized", "moe_linear_get_device_error", "moe_layer_forward_routed",
 )
 
 _lib = None
@@ -74,6 +74,7 @@ def load_library(path: str = LIB_PATH):
         "moe_plan_set_workspace": ([vp, vp, sz, i32], i32),
         "moe_plan_set_path": ([vp, i32], i32),
         "moe_layer_forward": ([vp, vp, i32, i32, vp, vp], i32),
+        "moe_layer_forward_routed": ([vp, vp, i32, vp, vp, vp, vp], i32),
         "moe_route": ([vp, vp, i32, vp, vp, vp, vp], i32),
         "moe_route_logits": ([vp, vp, i32, vp, vp, vp], i32),
         "moe_permute": ([vp, vp, i32, vp, vp, vp, vp, vp], i32),
@@ -297,7 +298,7 @@ class MoePlan:
 
     def __init__(self, E: int, k: int, d_model: int, d_ff: int, n_shared: int = 0, weight_dtype: str = "bf16"):
         self.lib = load_library()
-        wd = {"bf16": MOE_W_BF16, "mxfp4": MOE_W_MXFP4}[weight_dtype]
+        wd = {"bf16": MOE_W_BF16, "mxfp4": MOE_W_MXFP4, "fp8": MOE_W_FP8}[weight_dtype]
         self.E, self.k, self.d, self.f, self.n_shared, self.weight_dtype = E, k, d_model, d_ff, n_shared, weight_dtype
         self.f_s = 0
         h = self.lib.moe_plan_create(E, k, d_model, d_ff, n_shared, wd)
@@ -323,6 +324,12 @@ class MoePlan:
         if self.weight_dtype == "bf16":
             args += [_dev(w_gate, "w_gate", torch.bfloat16, (E, f, d)), _dev(w_up, "w_up", torch.bfloat16, (E, f, d)),
                      _dev(w_down, "w_down", torch.bfloat16, (E, d, f)), None, None, None]
+        elif self.weight_dtype == "fp8":
+            f8, bd, bf = torch.float8_e4m3fn, _blocks(d), _blocks(f)
+            args += [_dev(w_gate, "w_gate", f8, (E, f, d)), _dev(w_up, "w_up", f8, (E, f, d)),
+                     _dev(w_down, "w_down", f8, (E, d, f)),
+                     _dev(s_gate, "s_gate", torch.float32, (E, bf, bd)), _dev(s_up, "s_up", torch.float32, (E, bf, bd)),
+                     _dev(s_down, "s_down", torch.float32, (E, bd, bf))]
         else:
             args += [_dev(w_gate, "w_gate", torch.uint8, (E, f, d // 2)), _dev(w_up, "w_up", torch.uint8, (E, f, d // 2)),
                      _dev(w_down, "w_down", torch.uint8, (E, d, f // 2)),
@@ -360,6 +367,18 @@ class MoePlan:
             out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
         _check(self.lib.moe_layer_forward(self._h, _dev(x, "x", torch.bfloat16, (T, self.d)), T, n_prefill,
                                           _dev(out, "out", torch.bfloat16, (T, self.d)), _stream(stream)))
+        return out
+
+    def forward_routed(self, x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor,
+                       out: Optional[torch.Tensor] = None, stream=None):
+        """The layer for given ids and gates [T][k] (moe_layer_forward_routed)."""
+        T = x.shape[0]
+        if out is None:
+            out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
+        _check(self.lib.moe_layer_forward_routed(self._h, _dev(x, "x", torch.bfloat16, (T, self.d)), T,
+                                                 _dev(ids, "ids", torch.int32, (T, self.k)),
+                                                 _dev(gates, "gates", torch.float32, (T, self.k)),
+                                                 _dev(out, "out", torch.bfloat16, (T, self.d)), _stream(stream)))
         return out
 
     def route(self, x: torch.Tensor, want_logits: bool = True, stream=None):

@@ -56,6 +56,7 @@ struct WsLayout {
   size_t touched, y32;  // the one-launch small-step layer: touched-expert list, fp32 expert outputs
   size_t xq, xs;        // the block-scaled 4-bit gate/up: x as two e4m3 terms and their e8m0 scales
   size_t hq, hs;        // ... and down: h as two e4m3 terms and their e8m0 scales
+  size_t x8, x8s, h8, h8s;  // 8-bit weights: x and h in e4m3 blocks of 128 and their fp32 scales
   size_t total;
   int max_segs;
 };
@@ -95,6 +96,9 @@ struct moe_plan {
   // instead of the dequantising kernels (the default, faster as measured); env MOE_FP4_GATEUP /
   // MOE_FP4_DOWN = mx selects the former at plan creation
   bool fp4_mx = false, fp4_mx_down = false;
+  float* ws_gu = nullptr;    // 8-bit weights: block scales of the tiled w_gu and w_down
+  float* ws_down = nullptr;
+  CUtensorMap map_h8{};      // ... and h's codes as the down GEMM's operand
   // steps of at most 8 tokens with bf16 weights: the one-launch layer (layer_small.cu) instead of
   // the routing launch + tensor-core GEMMs + combine; env MOE_SMALL_STEP = fused | multi
   bool small_fused = false;
@@ -116,6 +120,9 @@ struct moe_plan {
   int launch_count = 0;
 
   bool router_tc_capable() const { return E % 128 == 0 && d % 64 == 0; }
+  // 8-bit path: K blocks of x and of h, and the gate/up tiles (128 features each)
+  int nk_x() const { return (d + 127) / 128; }
+  int nk_h() const { return (f + 127) / 128; }
 };
 
 static WsLayout layout_for(const moe_plan* p, int T_max) {
@@ -153,7 +160,8 @@ static WsLayout layout_for(const moe_plan* p, int T_max) {
   L.inv = take(R * sizeof(int32_t));
   L.segs = take(static_cast<size_t>(L.max_segs) * sizeof(Seg));
   L.n_segs = take(sizeof(int32_t));
-  L.h = take(R * p->f * 2);
+  const bool fp8 = p->wdtype == MOE_W_FP8;
+  L.h = take(fp8 ? 0 : R * p->f * 2);
   L.h_s = take(T * static_cast<size_t>(p->n_shared) * p->f_s * 2);
   L.y = take(R * p->d * 2);
   L.y_s = take(T * p->d * 2);
@@ -165,6 +173,10 @@ static WsLayout layout_for(const moe_plan* p, int T_max) {
   L.hq = take(p->wdtype == MOE_W_MXFP4 ? R * 2 * p->f : 0);
   L.hs = take(p->wdtype == MOE_W_MXFP4 ? R * 2 * static_cast<size_t>(mx_scale_bytes(p->f)) : 0);
   L.y32 = take(p->wdtype == MOE_W_BF16 ? T8 * (p->k + 1) * p->d * sizeof(float) : 0);
+  L.x8 = take(fp8 ? T * p->nk_x() * 128 : 0);
+  L.x8s = take(fp8 ? T * f8_scale_ld(p->nk_x()) * sizeof(float) : 0);
+  L.h8 = take(fp8 ? R * p->nk_h() * 128 : 0);
+  L.h8s = take(fp8 ? R * f8_scale_ld(p->nk_h()) * sizeof(float) : 0);
   L.total = o;
   return L;
 }
@@ -176,8 +188,10 @@ static Tp* ws_ptr(const moe_plan* p, size_t off) {
 
 // The tensor-core path: bf16 routed weights with d % 128 == 0 and d_ff % 64 == 0, or 4-bit
 // routed weights in the tiled layout whose scales all allow exact fp16 dequantisation; shared
-// experts need d_ff_shared % 64 == 0.
+// experts need d_ff_shared % 64 == 0.  8-bit weights have no other path (moe_plan_set_shared
+// refuses shared experts that it cannot run).
 static bool tc_shape_ok(const moe_plan* p) {
+  if (p->wdtype == MOE_W_FP8) return true;
   const bool routed = p->wdtype == MOE_W_BF16 ? (p->d % 128 == 0 && p->f % 64 == 0) : p->fp4_tc;
   return routed && (p->n_shared == 0 || p->f_s % 64 == 0);
 }
@@ -286,7 +300,7 @@ moe_status moe::make_map_f8(CUtensorMap* m, const void* base, uint64_t inner, ui
 
 static moe_status build_weight_maps(moe_plan* p) {
   // the tensor-core path reads the tile-contiguous weights directly (bulk copies, no maps)
-  const bool routed = p->wdtype == MOE_W_BF16 ? p->tiled : p->fp4_tc;
+  const bool routed = p->wdtype == MOE_W_BF16 ? p->tiled : p->wdtype == MOE_W_MXFP4 ? p->fp4_tc : true;
   p->maps_weights = tc_shape_ok(p) && p->weights_set && routed && (p->n_shared == 0 || (p->shared_set && p->tiled_s));
   return MOE_OK;
 }
@@ -297,10 +311,16 @@ static moe_status build_ws_maps(moe_plan* p) {
   const uint64_t R = static_cast<uint64_t>(p->T_max) * p->k;
   moe_status s;
   const CUtensorMapDataType F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  if ((s = make_map_16(&p->maps.h, p->ws + p->L.h, p->f, R, 32, F16)) != MOE_OK) return s;
+  if (p->wdtype == MOE_W_FP8) {
+    const uint64_t ldh = static_cast<uint64_t>(p->nk_h()) * 128;
+    if ((s = make_map_f8(&p->map_h8, p->ws + p->L.h8, ldh, R, ldh)) != MOE_OK) return s;
+  } else if ((s = make_map_16(&p->maps.h, p->ws + p->L.h, p->f, R, 32, F16)) != MOE_OK) {
+    return s;
+  }
   if (p->n_shared > 0 && p->f_s > 0) {
     if ((s = make_map_16(&p->maps.h_s, p->ws + p->L.h_s, static_cast<uint64_t>(p->n_shared) * p->f_s, p->T_max, 32, F16)) != MOE_OK)
       return s;
+    if (p->wdtype == MOE_W_FP8) p->maps.h = p->maps.h_s;  // the 16-bit kernels run shared units only
   }
   p->maps_ws = true;
   return MOE_OK;
@@ -314,7 +334,7 @@ extern "C" moe_plan* moe_plan_create(int E, int k, int d_model, int d_ff, int n_
     fail(MOE_ERR_INVALID_ARG, "need 1 <= k <= E <= 1024 and k <= 32 (E=%d k=%d)", E, k);
     return nullptr;
   }
-  if (weight_dtype != MOE_W_BF16 && weight_dtype != MOE_W_MXFP4) {
+  if (weight_dtype != MOE_W_BF16 && weight_dtype != MOE_W_MXFP4 && weight_dtype != MOE_W_FP8) {
     fail(MOE_ERR_INVALID_ARG, "unknown weight dtype %d", static_cast<int>(weight_dtype));
     return nullptr;
   }
@@ -341,7 +361,7 @@ extern "C" moe_plan* moe_plan_create(int E, int k, int d_model, int d_ff, int n_
   if (const char* env = getenv("MOE_FP4_DOWN")) p->fp4_mx_down = strcmp(env, "mx") == 0;
   if (const char* env = getenv("MOE_SMALL_STEP")) p->small_fused = strcmp(env, "fused") == 0;
   if (const char* env = getenv("MOE_FORCE_PATH")) {
-    if (!strcmp(env, "simt")) p->path = MOE_PATH_SIMT;
+    if (!strcmp(env, "simt") && weight_dtype != MOE_W_FP8) p->path = MOE_PATH_SIMT;
     else if (!strcmp(env, "tc")) p->path = MOE_PATH_TC;
   }
   g_last_error.clear();
@@ -358,6 +378,9 @@ static void free_weights(moe_plan* p) {
   cudaFree(p->s_gu);
   cudaFree(p->w_down);
   cudaFree(p->s_down);
+  cudaFree(p->ws_gu);
+  cudaFree(p->ws_down);
+  p->ws_gu = p->ws_down = nullptr;
   p->w_router = p->b_router = nullptr;
   p->w_gu = p->s_gu = p->w_down = p->s_down = nullptr;
   p->weights_set = false;
@@ -439,15 +462,18 @@ static moe_status copy_bf16_as_f16(uint16_t* dst, const void* src, size_t n) {
 }
 extern "C" moe_status moe_plan_set_weights(moe_plan* p, const float* w_router, const float* b_router,
                                            const void* w_gate, const void* w_up, const void* w_down,
-                                           const uint8_t* s_gate, const uint8_t* s_up, const uint8_t* s_down) {
+                                           const void* s_gate_p, const void* s_up_p, const void* s_down_p) {
   if (!p) return fail(MOE_ERR_INVALID_ARG, "plan is NULL");
   if (!w_router || !w_gate || !w_up || !w_down)
     return fail(MOE_ERR_INVALID_ARG, "w_router, w_gate, w_up and w_down are required");
-  const bool fp4 = p->wdtype == MOE_W_MXFP4;
-  if (fp4 && (!s_gate || !s_up || !s_down))
-    return fail(MOE_ERR_INVALID_ARG, "MOE_W_MXFP4 needs s_gate, s_up and s_down");
-  if (!fp4 && (s_gate || s_up || s_down))
-    return fail(MOE_ERR_INVALID_ARG, "scales are only valid with MOE_W_MXFP4");
+  const bool fp4 = p->wdtype == MOE_W_MXFP4, fp8 = p->wdtype == MOE_W_FP8;
+  const uint8_t* s_gate = static_cast<const uint8_t*>(s_gate_p);
+  const uint8_t* s_up = static_cast<const uint8_t*>(s_up_p);
+  const uint8_t* s_down = static_cast<const uint8_t*>(s_down_p);
+  if ((fp4 || fp8) && (!s_gate || !s_up || !s_down))
+    return fail(MOE_ERR_INVALID_ARG, "MOE_W_MXFP4 and MOE_W_FP8 need s_gate, s_up and s_down");
+  if (!fp4 && !fp8 && (s_gate || s_up || s_down))
+    return fail(MOE_ERR_INVALID_ARG, "scales are only valid with MOE_W_MXFP4 and MOE_W_FP8");
   moe_status s = ensure_err_word(p);
   if (s != MOE_OK) return s;
   cudaDeviceSynchronize();
@@ -470,6 +496,26 @@ extern "C" moe_status moe_plan_set_weights(moe_plan* p, const float* w_router, c
     MOE_CUDA_TRY(cudaMemcpy(p->b_router, b_router, E * sizeof(float), cudaMemcpyDeviceToDevice));
   else
     MOE_CUDA_TRY(cudaMemset(p->b_router, 0, E * sizeof(float)));
+  if (fp8) {
+    const size_t gu_halves = f8_halves(p->f, true), dn_halves = f8_halves(p->d, false);
+    MOE_CUDA_TRY(cudaMalloc(&p->w_gu, E * gu_halves * p->nk_x() * kF8TileBytes));
+    MOE_CUDA_TRY(cudaMalloc(&p->ws_gu, E * (gu_halves / 2) * p->nk_x() * 2 * sizeof(float)));
+    MOE_CUDA_TRY(cudaMalloc(&p->w_down, E * dn_halves * p->nk_h() * kF8TileBytes));
+    MOE_CUDA_TRY(cudaMalloc(&p->ws_down, E * ((dn_halves + 1) / 2) * p->nk_h() * 2 * sizeof(float)));
+    cudaError_t e = launch_tile_fp8(static_cast<const uint8_t*>(w_gate), static_cast<const float*>(s_gate_p),
+                                    static_cast<const uint8_t*>(w_up), static_cast<const float*>(s_up_p), p->w_gu, p->ws_gu,
+                                    p->E, p->f, p->d, 0);
+    if (e == cudaSuccess)
+      e = launch_tile_fp8(static_cast<const uint8_t*>(w_down), static_cast<const float*>(s_down_p), nullptr, nullptr,
+                          p->w_down, p->ws_down, p->E, p->d, p->f, 0);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) {
+      free_weights(p);
+      return fail(MOE_ERR_CUDA, "8-bit weight tiling: %s", cudaGetErrorString(e));
+    }
+    p->weights_set = true;
+    return build_weight_maps(p);
+  }
   const size_t gu_row = fp4 ? d / 2 : d * 2;     // bytes per gate/up row
   const size_t dn_row = fp4 ? f / 2 : f * 2;     // bytes per down row
   p->tiled = !fp4 && d % 128 == 0 && f % 64 == 0;
@@ -540,6 +586,8 @@ extern "C" moe_status moe_plan_set_shared(moe_plan* p, int d_ff_shared, const vo
   if (p->n_shared == 0) return fail(MOE_ERR_INVALID_ARG, "plan was created with n_shared = 0");
   if (d_ff_shared <= 0 || d_ff_shared % 8) return fail(MOE_ERR_INVALID_ARG, "d_ff_shared must be a positive multiple of 8");
   if (!w_gate || !w_up || !w_down) return fail(MOE_ERR_INVALID_ARG, "shared weights are required");
+  if (p->wdtype == MOE_W_FP8 && (p->d % 128 || d_ff_shared % 64))
+    return fail(MOE_ERR_UNSUPPORTED, "shared experts beside 8-bit weights need d_model %% 128 == 0 and d_ff_shared %% 64 == 0");
   if (p->ws && d_ff_shared != p->f_s)
     return fail(MOE_ERR_INVALID_ARG, "d_ff_shared changed after the workspace was set; set the workspace again");
   moe_status s = ensure_err_word(p);
@@ -609,6 +657,8 @@ extern "C" moe_status moe_plan_set_path(moe_plan* p, moe_path path) {
   if (!p) return fail(MOE_ERR_INVALID_ARG, "plan is NULL");
   if (path != MOE_PATH_AUTO && path != MOE_PATH_SIMT && path != MOE_PATH_TC)
     return fail(MOE_ERR_INVALID_ARG, "unknown path %d", static_cast<int>(path));
+  if (path == MOE_PATH_SIMT && p->wdtype == MOE_W_FP8)
+    return fail(MOE_ERR_UNSUPPORTED, "8-bit weights have no CUDA-core path");
   if (path == MOE_PATH_TC && !tc_shape_ok(p))
     return fail(MOE_ERR_UNSUPPORTED, "tensor-core path needs bf16 weights, d %% 128 == 0, d_ff %% 64 == 0, d_ff_shared %% 64 == 0");
   p->path = path;
@@ -722,7 +772,7 @@ static TcArgs shared_args(const moe_plan* p, const TcArgs& a, int T, bool gate_u
   return sh;
 }
 
-// With 4-bit routed weights the shared experts run on their own launches.  Their gate/up
+// With 4-bit or 8-bit routed weights the shared experts run on their own launches.  Their gate/up
 // depends on x alone, so when it fills at most half of the SMs it runs on the plan's second
 // stream beside the router and the grouping (which leave most SMs idle at such T) instead of
 // after them.  The shared down projection follows it there when kSharedDownBeside (it needs h_s
@@ -731,7 +781,7 @@ static TcArgs shared_args(const moe_plan* p, const TcArgs& a, int T, bool gate_u
 constexpr bool kSharedDownBeside = true;
 
 static bool shared_gate_up_beside(const moe_plan* p, int T) {
-  if (!use_tc(p) || p->wdtype != MOE_W_MXFP4 || p->n_shared == 0 || !p->side) return false;
+  if (!use_tc(p) || p->wdtype == MOE_W_BF16 || p->n_shared == 0 || !p->side) return false;
   const long tiles = static_cast<long>(p->n_shared) * p->f_s / 64;
   const int pair = tc_pair(p, T, false, true);
   const long units = static_cast<long>((T + kSegRowsMax - 1) / kSegRowsMax) * ((tiles + pair - 1) / pair);
@@ -753,18 +803,80 @@ static moe_status launch_shared_gate_up_beside(moe_plan* p, const uint16_t* x, i
   return MOE_OK;
 }
 
+// Arguments of the 8-bit gate/up launch (x's blocks ready in the workspace) and, from them, the down
+// launch's.
+static F8Args f8_args(const moe_plan* p, int T, const int32_t* perm) {
+  F8Args a;
+  a.halves = f8_halves(p->f, true);
+  a.nk = p->nk_x();
+  a.w = p->w_gu;
+  a.ws = p->ws_gu;
+  a.w_stride = static_cast<int64_t>(a.halves) * a.nk * kF8TileBytes;
+  a.a = ws_ptr<uint8_t>(p, p->L.x8);
+  a.lda = static_cast<int64_t>(p->nk_x()) * 128;
+  a.as = ws_ptr<float>(p, p->L.x8s);
+  a.lds = f8_scale_ld(p->nk_x());
+  a.segs = ws_ptr<Seg>(p, p->L.segs);
+  a.n_segs = ws_ptr<int32_t>(p, p->L.n_segs);
+  a.perm = perm;
+  a.hq = ws_ptr<uint8_t>(p, p->L.h8);
+  a.hs = ws_ptr<float>(p, p->L.h8s);
+  a.ldh = static_cast<int64_t>(p->nk_h()) * 128;
+  a.ldhs = f8_scale_ld(p->nk_h());
+  a.N = p->f;
+  a.T = T;
+  a.k = p->k;
+  a.err = p->err;
+  return a;
+}
+
+static F8Args f8_down_args(const moe_plan* p, const F8Args& gu, uint16_t* y) {
+  F8Args a = gu;
+  a.halves = f8_halves(p->d, false);
+  a.nk = p->nk_h();
+  a.w = p->w_down;
+  a.ws = p->ws_down;
+  a.w_stride = static_cast<int64_t>(a.halves) * a.nk * kF8TileBytes;
+  a.as = gu.hs;
+  a.lds = gu.ldhs;
+  a.out = y;
+  a.ldo = p->d;
+  a.out_type = MOE_FP16;
+  a.out_vec = (reinterpret_cast<uintptr_t>(y) & 31) == 0 && p->d % 16 == 0;
+  a.N = p->d;
+  return a;
+}
+
 // Expert FFN over grouped rows; y/y_s outputs, h/h_s in the workspace.  For the tensor-core
 // path `segs`/`n_segs` must already describe the routed segments.  shared_forked: the shared
 // expert was launched on the side stream (launch_shared_gate_up_beside); unless its down
 // projection went there too, st joins the side stream before launching it.  x16_ready: the
-// routing already wrote the 4-bit path's fp16 copy of x.
+// routing already wrote the 4-bit path's fp16 copy of x, or the 8-bit path's blocks of it.
 static moe_status run_experts(moe_plan* p, const uint16_t* x, int T, const int32_t* offsets, const int32_t* perm,
                               uint16_t* y, uint16_t* y_s, cudaStream_t st, bool shared_forked = false,
                               bool x16_ready = false) {
   if (use_tc(p)) {
     if (!p->maps_weights || !p->maps_ws) return fail(MOE_ERR_NOT_READY, "tensor maps not built");
     TcArgs a = tc_args(p, x, T, perm, y, y_s);
-    if (p->wdtype == MOE_W_MXFP4) {
+    if (p->wdtype == MOE_W_FP8) {
+      if (!x16_ready)
+        LAUNCH(p, "quant_rows", st,
+               launch_quant_rows(x, MOE_BF16, p->d, T, p->d, ws_ptr<uint8_t>(p, p->L.x8), p->nk_x() * 128,
+                                 ws_ptr<float>(p, p->L.x8s), f8_scale_ld(p->nk_x()), p->num_sms, st));
+      F8Args gu = f8_args(p, T, perm);
+      LAUNCH(p, "f8_gateup", st, launch_f8_gateup(gu, p->num_sms, st));
+      if (p->n_shared > 0 && !shared_forked) {
+        const TcArgs sh = shared_args(p, a, T, true);
+        LAUNCH(p, "tc_gateup_shared", st, launch_tc_gateup(&p->maps, sh, p->num_sms, st));
+      }
+      const F8Args dn = f8_down_args(p, gu, y);
+      LAUNCH(p, "f8_down", st, launch_f8_down(&p->map_h8, dn, p->num_sms, st));
+      if (p->n_shared > 0 && !(shared_forked && kSharedDownBeside)) {
+        if (shared_forked) MOE_CUDA_TRY(cudaStreamWaitEvent(st, p->ev_join, 0));
+        const TcArgs sh = shared_args(p, a, T, false);
+        LAUNCH(p, "tc_down_shared", st, launch_tc_down(&p->maps, sh, p->num_sms, st));
+      }
+    } else if (p->wdtype == MOE_W_MXFP4) {
       // routed experts on the 4-bit kernels (fp16 activations), shared experts on the 16-bit
       // kernels restricted to their units
       uint16_t* x16 = ws_ptr<uint16_t>(p, p->L.x16);
@@ -863,6 +975,20 @@ static moe_status route_step(moe_plan* p, const uint16_t* x, int T, float* logit
 // Device rows are read and written as 16-byte vectors (cp.async, TMA, uint4 stores).
 static bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15) == 0; }
 
+// The 8-bit blocks of x, made on the side by the launch that routes or groups the step (they depend
+// on x alone).
+static XConv x8_conv(const moe_plan* p, const uint16_t* x, int T) {
+  XConv c;
+  c.x = x;
+  c.xq = ws_ptr<uint8_t>(p, p->L.x8);
+  c.xs = ws_ptr<float>(p, p->L.x8s);
+  c.rows = T;
+  c.K = p->d;
+  c.ldq = static_cast<int64_t>(p->nk_x()) * 128;
+  c.lds = f8_scale_ld(p->nk_x());
+  return c;
+}
+
 extern "C" moe_status moe_layer_forward(moe_plan* p, const void* x, int T, int n_prefill, void* out,
                                         moe_stream_t stream) {
   moe_status s = check_ready(p, T, true);
@@ -933,6 +1059,7 @@ extern "C" moe_status moe_layer_forward(moe_plan* p, const void* x, int T, int n
     xc.x16 = ws_ptr<uint16_t>(p, p->L.x16);
     xc.n8 = static_cast<size_t>(T) * p->d / 8;
   }
+  if (p->wdtype == MOE_W_FP8) xc = x8_conv(p, xb, T);
   if (router_nsplit(p, T) == router_small_splits(p->d) && !(p->router_tc && T > kRouterTcMinT) &&
       router_route_tiny_ok(T, p->E, p->d, p->k)) {
     // tiny step: router, top-k and grouping in one launch
@@ -951,17 +1078,52 @@ extern "C" moe_status moe_layer_forward(moe_plan* p, const void* x, int T, int n
            launch_route_small(parts, ns, bias, T, p->E, p->k, ids, gates, counts, offsets, perm, inv, segs,
                               ws_ptr<int32_t>(p, p->L.n_segs), p->L.max_segs, p->err + 1, p->err, st, xc));
   } else {
-    xc = XConv{};
-    s = route_step(p, xb, T, nullptr, ids, gates, masks, st);
+    // (the 8-bit blocks stay with the top-k launch: a launch of their own costs more than it hides)
+    if (p->wdtype != MOE_W_FP8) xc = XConv{};
+    s = route_step(p, xb, T, nullptr, ids, gates, masks, st, xc);
     if (s != MOE_OK) return s;
     LAUNCH(p, "group", st,
            launch_group(ids, masks, T, p->E, p->k, counts, offsets, perm, inv, segs, ws_ptr<int32_t>(p, p->L.n_segs),
                         p->L.max_segs, p->err, st));
   }
-  s = run_experts(p, xb, T, offsets, perm, y, y_s, st, forked, xc.x16 != nullptr);
+  s = run_experts(p, xb, T, offsets, perm, y, y_s, st, forked, xc.x16 != nullptr || xc.xq != nullptr);
   if (s != MOE_OK) return s;
   if (forked && kSharedDownBeside) MOE_CUDA_TRY(cudaStreamWaitEvent(st, p->ev_join, 0));
   join.armed = false;  // joined (before the shared down projection or here)
+  LAUNCH(p, "combine", st, launch_combine(y, gates, inv, y_s, T, p->k, p->d, static_cast<uint16_t*>(out), st));
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_layer_forward_routed(moe_plan* p, const void* x, int T, const int32_t* ids, const float* gates,
+                                               void* out, moe_stream_t stream) {
+  moe_status s = check_ready(p, T, true);
+  if (s != MOE_OK) return s;
+  p->launch_count = 0;
+  if (T == 0) return MOE_OK;
+  if (!x || !ids || !gates || !out) return fail(MOE_ERR_INVALID_ARG, "x, ids, gates and out are required");
+  if (!aligned16(x) || !aligned16(out)) return fail(MOE_ERR_INVALID_ARG, "x and out must be 16-byte aligned");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const uint16_t* xb = static_cast<const uint16_t*>(x);
+  int32_t* counts = ws_ptr<int32_t>(p, p->L.counts);
+  int32_t* offsets = ws_ptr<int32_t>(p, p->L.offsets);
+  int32_t* perm = ws_ptr<int32_t>(p, p->L.perm);
+  int32_t* inv = ws_ptr<int32_t>(p, p->L.inv);
+  uint16_t* y = ws_ptr<uint16_t>(p, p->L.y);
+  uint16_t* y_s = p->n_shared > 0 ? ws_ptr<uint16_t>(p, p->L.y_s) : nullptr;
+  Seg* segs = use_tc(p) ? ws_ptr<Seg>(p, p->L.segs) : nullptr;
+  int32_t* n_segs = ws_ptr<int32_t>(p, p->L.n_segs);
+  const XConv xc = p->wdtype == MOE_W_FP8 ? x8_conv(p, xb, T) : XConv{};
+  if (route_small_ok(T, p->E, p->k, 1)) {
+    LAUNCH(p, "group_ids", st,
+           launch_group_ids(ids, T, p->E, p->k, counts, offsets, perm, inv, segs, n_segs, p->L.max_segs, p->err, st, xc));
+  } else {
+    uint32_t* masks = ws_ptr<uint32_t>(p, p->L.masks);
+    LAUNCH(p, "masks_from_ids", st, launch_masks_from_ids(ids, T, p->E, p->k, masks, p->err, st, xc));
+    LAUNCH(p, "group", st,
+           launch_group(ids, masks, T, p->E, p->k, counts, offsets, perm, inv, segs, n_segs, p->L.max_segs, p->err, st));
+  }
+  s = run_experts(p, xb, T, offsets, perm, y, y_s, st, false, xc.xq != nullptr);
+  if (s != MOE_OK) return s;
   LAUNCH(p, "combine", st, launch_combine(y, gates, inv, y_s, T, p->k, p->d, static_cast<uint16_t*>(out), st));
   return MOE_OK;
 }

@@ -2,9 +2,8 @@
 // writes such values, and the tensor-core helpers of the 8-bit product.
 //
 // One block of 128 elements (activations) or 128 x 128 (weights) with largest magnitude `amax`:
-//     s = max(amax / 448, 2^-126),   r = fl(1 / s),   q = e4m3(fl(v * r)),   v ~ q * s.
-// The scale and the two products are fp32 (each correctly rounded), the last step rounds to
-// nearest even; |v * r| <= 448 (1 + 2^-22), which e4m3 rounds to 448, its largest value.  An
+//     s = max(fl(amax * fl(1 / 448)), 2^-126),   r = fl(1 / s),   q = e4m3(fl(v * r)),   v ~ q * s.
+// fl is one correctly rounded fp32 operation; the last step rounds to nearest even; |v * r| <= 448 (1 + 2^-22), which e4m3 rounds to 448, its largest value.  An
 // all-zero block has s = 2^-126 and codes 0.  A NaN element keeps the code of NaN; an infinite
 // one makes s infinite and the block NaN.
 #pragma once
@@ -17,13 +16,95 @@ constexpr int kF8Block = 128;             // elements that share a scale
 constexpr float kE4m3Max = 448.0f;
 constexpr float kF8ScaleMin = 1.1754943508222875e-38f;  // 2^-126
 
-MOE_DEVICE float f8_scale(float amax) { return fmaxf(__fdiv_rn(amax, kE4m3Max), kF8ScaleMin); }
+MOE_DEVICE float f8_scale(float amax) { return fmaxf(__fmul_rn(amax, 1.0f / kE4m3Max), kF8ScaleMin); }
 
 // e4m3 codes of two values, `lo` in the low byte.
 MOE_DEVICE uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   uint16_t v;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
   return v;
+}
+
+template <typename T>
+struct Load8;  // 8 consecutive elements as fp32: one vector load, and a single element
+
+template <>
+struct Load8<__nv_bfloat16> {
+  MOE_DEVICE static void vec(const __nv_bfloat16* p, float (&o)[8]) { bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), o); }
+  MOE_DEVICE static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+};
+template <>
+struct Load8<__half> {
+  MOE_DEVICE static void vec(const __half* p, float (&o)[8]) { f16x8_to_f32(*reinterpret_cast<const uint4*>(p), o); }
+  MOE_DEVICE static float one(const __half* p) { return __half2float(*p); }
+};
+template <>
+struct Load8<float> {
+  MOE_DEVICE static void vec(const float* p, float (&o)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+  }
+  MOE_DEVICE static float one(const float* p) { return *p; }
+};
+
+// The half-warps first, first + step, ... of rows x [rows][K] in blocks of 128: each holds a block in
+// registers (8 elements a lane), takes its largest magnitude with four shuffles and writes 128
+// contiguous bytes of codes and the scale.  nb = ceil(K / 128); vec: the rows are 16-byte aligned.  Whole
+// warps call it, with step even and the lower half-warp's `first` even.
+template <typename T>
+MOE_DEVICE void quant_rows_part(const T* __restrict__ x, int64_t ldx, int rows, int K, int nb, bool vec,
+                                uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s, int64_t lds, int64_t first,
+                                int64_t step) {
+  const int64_t total = static_cast<int64_t>(rows) * nb;
+  const int lane = threadIdx.x & 15;
+  for (int64_t i0 = first & ~int64_t(1); i0 < total; i0 += step) {  // warp-uniform: the shuffles need every lane
+    const int64_t i = i0 + (first & 1);
+    const bool on = i < total;
+    const int64_t row = on ? i / nb : 0;
+    const int b = on ? static_cast<int>(i - row * nb) : 0;
+    const int k0 = b * kF8Block + 8 * lane;
+    const T* p = x + row * ldx + k0;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (on) {
+      if (vec && k0 + 8 <= K) {
+        Load8<T>::vec(p, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (k0 + j < K) v[j] = Load8<T>::one(p + j);
+      }
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float sc = f8_scale(amax);
+    const float r = __frcp_rn(sc);
+    uint2 w;
+    w.x = f32x2_to_e4m3x2(v[0] * r, v[1] * r) | (f32x2_to_e4m3x2(v[2] * r, v[3] * r) << 16);
+    w.y = f32x2_to_e4m3x2(v[4] * r, v[5] * r) | (f32x2_to_e4m3x2(v[6] * r, v[7] * r) << 16);
+    if (on) {
+      *reinterpret_cast<uint2*>(q + row * ldq + k0) = w;  // columns K .. 128 nb get the code of zero
+      if (lane == 0) s[row * lds + b] = sc;
+    }
+  }
+}
+
+// The conversion of x that a routing launch performs on the side: fp16 copy (4-bit experts) or 8-bit
+// blocks (8-bit experts), by blocks `block` of `blocks`.
+MOE_DEVICE void convert_x8(const XConv& c, int block, int blocks) {
+  const int per = blockDim.x >> 4;
+  quant_rows_part(reinterpret_cast<const __nv_bfloat16*>(c.x), c.K, c.rows, c.K, (c.K + kF8Block - 1) / kF8Block, true, c.xq,
+                  c.ldq, c.xs, c.lds, static_cast<int64_t>(block) * per + (threadIdx.x >> 4),
+                  static_cast<int64_t>(blocks) * per);
+}
+MOE_DEVICE void convert_x(const XConv& c, uint32_t* err) {
+  if (c.xq)
+    convert_x8(c, static_cast<int>((blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x),
+               static_cast<int>(gridDim.x * gridDim.y * gridDim.z));
+  else
+    convert_x16(c, err);
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f8f6f4 (e4m3 x e4m3, fp32 accumulate, K = 32).

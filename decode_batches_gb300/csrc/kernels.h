@@ -15,13 +15,18 @@ moe_status fail_message(moe_status s, const char* msg);
 // 8-bit rows as a GEMM operand.  Bytes beyond the extents read as zero (api.cu).
 moe_status make_map_f8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld);
 
-// A conversion x (bf16) -> x16 (fp16) of n8 * 8 elements that a kernel performs on the side with
-// every thread of its grid (the 4-bit path's activation copy; convert_x16 in common.cuh);
-// x16 == nullptr: none.
+// A conversion of x (bf16) that a kernel performs on the side with every thread of its grid: to x16
+// (fp16, n8 * 8 elements; the 4-bit path's activation copy, convert_x16 in common.cuh), or to xq / xs
+// (8-bit blocks of `rows` rows of K elements; the 8-bit path's operand, convert_x8 in fp8.cuh).
+// Both nullptr: none.
 struct XConv {
   const uint16_t* x = nullptr;
   uint16_t* x16 = nullptr;
   size_t n8 = 0;
+  uint8_t* xq = nullptr;
+  float* xs = nullptr;
+  int rows = 0, K = 0;
+  int64_t ldq = 0, lds = 0;
 };
 
 // Tokens per chunk of the grouping step: one 32-bit mask word per (chunk, expert).
@@ -89,8 +94,14 @@ cudaError_t launch_router_tc(const CUtensorMap* w3, const CUtensorMap* xm, int T
                              float* parts, uint32_t* err, int num_sms, cudaStream_t st);
 cudaError_t launch_split_router(const float* w, uint16_t* w3, size_t n, cudaStream_t st);
 // Per-chunk expert masks from given ids (validates range / duplicates).
+// xc: 8-bit blocks of x, made on the side by blocks of their own.
 cudaError_t launch_masks_from_ids(const int32_t* ids, int T, int E, int k, uint32_t* masks,
-                                  uint32_t* err, cudaStream_t st);
+                                  uint32_t* err, cudaStream_t st, const XConv& xc = XConv{});
+// Grouping of a small step (route_small_ok) from given ids in one launch: the masks and group
+// launches' results, and xc as above.
+cudaError_t launch_group_ids(const int32_t* ids, int T, int E, int k, int32_t* counts, int32_t* offsets, int32_t* perm,
+                             int32_t* inv, Seg* segs, int32_t* n_segs, int max_segs, uint32_t* err, cudaStream_t st,
+                             const XConv& xc = XConv{});
 // Grouping in one launch from the chunk masks and the ids: counts, offsets (exclusive scan of
 // counts, offsets[E] = total), perm / inv_perm (-1 for a dropped assignment) and, if segs is
 // given, the segment list of the routed experts for the grouped GEMMs.

@@ -1,37 +1,14 @@
 // Quantisation into e4m3 blocks, and the set-up repacking of 8-bit weights.
 //
 // quant_rows: rows [T][K] (bf16, fp16 or fp32, any row pitch) -> codes [T][ldq] and one fp32 scale
-//   per 128 elements of a row.  One pass: a half-warp holds a block in registers (8 elements a
-//   lane), takes its largest magnitude with four shuffles and writes 128 contiguous bytes.  Bound
-//   by memory: K (2 + 1) bytes a bf16 row.
+//   per 128 elements of a row, in one pass (quant_rows_part).  Bound by memory: K (2 + 1) bytes a
+//   bf16 row.
 // quant_blocks: a matrix [rows][K] -> codes and one scale per 128 x 128 block (weights; set-up).
 // tile_fp8: codes [n][rows][K] into the tile-contiguous, pre-swizzled layout of the 8-bit GEMMs.
 #include "fp8.cuh"
 #include "kernels.h"
 
 namespace moe {
-
-template <typename T>
-struct Load8;  // 8 consecutive elements as fp32: vector load, and a guarded element
-
-template <>
-struct Load8<__nv_bfloat16> {
-  MOE_DEVICE static void vec(const __nv_bfloat16* p, float (&o)[8]) { bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), o); }
-  MOE_DEVICE static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-};
-template <>
-struct Load8<__half> {
-  MOE_DEVICE static void vec(const __half* p, float (&o)[8]) { f16x8_to_f32(*reinterpret_cast<const uint4*>(p), o); }
-  MOE_DEVICE static float one(const __half* p) { return __half2float(*p); }
-};
-template <>
-struct Load8<float> {
-  MOE_DEVICE static void vec(const float* p, float (&o)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
-  }
-  MOE_DEVICE static float one(const float* p) { return *p; }
-};
 
 constexpr int kQuantThreads = 256;
 
@@ -41,43 +18,9 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const T* __re
                                                                    int64_t ldq, float* __restrict__ s, int64_t lds) {
   pdl_trigger();
   pdl_wait();
-  const int64_t total = static_cast<int64_t>(rows) * nb;
-  const int lane = threadIdx.x & 15;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 16);
-  // every lane of a warp runs the same number of steps (the shuffles are warp-wide)
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 16) + (threadIdx.x >> 4);
-  for (int64_t i0 = first & ~int64_t(1); i0 < total; i0 += step) {
-    const int64_t i = i0 + (first & 1);
-    const bool on = i < total;
-    const int64_t row = on ? i / nb : 0;
-    const int b = on ? static_cast<int>(i - row * nb) : 0;
-    const int k0 = b * kF8Block + 8 * lane;
-    const T* p = x + row * ldx + k0;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (on) {
-      if (vec && k0 + 8 <= K) {
-        Load8<T>::vec(p, v);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (k0 + j < K) v[j] = Load8<T>::one(p + j);
-      }
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float sc = f8_scale(amax);
-    const float r = __frcp_rn(sc);
-    uint2 w;
-    w.x = f32x2_to_e4m3x2(v[0] * r, v[1] * r) | (f32x2_to_e4m3x2(v[2] * r, v[3] * r) << 16);
-    w.y = f32x2_to_e4m3x2(v[4] * r, v[5] * r) | (f32x2_to_e4m3x2(v[6] * r, v[7] * r) << 16);
-    if (on) {
-      *reinterpret_cast<uint2*>(q + row * ldq + k0) = w;  // columns K .. 128 nb get the code of zero
-      if (lane == 0) s[row * lds + b] = sc;
-    }
-  }
+  quant_rows_part(x, ldx, rows, K, nb, vec != 0, q, ldq, s, lds,
+                  static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 16) + (threadIdx.x >> 4),
+                  static_cast<int64_t>(gridDim.x) * (kQuantThreads / 16));
 }
 
 static bool vec_ok(const void* p, int64_t ld, size_t elem) {

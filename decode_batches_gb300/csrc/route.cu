@@ -16,7 +16,7 @@
 // changing between runs (every chosen expert computed exactly once -> bijection checks).
 #include <float.h>
 
-#include "common.cuh"
+#include "fp8.cuh"
 #include "kernels.h"
 #include "topk.cuh"
 
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const float* __restr
   extern __shared__ uint32_t smask[];  // [E]: bits of this block's 16 tokens
   pdl_trigger();
   pdl_wait();
-  convert_x16(xc, err);
+  convert_x(xc, err);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x >> 1, half = blockIdx.x & 1;
   if (masks)
@@ -374,10 +374,14 @@ MOE_DEVICE bool assignment_valid(const int32_t* __restrict__ ids_row, int j, int
 
 __global__ void __launch_bounds__(256) masks_from_ids_kernel(const int32_t* __restrict__ ids, int T, int E,
                                                              int k, int n_chunks, uint32_t* __restrict__ masks,
-                                                             uint32_t* err) {
+                                                             uint32_t* err, const XConv xc) {
   extern __shared__ uint32_t smask[];
   pdl_trigger();
   pdl_wait();
+  if (static_cast<int>(blockIdx.x) >= n_chunks) {  // the blocks beyond the chunks quantise x
+    convert_x8(xc, blockIdx.x - n_chunks, gridDim.x - n_chunks);
+    return;
+  }
   const int c = blockIdx.x;
   for (int e = threadIdx.x; e < E; e += blockDim.x) smask[e] = 0u;
   __syncthreads();
@@ -398,12 +402,21 @@ __global__ void __launch_bounds__(256) masks_from_ids_kernel(const int32_t* __re
   for (int e = threadIdx.x; e < E; e += blockDim.x) masks[static_cast<size_t>(e) * mstride + c] = smask[e];
 }
 
+// Blocks of 256 threads that make xc's 8-bit blocks beside other work: two blocks of 128 elements a
+// thread group while the grid fills the GPU a few times over.
+static int side_blocks(const XConv& xc) {
+  if (!xc.xq) return 0;
+  const int64_t n = static_cast<int64_t>(xc.rows) * ((xc.K + 127) / 128);
+  const int64_t blocks = (n + 31) / 32;
+  return static_cast<int>(blocks < 1024 ? blocks : 1024);
+}
+
 cudaError_t launch_masks_from_ids(const int32_t* ids, int T, int E, int k, uint32_t* masks,
-                                  uint32_t* err, cudaStream_t st) {
+                                  uint32_t* err, cudaStream_t st, const XConv& xc) {
   if (T <= 0) return cudaSuccess;
   const int n_chunks = (T + kChunk - 1) / kChunk;
-  return launch_pdl(masks_from_ids_kernel, dim3(n_chunks), dim3(256), E * sizeof(uint32_t), st, ids, T, E, k, n_chunks,
-                    masks, err);
+  return launch_pdl(masks_from_ids_kernel, dim3(n_chunks + side_blocks(xc)), dim3(256), E * sizeof(uint32_t), st, ids, T,
+                    E, k, n_chunks, masks, err, xc);
 }
 
 // Exclusive scan over the block (blockDim.x a multiple of 32, <= 1024) of v; *total = block sum.
@@ -849,7 +862,7 @@ __global__ void __launch_bounds__(kRgThreads) route_group_kernel(
   __shared__ int s_last;
   pdl_trigger();
   pdl_wait();
-  convert_x16(xc, err);
+  convert_x(xc, err);
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x;
   {
@@ -905,6 +918,39 @@ __global__ void __launch_bounds__(kRgThreads) route_group_kernel(
   if (threadIdx.x == 0) *done = 0u;  // ready for the next launch (stream-ordered)
 }
 
+// Grouping of a small step from given ids: block 0 groups (the last block's part of
+// route_group_kernel), the others make xc's 8-bit blocks of x beside it.
+__global__ void __launch_bounds__(kRgThreads) group_ids_kernel(
+    const int32_t* __restrict__ ids, int T, int E, int k, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+    int32_t* __restrict__ perm, int32_t* __restrict__ inv, Seg* segs, int32_t* n_segs, int max_segs, uint32_t* err,
+    const XConv xc) {
+  extern __shared__ uint32_t sm[];
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x > 0) {
+    convert_x8(xc, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  const int nch = (T + kChunk - 1) / kChunk;
+  int32_t* sids = reinterpret_cast<int32_t*>(sm) + 2 * nch * E;
+  for (int i = threadIdx.x; i < T * k; i += kRgThreads) sids[i] = ids[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < T * k; i += kRgThreads)
+    if (!assignment_valid(sids + i / k * k, i % k, sids[i], E)) set_error(err, MOE_DEVERR_EXPERT_RANGE);
+  if (T * k <= kTinyGroupRows)
+    group_tiny(T, E, k, sids, counts, offsets, perm, inv, segs, n_segs, max_segs, err);
+  else
+    group_small(T, E, k, sm, counts, offsets, perm, inv, segs, n_segs, max_segs, err);
+}
+
+cudaError_t launch_group_ids(const int32_t* ids, int T, int E, int k, int32_t* counts, int32_t* offsets, int32_t* perm,
+                             int32_t* inv, Seg* segs, int32_t* n_segs, int max_segs, uint32_t* err, cudaStream_t st,
+                             const XConv& xc) {
+  if (!route_small_ok(T, E, k, 1)) return cudaErrorInvalidValue;
+  return launch_pdl(group_ids_kernel, dim3(1 + side_blocks(xc)), dim3(kRgThreads), route_small_smem(T, E, k), st, ids, T,
+                    E, k, counts, offsets, perm, inv, segs, n_segs, max_segs, err, xc);
+}
+
 // Router, top-k and grouping of a step of at most 8 tokens in one launch: every block forms its
 // K-split partial logits (router_parts_block); the last block to finish adds them (split order,
 // then the bias, as the top-k kernel does), selects each token's top k with one warp per token
@@ -920,7 +966,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) router_route_tiny_kernel(
   __shared__ int s_last;
   pdl_trigger();
   pdl_wait();
-  convert_x16(xc, err);
+  convert_x(xc, err);
   router_parts_block<8>(x, wr, T, E, d, parts, reinterpret_cast<uint16_t*>(sm));
   __threadfence();
   __syncthreads();

@@ -104,7 +104,8 @@ typedef enum {
  * Ultra" (Decode paragraph: a 384-expert router and an always-run shared expert).
  * Host-side only; no device memory is touched.
  * Limits: 1 <= k <= E <= 1024, k <= 32, d_model and d_ff multiples of 8 (multiples of 32
- * for MOE_W_MXFP4).  Returns NULL on bad arguments (moe_last_error() says why).
+ * for MOE_W_MXFP4; MOE_W_FP8 runs every such shape on the tensor cores and has no CUDA-core path,
+ * its shared experts need d_model % 128 == 0 and d_ff_shared % 64 == 0).  Returns NULL on bad arguments (moe_last_error() says why).
  */
 moe_plan* moe_plan_create(int E, int k, int d_model, int d_ff, int n_shared, moe_wdtype weight_dtype);
 
@@ -134,10 +135,12 @@ const char* moe_last_error(void);
  *   w_down    [E][d_model][d_ff]                bf16, or codes [E][d_model][d_ff/2]
  *   s_gate, s_up  uint8 [E][d_ff][d_model/32]   e8m0 scales (MOE_W_MXFP4), else NULL
  *   s_down        uint8 [E][d_model][d_ff/32]
+ * MOE_W_FP8: the weights are e4m3 codes of one byte in the bf16 shapes, the scales fp32
+ *   s_gate, s_up  [E][ceil(d_ff/128)][ceil(d_model/128)],  s_down [E][ceil(d_model/128)][ceil(d_ff/128)].
  */
 moe_status moe_plan_set_weights(moe_plan* plan, const float* w_router, const float* b_router,
                                 const void* w_gate, const void* w_up, const void* w_down,
-                                const uint8_t* s_gate, const uint8_t* s_up, const uint8_t* s_down);
+                                const void* s_gate, const void* s_up, const void* s_down);
 
 /*
  * Source: "DeepSeek V4.1F Q4 with native DSpark MTP on M3 Ultra", Decode paragraph (the shared
@@ -191,6 +194,18 @@ int moe_plan_resolved_path(const moe_plan* plan);
  */
 moe_status moe_layer_forward(moe_plan* plan, const void* x, int T, int n_prefill, void* out,
                              moe_stream_t stream);
+
+/*
+ * The layer for a step whose routing is already known (a router that lives elsewhere, or ids and
+ * gates from moe_route_logits): grouping, expert FFNs, combine and the shared experts, as
+ * moe_layer_forward does after its own routing.  Source: "moe-prefill-quantum", cause section (each
+ * token goes to k of the E experts); the pages have no counterpart to the separate call.
+ *   ids int32 [T][k], gates fp32 [T][k].  An id outside [0, E), or one that repeats an earlier slot
+ * of its token, sets MOE_DEVERR_EXPERT_RANGE and contributes nothing.  gates enter as they are (they
+ * need not sum to one).
+ */
+moe_status moe_layer_forward_routed(moe_plan* plan, const void* x, int T, const int32_t* ids, const float* gates,
+                                    void* out, moe_stream_t stream);
 
 /*
  * Router + top-k.  Source: "DeepSeek V4.1F Q4 with native DSpark MTP on M3 Ultra", Decode
@@ -268,7 +283,8 @@ moe_status moe_selftest_wait_expiry(uint32_t* err, uint32_t* result, moe_stream_
  *   y[r] = FFN_e(x[perm[r] / k]) for r in [offsets[e], offsets[e+1]),  fp16 [T*k][d_model],
  *   shared_y[t] = sum_s FFN_shared_s(x[t]) fp16 [T][d_model] (may be NULL if n_shared == 0).
  * FFN(x) = W_d (silu(W_g x) * (W_u x)) with fp32 accumulation; the hidden vector is rounded to
- * fp16 (it is the fp16 operand of the down GEMM) and y is rounded to fp16.  Values beyond the
+ * fp16 (it is the fp16 operand of the down GEMM; with MOE_W_FP8 x and the hidden vector are
+ * quantised in blocks of 128 instead, see moe_quantize_rows) and y is rounded to fp16.  Values beyond the
  * fp16 range are clamped and set MOE_DEVERR_RANGE.  offsets and perm as produced by
  * moe_permute (device pointers).
  */
@@ -344,8 +360,8 @@ moe_status moe_compose_prefill(int64_t start_pos, int64_t n_tokens, int32_t quan
  * DSpark MTP on M3 Ultra" (8-bit projections of a 6-row verify block); the format is this
  * library's choice.  A block of values with largest magnitude amax is stored as e4m3 codes q
  * (sign, 4 exponent bits, 3 mantissa bits, largest value 448, 0x7F / 0xFF NaN) and one fp32 scale s:
- *   s = max(amax / 448, 2^-126),  q = e4m3(v * (1 / s)),  v ~ q * s,
- * the quotients and the product in fp32, q rounded to nearest even.  A NaN element keeps the code
+ *   s = max(amax * (1 / 448), 2^-126),  q = e4m3(v * (1 / s)),  v ~ q * s,
+ * every quotient and product rounded to fp32 (1 / 448 too), q to nearest even.  A NaN element keeps the code
  * of NaN; an infinite element makes its block's scale infinite and the block NaN.
  *
  * moe_quantize_rows: rows [T][K] of x_dtype (row pitch ldx elements) in blocks of 1 x 128 along K

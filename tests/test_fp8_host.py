@@ -50,7 +50,7 @@ def test_reference_quantisation_is_the_rule():
     x = torch.zeros((1, 130))
     x[0, 0], x[0, 1], x[0, 2], x[0, 128] = 448.0, 17.0, -27.0, 7.0
     q, s = quantize_rows_ref(x)
-    assert s.tolist() == [[1.0, float(torch.tensor(7.0) / 448.0)]]
+    assert s.tolist() == [[1.0, float(torch.tensor(7.0) * (torch.tensor(1.0) / 448.0))]]
     assert q[0, 0] == 448 and q[0, 1] == 16 and q[0, 2] == -28 and q[0, 128] == 448   # 17, 27 tie to even
     z, sz = quantize_rows_ref(torch.zeros((1, 3)))
     assert not z.any() and float(sz) == 2.0 ** -126
