@@ -25,6 +25,7 @@ MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE, MOE_ERR_TIMEOUT = 4, 5, 6, 7
 MOE_W_BF16, MOE_W_MXFP4, MOE_W_FP8 = 0, 1, 3
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # moe_dtype
 FP8_BLOCK = 128  # elements (of a row), or rows and columns (of a weight), that share a scale
+SCORES = {"softmax": 0, "sigmoid": 1}
 PATHS = {"auto": 0, "simt": 1, "tc": 2}
 DEVERR_EXPERT_RANGE, DEVERR_NONFINITE, DEVERR_TIMEOUT, DEVERR_SEGMENT, DEVERR_RANGE = 0x1, 0x2, 0x4, 0x8, 0x10
 
@@ -37,6 +38,7 @@ EXPORTED = (
     "moe_plan_resolved_path", "moe_quantize_rows", "moe_quantize_blocks", "moe_linear_create", "moe_linear_destroy",
     "moe_linear_set_weights", "moe_linear_workspace_bytes", "moe_linear_set_workspace", "moe_linear_forward",
     "moe_linear_forward_quantized", "moe_linear_get_device_error", "moe_layer_forward_routed",
+    "moe_plan_set_routing",
 )
 
 _lib = None
@@ -45,6 +47,13 @@ _lib = None
 class PrefillCall(ctypes.Structure):
     """moe_prefill_call: one layer call of a prompt's prefill."""
     _fields_ = [("pos", ctypes.c_int64), ("n", ctypes.c_int32), ("piece", ctypes.c_int32)]
+
+
+class Routing(ctypes.Structure):
+    """moe_routing: how a plan scores and selects experts."""
+    _fields_ = [("score", ctypes.c_int), ("bias", ctypes.c_void_p), ("n_groups", ctypes.c_int),
+                ("topk_groups", ctypes.c_int), ("group_top", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -74,6 +83,7 @@ def load_library(path: str = LIB_PATH):
         "moe_plan_set_workspace": ([vp, vp, sz, i32], i32),
         "moe_plan_set_path": ([vp, i32], i32),
         "moe_layer_forward": ([vp, vp, i32, i32, vp, vp], i32),
+        "moe_plan_set_routing": ([vp, ctypes.POINTER(Routing)], i32),
         "moe_layer_forward_routed": ([vp, vp, i32, vp, vp, vp, vp], i32),
         "moe_route": ([vp, vp, i32, vp, vp, vp, vp], i32),
         "moe_route_logits": ([vp, vp, i32, vp, vp, vp], i32),
@@ -359,6 +369,17 @@ class MoePlan:
 
     def set_path(self, path: str):
         _check(self.lib.moe_plan_set_path(self._h, PATHS[path]))
+
+    def set_routing(self, score: Optional[str] = "softmax", bias: Optional[torch.Tensor] = None, n_groups: int = 1,
+                    topk_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0):
+        """Score and select experts as moe_plan_set_routing says; score=None restores the default
+        (the softmax of the k largest logits)."""
+        if score is None:
+            _check(self.lib.moe_plan_set_routing(self._h, None))
+            return
+        r = Routing(SCORES[score], _dev(bias, "bias", torch.float32, (self.E,)), n_groups, topk_groups, group_top,
+                    int(bool(renormalize)), scale)
+        _check(self.lib.moe_plan_set_routing(self._h, ctypes.byref(r)))
 
     # ---- step ---------------------------------------------------------------------------------
     def forward(self, x: torch.Tensor, n_prefill: int = 0, out: Optional[torch.Tensor] = None, stream=None):

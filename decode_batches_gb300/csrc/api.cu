@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -76,6 +77,8 @@ struct moe_plan {
   // plan-owned device memory
   float* w_router = nullptr;
   float* b_router = nullptr;
+  ScoreArgs score;            // moe_plan_set_routing; its bias is plan-owned
+  float* b_score = nullptr;
   uint16_t* w_router3 = nullptr;  // W_r split into three bf16 pieces [3][E][d] (tensor-core router)
   CUtensorMap map_router3{};
   CUtensorMap map_x{};  // the current call's x [T][d] (tensor-core router), encoded per call
@@ -204,7 +207,7 @@ static bool use_tc(const moe_plan* p) {
 // The one-launch small-step layer (layer_small.cu): MOE_PATH_AUTO at T <= 8 with bf16 routed
 // weights in the tensor-core tile layout (the kernel streams those tiles).
 static bool use_small_layer(const moe_plan* p, int T) {
-  return p->small_fused && p->path == MOE_PATH_AUTO && p->wdtype == MOE_W_BF16 && tc_shape_ok(p) && p->tiled &&
+  return p->small_fused && !p->score.on && p->path == MOE_PATH_AUTO && p->wdtype == MOE_W_BF16 && tc_shape_ok(p) && p->tiled &&
          (p->n_shared == 0 || p->tiled_s) && p->ls_sync &&
          layer_small_ok(T, p->E, p->k, p->d, p->f, p->n_shared, p->f_s);
 }
@@ -392,6 +395,7 @@ extern "C" void moe_plan_destroy(moe_plan* p) {
   free_weights(p);
   cudaFree(p->w_gu_s);
   cudaFree(p->w_down_s);
+  cudaFree(p->b_score);
   cudaFree(p->err);
   cudaFree(p->ls_sync);
   for (auto& t : p->timed) {
@@ -662,6 +666,42 @@ extern "C" moe_status moe_plan_set_path(moe_plan* p, moe_path path) {
   if (path == MOE_PATH_TC && !tc_shape_ok(p))
     return fail(MOE_ERR_UNSUPPORTED, "tensor-core path needs bf16 weights, d %% 128 == 0, d_ff %% 64 == 0, d_ff_shared %% 64 == 0");
   p->path = path;
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_plan_set_routing(moe_plan* p, const moe_routing* r) {
+  if (!p) return fail(MOE_ERR_INVALID_ARG, "plan is NULL");
+  if (!r) {  // back to the softmax of the k largest logits
+    p->score = ScoreArgs{};
+    return MOE_OK;
+  }
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_INVALID_ARG, "unknown score %d", static_cast<int>(r->score));
+  const int G = r->n_groups;
+  if (G < 1 || G > kMaxGroups || p->E % G)
+    return fail(MOE_ERR_INVALID_ARG, "n_groups=%d must divide E=%d and be at most %d", G, p->E, kMaxGroups);
+  if (r->topk_groups < 1 || r->topk_groups > G || r->topk_groups * (p->E / G) < p->k)
+    return fail(MOE_ERR_INVALID_ARG, "topk_groups=%d must be in [1, n_groups=%d] and leave at least k=%d experts",
+                r->topk_groups, G, p->k);
+  if ((r->group_top != 1 && r->group_top != 2) || r->group_top > p->E / G)
+    return fail(MOE_ERR_INVALID_ARG, "group_top=%d must be 1 or 2 and at most the group's size %d", r->group_top, p->E / G);
+  if (!std::isfinite(r->scale)) return fail(MOE_ERR_INVALID_ARG, "scale must be finite");
+  if (r->bias) {
+    MOE_CUDA_TRY(cudaDeviceSynchronize());  // queued calls still read the previous bias
+    if (!p->b_score) MOE_CUDA_TRY(cudaMalloc(&p->b_score, p->E * sizeof(float)));
+    MOE_CUDA_TRY(cudaMemcpy(p->b_score, r->bias, p->E * sizeof(float), cudaMemcpyDeviceToDevice));
+    MOE_CUDA_TRY(cudaDeviceSynchronize());
+  }
+  ScoreArgs a;
+  a.on = 1;
+  a.sigmoid = r->score == MOE_SCORE_SIGMOID;
+  a.groups = G;
+  a.keep = r->topk_groups;
+  a.top = r->group_top;
+  a.renorm = r->renormalize != 0;
+  a.scale = r->scale;
+  a.bias = r->bias ? p->b_score : nullptr;
+  p->score = a;
   return MOE_OK;
 }
 
@@ -968,7 +1008,7 @@ static moe_status route_step(moe_plan* p, const uint16_t* x, int T, float* logit
   int ns = 1;
   moe_status s = router_step(p, x, T, &parts, &ns, &bias, st);
   if (s != MOE_OK) return s;
-  LAUNCH(p, "topk", st, launch_topk(parts, ns, bias, logits_out, T, p->E, p->k, ids, gates, masks, p->err, st, xc));
+  LAUNCH(p, "topk", st, launch_topk(parts, ns, bias, logits_out, T, p->E, p->k, ids, gates, masks, p->err, st, xc, p->score));
   return MOE_OK;
 }
 
@@ -1066,7 +1106,7 @@ extern "C" moe_status moe_layer_forward(moe_plan* p, const void* x, int T, int n
     LAUNCH(p, "router_route", st,
            launch_router_route_tiny(xb, p->w_router, p->b_router, T, p->E, p->d, ws_ptr<float>(p, p->L.parts), p->k,
                                     ids, gates, counts, offsets, perm, inv, segs, ws_ptr<int32_t>(p, p->L.n_segs),
-                                    p->L.max_segs, p->err + 1, p->err, st, xc));
+                                    p->L.max_segs, p->err + 1, p->err, st, xc, p->score));
   } else if (route_small_ok(T, p->E, p->k, router_nsplit(p, T))) {
     // small step: the whole routing and grouping in one block after the router
     const float* parts = nullptr;
@@ -1076,7 +1116,7 @@ extern "C" moe_status moe_layer_forward(moe_plan* p, const void* x, int T, int n
     if (s != MOE_OK) return s;
     LAUNCH(p, "route_small", st,
            launch_route_small(parts, ns, bias, T, p->E, p->k, ids, gates, counts, offsets, perm, inv, segs,
-                              ws_ptr<int32_t>(p, p->L.n_segs), p->L.max_segs, p->err + 1, p->err, st, xc));
+                              ws_ptr<int32_t>(p, p->L.n_segs), p->L.max_segs, p->err + 1, p->err, st, xc, p->score));
   } else {
     // (the 8-bit blocks stay with the top-k launch: a launch of their own costs more than it hides)
     if (p->wdtype != MOE_W_FP8) xc = XConv{};
@@ -1151,7 +1191,8 @@ extern "C" moe_status moe_route_logits(moe_plan* p, const float* logits, int T, 
   if (T == 0) return MOE_OK;
   if (!logits || !ids || !gates) return fail(MOE_ERR_INVALID_ARG, "logits, ids and gates are required");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  LAUNCH(p, "topk", st, launch_topk(logits, 1, nullptr, nullptr, T, p->E, p->k, ids, gates, nullptr, p->err, st));
+  LAUNCH(p, "topk", st,
+         launch_topk(logits, 1, nullptr, nullptr, T, p->E, p->k, ids, gates, nullptr, p->err, st, XConv{}, p->score));
   return MOE_OK;
 }
 

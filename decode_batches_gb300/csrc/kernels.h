@@ -49,6 +49,17 @@ struct Seg {
   int pad0, pad1, pad2;
 };
 
+// Scored selection (scored.cuh); on == 0: the softmax of the k largest logits.
+constexpr int kMaxGroups = 32;  // a lane of the selecting warp holds a group's score
+struct ScoreArgs {
+  int on = 0;
+  int sigmoid = 0;                // else softmax
+  int groups = 1, keep = 1, top = 1;
+  int renorm = 1;
+  float scale = 1.0f;
+  const float* bias = nullptr;    // [E] or NULL
+};
+
 // ---- routing and grouping (route.cu) --------------------------------------------------------
 // logits[t][e] = x[t] . w_router[e] + b[e] (fp32 accumulation).
 cudaError_t launch_router_logits(const uint16_t* x, const float* w_router, const float* b_router, int T,
@@ -59,7 +70,7 @@ cudaError_t launch_router_logits(const uint16_t* x, const float* w_router, const
 // xc: an x -> fp16 conversion the launch performs on the side (none by default).
 cudaError_t launch_topk(const float* parts, int nsplit, const float* bias, float* logits_out, int T, int E, int k,
                         int32_t* ids, float* gates, uint32_t* masks, uint32_t* err, cudaStream_t st,
-                        const XConv& xc = XConv{});
+                        const XConv& xc = XConv{}, const ScoreArgs& sa = ScoreArgs{});
 
 // ---- tensor-core router (router_tc.cu) --------------------------------------------------------
 // parts[s][T][E] = x[T][k-range s] . W_r[E][k-range s]^T with W_r split into three bf16 pieces
@@ -81,13 +92,13 @@ cudaError_t launch_router_route_tiny(const uint16_t* x, const float* w_router, c
                                      float* parts, int k, int32_t* ids, float* gates, int32_t* counts,
                                      int32_t* offsets, int32_t* perm, int32_t* inv, Seg* segs, int32_t* n_segs,
                                      int max_segs, uint32_t* done, uint32_t* err, cudaStream_t st,
-                                     const XConv& xc = XConv{});
+                                     const XConv& xc = XConv{}, const ScoreArgs& sa = ScoreArgs{});
 
 // `done`: a device counter that is 0 between launches (the last block resets it).
 cudaError_t launch_route_small(const float* parts, int nsplit, const float* bias, int T, int E, int k, int32_t* ids,
                                float* gates, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, Seg* segs,
                                int32_t* n_segs, int max_segs, uint32_t* done, uint32_t* err, cudaStream_t st,
-                               const XConv& xc = XConv{});
+                               const XConv& xc = XConv{}, const ScoreArgs& sa = ScoreArgs{});
 // Persistent: min(items, num_sms) CTAs over the (expert tile, K split, token tile) items.
 // xm: x [T][d] bf16, box {64, 128}, 128-byte swizzle.
 cudaError_t launch_router_tc(const CUtensorMap* w3, const CUtensorMap* xm, int T, int E, int d, int nsplit,

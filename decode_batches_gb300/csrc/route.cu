@@ -18,7 +18,7 @@
 
 #include "fp8.cuh"
 #include "kernels.h"
-#include "topk.cuh"
+#include "scored.cuh"
 
 namespace moe {
 
@@ -265,10 +265,10 @@ constexpr int kTopkThreads = 32 * kTopkTokens;
 
 // Top-k of token t by one warp: sums the partial logits (split order fixed) and the bias,
 // optionally stores the logits, then selects (topk_select).
-template <int PL>
+template <int PL, bool kScored>
 MOE_DEVICE int topk_token(const float* __restrict__ parts, int nsplit, const float* __restrict__ bias,
                           float* __restrict__ logits_out, int t, int T, int E, int k, int32_t* __restrict__ ids,
-                          float* __restrict__ gates, uint32_t* err) {
+                          float* __restrict__ gates, uint32_t* err, const ScoreArgs& sa) {
   const int lane = threadIdx.x & 31;
   // U partial matrices in flight at a time (one L2 round trip per U splits), added in order
   constexpr int U = PL <= 8 ? 4 : (PL <= 16 ? 2 : 1);
@@ -300,17 +300,17 @@ MOE_DEVICE int topk_token(const float* __restrict__ parts, int nsplit, const flo
       if (logits_out) logits_out[static_cast<size_t>(t) * E + e] = v[i];
     }
   }
-  return topk_select<PL>(v, t, E, k, ids, gates, err);
+  return select_token<PL, kScored>(v, t, E, k, ids, gates, err, sa);
 }
 
-template <int PL>
+template <int PL, bool kScored>
 __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const float* __restrict__ parts, int nsplit,
                                                             const float* __restrict__ bias,
                                                             float* __restrict__ logits_out, int T, int E, int k,
                                                             int n_chunks, int32_t* __restrict__ ids,
                                                             float* __restrict__ gates,
                                                             uint32_t* __restrict__ masks, uint32_t* err,
-                                                            const XConv xc) {
+                                                            const XConv xc, const ScoreArgs sa) {
   extern __shared__ uint32_t smask[];  // [E]: bits of this block's 16 tokens
   pdl_trigger();
   pdl_wait();
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const float* __restr
   __syncthreads();
   const int t = c * kChunk + kTopkTokens * half + warp;
   if (t < T) {
-    const int sel = topk_token<PL>(parts, nsplit, bias, logits_out, t, T, E, k, ids, gates, err);
+    const int sel = topk_token<PL, kScored>(parts, nsplit, bias, logits_out, t, T, E, k, ids, gates, err, sa);
     if (masks && lane < k) atomicOr(&smask[sel], 1u << warp);
   }
   if (masks) {
@@ -338,18 +338,19 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const float* __restr
 template <int PL>
 static cudaError_t launch_topk_pl(const float* parts, int nsplit, const float* bias, float* logits_out, int T, int E,
                                   int k, int n_chunks, int32_t* ids, float* gates, uint32_t* masks, uint32_t* err,
-                                  const XConv& xc, cudaStream_t st) {
-  return launch_pdl(topk_kernel<PL>, dim3(2 * n_chunks), dim3(kTopkThreads), masks ? E * sizeof(uint32_t) : 0, st,
-                    parts, nsplit, bias, logits_out, T, E, k, n_chunks, ids, gates, masks, err, xc);
+                                  const XConv& xc, const ScoreArgs& sa, cudaStream_t st) {
+  return launch_pdl(sa.on ? topk_kernel<PL, true> : topk_kernel<PL, false>, dim3(2 * n_chunks), dim3(kTopkThreads), masks ? E * sizeof(uint32_t) : 0, st,
+                    parts, nsplit, bias, logits_out, T, E, k, n_chunks, ids, gates, masks, err, xc, sa);
 }
 
 cudaError_t launch_topk(const float* parts, int nsplit, const float* bias, float* logits_out, int T, int E, int k,
-                        int32_t* ids, float* gates, uint32_t* masks, uint32_t* err, cudaStream_t st, const XConv& xc) {
+                        int32_t* ids, float* gates, uint32_t* masks, uint32_t* err, cudaStream_t st, const XConv& xc,
+                        const ScoreArgs& sa) {
   if (T <= 0) return cudaSuccess;
   const int n_chunks = (T + kChunk - 1) / kChunk;
   const int pl = (E + 31) / 32;
 #define MOE_TOPK(PLV) \
-  launch_topk_pl<PLV>(parts, nsplit, bias, logits_out, T, E, k, n_chunks, ids, gates, masks, err, xc, st)
+  launch_topk_pl<PLV>(parts, nsplit, bias, logits_out, T, E, k, n_chunks, ids, gates, masks, err, xc, sa, st)
   if (pl <= 1) return MOE_TOPK(1);
   if (pl <= 2) return MOE_TOPK(2);
   if (pl <= 4) return MOE_TOPK(4);
@@ -852,12 +853,12 @@ MOE_DEVICE void group_tiny(int T, int E, int k, const int32_t* sids, int32_t* __
   }
 }
 
-template <int PL>
+template <int PL, bool kScored>
 __global__ void __launch_bounds__(kRgThreads) route_group_kernel(
     const float* __restrict__ parts, int nsplit, const float* __restrict__ bias, int T, int E, int k,
     int32_t* __restrict__ ids, float* __restrict__ gates, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
     int32_t* __restrict__ perm, int32_t* __restrict__ inv, Seg* segs, int32_t* n_segs, int max_segs,
-    uint32_t* done, uint32_t* err, const XConv xc) {
+    uint32_t* done, uint32_t* err, const XConv xc, const ScoreArgs sa) {
   extern __shared__ uint32_t sm[];
   __shared__ int s_last;
   pdl_trigger();
@@ -895,7 +896,7 @@ __global__ void __launch_bounds__(kRgThreads) route_group_kernel(
         const int e = lane + 32 * i;
         v[i] = e < E ? slog[e] : 0.f;
       }
-      topk_select<PL>(v, t, E, k, ids, gates, err);
+      select_token<PL, kScored>(v, t, E, k, ids, gates, err, sa);
     }
   }
   // publish this token's ids, then count finished blocks
@@ -955,13 +956,13 @@ cudaError_t launch_group_ids(const int32_t* ids, int T, int E, int k, int32_t* c
 // K-split partial logits (router_parts_block); the last block to finish adds them (split order,
 // then the bias, as the top-k kernel does), selects each token's top k with one warp per token
 // and groups the step (group_tiny, or group_small above 64 assignments).
-template <int PL>
+template <int PL, bool kScored>
 __global__ void __launch_bounds__(kRgThreads, 1) router_route_tiny_kernel(
     const uint16_t* __restrict__ x, const float* __restrict__ wr, const float* __restrict__ bias, int T, int E,
     int d, float* __restrict__ parts, int k, int32_t* __restrict__ ids, float* __restrict__ gates,
     int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ perm,
     int32_t* __restrict__ inv, Seg* segs, int32_t* n_segs, int max_segs, uint32_t* done, uint32_t* err,
-    const XConv xc) {
+    const XConv xc, const ScoreArgs sa) {
   extern __shared__ __align__(16) uint32_t sm[];
   __shared__ int s_last;
   pdl_trigger();
@@ -1003,7 +1004,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) router_route_tiny_kernel(
     if (bias)
 #pragma unroll
       for (int i = 0; i < PL; ++i) v[i] += bv[i];
-    const int sel = topk_select<PL>(v, t, E, k, ids, gates, err);
+    const int sel = select_token<PL, kScored>(v, t, E, k, ids, gates, err, sa);
     if (lane < k) sids[t * k + lane] = sel;
   }
   __syncthreads();
@@ -1023,25 +1024,25 @@ template <int PL>
 static cudaError_t launch_rrt_pl(const uint16_t* x, const float* wr, const float* bias, int T, int E, int d,
                                  float* parts, int k, int32_t* ids, float* gates, int32_t* counts, int32_t* offsets,
                                  int32_t* perm, int32_t* inv, Seg* segs, int32_t* n_segs, int max_segs, uint32_t* done,
-                                 uint32_t* err, const XConv& xc, cudaStream_t st) {
+                                 uint32_t* err, const XConv& xc, const ScoreArgs& sa, cudaStream_t st) {
   const size_t xs_bytes = 8 * kRouterKS * 2;
   const size_t g_bytes = route_small_smem(T, E, k);
   dim3 grid((E + 7) / 8, router_small_splits(d));
-  return launch_pdl(router_route_tiny_kernel<PL>, grid, dim3(kRgThreads), xs_bytes > g_bytes ? xs_bytes : g_bytes, st,
+  return launch_pdl(sa.on ? router_route_tiny_kernel<PL, true> : router_route_tiny_kernel<PL, false>, grid, dim3(kRgThreads), xs_bytes > g_bytes ? xs_bytes : g_bytes, st,
                     x, wr, bias, T, E, d, parts, k, ids, gates, counts, offsets, perm, inv, segs, n_segs, max_segs,
-                    done, err, xc);
+                    done, err, xc, sa);
 }
 
 cudaError_t launch_router_route_tiny(const uint16_t* x, const float* w_router, const float* bias, int T, int E, int d,
                                      float* parts, int k, int32_t* ids, float* gates, int32_t* counts,
                                      int32_t* offsets, int32_t* perm, int32_t* inv, Seg* segs, int32_t* n_segs,
                                      int max_segs, uint32_t* done, uint32_t* err, cudaStream_t st,
-                                     const XConv& xc) {
+                                     const XConv& xc, const ScoreArgs& sa) {
   if (!router_route_tiny_ok(T, E, d, k)) return cudaErrorInvalidValue;
   const int pl = (E + 31) / 32;
 #define MOE_RRT(PLV)                                                                                            \
   launch_rrt_pl<PLV>(x, w_router, bias, T, E, d, parts, k, ids, gates, counts, offsets, perm, inv, segs, n_segs, \
-                     max_segs, done, err, xc, st)
+                     max_segs, done, err, xc, sa, st)
   if (pl <= 1) return MOE_RRT(1);
   if (pl <= 2) return MOE_RRT(2);
   if (pl <= 4) return MOE_RRT(4);
@@ -1061,20 +1062,20 @@ template <int PL>
 static cudaError_t launch_route_small_pl(const float* parts, int nsplit, const float* bias, int T, int E, int k,
                                          int32_t* ids, float* gates, int32_t* counts, int32_t* offsets, int32_t* perm,
                                          int32_t* inv, Seg* segs, int32_t* n_segs, int max_segs, uint32_t* done,
-                                         uint32_t* err, const XConv& xc, cudaStream_t st) {
-  return launch_pdl(route_group_kernel<PL>, dim3(T), dim3(kRgThreads), route_small_smem(T, E, k), st, parts, nsplit,
-                    bias, T, E, k, ids, gates, counts, offsets, perm, inv, segs, n_segs, max_segs, done, err, xc);
+                                         uint32_t* err, const XConv& xc, const ScoreArgs& sa, cudaStream_t st) {
+  return launch_pdl(sa.on ? route_group_kernel<PL, true> : route_group_kernel<PL, false>, dim3(T), dim3(kRgThreads), route_small_smem(T, E, k), st, parts, nsplit,
+                    bias, T, E, k, ids, gates, counts, offsets, perm, inv, segs, n_segs, max_segs, done, err, xc, sa);
 }
 
 cudaError_t launch_route_small(const float* parts, int nsplit, const float* bias, int T, int E, int k, int32_t* ids,
                                float* gates, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, Seg* segs,
                                int32_t* n_segs, int max_segs, uint32_t* done, uint32_t* err, cudaStream_t st,
-                               const XConv& xc) {
+                               const XConv& xc, const ScoreArgs& sa) {
   if (!route_small_ok(T, E, k, nsplit)) return cudaErrorInvalidValue;
   const int pl = (E + 31) / 32;
 #define MOE_RS(PLV)                                                                                             \
   launch_route_small_pl<PLV>(parts, nsplit, bias, T, E, k, ids, gates, counts, offsets, perm, inv, segs, n_segs, \
-                             max_segs, done, err, xc, st)
+                             max_segs, done, err, xc, sa, st)
   if (pl <= 1) return MOE_RS(1);
   if (pl <= 2) return MOE_RS(2);
   if (pl <= 4) return MOE_RS(4);

@@ -18,6 +18,13 @@ MOE_DEVICE uint32_t rank_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// The value of an ordered key (NaN's is NaN; a key that is no value's counts as -inf).
+MOE_DEVICE float rank_value(uint32_t key) {
+  if (key == 2u) return __uint_as_float(0x7fc00000u);
+  if (key < 2u) return __uint_as_float(0xff800000u);
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
+
 // Selection and gates of token t by one warp from its logits v (lane l holds experts
 // l + 32 i): writes ids / gates of the token and returns, in lane j < k, the expert chosen in
 // round j.  Each round every lane offers its best remaining candidate (largest key, then lowest

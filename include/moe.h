@@ -170,6 +170,34 @@ moe_status moe_plan_set_workspace(moe_plan* plan, void* dev_ptr, size_t bytes, i
 moe_status moe_plan_set_path(moe_plan* plan, moe_path path);
 
 /*
+ * How the plan's routing scores and selects experts (moe_route, moe_route_logits, moe_layer_forward).
+ * Source: "moe-prefill-quantum", cause section (k of E experts chosen per token); the pages do not
+ * give a scoring rule, so the forms here have no counterpart on the pages.
+ *   s_e = softmax over all E logits, or sigmoid(l_e);
+ *   key_e = s_e + bias[e] (the bias selects and does not weigh); key_e = -inf where l_e = -inf (a
+ *     masked expert: chosen only when nothing else is left, with weight 0);
+ *   n_groups > 1: groups of E / n_groups consecutive experts are ranked by the sum of their group_top
+ *     (1 or 2) largest keys, and the experts outside the topk_groups best get key -inf;
+ *   ids: the k largest keys in order; weights w = s of those (0 where the key is -inf),
+ *     w / (sum of w + 1e-20) with renormalize, times scale.
+ * Orders are (value desc, index asc; +0 == -0; NaN lowest), all arithmetic fp32.  A selected logit
+ * that is NaN or +inf sets MOE_DEVERR_NONFINITE.  Softmax scores, one group, renormalize, scale 1
+ * and no bias weigh like the default up to rounding; NULL restores the default (the softmax of the
+ * k largest logits).  bias: device fp32 [E] or NULL, copied into plan memory (synchronous when given).
+ * n_groups divides E, 1 <= n_groups <= 32, 1 <= topk_groups <= n_groups with topk_groups * E / n_groups
+ * >= k, group_top <= E / n_groups, scale finite; else MOE_ERR_INVALID_ARG.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef struct {
+  moe_score score;
+  const float* bias;
+  int n_groups, topk_groups, group_top;
+  int renormalize;
+  float scale;
+} moe_routing;
+moe_status moe_plan_set_routing(moe_plan* plan, const moe_routing* routing);
+
+/*
  * The kernels the expert FFN will actually run on (no counterpart on the pages): MOE_PATH_TC
  * or MOE_PATH_SIMT, as MOE_PATH_AUTO (or a forced path) resolves for the plan's shapes and
  * weights -- the tensor-core path needs d_model % 128 == 0, d_ff % 64 == 0, d_ff_shared % 64
@@ -214,7 +242,7 @@ moe_status moe_layer_forward_routed(moe_plan* plan, const void* x, int T, const 
  * logits fp32 [T][E] (may be NULL: then kept in the workspace),
  * ids int32 [T][k], gates fp32 [T][k].  Slot j holds the (j+1)-th largest logit under the
  * order (value desc, index asc; +0 == -0; NaN lowest); gates are the softmax of the k
- * selected logits, computed in fp32.
+ * selected logits, computed in fp32.  moe_plan_set_routing replaces this rule.
  */
 moe_status moe_route(moe_plan* plan, const void* x, int T, float* logits, int32_t* ids,
                      float* gates, moe_stream_t stream);
