@@ -142,7 +142,7 @@ def _ptr(t: Optional[torch.Tensor]):
         return None
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()  # an int: the argument types of load_library make it a pointer
 
 
 def _dev(t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
@@ -152,15 +152,22 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return _ptr(t)
 
 
+# The current stream's handle without a Stream object around it (3 us of a small call's host time on
+# a Grace core), where this torch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _rows(t: torch.Tensor, name: str, dtypes, width: int):
@@ -169,13 +176,15 @@ def _rows(t: torch.Tensor, name: str, dtypes, width: int):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{name} must have shape (rows, {width}), got {tuple(t.shape)}")
-    if t.shape[0] and width > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name} must have shape (rows, {width}), got {tuple(shape)}")
+    pitch, step = t.stride()
+    if step != 1 and shape[0] and width > 1:
         raise ValueError(f"{name} must have dense rows")
-    # with one row (or none) the pitch is never used to step; keep it valid
-    pitch = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
-    return ctypes.c_void_p(t.data_ptr()), pitch
+    if shape[0] <= 1:  # with one row (or none) the pitch is never used to step; keep it valid
+        pitch = max(pitch, width)
+    return t.data_ptr(), pitch
 
 
 def _blocks(n: int) -> int:
@@ -265,7 +274,12 @@ class Fp8Linear:
 
     def _out(self, T, out, out_dtype, device):
         if out is None:
+            if out_dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"out must be bf16 or fp32, got {out_dtype}")
             out = torch.empty((T, self.N), dtype=out_dtype, device=device)
+            return out, out.data_ptr(), self.N
+        if out.shape[0] != T:
+            raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
         return out, *_rows(out, "out", (torch.bfloat16, torch.float32), self.N)
 
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None):
@@ -273,8 +287,6 @@ class Fp8Linear:
         px, ldx = _rows(x, "x", DTYPES, self.K)
         T = x.shape[0]
         out, po, ldo = self._out(T, out, out_dtype, x.device)
-        if out.shape[0] != T:
-            raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
         _check(self.lib.moe_linear_forward(self._h, px, DTYPES[x.dtype], ldx, T, po, DTYPES[out.dtype], ldo, _stream(stream)))
         return out
 
@@ -289,8 +301,6 @@ class Fp8Linear:
         if T == 1:  # a single row: its pitch may be anything; only its padding to the vector width matters
             ldq, lds = (ldq + 15) // 16 * 16, (lds + 3) // 4 * 4
         out, po, ldo = self._out(T, out, out_dtype, q.device)
-        if out.shape[0] != T:
-            raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
         _check(self.lib.moe_linear_forward_quantized(self._h, pq, ldq, ps, lds, T, po, DTYPES[out.dtype], ldo,
                                                      _stream(stream)))
         return out
@@ -413,11 +423,11 @@ class MoePlan:
         return logits, ids, gates
 
     def route_logits(self, logits: torch.Tensor, stream=None):
-        T = logits.shape[0]
-        ids = torch.empty((T, self.k), dtype=torch.int32, device=logits.device)
-        gates = torch.empty((T, self.k), dtype=torch.float32, device=logits.device)
-        _check(self.lib.moe_route_logits(self._h, _dev(logits, "logits", torch.float32, (T, self.E)), T, _ptr(ids),
-                                         _ptr(gates), _stream(stream)))
+        T, dev = logits.shape[0], logits.device
+        ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
+        gates = torch.empty((T, self.k), dtype=torch.float32, device=dev)
+        _check(self.lib.moe_route_logits(self._h, _dev(logits, "logits", torch.float32, (T, self.E)), T, ids.data_ptr(),
+                                         gates.data_ptr(), _stream(stream)))
         return ids, gates
 
     def permute(self, ids: torch.Tensor, stream=None):
