@@ -21,6 +21,12 @@
 // Roles (persistent CTAs, one per SM, every role walks the same unit sequence):
 //   warp 0      producer: weights by bulk copy (tile-contiguous, pre-swizzled); rows by TMA
 //   warp 1      TMEM owner and MMA issuer
+//   warp 2      unit list: decodes the CTA's units ahead of the other roles into a ring of shared-memory
+//               records (gate/up: with the source row of each grouped row), so that no role waits for
+//               a chain of global loads where one unit follows the other
+//   warp 3      scales: asynchronous copies of the rows' and the weight blocks' scales into shared memory,
+//               in groups of four K blocks, up to four groups ahead of the epilogue (which has no
+//               registers to hold them in; with a load one block ahead its latency set the pace)
 //   warps 4-11  epilogue: warps 4-7 the tile's first half, 8-11 the second; TMEM lanes 32 (warp % 4)
 //   warps 12-15 gate/up: cp.async gather of the rows, one warp per stage slot
 // Registers move from the first (and the gather) warps to the epilogue warps, which hold 128 sums a
@@ -35,34 +41,51 @@ namespace f8 {
 
 constexpr int kGateUp = 0, kDown = 1, kLinear = 2;
 constexpr int BM = 128;                           // activation rows per tile (MMA M)
-constexpr int kStages = 4;
 constexpr int kBBytes = 2 * kF8TileBytes;         // 256 weight rows x 128 K elements
 constexpr int kABytes = BM * kF8Block;
 constexpr int kStageBytes = kABytes + kBBytes;    // 48 KB
 constexpr int kAccCols = 256;
 constexpr int kTmemCols = 2 * kAccCols;
 constexpr int kEpiWarps = 8, kFirstEpi = 4, kFirstGather = 12;
-constexpr int kTokBytes = kStages * BM * 4;       // per gather warp: source row of each row
-constexpr int kXchBytes = 2 * 2 * BM * 4;         // row maxima of h: [unit parity][half][row]
-constexpr int kSmemBytes = kStages * kStageBytes + 1024 /*barriers*/ + 1024 /*align slack*/ + kTokBytes + kXchBytes;
-static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+constexpr int kRing = 4;                          // decoded units
+constexpr int kScGroups = 4;                      // groups of four K blocks of scales
+constexpr int kScGroupBytes = BM * 16 + 32;       // a row's four scales; the tile's four pairs
+constexpr int kScaleBytes = kScGroups * kScGroupBytes;
+constexpr int kTokBytes = kRing * BM * 4;         // gate/up, per unit: source row of each row
+constexpr int kXchBytes = 2 * 2 * BM * 4;         // gate/up, row maxima of h: [unit parity][half][row]
+constexpr int kOutPitch = 256 + 16;               // a staged row of results: 256 bytes, odd in 16-byte units
+constexpr int kOutBytes = 32 * kOutPitch;         // per epilogue warp
 
 template <int kMode>
 struct Cfg {
+  // gate/up keeps four stages in flight; the others trade one for the staged results
+  static constexpr int kStages = kMode == kGateUp ? 4 : 3;
+  static constexpr int kExtra = kMode == kGateUp ? kTokBytes + kXchBytes : kEpiWarps * kOutBytes;
+  static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /*barriers*/ + 1024 /*align slack*/ + kScaleBytes + kExtra;
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static constexpr int kThreads = kMode == kGateUp ? 512 : 384;
   // register split: the sums over the warpgroups equal the launch's (128 x 4 or 168 x 3)
-  static constexpr int kRegsEpi = kMode == kGateUp ? 208 : 216;
-  static constexpr int kRegsRest = kMode == kGateUp ? 48 : 72;
+  static constexpr int kRegsEpi = kMode == kGateUp ? 200 : 216;
+  static constexpr int kRegsRest = kMode == kGateUp ? 56 : 72;
+  // warps that read each unit record: producer, MMA, scales, epilogue, gather
+  static constexpr int kReaders = 3 + kEpiWarps + (kMode == kGateUp ? kStages : 0);
 };
 
 struct Unit {
-  int expert, row_start, rows, tile, ntile;  // ntile: halves of the tile (1 or 2)
+  int expert, row_start, rows, tile;  // rows == 0: the CTA's units are done
 };
 
-MOE_DEVICE Seg load_seg(const Seg* p) {  // through L2: the down kernel's producer reads them before its wait
+MOE_DEVICE Seg load_seg(const Seg* p) {  // through L2: read before the grid-dependency wait (down)
   const int4 lo = __ldcg(reinterpret_cast<const int4*>(p));
   const int4 hi = __ldcg(reinterpret_cast<const int4*>(p) + 1);
   return Seg{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+}
+
+// Part p of `parts` near-equal parts of `total` rows.
+MOE_DEVICE void part_of(int total, int parts, int p, int& first, int& rows) {
+  const int q = total / parts, rem = total % parts;
+  first = p * q + min(p, rem);
+  rows = q + (p < rem ? 1 : 0);
 }
 
 template <int kMode>
@@ -70,33 +93,55 @@ MOE_DEVICE Unit decode_unit(int u, const F8Args& a, int tiles) {
   Unit un;
   if (kMode == kLinear) {
     const int parts = (a.T + BM - 1) / BM;
-    const int p = u % parts, q = a.T / parts, rem = a.T % parts;
     un.expert = 0;
     un.tile = u / parts;
-    un.row_start = p * q + min(p, rem);
-    un.rows = q + (p < rem ? 1 : 0);
+    part_of(a.T, parts, u % parts, un.row_start, un.rows);
   } else {
-    const Seg any = load_seg(a.segs + u / tiles);
-    const int o = u - any.first * tiles;
-    const Seg s = load_seg(a.segs + any.first + o % any.nparts);
+    const Seg s = load_seg(a.segs + u / tiles);
+    const int o = u - s.first * tiles;
     un.expert = s.expert;
-    un.tile = o / any.nparts;
-    un.row_start = s.row_start;
-    un.rows = s.rows;
+    un.tile = o / s.nparts;
+    part_of(s.total, s.nparts, o % s.nparts, un.row_start, un.rows);
+    un.row_start += s.start;
   }
-  un.ntile = min(2, a.halves - 2 * un.tile);
   return un;
 }
 
+// The ring of decoded units: record j is read by every role's warps.
+struct Ring {
+  uint64_t *full, *empty;
+  const int4* rec;
+  volatile int* abort_flag;
+  uint32_t* err;
+  // Record j once it is there; a record without rows ends the loop (as does an expired wait).
+  MOE_DEVICE Unit get(uint32_t j) const {
+    if (!mbar_wait_warp(&full[j % kRing], (j / kRing) & 1u, abort_flag, err)) return Unit{0, 0, 0, 0};
+    const int4 v = rec[j % kRing];  // (the wait is a compiler barrier too)
+    return Unit{v.x, v.y, v.z, v.w};
+  }
+  // The calling warp no longer reads record j (nor the row table beside it).
+  MOE_DEVICE void done(uint32_t j) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[j % kRing]);
+  }
+};
+
 // Adds 128 columns of one K block, times the scales (s01 the first 64 columns', s23 the rest's), to
-// the thread's sums: 16-column loads, one in flight while the previous one is added.
-MOE_DEVICE void add_block(uint64_t (&acc)[64], uint32_t taddr, uint64_t s01, uint64_t s23) {
+// the thread's sums: 32-column loads, one in flight while the previous one is added.
+// The buffer is handed back once the last load is in registers.
+MOE_DEVICE void add_block(uint64_t (&acc)[64], uint32_t taddr, uint64_t s01, uint64_t s23, uint64_t* empty) {
   uint32_t r[2][16];
   tmem_ld_32x32b_x16(taddr, r[0]);
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    tmem_wait_ld16(r[c & 1]);
-    if (c < 7) tmem_ld_32x32b_x16(taddr + 16 * (c + 1), r[(c + 1) & 1]);
+    tmem_wait_ld(s01, s23);
+    if (c < 7) {
+      tmem_ld_32x32b_x16(taddr + 16 * (c + 1), r[(c + 1) & 1]);
+    } else {
+      tc_fence_before();
+      __syncwarp();
+      mbar_arrive_lane0(empty);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       fma_f32x2(acc[8 * c + i], pack_f32x2(__uint_as_float(r[c & 1][2 * i]), __uint_as_float(r[c & 1][2 * i + 1])),
@@ -110,70 +155,97 @@ MOE_DEVICE void st_global_v8(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-// One row's 128 columns (col0 .. of N) of type out_type.
-template <int kMode>
-MOE_DEVICE void store_row(const uint64_t (&acc)[64], const F8Args& a, int64_t row, int col0) {
-  const int n = a.N - col0;  // valid columns here
-  if (kMode == kDown || a.out_type == MOE_FP16) {
-    uint16_t* o = static_cast<uint16_t*>(a.out) + row * a.ldo + col0;
-    bool sat = false;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float lo, hi;
-        unpack_f32x2(acc[8 * c + i], lo, hi);
-        if (fabsf(lo) > kF16Max || lo != lo) sat |= 16 * c + 2 * i < n, lo = lo != lo ? lo : copysignf(kF16Max, lo);
-        if (fabsf(hi) > kF16Max || hi != hi) sat |= 16 * c + 2 * i + 1 < n, hi = hi != hi ? hi : copysignf(kF16Max, hi);
-        w[i] = static_cast<uint32_t>(f32_to_f16_bits_rn(lo)) | (static_cast<uint32_t>(f32_to_f16_bits_rn(hi)) << 16);
-      }
-      if (a.out_vec && 16 * c + 16 <= n) {
-        st_global_v8(o + 16 * c, w);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (16 * c + i < n) o[16 * c + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-      }
-    }
-    if (sat) set_error(a.err, MOE_DEVERR_RANGE);
-  } else if (a.out_type == MOE_BF16) {
-    uint16_t* o = static_cast<uint16_t*>(a.out) + row * a.ldo + col0;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float lo, hi;
-        unpack_f32x2(acc[8 * c + i], lo, hi);
-        w[i] = pack_bf16x2(lo, hi);
-      }
-      if (a.out_vec && 16 * c + 16 <= n) {
-        st_global_v8(o + 16 * c, w);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (16 * c + i < n) o[16 * c + i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-      }
+MOE_DEVICE uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+MOE_DEVICE uint16_t ld_shared_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+MOE_DEVICE uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+MOE_DEVICE void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Writes the warp's first `rows` staged rows, `cols` elements each, to out at (row0, col).  16 lanes take a
+// row's 256 bytes where rows and columns allow 16-byte stores, else 32 lanes one element each.  (Measured
+// on the mixed step's down projection, us: 32 bytes a lane to 32 rows each straight from the
+// registers 83; a bulk copy of each row 92; this 66.)
+template <typename E>
+MOE_DEVICE void send_rows(const F8Args& a, uint32_t stage, int64_t row0, int rows, int64_t col, int cols, uint64_t pol) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  if (a.out_vec) {
+    const int c = (lane & 15) * (16 / static_cast<int>(sizeof(E)));
+    if (c < cols) {
+      E* o = static_cast<E*>(a.out) + (row0 + (lane >> 4)) * a.ldo + col + c;
+      const uint32_t src = stage + (lane >> 4) * kOutPitch + (lane & 15) * 16;
+#pragma unroll 4
+      for (int i = 0; i < rows; i += 2)
+        if (i + (lane >> 4) < rows) st_global_v4_hint(o + static_cast<int64_t>(i) * a.ldo, ld_shared_v4(src + i * kOutPitch), pol);
     }
   } else {
-    float* o = static_cast<float*>(a.out) + row * a.ldo + col0;
+    for (int i = 0; i < rows; ++i) {
+      E* o = static_cast<E*>(a.out) + (row0 + i) * a.ldo + col;
+      for (int c = lane; c < cols; c += 32) {
+        if (sizeof(E) == 2)
+          *reinterpret_cast<uint16_t*>(o + c) = ld_shared_u16(stage + i * kOutPitch + 2 * c);
+        else
+          *reinterpret_cast<uint32_t*>(o + c) = ld_shared_u32(stage + i * kOutPitch + 4 * c);
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// The warp's rows row0 .. row0 + rows - 1 (a lane each; beyond 32 or below 1 clipped), 128 columns from
+// col0 (of N), through its staging space.
+template <int kMode>
+MOE_DEVICE void store_rows(const uint64_t (&acc)[64], const F8Args& a, uint32_t stage, int64_t row0, int rows, int col0,
+                           uint64_t pol) {
+  const int n = min(128, a.N - col0);  // valid columns here
+  const uint32_t mine = stage + (threadIdx.x & 31) * kOutPitch;
+  rows = min(rows, 32);
+  if (kMode == kDown || a.out_type != MOE_FP32) {
+    const bool f16 = kMode == kDown;
+    bool sat = false;
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
-      uint32_t w[8];
+      uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float lo, hi;
         unpack_f32x2(acc[4 * c + i], lo, hi);
-        w[2 * i] = __float_as_uint(lo), w[2 * i + 1] = __float_as_uint(hi);
+        if (f16) {
+          if (fabsf(lo) > kF16Max || lo != lo) sat |= 8 * c + 2 * i < n, lo = lo != lo ? lo : copysignf(kF16Max, lo);
+          if (fabsf(hi) > kF16Max || hi != hi) sat |= 8 * c + 2 * i + 1 < n, hi = hi != hi ? hi : copysignf(kF16Max, hi);
+          w[i] = static_cast<uint32_t>(f32_to_f16_bits_rn(lo)) | (static_cast<uint32_t>(f32_to_f16_bits_rn(hi)) << 16);
+        } else {
+          w[i] = pack_bf16x2(lo, hi);
+        }
       }
-      if (a.out_vec && 8 * c + 8 <= n) {
-        st_global_v8(o + 8 * c, w);
-      } else {
+      st_shared_v4(mine + 16 * c, w[0], w[1], w[2], w[3]);
+    }
+    if (f16 && sat && static_cast<int>(threadIdx.x & 31) < rows) set_error(a.err, MOE_DEVERR_RANGE);
+    send_rows<uint16_t>(a, stage, row0, rows, col0, n, pol);
+  } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (8 * c + i < n) o[8 * c + i] = __uint_as_float(w[i]);
+    for (int h = 0; h < 2; ++h) {  // 64 columns at a time
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        float v[4];
+        unpack_f32x2(acc[32 * h + 2 * c], v[0], v[1]);
+        unpack_f32x2(acc[32 * h + 2 * c + 1], v[2], v[3]);
+        st_shared_v4(mine + 16 * c, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
       }
+      send_rows<uint32_t>(a, stage, row0, rows, col0 + 64 * h, min(64, n - 64 * h), pol);
     }
   }
 }
@@ -181,6 +253,7 @@ MOE_DEVICE void store_row(const uint64_t (&acc)[64], const F8Args& a, int64_t ro
 template <int kMode>
 __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
     f8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const F8Args a) {
+  constexpr int kStages = Cfg<kMode>::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
@@ -188,11 +261,19 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* xch_bar = acc_empty + 2;   // per lane quarter: both halves published their row maxima
-  uint64_t* drain = xch_bar + 4;
+  uint64_t* ring_full = xch_bar + 4;
+  uint64_t* ring_empty = ring_full + kRing;
+  uint64_t* sc_full = ring_empty + kRing;
+  uint64_t* sc_empty = sc_full + kScGroups;
+  uint64_t* drain = sc_empty + kScGroups;
+  int4* ring_rec = reinterpret_cast<int4*>(smem + kStages * kStageBytes + 512);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* tok_tab = reinterpret_cast<int32_t*>(smem + kStages * kStageBytes + 1024);
-  volatile float* xch = reinterpret_cast<volatile float*>(smem + kStages * kStageBytes + 1024 + kTokBytes);
+  uint8_t* sc_tab = smem + kStages * kStageBytes + 1024;
+  uint8_t* extra = sc_tab + kScaleBytes;
+  int32_t* tok_tab = reinterpret_cast<int32_t*>(extra);                         // gate/up
+  volatile float* xch = reinterpret_cast<volatile float*>(extra + kTokBytes);   // gate/up
+  uint8_t* out_tab = extra;                                                     // linear, down
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -206,6 +287,14 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
       mbar_init(&acc_empty[b], kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&xch_bar[q], 2);
+    for (int i = 0; i < kScGroups; ++i) {
+      mbar_init(&sc_full[i], 32);  // each lane's copies
+      mbar_init(&sc_empty[i], kEpiWarps);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&ring_full[i], 1);
+      mbar_init(&ring_empty[i], Cfg<kMode>::kReaders);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -227,12 +316,12 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
     pdl_trigger();
   } else {
     pdl_trigger();
-    if (warp != 0) pdl_wait();
+    if (warp != 0 && warp != 2) pdl_wait();  // the unit list and the weights are there already
   }
 
   const int tiles = (a.halves + 1) / 2;
   const int nk = a.nk;
-  const int total_units = tiles * (kMode == kLinear ? (a.T + BM - 1) / BM : __ldcg(a.n_segs));
+  const Ring ring{ring_full, ring_empty, ring_rec, abort_flag, a.err};
 
   if (warp < kFirstEpi) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg<kMode>::kRegsRest));
@@ -242,14 +331,17 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
       const uint64_t pol_act = l2_policy_evict_last();
       uint32_t pre = 0;  // stages whose weights were requested before the dependency wait
       if (kMode != kGateUp) {
-        for (int u = blockIdx.x; u < total_units && pre < static_cast<uint32_t>(kStages); u += gridDim.x) {
-          const Unit un = decode_unit<kMode>(u, a, tiles);
+        // (at most kStages units, whose records stay in the ring until the main loop has read them)
+        for (uint32_t j = 0; pre < static_cast<uint32_t>(kStages); ++j) {
+          const Unit un = ring.get(j);
+          if (un.rows == 0) break;
+          const int ntile = min(2, a.halves - 2 * un.tile);
           const uint8_t* wb = a.w + un.expert * a.w_stride;
           for (int kb = 0; kb < nk && pre < static_cast<uint32_t>(kStages); ++kb, ++pre) {
             if (elect_one()) {  // a fresh slot: no wait; the arrival comes with the rows below
-              mbar_expect_tx(&full[pre], un.ntile * kF8TileBytes);
-              bulk_load(smem + pre * kStageBytes, wb + f8_half_offset(2 * un.tile, kb, a.halves, nk),
-                        un.ntile * kF8TileBytes, &full[pre], pol_w);
+              mbar_expect_tx(&full[pre], ntile * kF8TileBytes);
+              bulk_load(smem + pre * kStageBytes, wb + f8_half_offset(2 * un.tile, kb, a.halves, nk), ntile * kF8TileBytes,
+                        &full[pre], pol_w);
             }
             __syncwarp();
           }
@@ -258,8 +350,11 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
       }
       uint32_t g = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
-        const Unit un = decode_unit<kMode>(u, a, tiles);
+      for (uint32_t j = 0; ok; ++j) {
+        const Unit un = ring.get(j);
+        if (un.rows == 0) break;
+        ring.done(j);
+        const int ntile = min(2, a.halves - 2 * un.tile);
         const uint8_t* wb = a.w + un.expert * a.w_stride;
         const int nbox = kMode == kGateUp ? 0 : (un.rows + 31) / 32;
         for (int kb = 0; kb < nk; ++kb, ++g) {
@@ -268,10 +363,9 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
           if (elect_one()) {
             uint8_t* sb = smem + slot * kStageBytes;
             const bool early = g < pre;
-            mbar_arrive_expect_tx(&full[slot], (early ? 0 : un.ntile * kF8TileBytes) + nbox * 32 * kF8Block);
+            mbar_arrive_expect_tx(&full[slot], (early ? 0 : ntile * kF8TileBytes) + nbox * 32 * kF8Block);
             if (!early)
-              bulk_load(sb, wb + f8_half_offset(2 * un.tile, kb, a.halves, nk), un.ntile * kF8TileBytes, &full[slot],
-                        pol_w);
+              bulk_load(sb, wb + f8_half_offset(2 * un.tile, kb, a.halves, nk), ntile * kF8TileBytes, &full[slot], pol_w);
             if (kMode != kGateUp)
               for (int i = 0; i < nbox; ++i)
                 tma_load_2d(sb + kBBytes + i * 32 * kF8Block, &amap, &full[slot], kb * kF8Block, un.row_start + 32 * i,
@@ -281,89 +375,149 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
         }
       }
     } else if (warp == 1) {
-      // ---------------- MMA issuer: the warp waits, one elected lane issues ----------------
+      // ---------------- MMA issuer ----------------
+      // One elected lane runs a unit's whole K loop: it waits, issues a block's four MMAs and commits.
+      // Its own instructions set the pace of a deep K loop (measured in a loop that voted and
+      // computed descriptors per MMA: a vote 32 cycles, a barrier probe 46, an MMA 57), so the
+      // warp votes once per unit, slots and phases advance incrementally, and the next stage's
+      // barrier is probed right after this one's commits.
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), accf0 = smem_u32(acc_full);
+      const uint64_t b0 = smem_desc_sw128(smem_u32(smem));
       uint32_t g = 0;
-      bool ok = true, ready = false;  // ready: full[g % kStages] already seen complete for stage g
-      for (int u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
-        const Unit un = decode_unit<kMode>(u, a, tiles);
-        const uint32_t idesc = idesc_e4m3_f32(BM, 128u * un.ntile);
-        for (int kb = 0; kb < nk; ++kb, ++g) {
-          const int slot = g % kStages;
-          const uint32_t buf = g & 1u, use_acc = g >> 1;
-          if (!ready && !(ok = mbar_wait_warp(&full[slot], (g / kStages) & 1u, abort_flag, a.err))) break;
-          if (!(ok = mbar_wait_warp(&acc_empty[buf], (use_acc & 1u) ^ 1u, abort_flag, a.err))) break;
-          const uint32_t gn = g + 1;  // probe the next stage now, use the answer next iteration
-          const bool next = mbar_test(&full[gn % kStages], (gn / kStages) & 1u);
-          tc_fence_after();
-          const uint32_t sb = smem_u32(smem + slot * kStageBytes);
-          const uint64_t bdesc = smem_desc_sw128(sb);
-          const uint64_t adesc = smem_desc_sw128(sb + kBBytes);
-          const uint32_t d_tmem = tmem + buf * kAccCols;
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < kF8Block / 32; ++ks)  // K = 32 per MMA: +32 bytes = +2 in the address field
-              mma_f8_ss(d_tmem, adesc + 2 * ks, bdesc + 2 * ks, idesc, ks != 0);
-            mma_commit(&empty[slot]);
-            mma_commit(&acc_full[buf]);
+      bool ok = true;
+      for (uint32_t j = 0; ok; ++j) {
+        const Unit un = ring.get(j);
+        if (un.rows == 0) break;
+        ring.done(j);
+        const uint32_t idesc = idesc_e4m3_f32(BM, 128u * min(2, a.halves - 2 * un.tile));
+        if (elect_one()) {
+          uint32_t slot = g % kStages, ph = (g / kStages) & 1u, buf = g & 1u, aph = ((g >> 1) & 1u) ^ 1u;
+          bool ready = false;
+          for (int kb = 0; kb < nk; ++kb) {
+            if (!ready && !(ok = mbar_wait(&full[slot], ph, abort_flag, a.err))) break;
+            if (!(ok = mbar_wait(&acc_empty[buf], aph, abort_flag, a.err))) break;
+            tc_fence_after();
+            const uint64_t bdesc = b0 + slot * (kStageBytes >> 4);
+            mma_f8_block(tmem + buf * kAccCols, bdesc + (kBBytes >> 4), bdesc, idesc);
+            mma_commit_u32(empty0 + 8 * slot);
+            mma_commit_u32(accf0 + 8 * buf);
+            if (++slot == kStages) slot = 0, ph ^= 1u;
+            aph ^= buf;  // both buffers used: their next phase
+            buf ^= 1u;
+            ready = mbar_test_u32(full0 + 8 * slot, ph);
           }
-          __syncwarp();
-          ready = __all_sync(0xffffffffu, next);
         }
+        g += nk;
+        ok = __all_sync(0xffffffffu, ok);
       }
       // all MMAs issued by this warp have finished once `drain` completes
       if (elect_one()) mma_commit(drain);
       __syncwarp();
       mbar_wait_warp(drain, 0, nullptr, a.err);
+    } else if (warp == 2) {
+      // ---------------- unit list ----------------
+      const int total_units = tiles * (kMode == kLinear ? (a.T + BM - 1) / BM : __ldcg(a.n_segs));
+      uint32_t j = 0;
+      for (int u = blockIdx.x;; u += gridDim.x, ++j) {
+        const bool more = u < total_units;
+        const Unit un = more ? decode_unit<kMode>(u, a, tiles) : Unit{0, 0, 0, 0};
+        const int slot = j % kRing;
+        if (!mbar_wait_warp(&ring_empty[slot], ((j / kRing) & 1u) ^ 1u, abort_flag, a.err)) break;
+        if (kMode == kGateUp)
+          for (int n = lane; n < un.rows; n += 32) tok_tab[BM * slot + n] = a.perm[un.row_start + n] / a.k;
+        if (lane == 0) ring_rec[slot] = make_int4(un.expert, un.row_start, un.rows, un.tile);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ring_full[slot]);
+        if (!more) break;
+      }
+    } else {
+      // ---------------- scales ----------------
+      // Lane l copies the scales of rows l + 32 i of the tile; a lane's arrival on a group's barrier
+      // comes with its copies.
+      const int ng = (nk + 3) / 4;
+      uint32_t c = 0;
+      bool ok = true;
+      for (uint32_t j = 0; ok; ++j) {
+        const Unit un = ring.get(j);
+        if (un.rows == 0) break;
+        const float* row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = min(lane + 32 * i, un.rows - 1);
+          row[i] = a.as + (kMode == kGateUp ? tok_tab[BM * (j % kRing) + rr] : un.row_start + rr) * a.lds;
+        }
+        ring.done(j);
+        const float* sw = a.ws + (static_cast<int64_t>(un.expert) * tiles + un.tile) * f8_scale_ld(nk) * 2 + 4 * (lane & 1);
+        for (int gi = 0; gi < ng; ++gi, ++c) {
+          const int slot = c % kScGroups;
+          if (!(ok = mbar_wait_warp(&sc_empty[slot], ((c / kScGroups) & 1u) ^ 1u, abort_flag, a.err))) break;
+          const uint32_t dst = smem_u32(sc_tab + slot * kScGroupBytes);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (32 * i < un.rows) cp_async_16(dst + (lane + 32 * i) * 16, row[i] + 4 * gi);
+          if (lane < 2) cp_async_16(dst + BM * 16 + 16 * lane, sw + 8 * gi);
+          cp_async_arrive(&sc_full[slot]);
+        }
+      }
+      cp_async_commit();
+      cp_async_wait<0>();  // none is in flight when the CTA ends
     }
   } else if (warp < kFirstGather) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg<kMode>::kRegsEpi));
     // ---------------- epilogue ----------------
     const int q = warp & 3, half = (warp - kFirstEpi) >> 2;
     const int r = 32 * q + lane;  // row of the tile
-    uint32_t g = 0, nx = 0;  // nx: exchanges of row maxima so far
+    const uint32_t stage_out = smem_u32(out_tab + (warp - kFirstEpi) * kOutBytes);
+    // y is read back by the next launch: keep it in L2 ahead of the streamed weights
+    const uint64_t pol_out = kMode == kDown ? l2_policy_evict_last() : l2_policy_evict_first();
+    uint32_t g = 0, c = 0, nx = 0;  // K blocks, groups of scales, exchanges of row maxima so far
     bool ok = true;
-    for (int u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
-      const Unit un = decode_unit<kMode>(u, a, tiles);
-      const bool on = 32 * q < un.rows && half < un.ntile;  // warp-uniform: some row and column is wanted
-      const int64_t grow = un.row_start + min(r, un.rows - 1);
-      int64_t srow = grow;
-      if (kMode == kGateUp) srow = a.perm[grow] / a.k;
-      const float4* sa4 = reinterpret_cast<const float4*>(a.as + srow * a.lds);
-      const float2* sw = reinterpret_cast<const float2*>(a.ws) + (static_cast<int64_t>(un.expert) * tiles + un.tile) * nk;
+    for (uint32_t j = 0; ok; ++j) {
+      const Unit un = ring.get(j);
+      if (un.rows == 0) break;
+      ring.done(j);
+      const bool on = 32 * q < un.rows && half < a.halves - 2 * un.tile;  // some row and column is wanted
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      float4 sa_now = make_float4(0.f, 0.f, 0.f, 0.f), sa_next = sa_now;
-      float2 sw_next = make_float2(0.f, 0.f);
-      if (on) {
-        sa_next = sa4[0];
-        sw_next = __ldg(sw);
-      }
-      for (int kb = 0; kb < nk; ++kb, ++g) {
-        const uint32_t buf = g & 1u, use_acc = g >> 1;
-        const float2 w2 = sw_next;
-        if (on) {  // the next blocks' scales are requested a block (four blocks) ahead
-          if ((kb & 3) == 0) {
-            sa_now = sa_next;
-            if (kb + 4 < nk) sa_next = sa4[(kb >> 2) + 1];
+      if (!on) {  // (a loop of its own: a condition inside the other one costs it 90 register moves a block)
+        for (int kb = 0; kb < nk; ++kb, ++g) {
+          ok &= mbar_wait(&acc_full[g & 1u], (g >> 1) & 1u, abort_flag, a.err);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[g & 1u]);
+          if ((kb & 3) == 3 || kb == nk - 1) {
+            if (lane == 0) mbar_arrive(&sc_empty[c % kScGroups]);
+            ++c;
           }
-          if (kb + 1 < nk) sw_next = __ldg(sw + kb + 1);
         }
-        const float sa = (kb & 2) ? ((kb & 1) ? sa_now.w : sa_now.z) : ((kb & 1) ? sa_now.y : sa_now.x);
-        if (!(ok = mbar_wait_warp(&acc_full[buf], use_acc & 1u, abort_flag, a.err))) break;
-        if (on) {
-          tc_fence_after();
-          const float s0 = kMode == kGateUp ? sa * w2.x : sa * (half ? w2.y : w2.x);
-          const float s1 = kMode == kGateUp ? sa * w2.y : s0;
-          add_block(acc, tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * kAccCols + half * 128, pack_f32x2(s0, s0),
-                    pack_f32x2(s1, s1));
-          tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        ok = __all_sync(0xffffffffu, ok);
+        continue;
       }
+#pragma unroll 1
+      for (int kb = 0; kb < nk; ++kb, ++g) {
+        // (a lane whose wait expired goes on with whatever is there; the warp stops after the unit)
+        const uint32_t buf = g & 1u, slot = c % kScGroups;
+        const float* grp = reinterpret_cast<const float*>(sc_tab + slot * kScGroupBytes);
+        if ((kb & 3) == 0) ok &= mbar_wait(&sc_full[slot], (c / kScGroups) & 1u, abort_flag, a.err);
+        const float sa = grp[4 * r + (kb & 3)];
+        const float2 w = *reinterpret_cast<const float2*>(grp + 4 * BM + 2 * (kb & 3));
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&acc_full[buf], (g >> 1) & 1u))) {
+          ok &= mbar_wait(&acc_full[buf], (g >> 1) & 1u, abort_flag, a.err);
+          __syncwarp();
+        }
+        if ((kb & 3) == 3 || kb == nk - 1) {  // every lane has read the group's last scales
+          mbar_arrive_lane0(&sc_empty[slot]);
+          ++c;
+        }
+        tc_fence_after();
+        const float s0 = sa * (kMode == kGateUp || half == 0 ? w.x : w.y);
+        const float s1 = kMode == kGateUp ? sa * w.y : s0;
+        add_block(acc, tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * kAccCols + half * 128, pack_f32x2(s0, s0),
+                  pack_f32x2(s1, s1), &acc_empty[buf]);
+      }
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (!on) continue;
+      const int64_t grow = un.row_start + r;
       if (kMode == kGateUp) {
         // columns 0..63 gate, 64..127 up of features 64 half .. + 63 of the tile's 128
         float h[64], amax = 0.f;
@@ -402,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
           if (half == 0) a.hs[grow * a.ldhs + un.tile] = sc;
         }
       } else {
-        if (r < un.rows) store_row<kMode>(acc, a, grow, un.tile * 256 + half * 128);
+        store_rows<kMode>(acc, a, stage_out, un.row_start + 32 * q, un.rows - 32 * q, un.tile * 256 + half * 128, pol_out);
       }
     }
   } else {
@@ -412,22 +566,17 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
     // copies, fences them for the tensor core and arrives.  8 consecutive lanes copy one row's
     // 128 bytes.
     const int slot = warp - kFirstGather;
-    int32_t* tok = tok_tab + BM * slot;
     const int ch = lane & 7;
     const uint64_t pol_x = l2_policy_evict_last();
     uint32_t g = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
-      const Unit un = decode_unit<kMode>(u, a, tiles);
-      bool have_tok = false;
+    for (uint32_t j = 0; ok; ++j) {
+      const Unit un = ring.get(j);
+      if (un.rows == 0) break;
+      const int32_t* tok = tok_tab + BM * (j % kRing);
       for (int kb = 0; kb < nk; ++kb, ++g) {
         const int s = g % kStages;
         if (s != slot) continue;
-        if (!have_tok) {
-          for (int n = lane; n < un.rows; n += 32) tok[n] = a.perm[un.row_start + n] / a.k;
-          __syncwarp();
-          have_tok = true;
-        }
         if (!(ok = mbar_wait_warp(&empty[s], ((g / kStages) & 1u) ^ 1u, abort_flag, a.err))) break;
         const uint32_t sa = smem_u32(smem + s * kStageBytes + kBBytes);
         const int k0 = kb * kF8Block + ch * 16;
@@ -439,7 +588,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
       }
-      __syncwarp();  // the table is read by the whole warp before the next unit rewrites it
+      ring.done(j);
     }
   }
 
@@ -458,9 +607,9 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
 template <int kMode>
 static cudaError_t launch_f8(const CUtensorMap& m, const F8Args& a, int num_sms, cudaStream_t st) {
   auto kern = f8::f8_gemm_kernel<kMode>;
-  cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), f8::kSmemBytes);
+  cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), f8::Cfg<kMode>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(num_sms), dim3(f8::Cfg<kMode>::kThreads), f8::kSmemBytes, st, m, a);
+  return launch_pdl(kern, dim3(num_sms), dim3(f8::Cfg<kMode>::kThreads), f8::Cfg<kMode>::kSmemBytes, st, m, a);
 }
 
 cudaError_t launch_f8_gateup(const F8Args& a, int num_sms, cudaStream_t st) {

@@ -39,14 +39,15 @@ constexpr int kSegRowsMax = 128;
 
 // One segment of the grouped problem: `rows` consecutive grouped rows of one expert starting
 // at `row_start`.  An expert with more than kSegRowsMax rows has several parts; `first` is
-// the index of its first part in the segment list and `nparts` their number.
+// the index of its first part in the segment list, `nparts` their number, and `start` and `total`
+// the expert's rows over all parts, so that one record locates every part.
 struct Seg {
   int expert;
   int row_start;
   int rows;
   int first;
   int nparts;
-  int pad0, pad1, pad2;
+  int start, total, pad;
 };
 
 // Scored selection (scored.cuh); on == 0: the softmax of the k largest logits.
@@ -216,7 +217,7 @@ int mx_scale_bytes(int K);
 //   linear / down: half h = rows 128 h .. 128 h + 127 of the matrix;
 //   gate/up: half h = gate rows 64 h .. 64 h + 63, then the up rows of the same features; always
 //     whole tiles (128 features, the block that shares one activation scale of h).
-// Scales [matrix][tile][K block][2]: the two 128-row blocks', or gate's and up's.
+// Scales [matrix][tile][K block, padded to four][2]: the two 128-row blocks', or gate's and up's.
 constexpr int kF8TileBytes = 128 * 128;
 __host__ __device__ inline int f8_halves(int rows, bool gate_up) {
   return gate_up ? 2 * ((rows + 127) / 128) : (rows + 127) / 128;
@@ -239,7 +240,7 @@ cudaError_t launch_tile_fp8(const uint8_t* a, const float* sa, const uint8_t* b,
 
 struct F8Args {
   const uint8_t* w = nullptr;   // tiled weights; matrix stride w_stride bytes
-  const float* ws = nullptr;    // tiled scales; matrix stride tiles * nk * 2
+  const float* ws = nullptr;    // tiled scales
   int64_t w_stride = 0;
   const uint8_t* a = nullptr;   // gate/up: e4m3 rows of x (gathered by perm), pitch lda bytes
   int64_t lda = 0;
@@ -254,7 +255,7 @@ struct F8Args {
   void* out = nullptr;          // linear / down out [rows][ldo] of out_type, columns < N
   int64_t ldo = 0;
   int out_type = MOE_FP16;      // fp16 (the layer's y: clamped, flags MOE_DEVERR_RANGE), bf16 or fp32
-  int out_vec = 0;              // 32-byte stores are aligned
+  int out_vec = 0;              // rows start, and N ends, on 16-byte boundaries
   int N = 0, halves = 0, nk = 0;
   int T = 0, k = 0;
   uint32_t* err = nullptr;

@@ -106,7 +106,7 @@ extern "C" moe_status moe_linear_set_weights(moe_linear* l, const uint8_t* q, co
   }
   const size_t tiles = (l->halves + 1) / 2;
   if (!l->w) LIN_TRY(cudaMalloc(&l->w, static_cast<size_t>(l->halves) * l->nk * kF8TileBytes));
-  if (!l->ws) LIN_TRY(cudaMalloc(&l->ws, tiles * l->nk * 2 * sizeof(float)));
+  if (!l->ws) LIN_TRY(cudaMalloc(&l->ws, tiles * f8_scale_ld(l->nk) * 2 * sizeof(float)));
   LIN_TRY(launch_tile_fp8(q, s, nullptr, nullptr, l->w, l->ws, 1, l->N, l->K, 0));
   LIN_TRY(cudaDeviceSynchronize());
   l->weights_set = true;
@@ -157,7 +157,7 @@ static moe_status product(moe_linear* l, const uint8_t* q, int64_t ldq, const fl
   a.out = out;
   a.ldo = ldo;
   a.out_type = out_dtype;
-  a.out_vec = aligned(out, 32) && (ldo * elem_bytes(out_dtype)) % 32 == 0;
+  a.out_vec = aligned(out, 16) && (ldo * elem_bytes(out_dtype)) % 16 == 0 && (l->N * elem_bytes(out_dtype)) % 16 == 0;
   a.N = l->N;
   a.halves = l->halves;
   a.nk = l->nk;

@@ -129,19 +129,20 @@ __global__ void __launch_bounds__(256) tile_fp8_kernel(const uint8_t* __restrict
   }
 }
 
-// Scales [n][rb][nk] (one matrix, or gate and up) -> [n][tiles][nk][2].
+// Scales [n][rb][nk] (one matrix, or gate and up) -> [n][tiles][f8_scale_ld(nk)][2].
 __global__ void __launch_bounds__(256) tile_scales_kernel(const float* __restrict__ a, const float* __restrict__ b,
                                                           float* __restrict__ dst, int n, int rb, int tiles, int nk) {
-  const int64_t total = static_cast<int64_t>(n) * tiles * nk * 2;
+  const int ld = f8_scale_ld(nk);
+  const int64_t total = static_cast<int64_t>(n) * tiles * ld * 2;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
     const int w = static_cast<int>(i & 1);
     const int64_t o = i >> 1;
-    const int kb = static_cast<int>(o % nk);
-    const int t = static_cast<int>((o / nk) % tiles);
-    const int64_t m = o / nk / tiles;
+    const int kb = static_cast<int>(o % ld);
+    const int t = static_cast<int>((o / ld) % tiles);
+    const int64_t m = o / ld / tiles;
     const int blk = b ? t : 2 * t + w;
     const float* src = (b && w) ? b : a;
-    dst[i] = blk < rb ? src[(m * rb + blk) * nk + kb] : 0.f;
+    dst[i] = blk < rb && kb < nk ? src[(m * rb + blk) * nk + kb] : 0.f;
   }
 }
 
@@ -156,7 +157,7 @@ cudaError_t launch_tile_fp8(const uint8_t* a, const float* sa, const uint8_t* b,
                                                                                          chunks, vec);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t ns = static_cast<int64_t>(n) * tiles * nk * 2;
+  const int64_t ns = static_cast<int64_t>(n) * tiles * f8_scale_ld(nk) * 2;
   tile_scales_kernel<<<static_cast<unsigned>((ns + 255) / 256 < 4096 ? (ns + 255) / 256 : 4096), 256, 0, st>>>(sa, sb, sdst, n,
                                                                                                     rb, tiles, nk);
   return cudaGetLastError();

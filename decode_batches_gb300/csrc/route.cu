@@ -462,7 +462,7 @@ MOE_DEVICE void write_segments(Seg* segs, int base, int max_segs, int e, int sta
   for (int s = 0; s < ns; ++s) {
     const int rows = q + (s < rem ? 1 : 0);
     if (base + s < max_segs) {
-      segs[base + s] = Seg{e, r, rows, base, ns, 0, 0, 0};
+      segs[base + s] = Seg{e, r, rows, base, ns, start, total, 0};
     } else {
       set_error(err, MOE_DEVERR_SEGMENT);
     }
@@ -829,7 +829,7 @@ MOE_DEVICE void group_tiny(int T, int E, int k, const int32_t* sids, int32_t* __
         const uint64_t above = S & ~upto;
         const int next = above ? __ffsll(static_cast<long long>(above)) - 1 : n_valid;
         if (idx < max_segs)
-          segs[idx] = Seg{static_cast<int>(key[h] >> 8), p, next - p, idx, 1, 0, 0, 0};
+          segs[idx] = Seg{static_cast<int>(key[h] >> 8), p, next - p, idx, 1, p, next - p, 0};
         else
           set_error(err, MOE_DEVERR_SEGMENT);
       }
