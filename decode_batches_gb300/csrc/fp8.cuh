@@ -156,6 +156,14 @@ MOE_DEVICE void mbar_arrive_lane0(uint64_t* bar) {
       : "memory");
 }
 
+// Two fp16 values, `lo` in the low half, rounded to nearest even; magnitudes beyond fp16 become its
+// largest, NaN stays NaN.
+MOE_DEVICE uint32_t f32x2_to_f16x2_sat(float lo, float hi) {
+  uint32_t v;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+
 // Instruction descriptor, kind::f8f6f4: D fp32 (bits 4-5 = 1), A and B e4m3 (bits 7-9 and 10-12 =
 // 0), both K-major, N >> 3 in bits [17,23), M >> 4 in bits [24,29).
 MOE_DEVICE uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) { return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24); }

@@ -213,9 +213,9 @@ MOE_DEVICE void store_rows(const uint64_t (&acc)[64], const F8Args& a, uint32_t 
   const int n = min(128, a.N - col0);  // valid columns here
   const uint32_t mine = stage + (threadIdx.x & 31) * kOutPitch;
   rows = min(rows, 32);
-  if (kMode == kDown || a.out_type != MOE_FP32) {
-    const bool f16 = kMode == kDown;
-    bool sat = false;
+  if (kMode == kDown) {
+    // one straight run of few instructions: executed once a unit, it pays for its length in fetches
+    float m = 0.f;
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       uint32_t w[4];
@@ -223,17 +223,25 @@ MOE_DEVICE void store_rows(const uint64_t (&acc)[64], const F8Args& a, uint32_t 
       for (int i = 0; i < 4; ++i) {
         float lo, hi;
         unpack_f32x2(acc[4 * c + i], lo, hi);
-        if (f16) {
-          if (fabsf(lo) > kF16Max || lo != lo) sat |= 8 * c + 2 * i < n, lo = lo != lo ? lo : copysignf(kF16Max, lo);
-          if (fabsf(hi) > kF16Max || hi != hi) sat |= 8 * c + 2 * i + 1 < n, hi = hi != hi ? hi : copysignf(kF16Max, hi);
-          w[i] = static_cast<uint32_t>(f32_to_f16_bits_rn(lo)) | (static_cast<uint32_t>(f32_to_f16_bits_rn(hi)) << 16);
-        } else {
-          w[i] = pack_bf16x2(lo, hi);
-        }
+        m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));  // (columns beyond N have zero weights)
+        w[i] = f32x2_to_f16x2_sat(lo, hi);
       }
       st_shared_v4(mine + 16 * c, w[0], w[1], w[2], w[3]);
     }
-    if (f16 && sat && static_cast<int>(threadIdx.x & 31) < rows) set_error(a.err, MOE_DEVERR_RANGE);
+    if (m > kF16Max && static_cast<int>(threadIdx.x & 31) < rows) set_error(a.err, MOE_DEVERR_RANGE);
+    send_rows<uint16_t>(a, stage, row0, rows, col0, n, pol);
+  } else if (a.out_type == MOE_BF16) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack_f32x2(acc[4 * c + i], lo, hi);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
+      }
+      st_shared_v4(mine + 16 * c, w[0], w[1], w[2], w[3]);
+    }
     send_rows<uint16_t>(a, stage, row0, rows, col0, n, pol);
   } else {
 #pragma unroll
