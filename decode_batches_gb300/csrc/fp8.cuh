@@ -47,57 +47,61 @@ struct Load8<float> {
   MOE_DEVICE static float one(const float* p) { return *p; }
 };
 
-// The half-warps first, first + step, ... of rows x [rows][K] in blocks of 128: each holds a block in
-// registers (8 elements a lane), takes its largest magnitude with four shuffles and writes 128
-// contiguous bytes of codes and the scale.  nb = ceil(K / 128); vec: the rows are 16-byte aligned.  Whole
-// warps call it, with step even and the lower half-warp's `first` even.
+// Rows x [rows][K] in blocks of 128 by the warps first, first + step, ...: a warp takes eight blocks of
+// a row at a time, two per half-warp pair of loads, all four loads in flight.  A half-warp holds a
+// block in registers (8 elements a lane), takes its largest magnitude with four shuffles and writes
+// 128 contiguous bytes of codes and the scale.  nb = ceil(K / 128); vec: the rows are 16-byte aligned.
 template <typename T>
 MOE_DEVICE void quant_rows_part(const T* __restrict__ x, int64_t ldx, int rows, int K, int nb, bool vec,
-                                uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s, int64_t lds, int64_t first,
-                                int64_t step) {
-  const int64_t total = static_cast<int64_t>(rows) * nb;
-  const int lane = threadIdx.x & 15;
-  for (int64_t i0 = first & ~int64_t(1); i0 < total; i0 += step) {  // warp-uniform: the shuffles need every lane
-    const int64_t i = i0 + (first & 1);
-    const bool on = i < total;
-    const int64_t row = on ? i / nb : 0;
-    const int b = on ? static_cast<int>(i - row * nb) : 0;
-    const int k0 = b * kF8Block + 8 * lane;
-    const T* p = x + row * ldx + k0;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (on) {
+                                uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s, int64_t lds, uint32_t first,
+                                uint32_t step) {
+  const uint32_t chunks = (nb + 7) / 8;  // of a row
+  const int lane = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
+  const uint32_t step_row = step / chunks, step_chunk = step % chunks;
+  uint32_t row = first / chunks, chunk = first % chunks;
+  while (row < static_cast<uint32_t>(rows)) {
+    const T* xr = x + row * ldx;
+    float v[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k0 = (8 * chunk + 2 * u + half) * kF8Block + 8 * lane;
       if (vec && k0 + 8 <= K) {
-        Load8<T>::vec(p, v);
+        Load8<T>::vec(xr + k0, v[u]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (k0 + j < K) v[j] = Load8<T>::one(p + j);
+        for (int j = 0; j < 8; ++j) v[u][j] = k0 + j < K ? Load8<T>::one(xr + k0 + j) : 0.f;
       }
     }
-    float amax = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    for (int u = 0; u < 4; ++u) {
+      const int b = 8 * chunk + 2 * u + half;
+      float amax = 0.f;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float sc = f8_scale(amax);
-    const float r = __frcp_rn(sc);
-    uint2 w;
-    w.x = f32x2_to_e4m3x2(v[0] * r, v[1] * r) | (f32x2_to_e4m3x2(v[2] * r, v[3] * r) << 16);
-    w.y = f32x2_to_e4m3x2(v[4] * r, v[5] * r) | (f32x2_to_e4m3x2(v[6] * r, v[7] * r) << 16);
-    if (on) {
-      *reinterpret_cast<uint2*>(q + row * ldq + k0) = w;  // columns K .. 128 nb get the code of zero
-      if (lane == 0) s[row * lds + b] = sc;
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[u][j]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const float sc = f8_scale(amax);
+      const float r = __frcp_rn(sc);
+      uint2 w;
+      w.x = f32x2_to_e4m3x2(v[u][0] * r, v[u][1] * r) | (f32x2_to_e4m3x2(v[u][2] * r, v[u][3] * r) << 16);
+      w.y = f32x2_to_e4m3x2(v[u][4] * r, v[u][5] * r) | (f32x2_to_e4m3x2(v[u][6] * r, v[u][7] * r) << 16);
+      if (b < nb) {
+        *reinterpret_cast<uint2*>(q + row * ldq + b * kF8Block + 8 * lane) = w;  // columns K .. 128 nb: zero
+        if (lane == 0) s[row * lds + b] = sc;
+      }
     }
+    row += step_row;
+    chunk += step_chunk;
+    if (chunk >= chunks) chunk -= chunks, ++row;
   }
 }
 
 // The conversion of x that a routing launch performs on the side: fp16 copy (4-bit experts) or 8-bit
 // blocks (8-bit experts), by blocks `block` of `blocks`.
 MOE_DEVICE void convert_x8(const XConv& c, int block, int blocks) {
-  const int per = blockDim.x >> 4;
+  const uint32_t per = blockDim.x >> 5;
   quant_rows_part(reinterpret_cast<const __nv_bfloat16*>(c.x), c.K, c.rows, c.K, (c.K + kF8Block - 1) / kF8Block, true, c.xq,
-                  c.ldq, c.xs, c.lds, static_cast<int64_t>(block) * per + (threadIdx.x >> 4),
-                  static_cast<int64_t>(blocks) * per);
+                  c.ldq, c.xs, c.lds, block * per + (threadIdx.x >> 5), blocks * per);
 }
 MOE_DEVICE void convert_x(const XConv& c, uint32_t* err) {
   if (c.xq)

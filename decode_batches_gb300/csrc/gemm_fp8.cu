@@ -15,6 +15,9 @@
 //            quantises the 128 features (one activation block of h) and writes codes and scale.
 //   down     a = those rows of h; y in fp16 in grouped order for the combine.
 //   linear   a = the T rows of one matrix; bf16 or fp32 out.
+//   split    linear with few units: a cluster of S CTAs shares a unit, each a range of its K blocks;
+//            the fp32 sums meet in shared memory and every CTA adds up (in split order) and writes a
+//            1/S of the columns.
 // Routed units are ordered tile-major within an expert's parts, linear units tile-major over the
 // row parts: CTAs that share a weight tile run side by side and its second read is served by L2.
 //
@@ -36,10 +39,13 @@
 #include "fp8.cuh"
 #include "kernels.h"
 
+#include <map>
+#include <mutex>
+
 namespace moe {
 namespace f8 {
 
-constexpr int kGateUp = 0, kDown = 1, kLinear = 2;
+constexpr int kGateUp = 0, kDown = 1, kLinear = 2, kSplit = 3;
 constexpr int BM = 128;                           // activation rows per tile (MMA M)
 constexpr int kBBytes = 2 * kF8TileBytes;         // 256 weight rows x 128 K elements
 constexpr int kABytes = BM * kF8Block;
@@ -55,6 +61,8 @@ constexpr int kTokBytes = kRing * BM * 4;         // gate/up, per unit: source r
 constexpr int kXchBytes = 2 * 2 * BM * 4;         // gate/up, row maxima of h: [unit parity][half][row]
 constexpr int kOutPitch = 256 + 16;               // a staged row of results: 256 bytes, odd in 16-byte units
 constexpr int kOutBytes = 32 * kOutPitch;         // per epilogue warp
+constexpr int kSumPitch = 256 * 4 + 16;           // split: a row of fp32 sums (in the stages' space)
+static_assert(BM * kSumPitch <= 3 * kStageBytes, "sums in the stages");
 
 template <int kMode>
 struct Cfg {
@@ -91,7 +99,7 @@ MOE_DEVICE void part_of(int total, int parts, int p, int& first, int& rows) {
 template <int kMode>
 MOE_DEVICE Unit decode_unit(int u, const F8Args& a, int tiles) {
   Unit un;
-  if (kMode == kLinear) {
+  if (kMode >= kLinear) {
     const int parts = (a.T + BM - 1) / BM;
     un.expert = 0;
     un.tile = u / parts;
@@ -155,6 +163,21 @@ MOE_DEVICE void st_global_v8(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
+// Cluster barrier of every thread (arrive.release, wait.acquire), and 16 bytes of CTA `rank`'s shared memory
+// at this CTA's address `addr`.
+MOE_DEVICE void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+MOE_DEVICE float4 ld_cluster_v4(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
 MOE_DEVICE uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -329,6 +352,10 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
 
   const int tiles = (a.halves + 1) / 2;
   const int nk = a.nk;
+  // split: this CTA's share of the K blocks
+  const int split = kMode == kSplit ? static_cast<int>(blockIdx.x) % a.splits : 0;
+  const int kb0 = kMode == kSplit ? split * nk / a.splits : 0;
+  const int kb1 = kMode == kSplit ? (split + 1) * nk / a.splits : nk;
   const Ring ring{ring_full, ring_empty, ring_rec, abort_flag, a.err};
 
   if (warp < kFirstEpi) {
@@ -345,7 +372,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
           if (un.rows == 0) break;
           const int ntile = min(2, a.halves - 2 * un.tile);
           const uint8_t* wb = a.w + un.expert * a.w_stride;
-          for (int kb = 0; kb < nk && pre < static_cast<uint32_t>(kStages); ++kb, ++pre) {
+          for (int kb = kb0; kb < kb1 && pre < static_cast<uint32_t>(kStages); ++kb, ++pre) {
             if (elect_one()) {  // a fresh slot: no wait; the arrival comes with the rows below
               mbar_expect_tx(&full[pre], ntile * kF8TileBytes);
               bulk_load(smem + pre * kStageBytes, wb + f8_half_offset(2 * un.tile, kb, a.halves, nk), ntile * kF8TileBytes,
@@ -365,7 +392,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
         const int ntile = min(2, a.halves - 2 * un.tile);
         const uint8_t* wb = a.w + un.expert * a.w_stride;
         const int nbox = kMode == kGateUp ? 0 : (un.rows + 31) / 32;
-        for (int kb = 0; kb < nk; ++kb, ++g) {
+        for (int kb = kb0; kb < kb1; ++kb, ++g) {
           const int slot = g % kStages;
           if (!(ok = mbar_wait_warp(&empty[slot], ((g / kStages) & 1u) ^ 1u, abort_flag, a.err))) break;
           if (elect_one()) {
@@ -401,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
         if (elect_one()) {
           uint32_t slot = g % kStages, ph = (g / kStages) & 1u, buf = g & 1u, aph = ((g >> 1) & 1u) ^ 1u;
           bool ready = false;
-          for (int kb = 0; kb < nk; ++kb) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             if (!ready && !(ok = mbar_wait(&full[slot], ph, abort_flag, a.err))) break;
             if (!(ok = mbar_wait(&acc_empty[buf], aph, abort_flag, a.err))) break;
             tc_fence_after();
@@ -415,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
             ready = mbar_test_u32(full0 + 8 * slot, ph);
           }
         }
-        g += nk;
+        g += kb1 - kb0;
         ok = __all_sync(0xffffffffu, ok);
       }
       // all MMAs issued by this warp have finished once `drain` completes
@@ -424,9 +451,10 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
       mbar_wait_warp(drain, 0, nullptr, a.err);
     } else if (warp == 2) {
       // ---------------- unit list ----------------
-      const int total_units = tiles * (kMode == kLinear ? (a.T + BM - 1) / BM : __ldcg(a.n_segs));
+      const int total_units = tiles * (kMode >= kLinear ? (a.T + BM - 1) / BM : __ldcg(a.n_segs));
       uint32_t j = 0;
-      for (int u = blockIdx.x;; u += gridDim.x, ++j) {
+      int u = kMode == kSplit ? static_cast<int>(blockIdx.x) / a.splits : static_cast<int>(blockIdx.x);
+      for (;; u += kMode == kSplit ? total_units : static_cast<int>(gridDim.x), ++j) {
         const bool more = u < total_units;
         const Unit un = more ? decode_unit<kMode>(u, a, tiles) : Unit{0, 0, 0, 0};
         const int slot = j % kRing;
@@ -442,7 +470,6 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
       // ---------------- scales ----------------
       // Lane l copies the scales of rows l + 32 i of the tile; a lane's arrival on a group's barrier
       // comes with its copies.
-      const int ng = (nk + 3) / 4;
       uint32_t c = 0;
       bool ok = true;
       for (uint32_t j = 0; ok; ++j) {
@@ -456,7 +483,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
         }
         ring.done(j);
         const float* sw = a.ws + (static_cast<int64_t>(un.expert) * tiles + un.tile) * f8_scale_ld(nk) * 2 + 4 * (lane & 1);
-        for (int gi = 0; gi < ng; ++gi, ++c) {
+        for (int gi = kb0 / 4; 4 * gi < kb1; ++gi, ++c) {
           const int slot = c % kScGroups;
           if (!(ok = mbar_wait_warp(&sc_empty[slot], ((c / kScGroups) & 1u) ^ 1u, abort_flag, a.err))) break;
           const uint32_t dst = smem_u32(sc_tab + slot * kScGroupBytes);
@@ -489,11 +516,11 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
       if (!on) {  // (a loop of its own: a condition inside the other one costs it 90 register moves a block)
-        for (int kb = 0; kb < nk; ++kb, ++g) {
+        for (int kb = kb0; kb < kb1; ++kb, ++g) {
           ok &= mbar_wait(&acc_full[g & 1u], (g >> 1) & 1u, abort_flag, a.err);
           __syncwarp();
           if (lane == 0) mbar_arrive(&acc_empty[g & 1u]);
-          if ((kb & 3) == 3 || kb == nk - 1) {
+          if ((kb & 3) == 3 || kb == kb1 - 1) {
             if (lane == 0) mbar_arrive(&sc_empty[c % kScGroups]);
             ++c;
           }
@@ -502,18 +529,18 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
         continue;
       }
 #pragma unroll 1
-      for (int kb = 0; kb < nk; ++kb, ++g) {
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
         // (a lane whose wait expired goes on with whatever is there; the warp stops after the unit)
         const uint32_t buf = g & 1u, slot = c % kScGroups;
         const float* grp = reinterpret_cast<const float*>(sc_tab + slot * kScGroupBytes);
-        if ((kb & 3) == 0) ok &= mbar_wait(&sc_full[slot], (c / kScGroups) & 1u, abort_flag, a.err);
+        if ((kb & 3) == 0 || kb == kb0) ok &= mbar_wait(&sc_full[slot], (c / kScGroups) & 1u, abort_flag, a.err);
         const float sa = grp[4 * r + (kb & 3)];
         const float2 w = *reinterpret_cast<const float2*>(grp + 4 * BM + 2 * (kb & 3));
         if (!__all_sync(0xffffffffu, mbar_try_wait(&acc_full[buf], (g >> 1) & 1u))) {
           ok &= mbar_wait(&acc_full[buf], (g >> 1) & 1u, abort_flag, a.err);
           __syncwarp();
         }
-        if ((kb & 3) == 3 || kb == nk - 1) {  // every lane has read the group's last scales
+        if ((kb & 3) == 3 || kb == kb1 - 1) {  // every lane has read the group's last scales
           mbar_arrive_lane0(&sc_empty[slot]);
           ++c;
         }
@@ -563,6 +590,14 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
           }
           if (half == 0) a.hs[grow * a.ldhs + un.tile] = sc;
         }
+      } else if (kMode == kSplit) {
+        if (r < un.rows) {  // (every MMA of this CTA has read its operands: the stages are free)
+          const uint32_t mine = smem_u32(smem) + r * kSumPitch + half * 512;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            st_shared_v4(mine + 16 * c, static_cast<uint32_t>(acc[2 * c]), static_cast<uint32_t>(acc[2 * c] >> 32),
+                         static_cast<uint32_t>(acc[2 * c + 1]), static_cast<uint32_t>(acc[2 * c + 1] >> 32));
+        }
       } else {
         store_rows<kMode>(acc, a, stage_out, un.row_start + 32 * q, un.rows - 32 * q, un.tile * 256 + half * 128, pol_out);
       }
@@ -582,7 +617,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
       const Unit un = ring.get(j);
       if (un.rows == 0) break;
       const int32_t* tok = tok_tab + BM * (j % kRing);
-      for (int kb = 0; kb < nk; ++kb, ++g) {
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
         const int s = g % kStages;
         if (s != slot) continue;
         if (!(ok = mbar_wait_warp(&empty[s], ((g / kStages) & 1u) ^ 1u, abort_flag, a.err))) break;
@@ -600,6 +635,41 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
     }
   }
 
+  if (kMode == kSplit) {
+    // every thread of the cluster meets; then each CTA adds up its share of the columns
+    __syncthreads();
+    cluster_sync();
+    const int u = static_cast<int>(blockIdx.x) / a.splits;
+    const Unit un = decode_unit<kMode>(u, a, tiles);
+    const int cols = min(256, a.N - 256 * un.tile), per = 256 / a.splits;
+    const int c0 = split * per, quads = per / 4;
+    for (int i = threadIdx.x; i < un.rows * quads; i += Cfg<kMode>::kThreads) {
+      const int row = i / quads, c = c0 + 4 * (i % quads);
+      if (c >= cols) continue;
+      const uint32_t at = smem_u32(smem) + row * kSumPitch + 4 * c;
+      float4 v = ld_cluster_v4(at, 0);
+      for (int p = 1; p < a.splits; ++p) {
+        const float4 w = ld_cluster_v4(at, p);
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+      }
+      const int64_t o = (un.row_start + row) * a.ldo + 256 * un.tile + c;
+      const float f[4] = {v.x, v.y, v.z, v.w};
+      if (a.out_type == MOE_BF16) {
+        uint16_t* out = static_cast<uint16_t*>(a.out) + o;
+        if (a.out_vec && c + 4 <= cols)
+          *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+        else
+          for (int k = 0; k < 4 && c + k < cols; ++k) out[k] = f32_to_bf16_bits_rn(f[k]);
+      } else {
+        float* out = static_cast<float*>(a.out) + o;
+        if (a.out_vec && c + 4 <= cols)
+          *reinterpret_cast<float4*>(out) = v;
+        else
+          for (int k = 0; k < 4 && c + k < cols; ++k) out[k] = f[k];
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its sums
+  }
   tc_fence_before();
   __syncthreads();
   abort_quiesce(abort_flag);
@@ -626,8 +696,63 @@ cudaError_t launch_f8_gateup(const F8Args& a, int num_sms, cudaStream_t st) {
 cudaError_t launch_f8_down(const CUtensorMap* amap, const F8Args& a, int num_sms, cudaStream_t st) {
   return launch_f8<f8::kDown>(*amap, a, num_sms, st);
 }
+
+// Clusters of `s` CTAs of the split kernel that the device runs at the same time (0: unknown).
+static int split_clusters(int s) {
+  static std::mutex mu;
+  static std::map<std::pair<int, int>, int> known;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = known.find({dev, s});
+  if (it != known.end()) return it->second;
+  using C = f8::Cfg<f8::kSplit>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(s);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {static_cast<unsigned>(s), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, f8::f8_gemm_kernel<f8::kSplit>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[{dev, s}] = n;
+  return n;
+}
+
+// Units too few to fill the SMs (small T, or a small matrix) are split along K over clusters of 8, 4 or
+// 2 CTAs: as many as run at the same time with a K block or more each.
 cudaError_t launch_f8_linear(const CUtensorMap* amap, const F8Args& a, int num_sms, cudaStream_t st) {
   const int units = (a.halves + 1) / 2 * ((a.T + f8::BM - 1) / f8::BM);
+  if (2 * units <= num_sms && a.nk >= 2) {
+    auto kern = f8::f8_gemm_kernel<f8::kSplit>;
+    using C = f8::Cfg<f8::kSplit>;
+    cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    for (int s = 8; s >= 2; s /= 2) {
+      if (s > a.nk || units * s > num_sms || units > split_clusters(s)) continue;
+      F8Args b = a;
+      b.splits = s;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(units * s);
+      cfg.blockDim = dim3(C::kThreads);
+      cfg.dynamicSmemBytes = C::kSmemBytes;
+      cfg.stream = st;
+      cudaLaunchAttribute attr[2];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim = {static_cast<unsigned>(s), 1, 1};
+      cfg.attrs = attr;
+      cfg.numAttrs = 2;
+      return cudaLaunchKernelEx(&cfg, kern, *amap, b);
+    }
+  }
   return launch_f8<f8::kLinear>(*amap, a, units < num_sms ? units : num_sms, st);
 }
 

@@ -258,6 +258,7 @@ struct F8Args {
   int out_vec = 0;              // rows start, and N ends, on 16-byte boundaries
   int N = 0, halves = 0, nk = 0;
   int T = 0, k = 0;
+  int splits = 1;               // linear: CTAs of a cluster that share a unit's K blocks (set at launch)
   uint32_t* err = nullptr;
 };
 // amap: the activation rows [rows][K] as bytes, box {128, 32}, 128-byte swizzle (not gate/up).

@@ -18,9 +18,8 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const T* __re
                                                                    int64_t ldq, float* __restrict__ s, int64_t lds) {
   pdl_trigger();
   pdl_wait();
-  quant_rows_part(x, ldx, rows, K, nb, vec != 0, q, ldq, s, lds,
-                  static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 16) + (threadIdx.x >> 4),
-                  static_cast<int64_t>(gridDim.x) * (kQuantThreads / 16));
+  quant_rows_part(x, ldx, rows, K, nb, vec != 0, q, ldq, s, lds, blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5),
+                  gridDim.x * (kQuantThreads / 32));
 }
 
 static bool vec_ok(const void* p, int64_t ld, size_t elem) {
@@ -31,8 +30,9 @@ template <typename T>
 static cudaError_t launch_quant_rows_t(const void* x, int64_t ldx, int rows, int K, uint8_t* q, int64_t ldq, float* s,
                                        int64_t lds, int num_sms, cudaStream_t st) {
   const int nb = (K + kF8Block - 1) / kF8Block;
-  const int64_t blocks = (static_cast<int64_t>(rows) * nb + kQuantThreads / 16 - 1) / (kQuantThreads / 16);
-  const int64_t most = static_cast<int64_t>(num_sms) * 8;  // 8 resident blocks of 256 threads fill an SM
+  const int64_t warps = static_cast<int64_t>(rows) * ((nb + 7) / 8);
+  const int64_t blocks = (warps + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
+  const int64_t most = static_cast<int64_t>(num_sms) * 6;  // resident blocks of 256 threads, twice the loads an SM needs
   return launch_pdl(quant_rows_kernel<T>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
                     dim3(kQuantThreads), 0, st, static_cast<const T*>(x), ldx, rows, K, nb,
                     vec_ok(x, ldx, sizeof(T)) ? 1 : 0, q, ldq, s, lds);

@@ -403,12 +403,10 @@ __global__ void __launch_bounds__(256) masks_from_ids_kernel(const int32_t* __re
   for (int e = threadIdx.x; e < E; e += blockDim.x) masks[static_cast<size_t>(e) * mstride + c] = smask[e];
 }
 
-// Blocks of 256 threads that make xc's 8-bit blocks beside other work: two blocks of 128 elements a
-// thread group while the grid fills the GPU a few times over.
+// Blocks of 256 threads that make xc's 8-bit blocks beside other work: a warp per eight blocks of a row.
 static int side_blocks(const XConv& xc) {
   if (!xc.xq) return 0;
-  const int64_t n = static_cast<int64_t>(xc.rows) * ((xc.K + 127) / 128);
-  const int64_t blocks = (n + 31) / 32;
+  const int64_t blocks = (static_cast<int64_t>(xc.rows) * ((xc.K + 1023) / 1024) + 7) / 8;
   return static_cast<int>(blocks < 1024 ? blocks : 1024);
 }
 
