@@ -701,6 +701,9 @@ extern "C" moe_status moe_plan_set_routing(moe_plan* p, const moe_routing* r) {
   a.renorm = r->renormalize != 0;
   a.scale = r->scale;
   a.bias = r->bias ? p->b_score : nullptr;
+  while (2 * a.lanes * G <= 32) a.lanes *= 2;
+  const uint32_t per = p->E / G;
+  a.per_magic = ((1u << 20) + per - 1) / per;
   p->score = a;
   return MOE_OK;
 }

@@ -59,6 +59,10 @@ struct ScoreArgs {
   int renorm = 1;
   float scale = 1.0f;
   const float* bias = nullptr;    // [E] or NULL
+  // lanes that share a group's members (a power of two, groups * lanes <= 32); ceil(2^20 / group size),
+  // which divides an expert index exactly (index and size below 1024)
+  int lanes = 1;
+  uint32_t per_magic = 0;
 };
 
 // ---- routing and grouping (route.cu) --------------------------------------------------------

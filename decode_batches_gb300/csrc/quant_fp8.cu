@@ -13,7 +13,7 @@ namespace moe {
 constexpr int kQuantThreads = 256;
 
 template <typename T>
-__global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int rows, int K,
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 4 : 2) quant_rows_kernel(const T* __restrict__ x, int64_t ldx, int rows, int K,
                                                                    int nb, int vec, uint8_t* __restrict__ q,
                                                                    int64_t ldq, float* __restrict__ s, int64_t lds) {
   pdl_trigger();
@@ -32,7 +32,7 @@ static cudaError_t launch_quant_rows_t(const void* x, int64_t ldx, int rows, int
   const int nb = (K + kF8Block - 1) / kF8Block;
   const int64_t warps = static_cast<int64_t>(rows) * ((nb + 7) / 8);
   const int64_t blocks = (warps + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
-  const int64_t most = static_cast<int64_t>(num_sms) * 6;  // resident blocks of 256 threads, twice the loads an SM needs
+  const int64_t most = static_cast<int64_t>(num_sms) * 4;  // the resident blocks
   return launch_pdl(quant_rows_kernel<T>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
                     dim3(kQuantThreads), 0, st, static_cast<const T*>(x), ldx, rows, K, nb,
                     vec_ok(x, ldx, sizeof(T)) ? 1 : 0, q, ldq, s, lds);
@@ -47,6 +47,10 @@ cudaError_t launch_quant_rows(const void* x, moe_dtype dt, int64_t ldx, int rows
 }
 
 // ---- weights: 128 x 128 blocks ---------------------------------------------------------------
+MOE_DEVICE float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+MOE_DEVICE float to_f32(__half v) { return __half2float(v); }
+MOE_DEVICE float to_f32(float v) { return v; }
+
 template <typename T>
 __global__ void __launch_bounds__(256) quant_blocks_kernel(const T* __restrict__ w, int64_t ldw, int rows, int K,
                                                            uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s,
@@ -58,7 +62,7 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const T* __restrict__
 #pragma unroll
   for (int i = 0; i < 64; ++i) {
     const int r = r0 + 2 * i;
-    v[i] = (r < rows && k < K) ? Load8<T>::one(w + r * ldw + k) : 0.f;
+    v[i] = (r < rows && k < K) ? to_f32(w[r * ldw + k]) : 0.f;
     amax = fmaxf(amax, fabsf(v[i]));
   }
 #pragma unroll

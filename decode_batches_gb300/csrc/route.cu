@@ -268,7 +268,7 @@ constexpr int kTopkThreads = 32 * kTopkTokens;
 template <int PL, bool kScored>
 MOE_DEVICE int topk_token(const float* __restrict__ parts, int nsplit, const float* __restrict__ bias,
                           float* __restrict__ logits_out, int t, int T, int E, int k, int32_t* __restrict__ ids,
-                          float* __restrict__ gates, uint32_t* err, const ScoreArgs& sa) {
+                          float* __restrict__ gates, uint32_t* err, const ScoreArgs& sa, uint32_t* scr) {
   const int lane = threadIdx.x & 31;
   // U partial matrices in flight at a time (one L2 round trip per U splits), added in order
   constexpr int U = PL <= 8 ? 4 : (PL <= 16 ? 2 : 1);
@@ -300,7 +300,7 @@ MOE_DEVICE int topk_token(const float* __restrict__ parts, int nsplit, const flo
       if (logits_out) logits_out[static_cast<size_t>(t) * E + e] = v[i];
     }
   }
-  return select_token<PL, kScored>(v, t, E, k, ids, gates, err, sa);
+  return select_token<PL, kScored>(v, t, E, k, ids, gates, err, sa, scr);
 }
 
 template <int PL, bool kScored>
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const float* __restr
                                                             float* __restrict__ gates,
                                                             uint32_t* __restrict__ masks, uint32_t* err,
                                                             const XConv xc, const ScoreArgs sa) {
-  extern __shared__ uint32_t smask[];  // [E]: bits of this block's 16 tokens
+  extern __shared__ uint32_t smask[];  // [E]: bits of this block's 16 tokens; scored: [E] for each warp
   pdl_trigger();
   pdl_wait();
   convert_x(xc, err);
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const float* __restr
   __syncthreads();
   const int t = c * kChunk + kTopkTokens * half + warp;
   if (t < T) {
-    const int sel = topk_token<PL, kScored>(parts, nsplit, bias, logits_out, t, T, E, k, ids, gates, err, sa);
+    const int sel = topk_token<PL, kScored>(parts, nsplit, bias, logits_out, t, T, E, k, ids, gates, err, sa, smask + (masks ? E : 0) + warp * E);
     if (masks && lane < k) atomicOr(&smask[sel], 1u << warp);
   }
   if (masks) {
@@ -339,7 +339,13 @@ template <int PL>
 static cudaError_t launch_topk_pl(const float* parts, int nsplit, const float* bias, float* logits_out, int T, int E,
                                   int k, int n_chunks, int32_t* ids, float* gates, uint32_t* masks, uint32_t* err,
                                   const XConv& xc, const ScoreArgs& sa, cudaStream_t st) {
-  return launch_pdl(sa.on ? topk_kernel<PL, true> : topk_kernel<PL, false>, dim3(2 * n_chunks), dim3(kTopkThreads), masks ? E * sizeof(uint32_t) : 0, st,
+  auto kern = sa.on ? topk_kernel<PL, true> : topk_kernel<PL, false>;
+  const size_t smem = ((masks ? E : 0) + (sa.on ? kTopkTokens * static_cast<size_t>(E) : 0)) * sizeof(uint32_t);
+  if (smem > 48 * 1024) {
+    cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), 17 * 1024 * sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3(2 * n_chunks), dim3(kTopkThreads), smem, st,
                     parts, nsplit, bias, logits_out, T, E, k, n_chunks, ids, gates, masks, err, xc, sa);
 }
 
@@ -645,9 +651,14 @@ constexpr int kSmallSplitsMax = 16;
 constexpr int kRgThreads = 256;
 constexpr int kRgPer = 4;  // experts per thread (E <= 1024)
 
-size_t route_small_smem(int T, int E, int k) {
+// Words of shared memory that the grouping of a small step takes.
+__host__ __device__ inline int route_small_words(int T, int E, int k) {
   const int nch = (T + kChunk - 1) / kChunk;
-  const size_t grouping = (2 * static_cast<size_t>(nch) * E + static_cast<size_t>(T) * k + E + 1) * 4;
+  return 2 * nch * E + T * k + E + 1;
+}
+
+size_t route_small_smem(int T, int E, int k) {
+  const size_t grouping = static_cast<size_t>(route_small_words(T, E, k)) * 4;
   const size_t logits = static_cast<size_t>(E) * 4;
   return grouping > logits ? grouping : logits;
 }
@@ -894,7 +905,7 @@ __global__ void __launch_bounds__(kRgThreads) route_group_kernel(
         const int e = lane + 32 * i;
         v[i] = e < E ? slog[e] : 0.f;
       }
-      select_token<PL, kScored>(v, t, E, k, ids, gates, err, sa);
+      select_token<PL, kScored>(v, t, E, k, ids, gates, err, sa, sm + E);  // (sm holds 2 E words or more)
     }
   }
   // publish this token's ids, then count finished blocks
@@ -1002,7 +1013,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) router_route_tiny_kernel(
     if (bias)
 #pragma unroll
       for (int i = 0; i < PL; ++i) v[i] += bv[i];
-    const int sel = select_token<PL, kScored>(v, t, E, k, ids, gates, err, sa);
+    const int sel = select_token<PL, kScored>(v, t, E, k, ids, gates, err, sa,
+                                              sm + route_small_words(T, E, k) + (kScored ? warp * E : 0));
     if (lane < k) sids[t * k + lane] = sel;
   }
   __syncthreads();
@@ -1024,7 +1036,8 @@ static cudaError_t launch_rrt_pl(const uint16_t* x, const float* wr, const float
                                  int32_t* perm, int32_t* inv, Seg* segs, int32_t* n_segs, int max_segs, uint32_t* done,
                                  uint32_t* err, const XConv& xc, const ScoreArgs& sa, cudaStream_t st) {
   const size_t xs_bytes = 8 * kRouterKS * 2;
-  const size_t g_bytes = route_small_smem(T, E, k);
+  // (scored: a warp's scratch each beyond the grouping's words; E <= 1024 and T <= 8 keep it below 48 KB)
+  const size_t g_bytes = route_small_smem(T, E, k) + (sa.on ? static_cast<size_t>(T) * E * 4 : 0);
   dim3 grid((E + 7) / 8, router_small_splits(d));
   return launch_pdl(sa.on ? router_route_tiny_kernel<PL, true> : router_route_tiny_kernel<PL, false>, grid, dim3(kRgThreads), xs_bytes > g_bytes ? xs_bytes : g_bytes, st,
                     x, wr, bias, T, E, d, parts, k, ids, gates, counts, offsets, perm, inv, segs, n_segs, max_segs,
