@@ -275,7 +275,13 @@ MOE_DEVICE int topk_token(const float* __restrict__ parts, int nsplit, const flo
   float v[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) v[i] = 0.f;
-  for (int sp = 0; sp < nsplit; sp += U) {
+  if (nsplit == 1) {  // one matrix: a load an expert, no sums
+    const float* row = parts + static_cast<size_t>(t) * E + lane;
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+      if (lane + 32 * i < E) v[i] = row[32 * i];
+  }
+  for (int sp = nsplit == 1 ? 1 : 0; sp < nsplit; sp += U) {
     float w[U][PL];
 #pragma unroll
     for (int u = 0; u < U; ++u) {

@@ -33,7 +33,7 @@ MOE_DEVICE int score_select(const float (&v)[PL], int t, int E, int k, int32_t* 
   constexpr float kInf = __builtin_huge_valf();
   // scores
   float s[PL];
-  bool odd = false;  // a logit that is NaN or +inf
+  bool odd = false;  // some logit of the token is NaN or +inf
   if (sa.sigmoid) {
 #pragma unroll
     for (int i = 0; i < PL; ++i) s[i] = rcp_approx(1.0f + expf(-v[i]));
@@ -61,12 +61,20 @@ MOE_DEVICE int score_select(const float (&v)[PL], int t, int E, int k, int32_t* 
   const uint32_t none = rank_key(-kInf);
   uint32_t key[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = 1u;
-    if (e < E) {
-      key[i] = v[i] == -kInf ? none : rank_key(sa.bias ? s[i] + sa.bias[e] : s[i]);
-      odd |= !(v[i] < kInf);
+  for (int i = 0; i < PL; ++i) odd |= lane + 32 * i < E && !(v[i] < kInf);
+  odd = __any_sync(0xffffffffu, odd);
+  if (!odd && !sa.bias) {  // scores are numbers >= 0: their bits are in order
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const uint32_t kk = v[i] == -kInf ? none : (__float_as_uint(s[i]) | 0x80000000u);
+      key[i] = lane + 32 * i < E ? kk : 1u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const int e = lane + 32 * i;
+      key[i] = 1u;
+      if (e < E) key[i] = v[i] == -kInf ? none : rank_key(sa.bias ? s[i] + sa.bias[e] : s[i]);
     }
   }
   if (sa.groups > 1) {
@@ -79,12 +87,14 @@ MOE_DEVICE int score_select(const float (&v)[PL], int t, int E, int k, int32_t* 
     uint32_t b1 = 0u, b2 = 0u;  // the lane's two best keys of the group
     if (g < sa.groups) {
       const int n = (per - sub + sa.lanes - 1) / sa.lanes;  // members sub, sub + lanes, ...
-      int it = n > 0 ? g % n : 0;
-      for (int c = 0; c < n; ++c) {
-        const uint32_t kk = scr[g * per + sub + it * sa.lanes];
+      int at = min(g, n - 1) * sa.lanes;
+#pragma unroll 4
+      for (int c = 0; c < n; ++c) {  // (n == 0: a group smaller than its lanes)
+        const uint32_t kk = scr[g * per + sub + at];
         b2 = max(b2, min(b1, kk));
         b1 = max(b1, kk);
-        if (++it == n) it = 0;
+        at += sa.lanes;
+        at = at < n * sa.lanes ? at : 0;
       }
     }
     for (int o = 1; o < sa.lanes; o <<= 1) {
@@ -157,7 +167,7 @@ MOE_DEVICE int score_select(const float (&v)[PL], int t, int E, int k, int32_t* 
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     w = __fdiv_rn(w, sum + 1e-20f);
   }
-  if (__any_sync(0xffffffffu, odd)) {  // flagged if one of them was chosen
+  if (odd) {  // flagged if one of them was chosen
     float l = 0.f;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
