@@ -177,12 +177,24 @@ MOE_DEVICE void cp_async_arrive(uint64_t* bar) {
 
 // Lane 0 of a converged warp arrives, predicated inside the block: a branch around the arrival costs
 // the epilogue's K loop about a tenth of its time.
-MOE_DEVICE void mbar_arrive_lane0(uint64_t* bar) {
+MOE_DEVICE void mbar_arrive_lane0_u32(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
       "r"(threadIdx.x & 31)
       : "memory");
+}
+MOE_DEVICE void mbar_arrive_lane0(uint64_t* bar) { mbar_arrive_lane0_u32(smem_u32(bar)); }
+MOE_DEVICE bool mbar_try_wait_u32(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Two fp16 values, `lo` in the low half, rounded to nearest even; magnitudes beyond fp16 become its

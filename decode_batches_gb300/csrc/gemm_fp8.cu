@@ -54,6 +54,7 @@ constexpr int kAccCols = 256;
 constexpr int kTmemCols = 2 * kAccCols;
 constexpr int kEpiWarps = 8, kFirstEpi = 4, kFirstGather = 12;
 constexpr int kRing = 4;                          // decoded units
+constexpr uint32_t kSpinLimit = 1u << 20;         // tries of an epilogue wait: 1.4 s at 1.3 us a try
 constexpr int kScGroups = 4;                      // groups of four K blocks of scales
 constexpr int kScGroupBytes = BM * 16 + 32;       // a row's four scales; the tile's four pairs
 constexpr int kScaleBytes = kScGroups * kScGroupBytes;
@@ -137,7 +138,7 @@ struct Ring {
 // Adds 128 columns of one K block, times the scales (s01 the first 64 columns', s23 the rest's), to
 // the thread's sums: 32-column loads, one in flight while the previous one is added.
 // The buffer is handed back once the last load is in registers.
-MOE_DEVICE void add_block(uint64_t (&acc)[64], uint32_t taddr, uint64_t s01, uint64_t s23, uint64_t* empty) {
+MOE_DEVICE void add_block(uint64_t (&acc)[64], uint32_t taddr, uint64_t s01, uint64_t s23, uint32_t empty) {
   uint32_t r[2][16];
   tmem_ld_32x32b_x16(taddr, r[0]);
 #pragma unroll
@@ -148,7 +149,7 @@ MOE_DEVICE void add_block(uint64_t (&acc)[64], uint32_t taddr, uint64_t s01, uin
     } else {
       tc_fence_before();
       __syncwarp();
-      mbar_arrive_lane0(empty);
+      mbar_arrive_lane0_u32(empty);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -176,6 +177,16 @@ MOE_DEVICE float4 ld_cluster_v4(uint32_t addr, uint32_t rank) {
       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
       : "r"(addr), "r"(rank)
       : "memory");
+  return v;
+}
+MOE_DEVICE float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+MOE_DEVICE float2 ld_shared_v2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 MOE_DEVICE uint4 ld_shared_v4(uint32_t addr) {
@@ -507,6 +518,17 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
     const uint64_t pol_out = kMode == kDown ? l2_policy_evict_last() : l2_policy_evict_first();
     uint32_t g = 0, c = 0, nx = 0;  // K blocks, groups of scales, exchanges of row maxima so far
     bool ok = true;
+    const uint32_t accf0 = smem_u32(acc_full), acce0 = smem_u32(acc_empty);
+    const uint32_t tacc = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * 128;
+    uint32_t limit = kSpinLimit;
+    auto spin = [&](uint32_t bar, uint32_t parity) {
+      uint32_t n = 0;
+      while (!__all_sync(0xffffffffu, mbar_try_wait_u32(bar, parity)))
+        if (++n >= limit) {
+          limit = 0;
+          break;
+        }
+    };
     for (uint32_t j = 0; ok; ++j) {
       const Unit un = ring.get(j);
       if (un.rows == 0) break;
@@ -515,42 +537,47 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      if (!on) {  // (a loop of its own: a condition inside the other one costs it 90 register moves a block)
-        for (int kb = kb0; kb < kb1; ++kb, ++g) {
-          ok &= mbar_wait(&acc_full[g & 1u], (g >> 1) & 1u, abort_flag, a.err);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[g & 1u]);
-          if ((kb & 3) == 3 || kb == kb1 - 1) {
-            if (lane == 0) mbar_arrive(&sc_empty[c % kScGroups]);
-            ++c;
-          }
+      // The loop over K blocks is kept short, its waits included: its time follows its length in
+      // instructions (unrolled by two, the 8192-row product took 228 us instead of 133).  A wait is a
+      // bounded spin of the whole warp; one that gives up leaves limit 0, and the warp goes on without
+      // waiting to the end of the unit, where it reports.
+      int kb = kb0;
+      if (!on) {
+        for (; kb < kb1; ++kb, ++g) {
+          spin(accf0 + 8 * (g & 1u), (g >> 1) & 1u);
+          mbar_arrive_lane0(&acc_empty[g & 1u]);
+          if ((kb & 3) == 3 || kb == kb1 - 1) mbar_arrive_lane0(&sc_empty[c++ % kScGroups]);
         }
-        ok = __all_sync(0xffffffffu, ok);
-        continue;
       }
+      uint32_t buf = g & 1u, ph = (g >> 1) & 1u;
 #pragma unroll 1
-      for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        // (a lane whose wait expired goes on with whatever is there; the warp stops after the unit)
-        const uint32_t buf = g & 1u, slot = c % kScGroups;
-        const float* grp = reinterpret_cast<const float*>(sc_tab + slot * kScGroupBytes);
-        if ((kb & 3) == 0 || kb == kb0) ok &= mbar_wait(&sc_full[slot], (c / kScGroups) & 1u, abort_flag, a.err);
-        const float sa = grp[4 * r + (kb & 3)];
-        const float2 w = *reinterpret_cast<const float2*>(grp + 4 * BM + 2 * (kb & 3));
-        if (!__all_sync(0xffffffffu, mbar_try_wait(&acc_full[buf], (g >> 1) & 1u))) {
-          ok &= mbar_wait(&acc_full[buf], (g >> 1) & 1u, abort_flag, a.err);
-          __syncwarp();
+      while (kb < kb1) {  // a group of scales
+        const uint32_t slot = c % kScGroups;
+        spin(smem_u32(&sc_full[slot]), (c / kScGroups) & 1u);
+        const uint32_t grp = smem_u32(sc_tab + slot * kScGroupBytes);
+        uint32_t pa = grp + 16 * r + 4 * (kb & 3), pw = grp + 16 * BM + 8 * (kb & 3);
+        const int end = min((kb | 3) + 1, kb1);
+        g += end - kb;
+#pragma unroll 1
+        for (; kb < end; ++kb, pa += 4, pw += 8) {
+          const float sa = ld_shared_f32(pa);
+          const float2 w = ld_shared_v2(pw);
+          spin(accf0 + 8 * buf, ph);
+          tc_fence_after();
+          const float s0 = sa * (kMode == kGateUp || half == 0 ? w.x : w.y);
+          const float s1 = kMode == kGateUp ? sa * w.y : s0;
+          add_block(acc, tacc + buf * kAccCols, pack_f32x2(s0, s0), pack_f32x2(s1, s1), acce0 + 8 * buf);
+          ph ^= buf;  // both buffers used: their next phase
+          buf ^= 1u;
         }
-        if ((kb & 3) == 3 || kb == kb1 - 1) {  // every lane has read the group's last scales
-          mbar_arrive_lane0(&sc_empty[slot]);
-          ++c;
-        }
-        tc_fence_after();
-        const float s0 = sa * (kMode == kGateUp || half == 0 ? w.x : w.y);
-        const float s1 = kMode == kGateUp ? sa * w.y : s0;
-        add_block(acc, tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * kAccCols + half * 128, pack_f32x2(s0, s0),
-                  pack_f32x2(s1, s1), &acc_empty[buf]);
+        mbar_arrive_lane0(&sc_empty[slot]);  // (every lane has read the group's scales)
+        ++c;
       }
-      ok = __all_sync(0xffffffffu, ok);
+      if (limit == 0) {
+        set_error(a.err, MOE_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+        ok = false;
+      }
       if (!ok) break;
       const int64_t grow = un.row_start + r;
       if (kMode == kGateUp) {
