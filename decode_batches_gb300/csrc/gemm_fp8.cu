@@ -116,6 +116,18 @@ MOE_DEVICE Unit decode_unit(int u, const F8Args& a, int tiles) {
   return un;
 }
 
+// The unit of a CTA's step when half of the CTAs go through the list from its front and half from its
+// back, in turns (total: none is left).  Experts with many rows keep the epilogue busy (their parts share
+// weights through L2), experts with few rows the memory; where popularity follows the expert index,
+// front to back would run one kind after the other (Zipf layer, T = 2051: SKEWUS).  Neighbouring
+// units still run side by side.  An odd grid goes front to back.
+MOE_DEVICE int mixed_unit(int step, int total) {
+  if (gridDim.x & 1) return min(static_cast<int>(blockIdx.x + step * gridDim.x), total);
+  const int o = step * static_cast<int>(gridDim.x / 2) + static_cast<int>(blockIdx.x / 2);
+  if (((step ^ static_cast<int>(blockIdx.x)) & 1) == 0) return o < (total + 1) / 2 ? o : total;
+  return o < total / 2 ? total - 1 - o : total;
+}
+
 // The ring of decoded units: record j is read by every role's warps.
 struct Ring {
   uint64_t *full, *empty;
@@ -464,8 +476,14 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
       // ---------------- unit list ----------------
       const int total_units = tiles * (kMode >= kLinear ? (a.T + BM - 1) / BM : __ldcg(a.n_segs));
       uint32_t j = 0;
-      int u = kMode == kSplit ? static_cast<int>(blockIdx.x) / a.splits : static_cast<int>(blockIdx.x);
-      for (;; u += kMode == kSplit ? total_units : static_cast<int>(gridDim.x), ++j) {
+      for (int step = 0;; ++step, ++j) {
+        int u;
+        if (kMode == kSplit)
+          u = step == 0 ? static_cast<int>(blockIdx.x) / a.splits : total_units;
+        else if (kMode == kLinear)
+          u = blockIdx.x + step * gridDim.x;
+        else
+          u = mixed_unit(step, total_units);
         const bool more = u < total_units;
         const Unit un = more ? decode_unit<kMode>(u, a, tiles) : Unit{0, 0, 0, 0};
         const int slot = j % kRing;
