@@ -9,7 +9,7 @@
 // loop.  The rows of `a` are the MMA's M (TMEM lanes), the weight rows its N: a thread owns one row
 // of `a`, so a block has one scale for all of the thread's columns that share a weight block.
 //
-// Three uses of one kernel:
+// Uses of one kernel:
 //   gate/up  a = rows of x gathered by the permutation; a tile's 256 weight rows are two times (64
 //            gate rows, the same 64 features' up rows); the epilogue forms silu(g) * u in fp32,
 //            quantises the 128 features (one activation block of h) and writes codes and scale.
@@ -20,6 +20,11 @@
 //            1/S of the columns.
 // Routed units are ordered tile-major within an expert's parts, linear units tile-major over the
 // row parts: CTAs that share a weight tile run side by side and its second read is served by L2.
+//
+// What bounds them, measured on a GB300 (6.78 TB/s copy, 1.94 PFLOP/s bf16): up to about 100 rows an expert
+// the weight stream (256 experts, d 2048, f 512, 2051 tokens x 8: gate/up 90 us at 6.1 TB/s, down 55 us at
+// 5.2 TB/s); 8192 x 4096 x 4096 113 us, 2.4 PFLOP/s, the epilogue: about 830 cycles a block (256 of them
+// the FMA pipe's, 64 packed FMAs a thread at two cycles) against 512 of MMA; few rows, latency.
 //
 // Roles (persistent CTAs, one per SM, every role walks the same unit sequence):
 //   warp 0      producer: weights by bulk copy (tile-contiguous, pre-swizzled); rows by TMA
@@ -119,7 +124,8 @@ MOE_DEVICE Unit decode_unit(int u, const F8Args& a, int tiles) {
 // The unit of a CTA's step when half of the CTAs go through the list from its front and half from its
 // back, in turns (total: none is left).  Experts with many rows keep the epilogue busy (their parts share
 // weights through L2), experts with few rows the memory; where popularity follows the expert index,
-// front to back would run one kind after the other (Zipf layer, T = 2051: SKEWUS).  Neighbouring
+// front to back would run one kind after the other (Zipf layer, T = 2051: 488 us, and
+// 462 from both ends).  Neighbouring
 // units still run side by side.  An odd grid goes front to back.
 MOE_DEVICE int mixed_unit(int step, int total) {
   if (gridDim.x & 1) return min(static_cast<int>(blockIdx.x + step * gridDim.x), total);
@@ -221,9 +227,10 @@ MOE_DEVICE void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, 
 }
 
 // Writes the warp's first `rows` staged rows, `cols` elements each, to out at (row0, col).  16 lanes take a
-// row's 256 bytes where rows and columns allow 16-byte stores, else 32 lanes one element each.  (Measured
-// on the mixed step's down projection, us: 32 bytes a lane to 32 rows each straight from the
-// registers 83; a bulk copy of each row 92; this 66.)
+// row's 256 bytes where rows and columns allow 16-byte stores, else 32 lanes one element each.  (An odd
+// N, 517 x 1337: 35 us with each lane storing its own row's elements, 13 so.  With aligned rows it is as
+// fast as 32 bytes a lane to 32 rows straight from the registers; a bulk copy of each row, or TMA stores of 32
+// rows, gained nothing.)
 template <typename E>
 MOE_DEVICE void send_rows(const F8Args& a, uint32_t stage, int64_t row0, int rows, int64_t col, int cols, uint64_t pol) {
   const int lane = threadIdx.x & 31;
