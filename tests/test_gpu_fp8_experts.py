@@ -246,3 +246,19 @@ def test_refusals():
     z = torch.zeros
     with pytest.raises(MoeError):                 # shared experts that the 16-bit kernels cannot tile
         p3.set_shared(64, *(z(s, dtype=torch.bfloat16, device="cuda") for s in ((1, 64, 200), (1, 64, 200), (1, 200, 64))))
+
+
+@pytest.mark.parametrize("T", [5, 90])
+def test_forward_routed_on_the_cuda_core_path(T):
+    """A shape without tensor-core tiles (bf16, d not a multiple of 128): the same call on the CUDA cores."""
+    from decode_batches_gb300 import MoePlan
+    E, k, d, f = 6, 2, 72, 40
+    g = torch.Generator().manual_seed(0)
+    bf = lambda *s: (torch.randn(s, generator=g) * s[-1] ** -0.5).to(torch.bfloat16).cuda()
+    plan = MoePlan(E, k, d, f, 0, "bf16")
+    plan.set_weights(torch.randn((E, d), generator=g).cuda(), None, bf(E, f, d), bf(E, f, d), bf(E, d, f))
+    plan.allocate_workspace(T)
+    assert plan.resolved_path()[0] == "simt"
+    x = random_rows(T, d, 3).cuda()
+    _, ids, gates = plan.route(x)
+    assert torch.equal(plan.forward(x), plan.forward_routed(x, ids, gates))
