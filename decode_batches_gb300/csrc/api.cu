@@ -101,7 +101,7 @@ struct moe_plan {
   bool fp4_mx = false, fp4_mx_down = false;
   float* ws_gu = nullptr;    // 8-bit weights: block scales of the tiled w_gu and w_down
   float* ws_down = nullptr;
-  CUtensorMap map_h8{};      // ... and h's codes as the down GEMM's operand
+  CUtensorMap map_h8{}, map_h8_128{};  // ... and h's codes as the down GEMM's operand, by 32 and by 128 rows
   // steps of at most 8 tokens with bf16 weights: the one-launch layer (layer_small.cu) instead of
   // the routing launch + tensor-core GEMMs + combine; env MOE_SMALL_STEP = fused | multi
   bool small_fused = false;
@@ -287,12 +287,12 @@ static moe_status make_map_16(CUtensorMap* m, const void* base, uint64_t inner, 
   return MOE_OK;
 }
 
-moe_status moe::make_map_f8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld) {
+moe_status moe::make_map_f8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
   cuuint64_t dims[2] = {inner, rows};
   cuuint64_t strides[1] = {ld};
-  cuuint32_t box[2] = {128, 32};
+  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -316,7 +316,8 @@ static moe_status build_ws_maps(moe_plan* p) {
   const CUtensorMapDataType F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   if (p->wdtype == MOE_W_FP8) {
     const uint64_t ldh = static_cast<uint64_t>(p->nk_h()) * 128;
-    if ((s = make_map_f8(&p->map_h8, p->ws + p->L.h8, ldh, R, ldh)) != MOE_OK) return s;
+    if ((s = make_map_f8(&p->map_h8, p->ws + p->L.h8, ldh, R, ldh, 32)) != MOE_OK) return s;
+    if ((s = make_map_f8(&p->map_h8_128, p->ws + p->L.h8, ldh, R, ldh, 128)) != MOE_OK) return s;
   } else if ((s = make_map_16(&p->maps.h, p->ws + p->L.h, p->f, R, 32, F16)) != MOE_OK) {
     return s;
   }
@@ -913,7 +914,7 @@ static moe_status run_experts(moe_plan* p, const uint16_t* x, int T, const int32
         LAUNCH(p, "tc_gateup_shared", st, launch_tc_gateup(&p->maps, sh, p->num_sms, st));
       }
       const F8Args dn = f8_down_args(p, gu, y);
-      LAUNCH(p, "f8_down", st, launch_f8_down(&p->map_h8, dn, p->num_sms, st));
+      LAUNCH(p, "f8_down", st, launch_f8_down(&p->map_h8, &p->map_h8_128, dn, p->num_sms, st));
       if (p->n_shared > 0 && !(shared_forked && kSharedDownBeside)) {
         if (shared_forked) MOE_CUDA_TRY(cudaStreamWaitEvent(st, p->ev_join, 0));
         const TcArgs sh = shared_args(p, a, T, false);

@@ -52,6 +52,7 @@ namespace f8 {
 
 constexpr int kGateUp = 0, kDown = 1, kLinear = 2, kSplit = 3;
 constexpr int BM = 128;                           // activation rows per tile (MMA M)
+constexpr int kStages = 4;                        // (three: the 8192-row product waits for its loads, 133 us)
 constexpr int kBBytes = 2 * kF8TileBytes;         // 256 weight rows x 128 K elements
 constexpr int kABytes = BM * kF8Block;
 constexpr int kStageBytes = kABytes + kBBytes;    // 48 KB
@@ -65,15 +66,13 @@ constexpr int kScGroupBytes = BM * 16 + 32;       // a row's four scales; the ti
 constexpr int kScaleBytes = kScGroups * kScGroupBytes;
 constexpr int kTokBytes = kRing * BM * 4;         // gate/up, per unit: source row of each row
 constexpr int kXchBytes = 2 * 2 * BM * 4;         // gate/up, row maxima of h: [unit parity][half][row]
-constexpr int kOutPitch = 256 + 16;               // a staged row of results: 256 bytes, odd in 16-byte units
+constexpr int kOutPitch = 64 + 16;                // a staged row of results: 64 bytes, odd in 16-byte units
 constexpr int kOutBytes = 32 * kOutPitch;         // per epilogue warp
 constexpr int kSumPitch = 256 * 4 + 16;           // split: a row of fp32 sums (in the stages' space)
 static_assert(BM * kSumPitch <= 3 * kStageBytes, "sums in the stages");
 
 template <int kMode>
 struct Cfg {
-  // gate/up keeps four stages in flight; the others trade one for the staged results
-  static constexpr int kStages = kMode == kGateUp ? 4 : 3;
   static constexpr int kExtra = kMode == kGateUp ? kTokBytes + kXchBytes : kEpiWarps * kOutBytes;
   static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /*barriers*/ + 1024 /*align slack*/ + kScaleBytes + kExtra;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
@@ -226,8 +225,8 @@ MOE_DEVICE void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, 
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// Writes the warp's first `rows` staged rows, `cols` elements each, to out at (row0, col).  16 lanes take a
-// row's 256 bytes where rows and columns allow 16-byte stores, else 32 lanes one element each.  (An odd
+// Writes the warp's first `rows` staged rows, `cols` elements each, to out at (row0, col).  4 lanes take a
+// row's 64 bytes where rows and columns allow 16-byte stores, else 32 lanes one element each.  (An odd
 // N, 517 x 1337: 35 us with each lane storing its own row's elements, 13 so.  With aligned rows it is as
 // fast as 32 bytes a lane to 32 rows straight from the registers; a bulk copy of each row, or TMA stores of 32
 // rows, gained nothing.)
@@ -236,13 +235,13 @@ MOE_DEVICE void send_rows(const F8Args& a, uint32_t stage, int64_t row0, int row
   const int lane = threadIdx.x & 31;
   __syncwarp();
   if (a.out_vec) {
-    const int c = (lane & 15) * (16 / static_cast<int>(sizeof(E)));
+    const int c = (lane & 3) * (16 / static_cast<int>(sizeof(E)));
     if (c < cols) {
-      E* o = static_cast<E*>(a.out) + (row0 + (lane >> 4)) * a.ldo + col + c;
-      const uint32_t src = stage + (lane >> 4) * kOutPitch + (lane & 15) * 16;
-#pragma unroll 4
-      for (int i = 0; i < rows; i += 2)
-        if (i + (lane >> 4) < rows) st_global_v4_hint(o + static_cast<int64_t>(i) * a.ldo, ld_shared_v4(src + i * kOutPitch), pol);
+      E* o = static_cast<E*>(a.out) + (row0 + (lane >> 2)) * a.ldo + col + c;
+      const uint32_t src = stage + (lane >> 2) * kOutPitch + (lane & 3) * 16;
+#pragma unroll
+      for (int i = 0; i < 32; i += 8)
+        if (i + (lane >> 2) < rows) st_global_v4_hint(o + static_cast<int64_t>(i) * a.ldo, ld_shared_v4(src + i * kOutPitch), pol);
     }
   } else {
     for (int i = 0; i < rows; ++i) {
@@ -266,55 +265,47 @@ MOE_DEVICE void store_rows(const uint64_t (&acc)[64], const F8Args& a, uint32_t 
   const int n = min(128, a.N - col0);  // valid columns here
   const uint32_t mine = stage + (threadIdx.x & 31) * kOutPitch;
   rows = min(rows, 32);
-  if (kMode == kDown) {
-    // one straight run of few instructions: executed once a unit, it pays for its length in fetches
+  if (kMode == kDown || a.out_type == MOE_BF16) {
     float m = 0.f;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      uint32_t w[4];
+    for (int h = 0; h < 4; ++h) {  // 32 columns at a time
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float lo, hi;
-        unpack_f32x2(acc[4 * c + i], lo, hi);
-        m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));  // (columns beyond N have zero weights)
-        w[i] = f32x2_to_f16x2_sat(lo, hi);
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo, hi;
+          unpack_f32x2(acc[16 * h + 4 * c + i], lo, hi);
+          if (kMode == kDown) {
+            m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));  // (columns beyond N have zero weights)
+            w[i] = f32x2_to_f16x2_sat(lo, hi);
+          } else {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
+          }
+        }
+        st_shared_v4(mine + 16 * c, w[0], w[1], w[2], w[3]);
       }
-      st_shared_v4(mine + 16 * c, w[0], w[1], w[2], w[3]);
+      send_rows<uint16_t>(a, stage, row0, rows, col0 + 32 * h, min(32, n - 32 * h), pol);
     }
-    if (m > kF16Max && static_cast<int>(threadIdx.x & 31) < rows) set_error(a.err, MOE_DEVERR_RANGE);
-    send_rows<uint16_t>(a, stage, row0, rows, col0, n, pol);
-  } else if (a.out_type == MOE_BF16) {
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float lo, hi;
-        unpack_f32x2(acc[4 * c + i], lo, hi);
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
-      }
-      st_shared_v4(mine + 16 * c, w[0], w[1], w[2], w[3]);
-    }
-    send_rows<uint16_t>(a, stage, row0, rows, col0, n, pol);
+    if (kMode == kDown && m > kF16Max && static_cast<int>(threadIdx.x & 31) < rows) set_error(a.err, MOE_DEVERR_RANGE);
   } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // 64 columns at a time
+    for (int h = 0; h < 8; ++h) {  // 16 columns at a time
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
+      for (int c = 0; c < 4; ++c) {
         float v[4];
-        unpack_f32x2(acc[32 * h + 2 * c], v[0], v[1]);
-        unpack_f32x2(acc[32 * h + 2 * c + 1], v[2], v[3]);
+        unpack_f32x2(acc[8 * h + 2 * c], v[0], v[1]);
+        unpack_f32x2(acc[8 * h + 2 * c + 1], v[2], v[3]);
         st_shared_v4(mine + 16 * c, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
       }
-      send_rows<uint32_t>(a, stage, row0, rows, col0 + 64 * h, min(64, n - 64 * h), pol);
+      send_rows<uint32_t>(a, stage, row0, rows, col0 + 16 * h, min(16, n - 16 * h), pol);
     }
   }
 }
 
 template <int kMode>
 __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
-    f8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const F8Args a) {
-  constexpr int kStages = Cfg<kMode>::kStages;
+    f8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap amap128, const F8Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
@@ -413,31 +404,39 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
         }
         pdl_wait();
       }
+      // One elected lane runs a unit's K loop (as the MMA issuer does): with a vote and four row loads
+      // a block the producer was as slow as the epilogue.
+      const uint32_t full0 = smem_u32(full), base0 = smem_u32(smem);
       uint32_t g = 0;
       bool ok = true;
       for (uint32_t j = 0; ok; ++j) {
         const Unit un = ring.get(j);
         if (un.rows == 0) break;
         ring.done(j);
-        const int ntile = min(2, a.halves - 2 * un.tile);
-        const uint8_t* wb = a.w + un.expert * a.w_stride;
-        const int nbox = kMode == kGateUp ? 0 : (un.rows + 31) / 32;
-        for (int kb = kb0; kb < kb1; ++kb, ++g) {
-          const int slot = g % kStages;
-          if (!(ok = mbar_wait_warp(&empty[slot], ((g / kStages) & 1u) ^ 1u, abort_flag, a.err))) break;
-          if (elect_one()) {
-            uint8_t* sb = smem + slot * kStageBytes;
-            const bool early = g < pre;
-            mbar_arrive_expect_tx(&full[slot], (early ? 0 : ntile * kF8TileBytes) + nbox * 32 * kF8Block);
-            if (!early)
-              bulk_load(sb, wb + f8_half_offset(2 * un.tile, kb, a.halves, nk), ntile * kF8TileBytes, &full[slot], pol_w);
+        const uint32_t wbytes = min(2, a.halves - 2 * un.tile) * kF8TileBytes;
+        const uint8_t* wp = a.w + un.expert * a.w_stride + f8_half_offset(2 * un.tile, kb0, a.halves, nk);
+        // rows by boxes of a.box_rows (linear: a part's rows in one box), or of 128 where that many are wanted
+        const bool big = kMode == kDown && un.rows > 64;
+        const int box = big ? BM : a.box_rows;
+        const int nbox = kMode == kGateUp ? 0 : (un.rows + box - 1) / box;
+        const uint32_t abytes = nbox * box * kF8Block;
+        const CUtensorMap* map = big ? &amap128 : &amap;
+        if (elect_one()) {
+          uint32_t slot = g % kStages, ph = ((g / kStages) & 1u) ^ 1u, i = g;
+          for (int kb = kb0; kb < kb1; ++kb, ++i, wp += wbytes) {
+            if (!(ok = mbar_wait(&empty[slot], ph, abort_flag, a.err))) break;
+            const uint32_t bar = full0 + 8 * slot, sb = base0 + slot * kStageBytes;
+            const bool early = kMode != kGateUp && i < pre;
+            mbar_arrive_expect_tx_u32(bar, (early ? 0 : wbytes) + abytes);
+            if (!early) bulk_load_u32(sb, wp, wbytes, bar, pol_w);
             if (kMode != kGateUp)
-              for (int i = 0; i < nbox; ++i)
-                tma_load_2d(sb + kBBytes + i * 32 * kF8Block, &amap, &full[slot], kb * kF8Block, un.row_start + 32 * i,
-                            pol_act);
+              for (int b = 0; b < nbox; ++b)
+                tma_load_2d_u32(sb + kBBytes + b * box * kF8Block, map, bar, kb * kF8Block, un.row_start + box * b, pol_act);
+            if (++slot == kStages) slot = 0, ph ^= 1u;
           }
-          __syncwarp();
         }
+        g += kb1 - kb0;
+        ok = __all_sync(0xffffffffu, ok);
       }
     } else if (warp == 1) {
       // ---------------- MMA issuer ----------------
@@ -735,18 +734,19 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
 }  // namespace f8
 
 template <int kMode>
-static cudaError_t launch_f8(const CUtensorMap& m, const F8Args& a, int num_sms, cudaStream_t st) {
+static cudaError_t launch_f8(const CUtensorMap& m, const CUtensorMap& m128, const F8Args& a, int num_sms, cudaStream_t st) {
   auto kern = f8::f8_gemm_kernel<kMode>;
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), f8::Cfg<kMode>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(num_sms), dim3(f8::Cfg<kMode>::kThreads), f8::Cfg<kMode>::kSmemBytes, st, m, a);
+  return launch_pdl(kern, dim3(num_sms), dim3(f8::Cfg<kMode>::kThreads), f8::Cfg<kMode>::kSmemBytes, st, m, m128, a);
 }
 
 cudaError_t launch_f8_gateup(const F8Args& a, int num_sms, cudaStream_t st) {
-  return launch_f8<f8::kGateUp>(CUtensorMap{}, a, num_sms, st);
+  return launch_f8<f8::kGateUp>(CUtensorMap{}, CUtensorMap{}, a, num_sms, st);
 }
-cudaError_t launch_f8_down(const CUtensorMap* amap, const F8Args& a, int num_sms, cudaStream_t st) {
-  return launch_f8<f8::kDown>(*amap, a, num_sms, st);
+cudaError_t launch_f8_down(const CUtensorMap* amap, const CUtensorMap* amap128, const F8Args& a, int num_sms,
+                           cudaStream_t st) {
+  return launch_f8<f8::kDown>(*amap, *amap128, a, num_sms, st);
 }
 
 // Clusters of `s` CTAs of the split kernel that the device runs at the same time (0: unknown).
@@ -802,10 +802,10 @@ cudaError_t launch_f8_linear(const CUtensorMap* amap, const F8Args& a, int num_s
       attr[1].val.clusterDim = {static_cast<unsigned>(s), 1, 1};
       cfg.attrs = attr;
       cfg.numAttrs = 2;
-      return cudaLaunchKernelEx(&cfg, kern, *amap, b);
+      return cudaLaunchKernelEx(&cfg, kern, *amap, CUtensorMap{}, b);
     }
   }
-  return launch_f8<f8::kLinear>(*amap, a, units < num_sms ? units : num_sms, st);
+  return launch_f8<f8::kLinear>(*amap, CUtensorMap{}, a, units < num_sms ? units : num_sms, st);
 }
 
 }  // namespace moe

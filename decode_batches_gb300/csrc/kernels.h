@@ -11,9 +11,9 @@ namespace moe {
 
 // Sets the thread's moe_last_error() message and returns s (api.cu).
 moe_status fail_message(moe_status s, const char* msg);
-// 2-D byte tensor [rows][inner] (row pitch ld bytes, a multiple of 16), box {128, 32}, 128-byte swizzle:
-// 8-bit rows as a GEMM operand.  Bytes beyond the extents read as zero (api.cu).
-moe_status make_map_f8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld);
+// 2-D byte tensor [rows][inner] (row pitch ld bytes, a multiple of 16), box {128, box_rows}, 128-byte
+// swizzle: 8-bit rows as a GEMM operand.  Bytes beyond the extents read as zero (api.cu).
+moe_status make_map_f8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld, int box_rows);
 
 // A conversion of x (bf16) that a kernel performs on the side with every thread of its grid: to x16
 // (fp16, n8 * 8 elements; the 4-bit path's activation copy, convert_x16 in common.cuh), or to xq / xs
@@ -262,12 +262,15 @@ struct F8Args {
   int out_vec = 0;              // rows start, and N ends, on 16-byte boundaries
   int N = 0, halves = 0, nk = 0;
   int T = 0, k = 0;
+  int box_rows = 32;            // rows of amap's box (a multiple of 32)
   int splits = 1;               // linear: CTAs of a cluster that share a unit's K blocks (set at launch)
   uint32_t* err = nullptr;
 };
-// amap: the activation rows [rows][K] as bytes, box {128, 32}, 128-byte swizzle (not gate/up).
+// amap: the activation rows [rows][K] as bytes, box {128, a.box_rows}, 128-byte swizzle (not gate/up);
+// amap128: the same with 128 rows.
 cudaError_t launch_f8_gateup(const F8Args& a, int num_sms, cudaStream_t st);
-cudaError_t launch_f8_down(const CUtensorMap* amap, const F8Args& a, int num_sms, cudaStream_t st);
+cudaError_t launch_f8_down(const CUtensorMap* amap, const CUtensorMap* amap128, const F8Args& a, int num_sms,
+                           cudaStream_t st);
 cudaError_t launch_f8_linear(const CUtensorMap* amap, const F8Args& a, int num_sms, cudaStream_t st);
 
 // ---- one-launch layer of a small step (layer_small.cu) ------------------------------------------

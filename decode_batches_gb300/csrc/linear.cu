@@ -147,9 +147,12 @@ static moe_status check_out(const moe_linear* l, int T, const void* out, moe_dty
 static moe_status product(moe_linear* l, const uint8_t* q, int64_t ldq, const float* s, int64_t lds, int T, void* out,
                           moe_dtype out_dtype, int64_t ldo, cudaStream_t st) {
   CUtensorMap m;
-  moe_status r = make_map_f8(&m, q, l->K, T, ldq);
-  if (r != MOE_OK) return r;
   F8Args a;
+  // the rows are split into near-equal parts of at most 128: one box holds a part
+  const int parts = (T + 127) / 128, most = (T + parts - 1) / parts;
+  a.box_rows = (most + 31) / 32 * 32;
+  moe_status r = make_map_f8(&m, q, l->K, T, ldq, a.box_rows);
+  if (r != MOE_OK) return r;
   a.w = l->w;
   a.ws = l->ws;
   a.as = s;
