@@ -58,7 +58,7 @@ constexpr int kABytes = BM * kF8Block;
 constexpr int kStageBytes = kABytes + kBBytes;    // 48 KB
 constexpr int kAccCols = 256;
 constexpr int kTmemCols = 2 * kAccCols;
-constexpr int kEpiWarps = 8, kFirstEpi = 4, kFirstGather = 12;
+constexpr int kEpiWarps = 8, kFirstEpi = 4, kFirstGather = 12, kGatherWarps = 4;
 constexpr int kRing = 4;                          // decoded units
 constexpr uint32_t kSpinLimit = 1u << 20;         // tries of an epilogue wait: 1.4 s at 1.3 us a try
 constexpr int kScGroups = 4;                      // groups of four K blocks of scales
@@ -81,7 +81,7 @@ struct Cfg {
   static constexpr int kRegsEpi = kMode == kGateUp ? 200 : 216;
   static constexpr int kRegsRest = kMode == kGateUp ? 56 : 72;
   // warps that read each unit record: producer, MMA, scales, epilogue, gather
-  static constexpr int kReaders = 3 + kEpiWarps + (kMode == kGateUp ? kStages : 0);
+  static constexpr int kReaders = 3 + kEpiWarps + (kMode == kGateUp ? kGatherWarps : 0);
 };
 
 struct Unit {
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], kMode == kGateUp ? 2 : 1);
+      mbar_init(&full[s], kMode == kGateUp ? 1 + kGatherWarps : 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -656,34 +656,46 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg<kMode>::kRegsRest));
     // ---------------- gate/up: row gather (cp.async) ----------------
-    // Warp w owns stage slot w: it fills every stage g with g % kStages == w, waits for its own
-    // copies, fences them for the tensor core and arrives.  8 consecutive lanes copy one row's
-    // 128 bytes.
-    const int slot = warp - kFirstGather;
-    const int ch = lane & 7;
+    // Every warp copies a quarter of each stage's rows (8 consecutive lanes one row's 128 bytes, a lane 8
+    // rows, whose addresses it holds for the unit).  A stage's copies are waited for, fenced for the tensor
+    // core and announced kLag stages later, so up to three stages' are in flight and MMAs of the stage
+    // before never wait for the issue.  (Every warp a whole stage of its own, its addresses read per
+    // row and its copies waited for at once: busy tiles took 1200 cycles a block.)
+    constexpr uint32_t kLag = 2;
+    static_assert(kLag + 1 < kStages && kLag < kRing, "a stage's copies are announced before its slot's next wait");
+    const int n0 = 4 * (warp - kFirstGather) + (lane >> 3), ch = lane & 7;
+    const uint32_t dst0 = smem_u32(smem) + kBBytes + n0 * kF8Block + ((ch ^ (n0 & 7)) << 4);
     const uint64_t pol_x = l2_policy_evict_last();
     uint32_t g = 0;
     bool ok = true;
     for (uint32_t j = 0; ok; ++j) {
       const Unit un = ring.get(j);
       if (un.rows == 0) break;
-      const int32_t* tok = tok_tab + BM * (j % kRing);
-      for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        const int s = g % kStages;
-        if (s != slot) continue;
-        if (!(ok = mbar_wait_warp(&empty[s], ((g / kStages) & 1u) ^ 1u, abort_flag, a.err))) break;
-        const uint32_t sa = smem_u32(smem + s * kStageBytes + kBBytes);
-        const int k0 = kb * kF8Block + ch * 16;
-        for (int n = lane >> 3; n < un.rows; n += 4)
-          cp_async_16_hint(sa + n * 128 + ((ch ^ (n & 7)) << 4), a.a + static_cast<size_t>(tok[n]) * a.lda + k0, pol_x);
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
-      }
+      const uint8_t* src[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        src[i] = a.a + static_cast<size_t>(tok_tab[BM * (j % kRing) + min(n0 + 16 * i, un.rows - 1)]) * a.lda + ch * 16;
       ring.done(j);
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const uint32_t slot = g % kStages;
+        if (!(ok = mbar_wait_warp(&empty[slot], ((g / kStages) & 1u) ^ 1u, abort_flag, a.err))) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (n0 + 16 * i < un.rows)
+            cp_async_16_hint(dst0 + slot * kStageBytes + 16 * i * kF8Block, src[i] + kb * kF8Block, pol_x);
+        cp_async_commit();
+        if (g >= kLag) {
+          cp_async_wait<kLag>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          mbar_arrive_lane0(&full[(g - kLag) % kStages]);
+        }
+      }
     }
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    for (uint32_t i = g > kLag ? g - kLag : 0; i < g; ++i) mbar_arrive_lane0(&full[i % kStages]);
   }
 
   if (kMode == kSplit) {
