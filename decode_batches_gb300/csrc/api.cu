@@ -301,6 +301,20 @@ moe_status moe::make_map_f8(CUtensorMap* m, const void* base, uint64_t inner, ui
   return MOE_OK;
 }
 
+moe_status moe::make_map_bf16_out(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld) {
+  auto fn = encode_fn();
+  if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {ld * 2};
+  cuuint32_t box[2] = {64, 32};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return MOE_OK;
+}
+
 static moe_status build_weight_maps(moe_plan* p) {
   // the tensor-core path reads the tile-contiguous weights directly (bulk copies, no maps)
   const bool routed = p->wdtype == MOE_W_BF16 ? p->tiled : p->wdtype == MOE_W_MXFP4 ? p->fp4_tc : true;

@@ -14,7 +14,8 @@
 //            gate rows, the same 64 features' up rows); the epilogue forms silu(g) * u in fp32,
 //            quantises the 128 features (one activation block of h) and writes codes and scale.
 //   down     a = those rows of h; y in fp16 in grouped order for the combine.
-//   linear   a = the T rows of one matrix; bf16 or fp32 out.
+//   linear   a = the T rows of one matrix; bf16 or fp32 out.  Sets of 32 whole bf16 rows leave by TMA stores that
+//            nobody waits for.
 //   split    linear with few units: a cluster of S CTAs shares a unit, each a range of its K blocks;
 //            the fp32 sums meet in shared memory and every CTA adds up (in split order) and writes a
 //            1/S of the columns.
@@ -22,9 +23,11 @@
 // row parts: CTAs that share a weight tile run side by side and its second read is served by L2.
 //
 // What bounds them, measured on a GB300 (6.78 TB/s copy, 1.94 PFLOP/s bf16): up to about 100 rows an expert
-// the weight stream (256 experts, d 2048, f 512, 2051 tokens x 8: gate/up 90 us at 6.1 TB/s, down 55 us at
-// 5.2 TB/s); 8192 x 4096 x 4096 113 us, 2.4 PFLOP/s, the epilogue: about 830 cycles a block (256 of them
-// the FMA pipe's, 64 packed FMAs a thread at two cycles) against 512 of MMA; few rows, latency.
+// the weight stream (256 experts, d 2048, f 512, 2051 tokens x 8: gate/up 94 us at 5.9 TB/s, down 57 us at
+// 5.1 TB/s); 8192 x 4096 x 4096 108 us, 2.5 PFLOP/s, the epilogue's additions (256 cycles a block of the FMA
+// pipe, 64 packed FMAs a thread at two cycles, and as many TMEM loads) beside 512 cycles of MMA; full tiles of
+// gate/up (8 experts of 2051 rows, d 4096, f 1024: 160 us, 1.7 PFLOP/s) that and the row gather: 139 us
+// without the gather, 121 without the additions, 95 without both; few rows, latency.
 //
 // Roles (persistent CTAs, one per SM, every role walks the same unit sequence):
 //   warp 0      producer: weights by bulk copy (tile-contiguous, pre-swizzled); rows by TMA
@@ -52,7 +55,6 @@ namespace f8 {
 
 constexpr int kGateUp = 0, kDown = 1, kLinear = 2, kSplit = 3;
 constexpr int BM = 128;                           // activation rows per tile (MMA M)
-constexpr int kStages = 4;                        // (three: the 8192-row product waits for its loads, 133 us)
 constexpr int kBBytes = 2 * kF8TileBytes;         // 256 weight rows x 128 K elements
 constexpr int kABytes = BM * kF8Block;
 constexpr int kStageBytes = kABytes + kBBytes;    // 48 KB
@@ -68,12 +70,18 @@ constexpr int kTokBytes = kRing * BM * 4;         // gate/up, per unit: source r
 constexpr int kXchBytes = 2 * 2 * BM * 4;         // gate/up, row maxima of h: [unit parity][half][row]
 constexpr int kOutPitch = 64 + 16;                // a staged row of results: 64 bytes, odd in 16-byte units
 constexpr int kOutBytes = 32 * kOutPitch;         // per epilogue warp
+constexpr int kTmaOutBytes = 9 * 1024;            // linear: two boxes of 32 rows x 128 bytes (and alignment)
 constexpr int kSumPitch = 256 * 4 + 16;           // split: a row of fp32 sums (in the stages' space)
 static_assert(BM * kSumPitch <= 3 * kStageBytes, "sums in the stages");
 
 template <int kMode>
 struct Cfg {
-  static constexpr int kExtra = kMode == kGateUp ? kTokBytes + kXchBytes : kEpiWarps * kOutBytes;
+  // linear trades a stage for staging space of whole bf16 results, which TMA stores read while the next
+  // unit is under way (8192 x 4096 x 4096 with the quantisation: 129 us; four stages and row pieces 133;
+  // four stages and boxes of 32 columns through 2 KB, waited for in between, 134; without any stores 120)
+  static constexpr int kStages = kMode == kLinear ? 3 : 4;
+  static constexpr int kExtra = kMode == kGateUp ? kTokBytes + kXchBytes : kMode == kLinear ? kEpiWarps * kTmaOutBytes
+                                                                                        : kEpiWarps * kOutBytes;
   static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /*barriers*/ + 1024 /*align slack*/ + kScaleBytes + kExtra;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static constexpr int kThreads = kMode == kGateUp ? 512 : 384;
@@ -196,6 +204,17 @@ MOE_DEVICE float4 ld_cluster_v4(uint32_t addr, uint32_t rank) {
       : "memory");
   return v;
 }
+// TMA store of a box (64 x 32 elements, 128-byte swizzled in shared memory) at column c0, row c1; the bulk
+// groups of the issuing thread.
+MOE_DEVICE void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(src)
+               : "memory");
+}
+MOE_DEVICE void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+MOE_DEVICE void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+MOE_DEVICE void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 MOE_DEVICE float ld_shared_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -228,8 +247,7 @@ MOE_DEVICE void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, 
 // Writes the warp's first `rows` staged rows, `cols` elements each, to out at (row0, col).  4 lanes take a
 // row's 64 bytes where rows and columns allow 16-byte stores, else 32 lanes one element each.  (An odd
 // N, 517 x 1337: 35 us with each lane storing its own row's elements, 13 so.  With aligned rows it is as
-// fast as 32 bytes a lane to 32 rows straight from the registers; a bulk copy of each row, or TMA stores of 32
-// rows, gained nothing.)
+// fast as 32 bytes a lane to 32 rows straight from the registers.)
 template <typename E>
 MOE_DEVICE void send_rows(const F8Args& a, uint32_t stage, int64_t row0, int rows, int64_t col, int cols, uint64_t pol) {
   const int lane = threadIdx.x & 31;
@@ -260,11 +278,39 @@ MOE_DEVICE void send_rows(const F8Args& a, uint32_t stage, int64_t row0, int row
 // The warp's rows row0 .. row0 + rows - 1 (a lane each; beyond 32 or below 1 clipped), 128 columns from
 // col0 (of N), through its staging space.
 template <int kMode>
-MOE_DEVICE void store_rows(const uint64_t (&acc)[64], const F8Args& a, uint32_t stage, int64_t row0, int rows, int col0,
-                           uint64_t pol) {
+MOE_DEVICE void store_rows(const uint64_t (&acc)[64], const F8Args& a, const CUtensorMap* omap, uint32_t stage,
+                           int64_t row0, int rows, int col0, uint64_t pol) {
   const int n = min(128, a.N - col0);  // valid columns here
   const uint32_t mine = stage + (threadIdx.x & 31) * kOutPitch;
   rows = min(rows, 32);
+  if (kMode == kLinear) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) bulk_wait_read();  // an earlier TMA store still reads the staging space
+    __syncwarp();
+    // 32 whole rows leave as two TMA stores of 64 columns, which nobody waits for (128-byte swizzled
+    // staging rows); a partial set of rows, whose neighbours belong to others, as row pieces
+    if (a.out_vec && rows == 32 && a.out_type == MOE_BF16) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo, hi;
+          unpack_f32x2(acc[4 * c + i], lo, hi);
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
+        }
+        st_shared_v4(stage + lane * 128 + (c >> 3) * 4096 + (((c & 7) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(omap, stage, col0, static_cast<int>(row0));
+        if (n > 64) tma_store_2d(omap, stage + 4096, col0 + 64, static_cast<int>(row0));
+        bulk_commit();
+      }
+      return;
+    }
+  }
   if (kMode == kDown || a.out_type == MOE_BF16) {
     float m = 0.f;
 #pragma unroll
@@ -305,10 +351,17 @@ MOE_DEVICE void store_rows(const uint64_t (&acc)[64], const F8Args& a, uint32_t 
 
 template <int kMode>
 __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
-    f8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap amap128, const F8Args a) {
+    f8_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap amap128,
+                   const __grid_constant__ CUtensorMap omap, const F8Args a) {
+  constexpr int kStages = Cfg<kMode>::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint8_t* extra = smem + kStages * kStageBytes;
+  int32_t* tok_tab = reinterpret_cast<int32_t*>(extra);                         // gate/up
+  volatile float* xch = reinterpret_cast<volatile float*>(extra + kTokBytes);   // gate/up
+  uint8_t* out_tab = extra;                                                     // linear, down
+  uint8_t* bars = extra + Cfg<kMode>::kExtra;
+  uint64_t* full = reinterpret_cast<uint64_t*>(bars);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 2;
@@ -318,14 +371,10 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
   uint64_t* sc_full = ring_empty + kRing;
   uint64_t* sc_empty = sc_full + kScGroups;
   uint64_t* drain = sc_empty + kScGroups;
-  int4* ring_rec = reinterpret_cast<int4*>(smem + kStages * kStageBytes + 512);
+  int4* ring_rec = reinterpret_cast<int4*>(bars + 512);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint8_t* sc_tab = smem + kStages * kStageBytes + 1024;
-  uint8_t* extra = sc_tab + kScaleBytes;
-  int32_t* tok_tab = reinterpret_cast<int32_t*>(extra);                         // gate/up
-  volatile float* xch = reinterpret_cast<volatile float*>(extra + kTokBytes);   // gate/up
-  uint8_t* out_tab = extra;                                                     // linear, down
+  uint8_t* sc_tab = bars + 1024;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -537,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
     // ---------------- epilogue ----------------
     const int q = warp & 3, half = (warp - kFirstEpi) >> 2;
     const int r = 32 * q + lane;  // row of the tile
-    const uint32_t stage_out = smem_u32(out_tab + (warp - kFirstEpi) * kOutBytes);
+    const uint32_t stage_out = smem_u32(out_tab + (warp - kFirstEpi) * (kMode == kLinear ? kTmaOutBytes : kOutBytes));
     // y is read back by the next launch: keep it in L2 ahead of the streamed weights
     const uint64_t pol_out = kMode == kDown ? l2_policy_evict_last() : l2_policy_evict_first();
     uint32_t g = 0, c = 0, nx = 0;  // K blocks, groups of scales, exchanges of row maxima so far
@@ -650,9 +699,10 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
                          static_cast<uint32_t>(acc[2 * c + 1]), static_cast<uint32_t>(acc[2 * c + 1] >> 32));
         }
       } else {
-        store_rows<kMode>(acc, a, stage_out, un.row_start + 32 * q, un.rows - 32 * q, un.tile * 256 + half * 128, pol_out);
+        store_rows<kMode>(acc, a, &omap, stage_out, un.row_start + 32 * q, un.rows - 32 * q, un.tile * 256 + half * 128, pol_out);
       }
     }
+    if (kMode == kLinear && lane == 0) bulk_wait_all();  // the stores are done before the CTA is
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg<kMode>::kRegsRest));
     // ---------------- gate/up: row gather (cp.async) ----------------
@@ -662,7 +712,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
     // before never wait for the issue.  (Every warp a whole stage of its own, its addresses read per
     // row and its copies waited for at once: busy tiles took 1200 cycles a block.)
     constexpr uint32_t kLag = 2;
-    static_assert(kLag + 1 < kStages && kLag < kRing, "a stage's copies are announced before its slot's next wait");
+    static_assert(kMode != kGateUp || (kLag + 1 < kStages && kLag < kRing), "a stage's copies are announced before its slot's next wait");
     const int n0 = 4 * (warp - kFirstGather) + (lane >> 3), ch = lane & 7;
     const uint32_t dst0 = smem_u32(smem) + kBBytes + n0 * kF8Block + ((ch ^ (n0 & 7)) << 4);
     const uint64_t pol_x = l2_policy_evict_last();
@@ -746,19 +796,20 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
 }  // namespace f8
 
 template <int kMode>
-static cudaError_t launch_f8(const CUtensorMap& m, const CUtensorMap& m128, const F8Args& a, int num_sms, cudaStream_t st) {
+static cudaError_t launch_f8(const CUtensorMap& m, const CUtensorMap& m128, const CUtensorMap& o, const F8Args& a,
+                             int num_sms, cudaStream_t st) {
   auto kern = f8::f8_gemm_kernel<kMode>;
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), f8::Cfg<kMode>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(num_sms), dim3(f8::Cfg<kMode>::kThreads), f8::Cfg<kMode>::kSmemBytes, st, m, m128, a);
+  return launch_pdl(kern, dim3(num_sms), dim3(f8::Cfg<kMode>::kThreads), f8::Cfg<kMode>::kSmemBytes, st, m, m128, o, a);
 }
 
 cudaError_t launch_f8_gateup(const F8Args& a, int num_sms, cudaStream_t st) {
-  return launch_f8<f8::kGateUp>(CUtensorMap{}, CUtensorMap{}, a, num_sms, st);
+  return launch_f8<f8::kGateUp>(CUtensorMap{}, CUtensorMap{}, CUtensorMap{}, a, num_sms, st);
 }
 cudaError_t launch_f8_down(const CUtensorMap* amap, const CUtensorMap* amap128, const F8Args& a, int num_sms,
                            cudaStream_t st) {
-  return launch_f8<f8::kDown>(*amap, *amap128, a, num_sms, st);
+  return launch_f8<f8::kDown>(*amap, *amap128, CUtensorMap{}, a, num_sms, st);
 }
 
 // Clusters of `s` CTAs of the split kernel that the device runs at the same time (0: unknown).
@@ -791,7 +842,8 @@ static int split_clusters(int s) {
 
 // Units too few to fill the SMs (small T, or a small matrix) are split along K over clusters of 8, 4 or
 // 2 CTAs: as many as run at the same time with a K block or more each.
-cudaError_t launch_f8_linear(const CUtensorMap* amap, const F8Args& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_f8_linear(const CUtensorMap* amap, const CUtensorMap* omap, const F8Args& a, int num_sms,
+                             cudaStream_t st) {
   const int units = (a.halves + 1) / 2 * ((a.T + f8::BM - 1) / f8::BM);
   if (2 * units <= num_sms && a.nk >= 2) {
     auto kern = f8::f8_gemm_kernel<f8::kSplit>;
@@ -814,10 +866,10 @@ cudaError_t launch_f8_linear(const CUtensorMap* amap, const F8Args& a, int num_s
       attr[1].val.clusterDim = {static_cast<unsigned>(s), 1, 1};
       cfg.attrs = attr;
       cfg.numAttrs = 2;
-      return cudaLaunchKernelEx(&cfg, kern, *amap, CUtensorMap{}, b);
+      return cudaLaunchKernelEx(&cfg, kern, *amap, CUtensorMap{}, CUtensorMap{}, b);
     }
   }
-  return launch_f8<f8::kLinear>(*amap, CUtensorMap{}, a, units < num_sms ? units : num_sms, st);
+  return launch_f8<f8::kLinear>(*amap, CUtensorMap{}, *omap, a, units < num_sms ? units : num_sms, st);
 }
 
 }  // namespace moe

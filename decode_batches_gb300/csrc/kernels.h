@@ -14,6 +14,8 @@ moe_status fail_message(moe_status s, const char* msg);
 // 2-D byte tensor [rows][inner] (row pitch ld bytes, a multiple of 16), box {128, box_rows}, 128-byte
 // swizzle: 8-bit rows as a GEMM operand.  Bytes beyond the extents read as zero (api.cu).
 moe_status make_map_f8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld, int box_rows);
+// 2-D bf16 tensor [rows][inner] (row pitch ld elements, a multiple of 8), box {64, 32}, 128-byte swizzle.
+moe_status make_map_bf16_out(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t ld);
 
 // A conversion of x (bf16) that a kernel performs on the side with every thread of its grid: to x16
 // (fp16, n8 * 8 elements; the 4-bit path's activation copy, convert_x16 in common.cuh), or to xq / xs
@@ -271,7 +273,9 @@ struct F8Args {
 cudaError_t launch_f8_gateup(const F8Args& a, int num_sms, cudaStream_t st);
 cudaError_t launch_f8_down(const CUtensorMap* amap, const CUtensorMap* amap128, const F8Args& a, int num_sms,
                            cudaStream_t st);
-cudaError_t launch_f8_linear(const CUtensorMap* amap, const F8Args& a, int num_sms, cudaStream_t st);
+// omap: bf16 out with a.out_vec, [T][N], box {64, 32}, 128-byte swizzle (else unused).
+cudaError_t launch_f8_linear(const CUtensorMap* amap, const CUtensorMap* omap, const F8Args& a, int num_sms,
+                             cudaStream_t st);
 
 // ---- one-launch layer of a small step (layer_small.cu) ------------------------------------------
 constexpr int kLsTMax = 8;                  // tokens per step

@@ -167,7 +167,9 @@ static moe_status product(moe_linear* l, const uint8_t* q, int64_t ldq, const fl
   a.T = T;
   a.k = 1;
   a.err = l->err;
-  LIN_TRY(launch_f8_linear(&m, a, l->num_sms, st));
+  CUtensorMap o{};  // (fewer than 32 rows never leave as a box)
+  if (out_dtype == MOE_BF16 && a.out_vec && T >= 32 && (r = make_map_bf16_out(&o, out, l->N, T, ldo)) != MOE_OK) return r;
+  LIN_TRY(launch_f8_linear(&m, &o, a, l->num_sms, st));
   return MOE_OK;
 }
 

@@ -98,6 +98,24 @@ def test_linear_against_64_bits(T, N, K, out):
     assert lin.device_error() == 0
 
 
+# More units than half the SMs (no split): whole sets of 32 rows leave as boxes of 64 columns, the rest of
+# a part as row pieces; N ends before, at and behind a box's last column, and nothing outside is written.
+@pytest.mark.parametrize("N", [1320, 1344, 1352, 1536])
+@pytest.mark.parametrize("T", [2048, 2100])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_linear_many_rows_into_a_wider_output(T, N, out):
+    K = 384
+    lin, wq, ws = make_linear(N, K, T)
+    x = random_rows(T, K, 8)
+    wide = torch.full((T + 40, N + 24), 7.0, dtype=DT[out], device="cuda")
+    got = wide[16:16 + T, 16:16 + N]
+    lin.forward(x.cuda(), out=got, out_dtype=DT[out])
+    check(got, *quantize_rows_ref(x), wq, ws)
+    assert (wide[:16] == 7).all() and (wide[16 + T:] == 7).all()
+    assert (wide[:, :16] == 7).all() and (wide[:, 16 + N:] == 7).all()
+    assert lin.device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 def test_linear_strided_rows_and_output(dtype):
     T, N, K = 50, 264, 200
