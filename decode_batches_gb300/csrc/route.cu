@@ -16,6 +16,8 @@
 // changing between runs (every chosen expert computed exactly once -> bijection checks).
 #include <float.h>
 
+#include <type_traits>
+
 #include "fp8.cuh"
 #include "kernels.h"
 #include "scored.cuh"
@@ -254,14 +256,14 @@ cudaError_t launch_router_logits(const uint16_t* x, const float* w_router, const
 // Top-k with gates
 // ============================================================================================
 
-// Two blocks per 32-token chunk (16 tokens each), one warp per token.  Lane l holds the
+// Two blocks per 32-token chunk (16 tokens each; four of 8, if scored), one warp per token.  Lane l holds the
 // logits of experts l, l + 32, ..., l + 32 (PL - 1); topk_select takes k rounds of a warp-wide
 // maximum.  Masks are stored expert-major, masks[e * mstride + c], bit tl for token tl of the
-// chunk: each block writes its 16-bit half of the word.  The logits are the sum of `nsplit`
+// chunk: each block writes its 16 or 8 bits of the word.  The logits are the sum of `nsplit`
 // partial matrices parts[s][T][E] (s ascending) plus the optional bias; they are written to
 // logits_out if given.
-constexpr int kTopkTokens = kChunk / 2;       // tokens per block
-constexpr int kTopkThreads = 32 * kTopkTokens;
+template <bool kScored>
+constexpr int topk_tokens = kScored ? kChunk / 4 : kChunk / 2;  // tokens per block
 
 // Top-k of token t by one warp: sums the partial logits (split order fixed) and the bias,
 // optionally stores the logits, then selects (topk_select).
@@ -309,35 +311,40 @@ MOE_DEVICE int topk_token(const float* __restrict__ parts, int nsplit, const flo
   return select_token<PL, kScored>(v, t, E, k, ids, gates, err, sa, scr);
 }
 
+// Scored selection is bound by its instructions, so the busiest SM's tokens count: blocks of 8 tokens
+// spread 8195 of them as 56 an SM at most, blocks of 16 as 64 and with a longer wait for a block's slowest
+// warp (E = 384, 12 groups: 15.4 and 22.5 us; T = 48: 4.3 and 5.3).
 template <int PL, bool kScored>
-__global__ void __launch_bounds__(kTopkThreads) topk_kernel(const float* __restrict__ parts, int nsplit,
+__global__ void __launch_bounds__(32 * topk_tokens<kScored>, kScored && PL <= 12 ? 4 : 1) topk_kernel(const float* __restrict__ parts, int nsplit,
                                                             const float* __restrict__ bias,
                                                             float* __restrict__ logits_out, int T, int E, int k,
                                                             int n_chunks, int32_t* __restrict__ ids,
                                                             float* __restrict__ gates,
                                                             uint32_t* __restrict__ masks, uint32_t* err,
                                                             const XConv xc, const ScoreArgs sa) {
-  extern __shared__ uint32_t smask[];  // [E]: bits of this block's 16 tokens; scored: [E] for each warp
+  constexpr int kTokens = topk_tokens<kScored>, kParts = kChunk / kTokens;
+  extern __shared__ uint32_t smask[];  // [E]: bits of this block's tokens; scored: [E] for each warp
   pdl_trigger();
   pdl_wait();
   convert_x(xc, err);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x >> 1, half = blockIdx.x & 1;
+  const int c = blockIdx.x / kParts, part = blockIdx.x % kParts;
   if (masks)
     for (int e = threadIdx.x; e < E; e += blockDim.x) smask[e] = 0u;
   __syncthreads();
-  const int t = c * kChunk + kTopkTokens * half + warp;
+  const int t = c * kChunk + kTokens * part + warp;
   if (t < T) {
     const int sel = topk_token<PL, kScored>(parts, nsplit, bias, logits_out, t, T, E, k, ids, gates, err, sa, smask + (masks ? E : 0) + warp * E);
     if (masks && lane < k) atomicOr(&smask[sel], 1u << warp);
   }
   if (masks) {
     __syncthreads();
-    // little-endian: half h of the 32-bit mask word is the 16-bit word 2 w + h
-    uint16_t* m16 = reinterpret_cast<uint16_t*>(masks);
+    // little-endian: part p of the 32-bit mask word is the 16- or 8-bit word kParts * w + p
+    using Part = std::conditional_t<kTokens == 16, uint16_t, uint8_t>;
+    Part* m = reinterpret_cast<Part*>(masks);
     const size_t mstride = group_mask_stride(n_chunks);
     for (int e = threadIdx.x; e < E; e += blockDim.x)
-      m16[2 * (static_cast<size_t>(e) * mstride + c) + half] = static_cast<uint16_t>(smask[e]);
+      m[kParts * (static_cast<size_t>(e) * mstride + c) + part] = static_cast<Part>(smask[e]);
   }
 }
 
@@ -346,12 +353,10 @@ static cudaError_t launch_topk_pl(const float* parts, int nsplit, const float* b
                                   int k, int n_chunks, int32_t* ids, float* gates, uint32_t* masks, uint32_t* err,
                                   const XConv& xc, const ScoreArgs& sa, cudaStream_t st) {
   auto kern = sa.on ? topk_kernel<PL, true> : topk_kernel<PL, false>;
-  const size_t smem = ((masks ? E : 0) + (sa.on ? kTopkTokens * static_cast<size_t>(E) : 0)) * sizeof(uint32_t);
-  if (smem > 48 * 1024) {
-    cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), 17 * 1024 * sizeof(uint32_t));
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(kern, dim3(2 * n_chunks), dim3(kTopkThreads), smem, st,
+  const int tokens = sa.on ? topk_tokens<true> : topk_tokens<false>;
+  // (at most 36 KB: nine times 1024 experts)
+  const size_t smem = ((masks ? E : 0) + (sa.on ? tokens * static_cast<size_t>(E) : 0)) * sizeof(uint32_t);
+  return launch_pdl(kern, dim3(n_chunks * (kChunk / tokens)), dim3(32 * tokens), smem, st,
                     parts, nsplit, bias, logits_out, T, E, k, n_chunks, ids, gates, masks, err, xc, sa);
 }
 
