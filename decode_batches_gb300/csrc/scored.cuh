@@ -25,7 +25,8 @@ MOE_DEVICE float rcp_approx(float x) {  // 1 ulp
 // warp, so what bounds the kernel is their number: a lane keeps its two best keys in registers (a
 // rescan, under a warp-uniform branch, when both are taken), a group's members are divided over the
 // lanes through scr, and the chosen scores are fetched through it.  Against rounds that rescan every
-// key and groups reduced one after the other: E = 384, 12 groups, 8195 tokens 37 -> 22 us (blocks of 16 tokens; 15 in blocks of 8).
+// key and groups reduced one after the other: E = 384, 12 groups, 8195 tokens 37 -> 22 us (in blocks of 16
+// tokens; 15 in the blocks of 8 that route.cu takes).
 template <int PL>
 MOE_DEVICE int score_select(const float (&v)[PL], int t, int E, int k, int32_t* __restrict__ ids,
                             float* __restrict__ gates, uint32_t* err, const ScoreArgs& sa, uint32_t* scr) {
