@@ -26,8 +26,8 @@
 // the weight stream (256 experts, d 2048, f 512, 2051 tokens x 8: gate/up 94 us at 5.9 TB/s, down 57 us at
 // 5.1 TB/s); 8192 x 4096 x 4096 108 us, 2.5 PFLOP/s, the epilogue's additions (256 cycles a block of the FMA
 // pipe, 64 packed FMAs a thread at two cycles, and as many TMEM loads) beside 512 cycles of MMA; full tiles of
-// gate/up (8 experts of 2051 rows, d 4096, f 1024: 160 us, 1.7 PFLOP/s) that and the row gather: 139 us
-// without the gather, 121 without the additions, 95 without both; few rows, latency.
+// gate/up (8 experts of 2051 rows, d 4096, f 1024: 166 us, 1.65 PFLOP/s) that and the row gather: 139 us
+// without the gather's copies, 95 without the additions as well; few rows, latency.
 //
 // Roles (persistent CTAs, one per SM, every role walks the same unit sequence):
 //   warp 0      producer: weights by bulk copy (tile-contiguous, pre-swizzled); rows by TMA
@@ -39,7 +39,7 @@
 //               in groups of four K blocks, up to four groups ahead of the epilogue (which has no
 //               registers to hold them in; with a load one block ahead its latency set the pace)
 //   warps 4-11  epilogue: warps 4-7 the tile's first half, 8-11 the second; TMEM lanes 32 (warp % 4)
-//   warps 12-15 gate/up: cp.async gather of the rows, a quarter of them a warp
+//   warps 12-15 gate/up: cp.async gather of the rows, one warp per stage slot
 // Registers move from the first (and the gather) warps to the epilogue warps, which hold 128 sums a
 // thread.  TMEM: two buffers of 256 columns, so one block's MMAs overlap the previous block's sums.
 // Rows of a tile beyond the segment's are never copied: whatever the slot held lands in lanes that
@@ -60,7 +60,7 @@ constexpr int kABytes = BM * kF8Block;
 constexpr int kStageBytes = kABytes + kBBytes;    // 48 KB
 constexpr int kAccCols = 256;
 constexpr int kTmemCols = 2 * kAccCols;
-constexpr int kEpiWarps = 8, kFirstEpi = 4, kFirstGather = 12, kGatherWarps = 4;
+constexpr int kEpiWarps = 8, kFirstEpi = 4, kFirstGather = 12;
 constexpr int kRing = 4;                          // decoded units
 constexpr uint32_t kSpinLimit = 1u << 20;         // tries of an epilogue wait: 1.4 s at 1.3 us a try
 constexpr int kScGroups = 4;                      // groups of four K blocks of scales
@@ -89,7 +89,7 @@ struct Cfg {
   static constexpr int kRegsEpi = kMode == kGateUp ? 200 : 216;
   static constexpr int kRegsRest = kMode == kGateUp ? 56 : 72;
   // warps that read each unit record: producer, MMA, scales, epilogue, gather
-  static constexpr int kReaders = 3 + kEpiWarps + (kMode == kGateUp ? kGatherWarps : 0);
+  static constexpr int kReaders = 3 + kEpiWarps + (kMode == kGateUp ? kStages : 0);
 };
 
 struct Unit {
@@ -132,8 +132,7 @@ MOE_DEVICE Unit decode_unit(int u, const F8Args& a, int tiles) {
 // back, in turns (total: none is left).  Experts with many rows keep the epilogue busy (their parts share
 // weights through L2), experts with few rows the memory; where popularity follows the expert index,
 // front to back would run one kind after the other (Zipf layer, T = 2051: 488 us, and
-// 462 from both ends).  Neighbouring
-// units still run side by side.  An odd grid goes front to back.
+// 462 from both ends).  Neighbouring units still run side by side.  An odd grid goes front to back.
 MOE_DEVICE int mixed_unit(int step, int total) {
   if (gridDim.x & 1) return min(static_cast<int>(blockIdx.x + step * gridDim.x), total);
   const int o = step * static_cast<int>(gridDim.x / 2) + static_cast<int>(blockIdx.x / 2);
@@ -380,7 +379,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], kMode == kGateUp ? 1 + kGatherWarps : 1);
+      mbar_init(&full[s], kMode == kGateUp ? 2 : 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -706,47 +705,42 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg<kMode>::kRegsRest));
     // ---------------- gate/up: row gather (cp.async) ----------------
-    // Every warp copies a quarter of each stage's rows (8 consecutive lanes one row's 128 bytes, a lane 8
-    // rows, whose addresses it holds for the unit).  A stage's copies are waited for, fenced for the tensor
-    // core and announced kLag stages later, so up to three stages' are in flight and MMAs of the stage
-    // before never wait for the issue.  (Every warp a whole stage of its own, its addresses read per
-    // row and its copies waited for at once: 167 us instead of 160 for 8 experts of 2051 rows, and 145 instead
-    // of 121 without the additions.  TMA gathers of four rows: 329 us, about 85 cycles each from one warp.)
-    constexpr uint32_t kLag = 2;
-    static_assert(kMode != kGateUp || (kLag + 1 < kStages && kLag < kRing), "announced before the slot is waited for again");
-    const int n0 = 4 * (warp - kFirstGather) + (lane >> 3), ch = lane & 7;
-    const uint32_t dst0 = smem_u32(smem) + kBBytes + n0 * kF8Block + ((ch ^ (n0 & 7)) << 4);
+    // Warp w owns stage slot w: it fills every stage g with g % kStages == w, waits for its own copies, fences
+    // them for the tensor core and arrives.  8 consecutive lanes copy one row's 128 bytes; the addresses of 8
+    // rows a lane are formed before their copies, so that the reads of the row table overlap.  (One row
+    // after the other: Zipf layer 460 us instead of 452.  A quarter of each stage a warp, announced two stages
+    // later: 452, but 2% more for a decode step.  TMA gathers of four rows, about 85 cycles each: 587.)
+    const int slot = warp - kFirstGather;
+    const int ch = lane & 7, nl = lane >> 3;
+    const uint32_t d0 = smem_u32(smem + slot * kStageBytes + kBBytes) + nl * 128;
+    const uint32_t dx[2] = {d0 + ((ch ^ nl) << 4), d0 + ((ch ^ (nl + 4)) << 4)};
     const uint64_t pol_x = l2_policy_evict_last();
     uint32_t g = 0;
     bool ok = true;
     for (uint32_t j = 0; ok; ++j) {
       const Unit un = ring.get(j);
       if (un.rows == 0) break;
-      const uint8_t* src[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        src[i] = a.a + static_cast<size_t>(tok_tab[BM * (j % kRing) + min(n0 + 16 * i, un.rows - 1)]) * a.lda + ch * 16;
-      ring.done(j);
+      const int32_t* tok = tok_tab + BM * (j % kRing);
       for (int kb = kb0; kb < kb1; ++kb, ++g) {
-        const uint32_t slot = g % kStages;
+        if (static_cast<int>(g % kStages) != slot) continue;
         if (!(ok = mbar_wait_warp(&empty[slot], ((g / kStages) & 1u) ^ 1u, abort_flag, a.err))) break;
+        const uint8_t* base = a.a + kb * kF8Block + ch * 16;
+        for (int n = nl; n < un.rows; n += 4 * 8) {
+          const uint8_t* src[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n0 + 16 * i < un.rows)
-            cp_async_16_hint(dst0 + slot * kStageBytes + 16 * i * kF8Block, src[i] + kb * kF8Block, pol_x);
-        cp_async_commit();
-        if (g >= kLag) {
-          cp_async_wait<kLag>();
-          fence_proxy_async_smem();
-          __syncwarp();
-          mbar_arrive_lane0(&full[(g - kLag) % kStages]);
+          for (int i = 0; i < 8; ++i) src[i] = base + static_cast<size_t>(tok[min(n + 4 * i, un.rows - 1)]) * a.lda;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n + 4 * i < un.rows) cp_async_16_hint(dx[i & 1] + (n - nl + 4 * i) * 128, src[i], pol_x);
         }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        mbar_arrive_lane0(&full[slot]);
       }
+      ring.done(j);
     }
-    cp_async_wait<0>();
-    fence_proxy_async_smem();
-    __syncwarp();
-    for (uint32_t i = g > kLag ? g - kLag : 0; i < g; ++i) mbar_arrive_lane0(&full[i % kStages]);
   }
 
   if (kMode == kSplit) {
