@@ -7,6 +7,9 @@
 //       keep the `keep` best, key_e = -inf in the others
 //     the k largest keys, in order;  w = s (0 where the key is -inf);  w / (sum w + 1e-20) if renorm;
 //       times scale
+// A softmax over a NaN would make every score NaN, and masked experts, whose key is a number, would rank
+// first.  So NaN logits keep a score of NaN of their own and stay out of the sum, +inf ones share the score
+// 1 as in the limit, and the error bit says so whichever experts are chosen.
 // Every order is the total order of rank_key: larger first, lower index on ties, NaN below -inf.  All in
 // fp32 with expf and reciprocals good to 1 ulp: the scores are within a few units in the last place.
 #pragma once
@@ -37,7 +40,11 @@ MOE_DEVICE int score_select(const float (&v)[PL], int t, int E, int k, int32_t* 
   bool odd = false;  // some logit of the token is NaN or +inf
   if (sa.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] = rcp_approx(1.0f + expf(-v[i]));
+    for (int i = 0; i < PL; ++i) {
+      s[i] = rcp_approx(1.0f + expf(-v[i]));
+      odd |= lane + 32 * i < E && !(v[i] < kInf);
+    }
+    odd = __any_sync(0xffffffffu, odd);
   } else {
     float m = -kInf;
 #pragma unroll
@@ -54,16 +61,24 @@ MOE_DEVICE int score_select(const float (&v)[PL], int t, int E, int k, int32_t* 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float r = sum > 0.f ? __frcp_rn(sum) : (sum != sum ? sum : 0.f);
+    odd = sum != sum;  // exp(NaN), or inf - inf
+    if (odd) {  // again without the NaN logits, inf - inf as 0
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < PL; ++i) {
+        if (lane + 32 * i < E && v[i] == m) s[i] = 1.f;
+        sum += s[i] == s[i] ? s[i] : 0.f;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    const float r = sum > 0.f ? __frcp_rn(sum) : 0.f;
 #pragma unroll
     for (int i = 0; i < PL; ++i) s[i] *= r;
   }
   // keys (rank_key order): 1 a padding lane, 2 NaN, above them the values
   const uint32_t none = rank_key(-kInf);
   uint32_t key[PL];
-#pragma unroll
-  for (int i = 0; i < PL; ++i) odd |= lane + 32 * i < E && !(v[i] < kInf);
-  odd = __any_sync(0xffffffffu, odd);
   if (!odd && !sa.bias) {  // scores are numbers >= 0: their bits are in order
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
@@ -168,14 +183,15 @@ MOE_DEVICE int score_select(const float (&v)[PL], int t, int E, int k, int32_t* 
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     w = __fdiv_rn(w, sum + 1e-20f);
   }
-  if (odd) {  // flagged if one of them was chosen
+  if (odd) {  // flagged: with sigmoid scores, which stand alone, if one of them was chosen
     float l = 0.f;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
       const float li = __shfl_sync(0xffffffffu, v[i], sel_e & 31);
       if (i == (sel_e >> 5)) l = li;
     }
-    if (__any_sync(0xffffffffu, lane < k && !(l < kInf)) && lane == 0) set_error(err, MOE_DEVERR_NONFINITE);
+    if (__any_sync(0xffffffffu, !sa.sigmoid || (lane < k && !(l < kInf))) && lane == 0)
+      set_error(err, MOE_DEVERR_NONFINITE);
   }
   if (lane < k) {
     ids[static_cast<size_t>(t) * k + lane] = sel_e;

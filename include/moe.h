@@ -180,8 +180,10 @@ moe_status moe_plan_set_path(moe_plan* plan, moe_path path);
  *     (1 or 2) largest keys, and the experts outside the topk_groups best get key -inf;
  *   ids: the k largest keys in order; weights w = s of those (0 where the key is -inf),
  *     w / (sum of w + 1e-20) with renormalize, times scale.
- * Orders are (value desc, index asc; +0 == -0; NaN lowest), all arithmetic fp32.  A selected logit
- * that is NaN or +inf sets MOE_DEVERR_NONFINITE.  Softmax scores, one group, renormalize, scale 1
+ * Orders are (value desc, index asc; +0 == -0; NaN lowest), all arithmetic fp32.  With sigmoid scores a
+ * selected logit that is NaN or +inf sets MOE_DEVERR_NONFINITE; with softmax scores any such logit of the
+ * token does, selected or not: a NaN logit's score is NaN and is left out of the sum, logits of +inf
+ * share the score 1.  Softmax scores, one group, renormalize, scale 1
  * and no bias weigh like the default up to rounding; NULL restores the default (the softmax of the
  * k largest logits).  bias: device fp32 [E] or NULL, copied into plan memory (synchronous when given).
  * n_groups divides E, 1 <= n_groups <= 32, 1 <= topk_groups <= n_groups with topk_groups * E / n_groups
