@@ -282,7 +282,11 @@ MOE_DEVICE void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* 
 MOE_DEVICE void cp_async_16(uint32_t dst_smem, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
 }
-// Same with an L2 cache-eviction policy (e.g. evict_last for activations re-read by many CTAs).
+// 16 bytes of which only the first `bytes` are read; the rest become zero.
+MOE_DEVICE void cp_async_16_part(uint32_t dst_smem, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(bytes) : "memory");
+}
+// Same as cp_async_16 with an L2 cache-eviction policy (e.g. evict_last for activations re-read by many CTAs).
 MOE_DEVICE void cp_async_16_hint(uint32_t dst_smem, const void* src, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "l"(policy)
                : "memory");

@@ -570,9 +570,10 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
           const int slot = c % kScGroups;
           if (!(ok = mbar_wait_warp(&sc_empty[slot], ((c / kScGroups) & 1u) ^ 1u, abort_flag, a.err))) break;
           const uint32_t dst = smem_u32(sc_tab + slot * kScGroupBytes);
+          const uint32_t bytes = 4u * min(4, nk - 4 * gi);  // a row may end with its last block's scale
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (32 * i < un.rows) cp_async_16(dst + (lane + 32 * i) * 16, row[i] + 4 * gi);
+            if (32 * i < un.rows) cp_async_16_part(dst + (lane + 32 * i) * 16, row[i] + 4 * gi, bytes);
           if (lane < 2) cp_async_16(dst + BM * 16 + 16 * lane, sw + 8 * gi);
           cp_async_arrive(&sc_full[slot]);
         }

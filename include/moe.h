@@ -420,7 +420,8 @@ moe_status moe_quantize_blocks(const void* w, moe_dtype w_dtype, int rows, int K
  *                               multiplied; out [T][N] (pitch ldo) in out_dtype, MOE_BF16 or MOE_FP32.
  *   moe_linear_forward_quantized   the same for rows that are already codes (pitch ldq, a multiple
  *                               of 16, 16-byte aligned) with their scales (pitch lds, a multiple of 4,
- *                               16-byte aligned); columns beyond K are not read; needs no workspace.
+ *                               16-byte aligned); neither columns beyond K nor scales beyond
+ *                               ceil(K / 128) are read; needs no workspace.
  *   moe_linear_get_device_error    as moe_plan_get_device_error, for the handle's calls.
  * The forward calls only enqueue work, and a NULL or not-ready handle, T < 0 or T > T_max, a pitch
  * below the width or an unknown type is an error before any launch.
