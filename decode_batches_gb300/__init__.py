@@ -12,6 +12,7 @@ if the library is not built, importing a plan raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -170,6 +171,16 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+_here = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Context in which a call for `stream` allocates and fills its own tensors: memory that this
+    stream uses, in the order of its work.  (The current stream's pool could hand out memory that work
+    queued there still reads.)"""
+    return _here if stream is None else torch.cuda.stream(stream)
+
+
 def _rows(t: torch.Tensor, name: str, dtypes, width: int):
     """(pointer, row pitch in elements) of a 2-D CUDA tensor [rows][width] whose rows are dense."""
     if not t.is_cuda:
@@ -203,8 +214,9 @@ def quantize_fp8(x: torch.Tensor, stream=None):
         raise ValueError("x must have at least one column")
     px, ldx = _rows(x, "x", DTYPES, K)
     nb = _blocks(K)
-    q = torch.empty((T, nb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
-    s = torch.empty((T, (nb + 3) // 4 * 4), dtype=torch.float32, device=x.device)
+    with _on(stream):
+        q = torch.empty((T, nb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
+        s = torch.empty((T, (nb + 3) // 4 * 4), dtype=torch.float32, device=x.device)
     _check(lib.moe_quantize_rows(px, DTYPES[x.dtype], ldx, T, K, _ptr(q), q.shape[1], _ptr(s), s.shape[1],
                                  _stream(stream)))
     return q[:, :K], s[:, :nb]
@@ -219,9 +231,10 @@ def quantize_fp8_weight(w: torch.Tensor, stream=None):
     if not w.is_cuda or w.dtype not in DTYPES:
         raise ValueError("w must be a CUDA tensor of bf16, fp16 or fp32")
     rows, K = w.shape[-2:]
-    w = w.contiguous()
-    q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
-    s = torch.empty((*w.shape[:-2], _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
+    with _on(stream):
+        w = w.contiguous()
+        q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
+        s = torch.empty((*w.shape[:-2], _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
     for wm, qm, sm in zip(w.view(-1, rows, K), q.view(-1, rows, K), s.view(-1, s.shape[-2], s.shape[-1])):
         _check(lib.moe_quantize_blocks(_ptr(wm), DTYPES[w.dtype], rows, K, _ptr(qm), _ptr(sm), _stream(stream)))
     return q, s
@@ -272,11 +285,12 @@ class Fp8Linear:
         self.set_workspace(buf, T_max)
         return buf
 
-    def _out(self, T, out, out_dtype, device):
+    def _out(self, T, out, out_dtype, device, stream):
         if out is None:
             if out_dtype not in (torch.bfloat16, torch.float32):
                 raise ValueError(f"out must be bf16 or fp32, got {out_dtype}")
-            out = torch.empty((T, self.N), dtype=out_dtype, device=device)
+            with _on(stream):
+                out = torch.empty((T, self.N), dtype=out_dtype, device=device)
             return out, out.data_ptr(), self.N
         if out.shape[0] != T:
             raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
@@ -286,7 +300,7 @@ class Fp8Linear:
         """x [T][K] (bf16, fp16 or fp32; rows may have a pitch) -> [T][N] in bf16 or fp32."""
         px, ldx = _rows(x, "x", DTYPES, self.K)
         T = x.shape[0]
-        out, po, ldo = self._out(T, out, out_dtype, x.device)
+        out, po, ldo = self._out(T, out, out_dtype, x.device, stream)
         _check(self.lib.moe_linear_forward(self._h, px, DTYPES[x.dtype], ldx, T, po, DTYPES[out.dtype], ldo, _stream(stream)))
         return out
 
@@ -300,7 +314,7 @@ class Fp8Linear:
             raise ValueError(f"s must have {T} rows, got {s.shape[0]}")
         if T == 1:  # a single row: its pitch may be anything; only its padding to the vector width matters
             ldq, lds = (ldq + 15) // 16 * 16, (lds + 3) // 4 * 4
-        out, po, ldo = self._out(T, out, out_dtype, q.device)
+        out, po, ldo = self._out(T, out, out_dtype, q.device, stream)
         _check(self.lib.moe_linear_forward_quantized(self._h, pq, ldq, ps, lds, T, po, DTYPES[out.dtype], ldo,
                                                      _stream(stream)))
         return out
@@ -395,7 +409,8 @@ class MoePlan:
     def forward(self, x: torch.Tensor, n_prefill: int = 0, out: Optional[torch.Tensor] = None, stream=None):
         T = x.shape[0]
         if out is None:
-            out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
+            with _on(stream):
+                out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
         _check(self.lib.moe_layer_forward(self._h, _dev(x, "x", torch.bfloat16, (T, self.d)), T, n_prefill,
                                           _dev(out, "out", torch.bfloat16, (T, self.d)), _stream(stream)))
         return out
@@ -405,7 +420,8 @@ class MoePlan:
         """The layer for given ids and gates [T][k] (moe_layer_forward_routed)."""
         T = x.shape[0]
         if out is None:
-            out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
+            with _on(stream):
+                out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
         _check(self.lib.moe_layer_forward_routed(self._h, _dev(x, "x", torch.bfloat16, (T, self.d)), T,
                                                  _dev(ids, "ids", torch.int32, (T, self.k)),
                                                  _dev(gates, "gates", torch.float32, (T, self.k)),
@@ -415,17 +431,19 @@ class MoePlan:
     def route(self, x: torch.Tensor, want_logits: bool = True, stream=None):
         T = x.shape[0]
         dev = x.device
-        logits = torch.empty((T, self.E), dtype=torch.float32, device=dev) if want_logits else None
-        ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
-        gates = torch.empty((T, self.k), dtype=torch.float32, device=dev)
+        with _on(stream):
+            logits = torch.empty((T, self.E), dtype=torch.float32, device=dev) if want_logits else None
+            ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
+            gates = torch.empty((T, self.k), dtype=torch.float32, device=dev)
         _check(self.lib.moe_route(self._h, _dev(x, "x", torch.bfloat16, (T, self.d)), T, _ptr(logits), _ptr(ids),
                                   _ptr(gates), _stream(stream)))
         return logits, ids, gates
 
     def route_logits(self, logits: torch.Tensor, stream=None):
         T, dev = logits.shape[0], logits.device
-        ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
-        gates = torch.empty((T, self.k), dtype=torch.float32, device=dev)
+        with _on(stream):
+            ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
+            gates = torch.empty((T, self.k), dtype=torch.float32, device=dev)
         _check(self.lib.moe_route_logits(self._h, _dev(logits, "logits", torch.float32, (T, self.E)), T, ids.data_ptr(),
                                          gates.data_ptr(), _stream(stream)))
         return ids, gates
@@ -433,18 +451,20 @@ class MoePlan:
     def permute(self, ids: torch.Tensor, stream=None):
         T = ids.shape[0]
         dev = ids.device
-        counts = torch.empty(self.E, dtype=torch.int32, device=dev)
-        offsets = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
-        perm = torch.full((T * self.k,), -1, dtype=torch.int32, device=dev)
-        inv = torch.empty(T * self.k, dtype=torch.int32, device=dev)
+        with _on(stream):
+            counts = torch.empty(self.E, dtype=torch.int32, device=dev)
+            offsets = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
+            perm = torch.full((T * self.k,), -1, dtype=torch.int32, device=dev)
+            inv = torch.empty(T * self.k, dtype=torch.int32, device=dev)
         _check(self.lib.moe_permute(self._h, _dev(ids, "ids", torch.int32, (T, self.k)), T, _ptr(counts), _ptr(offsets),
                                     _ptr(perm), _ptr(inv), _stream(stream)))
         return counts, offsets, perm, inv
 
     def experts(self, x: torch.Tensor, offsets: torch.Tensor, perm: torch.Tensor, stream=None):
         T = x.shape[0]
-        y = torch.empty((T * self.k, self.d), dtype=torch.float16, device=x.device)
-        ys = torch.empty((T, self.d), dtype=torch.float16, device=x.device) if self.n_shared else None
+        with _on(stream):
+            y = torch.empty((T * self.k, self.d), dtype=torch.float16, device=x.device)
+            ys = torch.empty((T, self.d), dtype=torch.float16, device=x.device) if self.n_shared else None
         _check(self.lib.moe_experts(self._h, _dev(x, "x", torch.bfloat16, (T, self.d)), T,
                                     _dev(offsets, "offsets", torch.int32, (self.E + 1,)),
                                     _dev(perm, "perm", torch.int32, (T * self.k,)), _ptr(y), _ptr(ys), _stream(stream)))
@@ -454,7 +474,8 @@ class MoePlan:
                 out: Optional[torch.Tensor] = None, stream=None):
         T = gates.shape[0]
         if out is None:
-            out = torch.empty((T, self.d), dtype=torch.bfloat16, device=y.device)
+            with _on(stream):
+                out = torch.empty((T, self.d), dtype=torch.bfloat16, device=y.device)
         _check(self.lib.moe_combine(self._h, _dev(y, "y", torch.float32, (T * self.k, self.d)),
                                     _dev(gates, "gates", torch.float32, (T, self.k)),
                                     _dev(inv, "inv", torch.int32, (T * self.k,)),
