@@ -12,7 +12,6 @@ if the library is not built, importing a plan raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -158,27 +157,18 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
     return _ptr(t)
 
 
+# A call that is given a stream runs under it (torch.cuda.stream), so that what it allocates, fills or
+# copies lies in memory that this stream uses, in the order of its work: the current stream's pool could
+# hand out memory that work queued there still reads.
 # The current stream's handle without a Stream object around it (3 us of a small call's host time on
 # a Grace core), where this torch has the call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
+def _stream():
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
-
-
-_here = contextlib.nullcontext()
-
-
-def _on(stream):
-    """Context in which a call for `stream` allocates and fills its own tensors: memory that this
-    stream uses, in the order of its work.  (The current stream's pool could hand out memory that work
-    queued there still reads.)"""
-    return _here if stream is None else torch.cuda.stream(stream)
 
 
 def _rows(t: torch.Tensor, name: str, dtypes, width: int):
@@ -206,6 +196,9 @@ def quantize_fp8(x: torch.Tensor, stream=None):
     """Rows x [T][K] (bf16, fp16 or fp32, any row pitch) as e4m3 codes [T][K] and fp32 scales
     [T][ceil(K/128)] of 1 x 128 blocks (moe_quantize_rows).  Both are views of padded rows, as
     ``Fp8Linear.forward_quantized`` takes them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_fp8(x)
     lib = load_library()
     if x.dim() != 2:
         raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
@@ -214,29 +207,30 @@ def quantize_fp8(x: torch.Tensor, stream=None):
         raise ValueError("x must have at least one column")
     px, ldx = _rows(x, "x", DTYPES, K)
     nb = _blocks(K)
-    with _on(stream):
-        q = torch.empty((T, nb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
-        s = torch.empty((T, (nb + 3) // 4 * 4), dtype=torch.float32, device=x.device)
+    q = torch.empty((T, nb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=x.device)
+    s = torch.empty((T, (nb + 3) // 4 * 4), dtype=torch.float32, device=x.device)
     _check(lib.moe_quantize_rows(px, DTYPES[x.dtype], ldx, T, K, _ptr(q), q.shape[1], _ptr(s), s.shape[1],
-                                 _stream(stream)))
+                                 _stream()))
     return q[:, :K], s[:, :nb]
 
 
 def quantize_fp8_weight(w: torch.Tensor, stream=None):
     """A weight [..., rows, K] as e4m3 codes of the same shape and fp32 scales
     [..., ceil(rows/128), ceil(K/128)] of 128 x 128 blocks (moe_quantize_blocks, a call per matrix)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_fp8_weight(w)
     lib = load_library()
     if w.dim() < 2 or w.shape[-1] < 1:
         raise ValueError(f"w must be a matrix or a batch of matrices, got {tuple(w.shape)}")
     if not w.is_cuda or w.dtype not in DTYPES:
         raise ValueError("w must be a CUDA tensor of bf16, fp16 or fp32")
     rows, K = w.shape[-2:]
-    with _on(stream):
-        w = w.contiguous()
-        q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
-        s = torch.empty((*w.shape[:-2], _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
+    w = w.contiguous()
+    q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
+    s = torch.empty((*w.shape[:-2], _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
     for wm, qm, sm in zip(w.view(-1, rows, K), q.view(-1, rows, K), s.view(-1, s.shape[-2], s.shape[-1])):
-        _check(lib.moe_quantize_blocks(_ptr(wm), DTYPES[w.dtype], rows, K, _ptr(qm), _ptr(sm), _stream(stream)))
+        _check(lib.moe_quantize_blocks(_ptr(wm), DTYPES[w.dtype], rows, K, _ptr(qm), _ptr(sm), _stream()))
     return q, s
 
 
@@ -285,12 +279,11 @@ class Fp8Linear:
         self.set_workspace(buf, T_max)
         return buf
 
-    def _out(self, T, out, out_dtype, device, stream):
+    def _out(self, T, out, out_dtype, device):
         if out is None:
             if out_dtype not in (torch.bfloat16, torch.float32):
                 raise ValueError(f"out must be bf16 or fp32, got {out_dtype}")
-            with _on(stream):
-                out = torch.empty((T, self.N), dtype=out_dtype, device=device)
+            out = torch.empty((T, self.N), dtype=out_dtype, device=device)
             return out, out.data_ptr(), self.N
         if out.shape[0] != T:
             raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
@@ -298,15 +291,21 @@ class Fp8Linear:
 
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None):
         """x [T][K] (bf16, fp16 or fp32; rows may have a pitch) -> [T][N] in bf16 or fp32."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, out, out_dtype)
         px, ldx = _rows(x, "x", DTYPES, self.K)
         T = x.shape[0]
-        out, po, ldo = self._out(T, out, out_dtype, x.device, stream)
-        _check(self.lib.moe_linear_forward(self._h, px, DTYPES[x.dtype], ldx, T, po, DTYPES[out.dtype], ldo, _stream(stream)))
+        out, po, ldo = self._out(T, out, out_dtype, x.device)
+        _check(self.lib.moe_linear_forward(self._h, px, DTYPES[x.dtype], ldx, T, po, DTYPES[out.dtype], ldo, _stream()))
         return out
 
     def forward_quantized(self, q: torch.Tensor, s: torch.Tensor, out: Optional[torch.Tensor] = None,
                           out_dtype=torch.bfloat16, stream=None):
         """The same for rows that ``quantize_fp8`` already quantised (several projections of one x)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward_quantized(q, s, out, out_dtype)
         pq, ldq = _rows(q, "q", (torch.float8_e4m3fn,), self.K)
         ps, lds = _rows(s, "s", (torch.float32,), _blocks(self.K))
         T = q.shape[0]
@@ -314,9 +313,9 @@ class Fp8Linear:
             raise ValueError(f"s must have {T} rows, got {s.shape[0]}")
         if T == 1:  # a single row: its pitch may be anything; only its padding to the vector width matters
             ldq, lds = (ldq + 15) // 16 * 16, (lds + 3) // 4 * 4
-        out, po, ldo = self._out(T, out, out_dtype, q.device, stream)
+        out, po, ldo = self._out(T, out, out_dtype, q.device)
         _check(self.lib.moe_linear_forward_quantized(self._h, pq, ldq, ps, lds, T, po, DTYPES[out.dtype], ldo,
-                                                     _stream(stream)))
+                                                     _stream()))
         return out
 
     def device_error(self) -> int:
@@ -407,80 +406,94 @@ class MoePlan:
 
     # ---- step ---------------------------------------------------------------------------------
     def forward(self, x: torch.Tensor, n_prefill: int = 0, out: Optional[torch.Tensor] = None, stream=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, n_prefill, out)
         T = x.shape[0]
         if out is None:
-            with _on(stream):
-                out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
+            out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
         _check(self.lib.moe_layer_forward(self._h, _dev(x, "x", torch.bfloat16, (T, self.d)), T, n_prefill,
-                                          _dev(out, "out", torch.bfloat16, (T, self.d)), _stream(stream)))
+                                          _dev(out, "out", torch.bfloat16, (T, self.d)), _stream()))
         return out
 
     def forward_routed(self, x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor,
                        out: Optional[torch.Tensor] = None, stream=None):
         """The layer for given ids and gates [T][k] (moe_layer_forward_routed)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward_routed(x, ids, gates, out)
         T = x.shape[0]
         if out is None:
-            with _on(stream):
-                out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
+            out = torch.empty((T, self.d), dtype=torch.bfloat16, device=x.device)
         _check(self.lib.moe_layer_forward_routed(self._h, _dev(x, "x", torch.bfloat16, (T, self.d)), T,
                                                  _dev(ids, "ids", torch.int32, (T, self.k)),
                                                  _dev(gates, "gates", torch.float32, (T, self.k)),
-                                                 _dev(out, "out", torch.bfloat16, (T, self.d)), _stream(stream)))
+                                                 _dev(out, "out", torch.bfloat16, (T, self.d)), _stream()))
         return out
 
     def route(self, x: torch.Tensor, want_logits: bool = True, stream=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.route(x, want_logits)
         T = x.shape[0]
         dev = x.device
-        with _on(stream):
-            logits = torch.empty((T, self.E), dtype=torch.float32, device=dev) if want_logits else None
-            ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
-            gates = torch.empty((T, self.k), dtype=torch.float32, device=dev)
+        logits = torch.empty((T, self.E), dtype=torch.float32, device=dev) if want_logits else None
+        ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
+        gates = torch.empty((T, self.k), dtype=torch.float32, device=dev)
         _check(self.lib.moe_route(self._h, _dev(x, "x", torch.bfloat16, (T, self.d)), T, _ptr(logits), _ptr(ids),
-                                  _ptr(gates), _stream(stream)))
+                                  _ptr(gates), _stream()))
         return logits, ids, gates
 
     def route_logits(self, logits: torch.Tensor, stream=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.route_logits(logits)
         T, dev = logits.shape[0], logits.device
-        with _on(stream):
-            ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
-            gates = torch.empty((T, self.k), dtype=torch.float32, device=dev)
+        ids = torch.empty((T, self.k), dtype=torch.int32, device=dev)
+        gates = torch.empty((T, self.k), dtype=torch.float32, device=dev)
         _check(self.lib.moe_route_logits(self._h, _dev(logits, "logits", torch.float32, (T, self.E)), T, ids.data_ptr(),
-                                         gates.data_ptr(), _stream(stream)))
+                                         gates.data_ptr(), _stream()))
         return ids, gates
 
     def permute(self, ids: torch.Tensor, stream=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.permute(ids)
         T = ids.shape[0]
         dev = ids.device
-        with _on(stream):
-            counts = torch.empty(self.E, dtype=torch.int32, device=dev)
-            offsets = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
-            perm = torch.full((T * self.k,), -1, dtype=torch.int32, device=dev)
-            inv = torch.empty(T * self.k, dtype=torch.int32, device=dev)
+        counts = torch.empty(self.E, dtype=torch.int32, device=dev)
+        offsets = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
+        perm = torch.full((T * self.k,), -1, dtype=torch.int32, device=dev)
+        inv = torch.empty(T * self.k, dtype=torch.int32, device=dev)
         _check(self.lib.moe_permute(self._h, _dev(ids, "ids", torch.int32, (T, self.k)), T, _ptr(counts), _ptr(offsets),
-                                    _ptr(perm), _ptr(inv), _stream(stream)))
+                                    _ptr(perm), _ptr(inv), _stream()))
         return counts, offsets, perm, inv
 
     def experts(self, x: torch.Tensor, offsets: torch.Tensor, perm: torch.Tensor, stream=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.experts(x, offsets, perm)
         T = x.shape[0]
-        with _on(stream):
-            y = torch.empty((T * self.k, self.d), dtype=torch.float16, device=x.device)
-            ys = torch.empty((T, self.d), dtype=torch.float16, device=x.device) if self.n_shared else None
+        y = torch.empty((T * self.k, self.d), dtype=torch.float16, device=x.device)
+        ys = torch.empty((T, self.d), dtype=torch.float16, device=x.device) if self.n_shared else None
         _check(self.lib.moe_experts(self._h, _dev(x, "x", torch.bfloat16, (T, self.d)), T,
                                     _dev(offsets, "offsets", torch.int32, (self.E + 1,)),
-                                    _dev(perm, "perm", torch.int32, (T * self.k,)), _ptr(y), _ptr(ys), _stream(stream)))
+                                    _dev(perm, "perm", torch.int32, (T * self.k,)), _ptr(y), _ptr(ys), _stream()))
         return y, ys
 
     def combine(self, y: torch.Tensor, gates: torch.Tensor, inv: torch.Tensor, shared_y: Optional[torch.Tensor] = None,
                 out: Optional[torch.Tensor] = None, stream=None):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.combine(y, gates, inv, shared_y, out)
         T = gates.shape[0]
         if out is None:
-            with _on(stream):
-                out = torch.empty((T, self.d), dtype=torch.bfloat16, device=y.device)
+            out = torch.empty((T, self.d), dtype=torch.bfloat16, device=y.device)
         _check(self.lib.moe_combine(self._h, _dev(y, "y", torch.float32, (T * self.k, self.d)),
                                     _dev(gates, "gates", torch.float32, (T, self.k)),
                                     _dev(inv, "inv", torch.int32, (T * self.k,)),
                                     _dev(shared_y, "shared_y", torch.float32, (T, self.d)), T,
-                                    _dev(out, "out", torch.bfloat16, (T, self.d)), _stream(stream)))
+                                    _dev(out, "out", torch.bfloat16, (T, self.d)), _stream()))
         return out
 
     # ---- diagnostics ----------------------------------------------------------------------------
