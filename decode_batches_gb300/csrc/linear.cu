@@ -37,6 +37,9 @@ static bool known(moe_dtype t) { return t == MOE_BF16 || t == MOE_FP16 || t == M
 static size_t elem_bytes(moe_dtype t) { return t == MOE_FP32 ? 4 : 2; }
 static bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// Rows and columns a call takes: an index past the end of a partial block or tile stays below 2^31.
+constexpr int kMaxLen = 0x7fffffff - 2047;
+
 static int current_sms() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
@@ -48,6 +51,7 @@ extern "C" moe_status moe_quantize_rows(const void* x, moe_dtype x_dtype, int64_
                                         int64_t ldq, float* s, int64_t lds, moe_stream_t stream) {
   if (T < 0 || K < 1) return bad(MOE_ERR_INVALID_ARG, "T must be >= 0 and K >= 1");
   if (!known(x_dtype)) return bad(MOE_ERR_INVALID_ARG, "unknown element type");
+  if (K > kMaxLen) return bad(MOE_ERR_UNSUPPORTED, "at most 2^31 - 2048 columns");
   if (T == 0) return MOE_OK;
   if (!x || !q || !s) return bad(MOE_ERR_INVALID_ARG, "x, q and s are required");
   const int64_t nb = (K + kF8Block - 1) / kF8Block;
@@ -63,6 +67,7 @@ extern "C" moe_status moe_quantize_blocks(const void* w, moe_dtype w_dtype, int 
                                           moe_stream_t stream) {
   if (rows < 0 || K < 1) return bad(MOE_ERR_INVALID_ARG, "rows must be >= 0 and K >= 1");
   if (!known(w_dtype)) return bad(MOE_ERR_INVALID_ARG, "unknown element type");
+  if (K > kMaxLen) return bad(MOE_ERR_UNSUPPORTED, "at most 2^31 - 2048 columns");
   if (rows == 0) return MOE_OK;
   if (!w || !q || !s) return bad(MOE_ERR_INVALID_ARG, "w, q and s are required");
   if (rows > 65535 * kF8Block) return bad(MOE_ERR_UNSUPPORTED, "at most 8388480 rows a call");
@@ -126,6 +131,7 @@ extern "C" size_t moe_linear_workspace_bytes(const moe_linear* l, int T_max) {
 extern "C" moe_status moe_linear_set_workspace(moe_linear* l, void* dev_ptr, size_t bytes, int T_max) {
   if (!l) return bad(MOE_ERR_INVALID_ARG, "the handle is NULL");
   if (!dev_ptr || T_max < 1) return bad(MOE_ERR_INVALID_ARG, "workspace pointer and T_max >= 1 required");
+  if (T_max > kMaxLen) return bad(MOE_ERR_UNSUPPORTED, "at most 2^31 - 2048 rows");
   if (!aligned(dev_ptr, 256)) return bad(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   if (bytes < moe_linear_workspace_bytes(l, T_max)) return bad(MOE_ERR_WORKSPACE, "workspace too small for T_max");
   l->ws_ptr = static_cast<uint8_t*>(dev_ptr);
@@ -136,6 +142,7 @@ extern "C" moe_status moe_linear_set_workspace(moe_linear* l, void* dev_ptr, siz
 static moe_status check_out(const moe_linear* l, int T, const void* out, moe_dtype out_dtype, int64_t ldo) {
   if (!l) return bad(MOE_ERR_INVALID_ARG, "the handle is NULL");
   if (T < 0) return bad(MOE_ERR_INVALID_ARG, "T must be >= 0");
+  if (T > kMaxLen) return bad(MOE_ERR_UNSUPPORTED, "at most 2^31 - 2048 rows");
   if (!l->weights_set) return bad(MOE_ERR_NOT_READY, "weights not set");
   if (out_dtype != MOE_BF16 && out_dtype != MOE_FP32) return bad(MOE_ERR_INVALID_ARG, "out must be bf16 or fp32");
   if (T == 0) return MOE_OK;

@@ -399,7 +399,7 @@ moe_status moe_compose_prefill(int64_t start_pos, int64_t n_tokens, int32_t quan
  *   columns from K to the end of the last block are zeroed), scales fp32 [T][lds], lds >= ceil(K / 128).
  * moe_quantize_blocks: a matrix [rows][K] in blocks of 128 x 128: codes [rows][K] without
  *   padding, scales [ceil(rows / 128)][ceil(K / 128)].
- * Both only enqueue work; codes must be 16-byte aligned.  T == 0 or rows == 0 enqueues nothing.
+ * Both only enqueue work; moe_quantize_rows' codes must be 16-byte aligned; K <= 2^31 - 2048.  T == 0 or rows == 0 enqueues nothing.
  */
 moe_status moe_quantize_rows(const void* x, moe_dtype x_dtype, int64_t ldx, int T, int K, uint8_t* q, int64_t ldq,
                             float* s, int64_t lds, moe_stream_t stream);
@@ -424,7 +424,7 @@ moe_status moe_quantize_blocks(const void* w, moe_dtype w_dtype, int rows, int K
  *                               ceil(K / 128) are read; needs no workspace.
  *   moe_linear_get_device_error    as moe_plan_get_device_error, for the handle's calls.
  * The forward calls only enqueue work, and a NULL or not-ready handle, T < 0 or T > T_max, a pitch
- * below the width or an unknown type is an error before any launch.
+ * below the width or an unknown type is an error before any launch; so are more than 2^31 - 2048 rows.
  */
 typedef struct moe_linear moe_linear; /* opaque */
 
