@@ -229,6 +229,8 @@ def quantize_fp8_weight(w: torch.Tensor, stream=None):
     w = w.contiguous()
     q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
     s = torch.empty((*w.shape[:-2], _blocks(rows), _blocks(K)), dtype=torch.float32, device=w.device)
+    if w.numel() == 0:
+        return q, s
     for wm, qm, sm in zip(w.view(-1, rows, K), q.view(-1, rows, K), s.view(-1, s.shape[-2], s.shape[-1])):
         _check(lib.moe_quantize_blocks(_ptr(wm), DTYPES[w.dtype], rows, K, _ptr(qm), _ptr(sm), _stream()))
     return q, s

@@ -33,3 +33,10 @@ def test_last_row_of_the_scales_may_be_unpadded():
     cut = store.as_strided((T, 5), (8, 1))
     cut.copy_(s)
     check(lin.forward_quantized(q, cut, out_dtype=torch.float32), *quantize_rows_ref(x), wq, ws)
+
+
+@pytest.mark.parametrize("shape", [(0, 128), (0, 5), (3, 0, 130), (0, 64, 130), (0, 0, 7), (2, 0, 3, 9)])
+def test_a_weight_without_rows_has_no_codes(shape):
+    q, s = pkg().quantize_fp8_weight(torch.empty(shape, dtype=torch.bfloat16, device="cuda"))
+    assert q.shape == shape and q.dtype == torch.float8_e4m3fn
+    assert s.shape == (*shape[:-2], blocks(shape[-2]), blocks(shape[-1])) and s.dtype == torch.float32
