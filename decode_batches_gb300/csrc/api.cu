@@ -9,6 +9,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -20,15 +21,13 @@ using namespace moe;
 // ============================================================================================
 // errors
 // ============================================================================================
-static thread_local std::string g_last_error;
+static thread_local char g_last_error[512];  // (no allocation: an error is reported when memory is out, too)
 
 static moe_status fail(moe_status s, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return s;
 }
 
@@ -38,11 +37,10 @@ static moe_status fail(moe_status s, const char* fmt, ...) {
     if (_e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", #expr, cudaGetErrorString(_e)); \
   } while (0)
 
-extern "C" const char* moe_last_error(void) { return g_last_error.c_str(); }
+extern "C" const char* moe_last_error(void) { return g_last_error; }
 
 moe_status moe::fail_message(moe_status s, const char* msg) {
-  g_last_error = msg;
-  return s;
+  return fail(s, "%s", msg);
 }
 
 // ============================================================================================
@@ -239,11 +237,16 @@ struct LaunchScope {
   ~LaunchScope() {
     if (p->timing && start) {
       cudaEvent_t stop = pool_event(p);
-      if (stop) {
-        cudaEventRecord(stop, st);
-        p->timed.push_back(TimedLaunch{name, start, stop});
-      } else {
-        p->event_pool.push_back(start);
+      try {
+        if (stop) {
+          cudaEventRecord(stop, st);
+          p->timed.push_back(TimedLaunch{name, start, stop});
+        } else {
+          p->event_pool.push_back(start);
+        }
+      } catch (...) {  // no memory for the record: the launch goes untimed
+        cudaEventDestroy(start);
+        if (stop) cudaEventDestroy(stop);
       }
     }
   }
@@ -365,7 +368,11 @@ extern "C" moe_plan* moe_plan_create(int E, int k, int d_model, int d_ff, int n_
     fail(MOE_ERR_INVALID_ARG, "n_shared must be in [0, 64] (%d)", n_shared);
     return nullptr;
   }
-  moe_plan* p = new moe_plan();
+  moe_plan* p = new (std::nothrow) moe_plan();
+  if (!p) {
+    fail(MOE_ERR_CUDA, "out of host memory");
+    return nullptr;
+  }
   p->E = E;
   p->k = k;
   p->d = d_model;
@@ -382,7 +389,7 @@ extern "C" moe_plan* moe_plan_create(int E, int k, int d_model, int d_ff, int n_
     if (!strcmp(env, "simt") && weight_dtype != MOE_W_FP8) p->path = MOE_PATH_SIMT;
     else if (!strcmp(env, "tc")) p->path = MOE_PATH_TC;
   }
-  g_last_error.clear();
+  g_last_error[0] = 0;
   return p;
 }
 
@@ -1285,8 +1292,9 @@ extern "C" moe_status moe_plan_enable_timing(moe_plan* p, int enable) {
   return MOE_OK;
 }
 
-extern "C" size_t moe_plan_timing_report(moe_plan* p, char* buf, size_t len) {
+extern "C" size_t moe_plan_timing_report(moe_plan* p, char* buf, size_t len) try {
   if (!p) return 0;
+  p->event_pool.reserve(p->event_pool.size() + 2 * p->timed.size());
   std::map<std::string, std::pair<long, double>> agg;
   std::vector<std::string> order;
   for (auto& t : p->timed) {
@@ -1301,22 +1309,26 @@ extern "C" size_t moe_plan_timing_report(moe_plan* p, char* buf, size_t len) {
       it->second.first += 1;
       it->second.second += ms;
     }
-    p->event_pool.push_back(t.start);
-    p->event_pool.push_back(t.stop);
   }
-  p->timed.clear();
   std::string rep;
   for (auto& n : order) {
     char line[256];
     snprintf(line, sizeof line, "%s %ld %.6f\n", n.c_str(), agg[n].first, agg[n].second);
     rep += line;
   }
+  for (auto& t : p->timed) {
+    p->event_pool.push_back(t.start);
+    p->event_pool.push_back(t.stop);
+  }
+  p->timed.clear();
   if (buf && len > 0) {
     const size_t n = rep.size() < len - 1 ? rep.size() : len - 1;
     memcpy(buf, rep.data(), n);
     buf[n] = '\0';
   }
   return rep.size() + 1;
+} catch (...) {  // no host memory: nothing is reported and the records stay
+  return 0;
 }
 
 extern "C" int moe_plan_last_launch_count(const moe_plan* p) { return p ? p->launch_count : 0; }

@@ -96,7 +96,10 @@ inline cudaError_t ensure_max_dynamic_smem(const void* kern, int bytes) {
   std::lock_guard<std::mutex> lock(mu);
   if (done.count({ctx, kern})) return cudaSuccess;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.insert({ctx, kern});
+  if (e == cudaSuccess) try {
+      done.insert({ctx, kern});
+    } catch (...) {  // no memory for the note: the next call sets it again
+    }
   return e;
 }
 

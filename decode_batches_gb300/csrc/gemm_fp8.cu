@@ -832,7 +832,10 @@ static int split_clusters(int s) {
     cudaGetLastError();
     n = 0;
   }
-  known[{dev, s}] = n;
+  try {
+    known[{dev, s}] = n;
+  } catch (...) {  // no memory for the note: the next call asks again
+  }
   return n;
 }
 

@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <cstdio>
+#include <new>
 
 #include "fp8.cuh"
 #include "kernels.h"
@@ -81,7 +82,11 @@ extern "C" moe_linear* moe_linear_create(int N, int K) {
     bad(MOE_ERR_INVALID_ARG, "need 1 <= N, K <= 2^20");
     return nullptr;
   }
-  moe_linear* l = new moe_linear();
+  moe_linear* l = new (std::nothrow) moe_linear();
+  if (!l) {
+    bad(MOE_ERR_CUDA, "out of host memory");
+    return nullptr;
+  }
   l->N = N;
   l->K = K;
   l->nk = (K + kF8Block - 1) / kF8Block;
