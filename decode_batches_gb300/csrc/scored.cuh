@@ -11,7 +11,8 @@
 // first.  So NaN logits keep a score of NaN of their own and stay out of the sum, +inf ones share the score
 // 1 as in the limit, and the error bit says so whichever experts are chosen.
 // Every order is the total order of rank_key: larger first, lower index on ties, NaN below -inf.  All in
-// fp32 with expf and reciprocals good to 1 ulp: the scores are within a few units in the last place.
+// fp32 with expf (2 ulp) and reciprocals good to 1 ulp.  A sigmoid is within a few units in the last place;
+// a softmax score besides by the rounding of its difference, |l - max| 2^-24 relative, and of the sum.
 #pragma once
 
 #include "topk.cuh"
