@@ -160,7 +160,7 @@ struct Ring {
 };
 
 // Adds 128 columns of one K block, times the scales (s01 the first 64 columns', s23 the rest's), to
-// the thread's sums: 32-column loads, one in flight while the previous one is added.
+// the thread's sums: 16-column loads, one in flight while the previous one is added.
 // The buffer is handed back once the last load is in registers.
 MOE_DEVICE void add_block(uint64_t (&acc)[64], uint32_t taddr, uint64_t s01, uint64_t s23, uint32_t empty) {
   uint32_t r[2][16];
