@@ -440,6 +440,7 @@ static moe_status ensure_err_word(moe_plan* p) {
   if (p->err) return MOE_OK;
   MOE_CUDA_TRY(cudaMalloc(&p->err, kPlanWords * sizeof(uint32_t)));
   MOE_CUDA_TRY(cudaMemset(p->err, 0, kPlanWords * sizeof(uint32_t)));
+  MOE_CUDA_TRY(cudaStreamSynchronize(0));  // (a memset need not be over when it returns, nor precede other streams' work)
   return MOE_OK;
 }
 
@@ -675,6 +676,7 @@ extern "C" moe_status moe_plan_set_workspace(moe_plan* p, void* dev_ptr, size_t 
   if (!p->ls_sync) {
     MOE_CUDA_TRY(cudaMalloc(&p->ls_sync, kLsSyncWords * sizeof(uint32_t)));
     MOE_CUDA_TRY(cudaMemset(p->ls_sync, 0, kLsSyncWords * sizeof(uint32_t)));
+    MOE_CUDA_TRY(cudaStreamSynchronize(0));
   }
   return build_ws_maps(p);
 }
@@ -1282,6 +1284,7 @@ extern "C" moe_status moe_plan_get_device_error(moe_plan* p, uint32_t* code) {
   if (!p->err) return MOE_OK;
   MOE_CUDA_TRY(cudaMemcpy(code, p->err, sizeof(uint32_t), cudaMemcpyDeviceToHost));
   MOE_CUDA_TRY(cudaMemset(p->err, 0, sizeof(uint32_t)));
+  MOE_CUDA_TRY(cudaDeviceSynchronize());  // cleared before a later call, on any stream, sets a bit
   if (*code) return fail(MOE_ERR_DEVICE, "device error bits 0x%x", *code);
   return MOE_OK;
 }

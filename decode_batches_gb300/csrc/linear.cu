@@ -222,5 +222,6 @@ extern "C" moe_status moe_linear_get_device_error(moe_linear* l, uint32_t* code)
   if (!l->err) return MOE_OK;
   LIN_TRY(cudaMemcpy(code, l->err, sizeof(uint32_t), cudaMemcpyDeviceToHost));
   LIN_TRY(cudaMemset(l->err, 0, sizeof(uint32_t)));
+  LIN_TRY(cudaDeviceSynchronize());  // cleared before a later call, on any stream, sets a bit
   return *code ? bad(MOE_ERR_DEVICE, "device error bits are set") : MOE_OK;
 }

@@ -71,3 +71,19 @@ def test_transposed_weight_on_another_stream():
     q, s = beside_busy_work((300, 260), torch.float32, lambda st: pkg().quantize_fp8_weight(wc, stream=st))
     rq, rs = quantize_weight_ref(w)
     assert torch.equal(q.float().cpu(), rq.float()) and torch.equal(s.cpu(), rs)
+
+
+def test_an_error_right_after_the_word_was_read_is_kept():
+    """Reading the error word clears it before the call returns, so a fault on another stream just after it
+    is not cleared away."""
+    from decode_batches_gb300 import DEVERR_EXPERT_RANGE
+    T, E, k, d = 4, 8, 2, 128
+    plan, *_ = make_plan(E, k, d, 128, T)
+    x, gates = random_rows(T, d, 3).cuda(), torch.ones((T, k), device="cuda")
+    bad = torch.full((T, k), E, dtype=torch.int32, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        for _ in range(200):
+            plan.forward_routed(x, bad, gates)
+            assert plan.device_error() == DEVERR_EXPERT_RANGE
