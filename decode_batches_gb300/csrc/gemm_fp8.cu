@@ -23,11 +23,13 @@
 // row parts: CTAs that share a weight tile run side by side and its second read is served by L2.
 //
 // What bounds them, measured on a GB300 (6.78 TB/s copy, 1.94 PFLOP/s bf16): up to about 100 rows an expert
-// the weight stream (256 experts, d 2048, f 512, 2051 tokens x 8: gate/up 94 us at 5.9 TB/s, down 57 us at
-// 5.1 TB/s); 8192 x 4096 x 4096 108 us, 2.5 PFLOP/s, the epilogue's additions (256 cycles a block of the FMA
-// pipe, 64 packed FMAs a thread at two cycles, and as many TMEM loads) beside 512 cycles of MMA; full tiles of
-// gate/up (8 experts of 2051 rows, d 4096, f 1024: 166 us, 1.65 PFLOP/s) that and the row gather: 139 us
-// without the gather's copies, 95 without the additions as well; few rows, latency.
+// the weight stream (256 experts, d 2048, f 512, 2051 tokens x 8: gate/up 91 us at 6.0 TB/s, down 55 us at
+// 5.2 TB/s); 8192 x 4096 x 4096, 111 us, 2.5 PFLOP/s, three things at once: the MMAs (512 cycles a K block), the
+// epilogue's additions (64 packed FMAs a thread at two cycles, and as many TMEM loads) and the operands'
+// way from L2 (48 KB a block, 768 cycles at 64 bytes a cycle).  Without the results' stores any two of them
+// take 89 to 96 us and all three 101; full tiles of gate/up (8 experts of 2051 rows, d 4096, f 1024: 166 us,
+// 1.65 PFLOP/s) the additions and the row gather: 139 us without the gather's copies, 95 without the additions
+// as well; few rows, latency.
 //
 // Roles (persistent CTAs, one per SM, every role walks the same unit sequence):
 //   warp 0      producer: weights by bulk copy (tile-contiguous, pre-swizzled); rows by TMA
@@ -77,8 +79,8 @@ static_assert(BM * kSumPitch <= 3 * kStageBytes, "sums in the stages");
 template <int kMode>
 struct Cfg {
   // linear trades a stage for staging space of whole bf16 results, which TMA stores read while the next
-  // unit is under way (8192 x 4096 x 4096 with the quantisation: 129 us; four stages and row pieces 133;
-  // four stages and boxes of 32 columns through 2 KB, waited for in between, 134; without any stores 120)
+  // unit is under way (8192 x 4096 x 4096 with the quantisation: 126-130 us; four stages and row pieces 133;
+  // four stages and boxes of 32 columns through 2 KB, waited for in between, 134; without any stores 114)
   static constexpr int kStages = kMode == kLinear ? 3 : 4;
   static constexpr int kExtra = kMode == kGateUp ? kTokBytes + kXchBytes : kMode == kLinear ? kEpiWarps * kTmaOutBytes
                                                                                         : kEpiWarps * kOutBytes;
@@ -130,9 +132,12 @@ MOE_DEVICE Unit decode_unit(int u, const F8Args& a, int tiles) {
 
 // The unit of a CTA's step when half of the CTAs go through the list from its front and half from its
 // back, in turns (total: none is left).  Experts with many rows keep the epilogue busy (their parts share
-// weights through L2), experts with few rows the memory; where popularity follows the expert index,
-// front to back would run one kind after the other (Zipf layer, T = 2051: 488 us, and
-// 462 from both ends).  Neighbouring units still run side by side.  An odd grid goes front to back.
+// weights through L2), experts with few rows the memory; where busy experts lie together, front to back
+// would run one kind after the other.  Zipf layer, T = 2051, front to back / from both ends: popularity
+// along the expert index 494 / 460 us, against it 502 / 459; popular experts anywhere (four permutations)
+// 468, 455, 461, 453 / 475, 466, 468, 476.  So this order costs up to 5% where experts are mixed already and
+// saves 7 to 9% where they are not; uniform load is the same.  Neighbouring units still run side by side.
+// An odd grid goes front to back.
 MOE_DEVICE int mixed_unit(int step, int total) {
   if (gridDim.x & 1) return min(static_cast<int>(blockIdx.x + step * gridDim.x), total);
   const int o = step * static_cast<int>(gridDim.x / 2) + static_cast<int>(blockIdx.x / 2);
@@ -244,9 +249,8 @@ MOE_DEVICE void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, 
 }
 
 // Writes the warp's first `rows` staged rows, `cols` elements each, to out at (row0, col).  4 lanes take a
-// row's 64 bytes where rows and columns allow 16-byte stores, else 32 lanes one element each.  (An odd
-// N, 517 x 1337: 35 us with each lane storing its own row's elements, 13 so.  With aligned rows it is as
-// fast as 32 bytes a lane to 32 rows straight from the registers.)
+// row's 64 bytes where rows and columns allow 16-byte stores, else 32 lanes one element each (8192 rows,
+// K = 1000, bf16 / fp32 out, quantisation included: N = 1344 23 / 31 us, N = 1337 36 / 58).
 template <typename E>
 MOE_DEVICE void send_rows(const F8Args& a, uint32_t stage, int64_t row0, int rows, int64_t col, int cols, uint64_t pol) {
   const int lane = threadIdx.x & 31;
@@ -322,6 +326,9 @@ MOE_DEVICE void store_rows(const uint64_t (&acc)[64], const F8Args& a, const CUt
           float lo, hi;
           unpack_f32x2(acc[16 * h + 4 * c + i], lo, hi);
           if (kMode == kDown) {
+            // y in fp16, what the experts' entry returns and the combine reads, for every weight type: half the
+            // bytes of fp32.  2e-4 of its size (rms), 9e-4 after the layer's bf16 rounding, where other orders
+            // of the fp32 sums alone give 4e-4 by h's open roundings; from fp64 1.67e-3 with it and without.
             m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));  // (columns beyond N have zero weights)
             w[i] = f32x2_to_f16x2_sat(lo, hi);
           } else {
@@ -611,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<kMode>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
       // The loop over K blocks is kept short, its waits included: its time follows its length in
-      // instructions (unrolled by two, the 8192-row product took 228 us instead of 133).  A wait is a
+      // instructions (unrolled by two, the 8192-row product of an earlier form, 133 us, took 228).  A wait is a
       // bounded spin of the whole warp; one that gives up leaves limit 0, and the warp goes on without
       // waiting to the end of the unit, where it reports.
       int kb = kb0;
