@@ -38,7 +38,7 @@ EXPORTED = (
     "moe_plan_resolved_path", "moe_quantize_rows", "moe_quantize_blocks", "moe_linear_create", "moe_linear_destroy",
     "moe_linear_set_weights", "moe_linear_workspace_bytes", "moe_linear_set_workspace", "moe_linear_forward",
     "moe_linear_forward_quantized", "moe_linear_get_device_error", "moe_layer_forward_routed",
-    "moe_plan_set_routing",
+    "moe_plan_set_routing", "moe_sort_rows", "moe_sort_rows_backward", "moe_combine_rows", "moe_combine_rows_backward",
 )
 
 _lib = None
@@ -109,6 +109,10 @@ def load_library(path: str = LIB_PATH):
         "moe_linear_forward": ([vp, vp, i32, i64, i32, vp, i32, i64, vp], i32),
         "moe_linear_forward_quantized": ([vp, vp, i64, vp, i64, i32, vp, i32, i64, vp], i32),
         "moe_linear_get_device_error": ([vp, u32p], i32),
+        "moe_sort_rows": ([vp, i32, i64, i32, i32, i32, vp, vp, vp, i64, i64, vp], i32),
+        "moe_sort_rows_backward": ([vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, i64, vp, i64, vp, vp], i32),
+        "moe_combine_rows": ([vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, i32, i64, vp, i32, i64, vp], i32),
+        "moe_combine_rows_backward": ([vp, i32, i64, i32, i32, i32, vp, vp, vp, i64, vp, i32, i64, i64, vp, vp], i32),
     })
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -234,6 +238,149 @@ def quantize_fp8_weight(w: torch.Tensor, stream=None):
     for wm, qm, sm in zip(w.view(-1, rows, K), q.view(-1, rows, K), s.view(-1, s.shape[-2], s.shape[-1])):
         _check(lib.moe_quantize_blocks(_ptr(wm), DTYPES[w.dtype], rows, K, _ptr(qm), _ptr(sm), _stream()))
     return q, s
+
+
+def _here(*tensors):
+    """The tensors' device, which has to be the current one (launches go to its current stream)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"tensors must be on the current CUDA device ({dev}), got {t.device}")
+
+
+def _assignments(inv: torch.Tensor, weights: Optional[torch.Tensor]):
+    """(T, k, inv's pointer, weights' pointer) of the assignments' rows."""
+    if inv.dim() != 2:
+        raise ValueError(f"inv must have shape (T, k), got {tuple(inv.shape)}")
+    T, k = inv.shape
+    return T, k, _dev(inv, "inv", torch.int32), _dev(weights, "weights", torch.float32, (T, k))
+
+
+def _outside(out: torch.Tensor, *inputs):
+    """out must not share memory with an input (the extents of their rows are compared)."""
+    def extent(t):
+        n = t.numel() and 1 + sum((s - 1) * st for s, st in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + n * t.element_size()
+    lo, hi = extent(out)
+    for t in inputs:
+        if t is not None:
+            a, b = extent(t)
+            if a < hi and lo < b:
+                raise ValueError("an output overlaps an input")
+
+
+def sort_rows(x: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None, stream=None):
+    """Token rows x [T][d] (bf16, fp16 or fp32, any row pitch) in expert order: out[inv[t, j]] = weights[t, j] x[t]
+    (moe_sort_rows).  inv int32 [T][k] is ``MoePlan.permute``'s, viewed as (T, k); -1: dropped.  out [rows][d] of
+    x's type (default T * k rows) keeps the rows that no entry names; a new one's are undefined."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return sort_rows(x, inv, weights, out)
+    _here(x, inv, weights, out)
+    T, k, pi, pw = _assignments(inv, weights)
+    d = x.shape[-1]
+    px, ldx = _rows(x, "x", DTYPES, d)
+    if x.shape[0] != T:
+        raise ValueError(f"x must have {T} rows, got {x.shape[0]}")
+    if out is None:
+        out = torch.empty((T * k, d), dtype=x.dtype, device=x.device)
+    else:
+        _outside(out, x, inv, weights)
+    po, ldo = _rows(out, "out", (x.dtype,), d)
+    _check(load_library().moe_sort_rows(px, DTYPES[x.dtype], ldx, T, k, d, pi, pw, po, ldo, out.shape[0], _stream()))
+    return out
+
+
+def sort_rows_backward(grad: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                       x: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None):
+    """The gradient of ``sort_rows``: grad [rows][d] in expert order -> dx [T][d] (dx[t] = sum_j weights[t, j]
+    grad[inv[t, j]]) and, when x is given, (dx, dweights) with dweights[t, j] = <x[t], grad[inv[t, j]]> in fp32."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return sort_rows_backward(grad, inv, weights, x, out)
+    _here(grad, inv, weights, x, out)
+    T, k, pi, pw = _assignments(inv, weights)
+    d = grad.shape[-1]
+    pg, ldg = _rows(grad, "grad", DTYPES, d)
+    px = ldx = dw = None
+    if x is not None:
+        px, ldx = _rows(x, "x", (grad.dtype,), d)
+        if x.shape[0] != T:
+            raise ValueError(f"x must have {T} rows, got {x.shape[0]}")
+        dw = torch.empty((T, k), dtype=torch.float32, device=grad.device)
+    if out is None:
+        out = torch.empty((T, d), dtype=grad.dtype, device=grad.device)
+    else:
+        _outside(out, grad, inv, weights, x)
+    po, ldo = _rows(out, "out", (grad.dtype,), d)
+    if out.shape[0] != T:
+        raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
+    _check(load_library().moe_sort_rows_backward(pg, DTYPES[grad.dtype], ldg, grad.shape[0], T, k, d, pi, pw, px, ldx or 0,
+                                                 po, ldo, _ptr(dw), _stream()))
+    return out if dw is None else (out, dw)
+
+
+def combine_rows(y: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                 shared: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, out_dtype=None, stream=None):
+    """Rows y [rows][d] in expert order back to the tokens: out[t] = sum_j weights[t, j] y[inv[t, j]] + shared[t]
+    (moe_combine_rows), in out_dtype (default y's).  y, shared and out: bf16, fp16 or fp32 each, any row pitch."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return combine_rows(y, inv, weights, shared, out, out_dtype)
+    _here(y, inv, weights, shared, out)
+    T, k, pi, pw = _assignments(inv, weights)
+    d = y.shape[-1]
+    py, ldy = _rows(y, "y", DTYPES, d)
+    ps, lds, sdt = None, 0, 0
+    if shared is not None:
+        ps, lds = _rows(shared, "shared", DTYPES, d)
+        sdt = DTYPES[shared.dtype]
+        if shared.shape[0] != T:
+            raise ValueError(f"shared must have {T} rows, got {shared.shape[0]}")
+    if out is None:
+        out = torch.empty((T, d), dtype=out_dtype or y.dtype, device=y.device)
+    else:
+        _outside(out, y, inv, weights, shared)
+    po, ldo = _rows(out, "out", DTYPES if out_dtype is None else (out_dtype,), d)
+    if out.shape[0] != T:
+        raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
+    if out.dtype not in DTYPES:
+        raise ValueError(f"out must be bf16, fp16 or fp32, got {out.dtype}")
+    _check(load_library().moe_combine_rows(py, DTYPES[y.dtype], ldy, y.shape[0], T, k, d, pi, pw, ps, sdt, lds, po,
+                                           DTYPES[out.dtype], ldo, _stream()))
+    return out
+
+
+def combine_rows_backward(grad: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                          y: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None):
+    """The gradient of ``combine_rows``: grad [T][d] -> dy [rows][d] in expert order (dy[inv[t, j]] = weights[t, j]
+    grad[t]) and, when y is given, (dy, dweights) with dweights[t, j] = <grad[t], y[inv[t, j]]> in fp32.  dy has y's
+    type and rows (without y: out's, or T * k rows of grad's type); rows that no entry names keep out's contents, in
+    a new dy they are undefined.  The gradient of ``shared`` is grad itself."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return combine_rows_backward(grad, inv, weights, y, out)
+    _here(grad, inv, weights, y, out)
+    T, k, pi, pw = _assignments(inv, weights)
+    d = grad.shape[-1]
+    pg, ldg = _rows(grad, "grad", DTYPES, d)
+    if grad.shape[0] != T:
+        raise ValueError(f"grad must have {T} rows, got {grad.shape[0]}")
+    py = ldy = dw = None
+    if y is not None:
+        py, ldy = _rows(y, "y", DTYPES, d)
+        dw = torch.empty((T, k), dtype=torch.float32, device=grad.device)
+    if out is None:
+        out = torch.empty((T * k if y is None else y.shape[0], d), dtype=(grad if y is None else y).dtype, device=grad.device)
+    else:
+        _outside(out, grad, inv, weights, y)
+    po, ldo = _rows(out, "out", DTYPES if y is None else (y.dtype,), d)
+    if y is not None and out.shape[0] != y.shape[0]:
+        raise ValueError(f"out must have {y.shape[0]} rows, got {out.shape[0]}")
+    _check(load_library().moe_combine_rows_backward(pg, DTYPES[grad.dtype], ldg, T, k, d, pi, pw, py, ldy or 0, po,
+                                                    DTYPES[out.dtype], ldo, out.shape[0], _ptr(dw), _stream()))
+    return out if dw is None else (out, dw)
 
 
 class Fp8Linear:

@@ -2,9 +2,9 @@
 // weight set-up and the two launches of a call (quantise the rows, multiply).
 #include <cudaTypedefs.h>
 
-#include <cstdio>
 #include <new>
 
+#include "abi_checks.h"
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -21,32 +21,8 @@ struct moe_linear {
   int T_max = 0;
 };
 
-static moe_status bad(moe_status s, const char* msg) { return fail_message(s, msg); }
-
-static moe_status cuda_fail(const char* what, cudaError_t e) {
-  char buf[256];
-  snprintf(buf, sizeof buf, "%s: %s", what, cudaGetErrorString(e));
-  return fail_message(MOE_ERR_CUDA, buf);
-}
-#define LIN_TRY(expr)                                      \
-  do {                                                     \
-    const cudaError_t _e = (expr);                         \
-    if (_e != cudaSuccess) return cuda_fail(#expr, _e);    \
-  } while (0)
-
-static bool known(moe_dtype t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
-static size_t elem_bytes(moe_dtype t) { return t == MOE_FP32 ? 4 : 2; }
-static bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
 // Rows and columns a call takes: an index past the end of a partial block or tile stays below 2^31.
 constexpr int kMaxLen = 0x7fffffff - 2047;
-
-static int current_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
 
 extern "C" moe_status moe_quantize_rows(const void* x, moe_dtype x_dtype, int64_t ldx, int T, int K, uint8_t* q,
                                         int64_t ldq, float* s, int64_t lds, moe_stream_t stream) {

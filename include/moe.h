@@ -440,6 +440,40 @@ moe_status moe_linear_forward_quantized(moe_linear* lin, const uint8_t* q, int64
                                             moe_stream_t stream);
 moe_status moe_linear_get_device_error(moe_linear* lin, uint32_t* code);
 
+/*
+ * Rows between token order and expert order, in any element type, with the gradients.  Source:
+ * "Why SSD-streamed MoE was slow: 8GB Jetson Orin Nano, part 2", first-cache section (the grouped
+ * expert matmul needs each expert's rows together); the pages have no counterpart to the gradients.
+ * For experts computed outside this library (moe_experts gathers and scatters on its own).
+ * inv_perm int32 [T][k] as moe_permute writes it: the row, in expert order, of token t's assignment
+ * j.  An entry below 0 or at n_rows and above is a dropped assignment and contributes nothing; no
+ * two entries may name the same row.  weights fp32 [T][k], or NULL for 1.
+ *   moe_sort_rows              out[inv[t,j]] = w[t,j] x[t]
+ *   moe_sort_rows_backward     dx[t] = sum_j w[t,j] grad[inv[t,j]],  dweights[t,j] = <x[t], grad[inv[t,j]]>
+ *   moe_combine_rows           out[t] = sum_j w[t,j] y[inv[t,j]] + shared[t]
+ *   moe_combine_rows_backward  dy[inv[t,j]] = w[t,j] grad[t],  dweights[t,j] = <grad[t], y[inv[t,j]]>
+ *     (the gradient of shared is grad itself)
+ * Token rows [T][d] and rows in expert order [n_rows][d] have any pitch (elements) >= d, aligned to
+ * their elements; 16-byte aligned rows with d % 8 == 0 take the faster accesses.  Rows of out / dy
+ * that no entry names are left as they are.  Sums are fp32 in slot order, the shared term last, rounded
+ * once to the output's type (beyond fp16's range: infinity); sums over d are fp32 in a fixed order.
+ * dweights fp32 [T][k] or NULL (x / y is then not read and may be NULL); 0 for a dropped assignment.
+ * moe_sort_rows without weights copies the bits.  Outputs do not overlap inputs.  1 <= k <= 32,
+ * T k and n_rows <= 2^31 - 1, d <= 2^24.  The calls only enqueue work, need no plan and no workspace.
+ */
+moe_status moe_sort_rows(const void* x, moe_dtype x_dtype, int64_t ldx, int T, int k, int d, const int32_t* inv_perm,
+                         const float* weights, void* out, int64_t ldo, int64_t n_rows, moe_stream_t stream);
+moe_status moe_sort_rows_backward(const void* grad, moe_dtype dtype, int64_t ldg, int64_t n_rows, int T, int k, int d,
+                                  const int32_t* inv_perm, const float* weights, const void* x, int64_t ldx, void* dx,
+                                  int64_t lddx, float* dweights, moe_stream_t stream);
+moe_status moe_combine_rows(const void* y, moe_dtype y_dtype, int64_t ldy, int64_t n_rows, int T, int k, int d,
+                            const int32_t* inv_perm, const float* weights, const void* shared, moe_dtype shared_dtype,
+                            int64_t lds, void* out, moe_dtype out_dtype, int64_t ldo, moe_stream_t stream);
+moe_status moe_combine_rows_backward(const void* grad, moe_dtype grad_dtype, int64_t ldg, int T, int k, int d,
+                                     const int32_t* inv_perm, const float* weights, const void* y, int64_t ldy, void* dy,
+                                     moe_dtype y_dtype, int64_t lddy, int64_t n_rows, float* dweights,
+                                     moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
