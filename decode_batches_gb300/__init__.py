@@ -39,6 +39,7 @@ EXPORTED = (
     "moe_linear_set_weights", "moe_linear_workspace_bytes", "moe_linear_set_workspace", "moe_linear_forward",
     "moe_linear_forward_quantized", "moe_linear_get_device_error", "moe_layer_forward_routed",
     "moe_plan_set_routing", "moe_sort_rows", "moe_sort_rows_backward", "moe_combine_rows", "moe_combine_rows_backward",
+    "moe_verify_drafts",
 )
 
 _lib = None
@@ -113,6 +114,7 @@ def load_library(path: str = LIB_PATH):
         "moe_sort_rows_backward": ([vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, i64, vp, i64, vp, vp], i32),
         "moe_combine_rows": ([vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, i32, i64, vp, i32, i64, vp], i32),
         "moe_combine_rows_backward": ([vp, i32, i64, i32, i32, i32, vp, vp, vp, i64, vp, i32, i64, i64, vp, vp], i32),
+        "moe_verify_drafts": ([vp, i32, i64, vp, i64, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp], i32),
     })
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -381,6 +383,47 @@ def combine_rows_backward(grad: torch.Tensor, inv: torch.Tensor, weights: Option
     _check(load_library().moe_combine_rows_backward(pg, DTYPES[grad.dtype], ldg, T, k, d, pi, pw, py, ldy or 0, po,
                                                     DTYPES[out.dtype], ldo, out.shape[0], _ptr(dw), _stream()))
     return out if dw is None else (out, dw)
+
+
+def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, offsets: torch.Tensor, u: torch.Tensor,
+                  u_sample: torch.Tensor, draft_probs: Optional[torch.Tensor] = None,
+                  tokens: Optional[torch.Tensor] = None, accepted: Optional[torch.Tensor] = None, stream=None):
+    """Drafted tokens against the target's probabilities, from given uniform numbers (moe_verify_drafts).
+
+    target [R][V] (bf16, fp16 or fp32, any row pitch): the probabilities of a step's verify rows; offsets int32
+    [B + 1]: request b owns rows offsets[b] .. offsets[b + 1] - 1, one a draft and one behind the last; drafts int32
+    [R]; draft_probs like target, or None for drafts that were certain; u fp32 [R] decides the drafts, u_sample fp32
+    [B] draws the token behind the accepted ones.  Returns (tokens int32 [R], accepted int32 [B]): in a request's
+    rows the accepted drafts, the drawn token, then -1.  Rows of no request keep the contents of tokens; in a
+    new tensor they are undefined."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return verify_drafts(target, drafts, offsets, u, u_sample, draft_probs, tokens, accepted)
+    _here(target, drafts, offsets, u, u_sample, draft_probs, tokens, accepted)
+    if target.dim() != 2 or u_sample.dim() != 1:
+        raise ValueError(f"target must be 2-D and u_sample 1-D, got {tuple(target.shape)} and {tuple(u_sample.shape)}")
+    (R, V), B = target.shape, u_sample.shape[0]
+    pt, ldt = _rows(target, "target", DTYPES, V)
+    pd = ldd = None
+    if draft_probs is not None:
+        pd, ldd = _rows(draft_probs, "draft_probs", (target.dtype,), V)
+        if draft_probs.shape[0] != R:
+            raise ValueError(f"draft_probs must have {R} rows, got {draft_probs.shape[0]}")
+    if tokens is None:
+        tokens = torch.empty((R,), dtype=torch.int32, device=target.device)
+    else:
+        _outside(tokens, target, drafts, offsets, u, u_sample, draft_probs)
+    if accepted is None:
+        accepted = torch.empty((B,), dtype=torch.int32, device=target.device)
+    else:
+        _outside(accepted, target, drafts, offsets, u, u_sample, draft_probs, tokens)
+    i32 = torch.int32
+    _check(load_library().moe_verify_drafts(
+        pt, DTYPES[target.dtype], ldt, pd, ldd or 0, R, V, _dev(drafts, "drafts", i32, (R,)),
+        _dev(offsets, "offsets", i32, (B + 1,)), B, _dev(u, "u", torch.float32, (R,)),
+        _dev(u_sample, "u_sample", torch.float32, (B,)), _dev(tokens, "tokens", i32, (R,)),
+        _dev(accepted, "accepted", i32, (B,)), _stream()))
+    return tokens, accepted
 
 
 class Fp8Linear:

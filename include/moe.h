@@ -474,6 +474,33 @@ moe_status moe_combine_rows_backward(const void* grad, moe_dtype grad_dtype, int
                                      moe_dtype y_dtype, int64_t lddy, int64_t n_rows, float* dweights,
                                      moe_stream_t stream);
 
+/*
+ * Verification of drafted tokens.  Source: "DeepSeek V4.1F Q4 with native DSpark MTP on M3 Ultra", DSpark
+ * paragraph (a block of 6 rows verifies drafted tokens); the acceptance rule has no counterpart on the pages.
+ * B requests own consecutive rows of the step's R verify rows: request b the rows offsets[b] .. offsets[b+1] - 1
+ * (int32 [B+1], device), one for each of its n = rows - 1 drafts and one behind the last.  Row r of target [R][V]
+ * holds the probabilities of the token that follows; drafts[r] (int32 [R]; not read in a request's last row) is the
+ * token that row r verifies, and row r of draft_probs [R][V] the distribution q it was drawn from (not read in a
+ * request's last row; NULL: the draft was certain, q = 1 at the drafted token and 0 elsewhere).  u fp32 [R] and
+ * u_sample fp32 [B] are uniform numbers in [0, 1).
+ *   Draft i is accepted while u_i q_i(draft) < p_i(draft), up to the first that is not.
+ *   Behind the accepted drafts comes one token: from r = max(p - q, 0) of the refused row (without draft_probs: p
+ *   without the refused draft), or from p of the last row when no draft was refused: the lowest index whose
+ *   cumulative sum of r exceeds u_sample[b] * (sum of r); the last index with r > 0 if none does.  Where r sums to 0
+ *   the token is drawn from that row's p, where p does too it is -1.
+ * Probabilities need not sum to one.  A value that is NaN, negative or above 2^64 counts as 0; a draft outside
+ * [0, V) is refused.  The products u q are exact, sums have some 48 bits.
+ *   tokens   int32 [R]: the accepted drafts, the drawn token, then -1, in the request's rows; rows of no request
+ *            are left as they are.
+ *   accepted int32 [B]: the number of accepted drafts; 0 for a request without rows; -1 (and no token is written)
+ *            where offsets[b] < 0, offsets[b] > offsets[b+1] or offsets[b+1] > R.
+ * target and draft_probs have one element type and row pitches ldt, ldd >= V.  V <= 2^30, B <= 65535.  Only
+ * enqueues work (one launch), needs no plan and no workspace.
+ */
+moe_status moe_verify_drafts(const void* target, moe_dtype dtype, int64_t ldt, const void* draft_probs, int64_t ldd,
+                             int R, int V, const int32_t* drafts, const int32_t* offsets, int B, const float* u,
+                             const float* u_sample, int32_t* tokens, int32_t* accepted, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
