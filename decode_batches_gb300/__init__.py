@@ -39,7 +39,8 @@ EXPORTED = (
     "moe_linear_set_weights", "moe_linear_workspace_bytes", "moe_linear_set_workspace", "moe_linear_forward",
     "moe_linear_forward_quantized", "moe_linear_get_device_error", "moe_layer_forward_routed",
     "moe_plan_set_routing", "moe_sort_rows", "moe_sort_rows_backward", "moe_combine_rows", "moe_combine_rows_backward",
-    "moe_verify_drafts",
+    "moe_verify_drafts", "moe_adapters_create", "moe_adapters_destroy", "moe_adapters_set", "moe_adapters_workspace_bytes",
+    "moe_adapters_set_workspace", "moe_adapters_forward", "moe_adapters_get_device_error",
 )
 
 _lib = None
@@ -115,6 +116,13 @@ def load_library(path: str = LIB_PATH):
         "moe_combine_rows": ([vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, i32, i64, vp, i32, i64, vp], i32),
         "moe_combine_rows_backward": ([vp, i32, i64, i32, i32, i32, vp, vp, vp, i64, vp, i32, i64, i64, vp, vp], i32),
         "moe_verify_drafts": ([vp, i32, i64, vp, i64, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp], i32),
+        "moe_adapters_create": ([i32, i32, i32, i32, i32], vp),
+        "moe_adapters_destroy": ([vp], None),
+        "moe_adapters_set": ([vp, i32, vp, vp, i32, ctypes.c_float], i32),
+        "moe_adapters_workspace_bytes": ([vp, i32], sz),
+        "moe_adapters_set_workspace": ([vp, vp, sz, i32], i32),
+        "moe_adapters_forward": ([vp, vp, i64, i32, vp, vp, i64, vp, i32, i64, vp], i32),
+        "moe_adapters_get_device_error": ([vp, u32p], i32),
     })
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -481,15 +489,23 @@ class Fp8Linear:
             raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
         return out, *_rows(out, "out", (torch.bfloat16, torch.float32), self.N)
 
-    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None):
-        """x [T][K] (bf16, fp16 or fp32; rows may have a pitch) -> [T][N] in bf16 or fp32."""
+    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None,
+                adapters: Optional["LowRankAdapters"] = None, adapter_ids: Optional[torch.Tensor] = None):
+        """x [T][K] (bf16, fp16 or fp32; rows may have a pitch) -> [T][N] in bf16 or fp32.  With adapters (of the same N
+        and K, x in their type) and adapter_ids int32 [T], each row's adapter is added to the rounded projection."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.forward(x, out, out_dtype)
+                return self.forward(x, out, out_dtype, None, adapters, adapter_ids)
+        if (adapters is None) != (adapter_ids is None):
+            raise ValueError("adapters and adapter_ids go together")
+        if adapters is not None:
+            adapters._beside(self, x, adapter_ids)
         px, ldx = _rows(x, "x", DTYPES, self.K)
         T = x.shape[0]
         out, po, ldo = self._out(T, out, out_dtype, x.device)
         _check(self.lib.moe_linear_forward(self._h, px, DTYPES[x.dtype], ldx, T, po, DTYPES[out.dtype], ldo, _stream()))
+        if adapters is not None:
+            adapters.forward(x, adapter_ids, out, out=out)
         return out
 
     def forward_quantized(self, q: torch.Tensor, s: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -513,6 +529,112 @@ class Fp8Linear:
     def device_error(self) -> int:
         code = ctypes.c_uint32(0)
         st = self.lib.moe_linear_get_device_error(self._h, ctypes.byref(code))
+        if st not in (MOE_OK, MOE_ERR_DEVICE):
+            _check(st)
+        return int(code.value)
+
+
+class LowRankAdapters:
+    """Low-rank adapters of many requests beside a shared projection (C ABI ``moe_adapters``).
+
+        ad = LowRankAdapters(n, N, K, rank)          # n slots for A [r][K], B [N][r], r <= rank
+        ad.set(slot, A, B, scale)
+        ad.allocate_workspace(T_max)
+        out = ad.forward(x, ids, base)               # base[t] + scale_a B_a (A_a x[t]), a = ids[t] (-1: none)
+        out = lin.forward(x, adapters=ad, adapter_ids=ids)    # beside an Fp8Linear
+    """
+
+    def __init__(self, n: int, N: int, K: int, rank: int, dtype=torch.bfloat16):
+        self.lib = load_library()
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"dtype must be bf16 or fp16, got {dtype}")
+        self.n, self.N, self.K, self.rank, self.dtype = n, N, K, rank, dtype
+        h = self.lib.moe_adapters_create(n, N, K, rank, DTYPES[dtype])
+        if not h:
+            raise MoeError(MOE_ERR_INVALID_ARG, self.lib.moe_last_error().decode())
+        self._h = ctypes.c_void_p(h)
+        self._ws = None
+        self.T_max = 0
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value:
+            self.lib.moe_adapters_destroy(h)
+            self._h = None
+
+    close = __del__
+
+    def set(self, slot: int, A: torch.Tensor, B: torch.Tensor, scale: float = 1.0):
+        """A [r][K] and B [N][r] of the handle's type into slot `slot` (copied; synchronous)."""
+        _here(A, B)
+        if A.dim() != 2:
+            raise ValueError(f"A must be 2-D, got {tuple(A.shape)}")
+        r = A.shape[0]
+        _check(self.lib.moe_adapters_set(self._h, slot, _dev(A, "A", self.dtype, (r, self.K)),
+                                         _dev(B, "B", self.dtype, (self.N, r)), r, scale))
+
+    def clear(self, slot: int):
+        """Empty slot `slot`: rows that ask for it get the base alone."""
+        _check(self.lib.moe_adapters_set(self._h, slot, None, None, 0, 1.0))
+
+    def workspace_bytes(self, T_max: int) -> int:
+        return int(self.lib.moe_adapters_workspace_bytes(self._h, T_max))
+
+    def set_workspace(self, buf: torch.Tensor, T_max: int):
+        _check(self.lib.moe_adapters_set_workspace(self._h, _dev(buf, "workspace"), buf.numel() * buf.element_size(), T_max))
+        self._ws = buf
+        self.T_max = T_max
+
+    def allocate_workspace(self, T_max: int, device=None) -> torch.Tensor:
+        buf = torch.empty(self.workspace_bytes(T_max), dtype=torch.uint8, device=device or "cuda")
+        self.set_workspace(buf, T_max)
+        return buf
+
+    def _beside(self, lin, x, ids):
+        """The checks of a projection's call with these adapters, before anything of it is queued."""
+        if (lin.N, lin.K) != (self.N, self.K):
+            raise ValueError(f"adapters of {self.N} x {self.K} beside a projection of {lin.N} x {lin.K}")
+        _here(x, ids)
+        _rows(x, "x", (self.dtype,), self.K)
+        _dev(ids, "adapter_ids", torch.int32, (x.shape[0],))
+        if x.shape[0] > self.T_max:
+            raise ValueError(f"the adapters' workspace holds {self.T_max} rows, got {x.shape[0]}")
+
+    def forward(self, x: torch.Tensor, ids: torch.Tensor, base: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, out_dtype=None, stream=None):
+        """x [T][K] of the handle's type, ids int32 [T], base [T][N] (None: zero) -> [T][N] in base's type, else in
+        out_dtype (default the handle's).  Rows may have a pitch; out may be base."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, ids, base, out, out_dtype)
+        _here(x, ids, base, out)
+        px, ldx = _rows(x, "x", (self.dtype,), self.K)
+        T = x.shape[0]
+        pb, ldb = None, 0
+        if base is not None:
+            if out_dtype is not None and out_dtype != base.dtype:
+                raise ValueError(f"out has base's type {base.dtype}, got {out_dtype}")
+            out_dtype = base.dtype
+            pb, ldb = _rows(base, "base", DTYPES, self.N)
+            if base.shape[0] != T:
+                raise ValueError(f"base must have {T} rows, got {base.shape[0]}")
+        if out is None:
+            out = torch.empty((T, self.N), dtype=out_dtype or self.dtype, device=x.device)
+            if out.dtype not in DTYPES:
+                raise ValueError(f"out must be bf16, fp16 or fp32, got {out.dtype}")
+            po, ldo = out.data_ptr(), self.N
+        else:
+            po, ldo = _rows(out, "out", DTYPES if out_dtype is None else (out_dtype,), self.N)
+            if out.shape[0] != T:
+                raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
+            _outside(out, x, ids, base if pb != po or ldb != ldo else None)
+        _check(self.lib.moe_adapters_forward(self._h, px, ldx, T, _dev(ids, "ids", torch.int32, (T,)), pb, ldb, po,
+                                             DTYPES[out.dtype], ldo, _stream()))
+        return out
+
+    def device_error(self) -> int:
+        code = ctypes.c_uint32(0)
+        st = self.lib.moe_adapters_get_device_error(self._h, ctypes.byref(code))
         if st not in (MOE_OK, MOE_ERR_DEVICE):
             _check(st)
         return int(code.value)

@@ -1,0 +1,453 @@
+// Low-rank adapters of many requests (include/moe.h: moe_adapters_forward):
+//   out[t] = base[t] + B_a (s_a A_a x[t]),  a = ids[t].
+//
+// A tile is up to M rows of one adapter; a cluster of CTAs computes it in one pass: each warp multiplies its
+// own range of K (shrink), the partial sums of u = A x meet in shared memory and then over the cluster, every
+// CTA holds the whole u, and each warp multiplies its own range of the features (expand), adds the base and
+// writes.  So x, base and the weights are read once and u never leaves the chip.
+//
+// Bound by memory (2 r / 3 operations a byte at most for 16-bit tensors), so the products run on warp-level
+// fragments whose operands come from global memory straight into registers, without staging: the weights are
+// packed in fragment order, and the k index of the shrink (any order will do) is dealt to the lanes such that
+// a lane's share of a row is 16 contiguous bytes.  The expand's features are dealt so that a lane's results
+// are eight neighbours of a row.
+//
+// u is split in two 16-bit terms, u = hi + lo (relative error 2^-16 or less of it in bf16, 2^-22 in fp16),
+// since one term's 2^-8 would dominate an fp32 result.  In fp16 a row's u is first brought to [1, 2) by a power
+// of two, so that neither term leaves the type's range.
+#include "adapters.cuh"
+#include "cluster.cuh"
+#include "elems.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+template <bool kFp16>
+MOE_DEVICE void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (kFp16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Eight elements of a row of x from column c (zeros past K).
+MOE_DEVICE uint4 load_x(const uint16_t* row, int c, int K, bool vec) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (vec) {
+    if (c < K) v = *reinterpret_cast<const uint4*>(row + c);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = c + 2 * i < K ? row[c + 2 * i] : 0u, hi = c + 2 * i + 1 < K ? row[c + 2 * i + 1] : 0u;
+      w[i] = lo | (hi << 16);
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+
+// out[c .. c + 7] = base + v, one rounding.
+template <typename E>
+MOE_DEVICE void add_store(const E* base, E* out, int c, int N, bool vec, const float (&v)[8]) {
+  if (vec) {
+    if (c >= N) return;
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (base) {
+      Raw8<E> r;
+      r.load(base + c);
+      r.to_f32(f);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] += v[i];
+    store8(out + c, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < N) out[c + i] = E::of((base ? base[c + i].f32() : 0.0f) + v[i]);
+  }
+}
+MOE_DEVICE void add_store(const AdapterArgs& p, int64_t row, int c, const float (&v)[8]) {
+  const bool vec = p.out_vec;
+  if (p.out_type == MOE_BF16)
+    add_store(p.base ? static_cast<const Bf16*>(p.base) + row * p.ld_base : nullptr,
+              static_cast<Bf16*>(p.out) + row * p.ld_out, c, p.N, vec, v);
+  else if (p.out_type == MOE_FP16)
+    add_store(p.base ? static_cast<const Fp16*>(p.base) + row * p.ld_base : nullptr,
+              static_cast<Fp16*>(p.out) + row * p.ld_out, c, p.N, vec, v);
+  else
+    add_store(p.base ? static_cast<const Fp32*>(p.base) + row * p.ld_base : nullptr,
+              static_cast<Fp32*>(p.out) + row * p.ld_out, c, p.N, vec, v);
+}
+
+template <int M, int R>
+struct Smem {
+  static constexpr int kPitch = R + (R % 32 == 0 ? 16 : 0);  // 16-bit elements: rows 8 apart share no bank
+  float warp_part[kWarps][M][R];
+  float part[M][R];
+  alignas(16) uint16_t u[2][M][kPitch];  // hi, lo
+  float row_scale[M];                    // (fp16) the power of two that a row's u was divided by
+  int rows[M];                           // the tile's rows, -1 past the last
+  uint32_t match[kAdapterScan / 32];
+};
+
+// The tile of the cluster: small steps look for it in ids, larger ones read it from the list.  Returns the slot
+// (-1: no adapter), or -2: nothing to do.  The same for every thread of the cluster.
+template <int M, int R>
+MOE_DEVICE int find_tile(const AdapterArgs& p, Smem<M, R>& s) {
+  const int idx = blockIdx.x / p.ctas;
+  if (threadIdx.x < M) s.rows[threadIdx.x] = -1;
+  if (p.tiles) {
+    if (idx >= *p.n_tiles) return -2;
+    const AdapterTile t = p.tiles[idx];
+    __syncthreads();
+    if (threadIdx.x < t.rows) s.rows[threadIdx.x] = p.order[t.start + threadIdx.x];
+    __syncthreads();
+    return t.slot;
+  }
+  // Rows of equal id, 0, 1, 2, ... in order: row idx leads a tile when its number is a multiple of M.
+  int own = p.ids[idx];
+  if (own < -1 || own >= p.n) {
+    if (threadIdx.x == 0) set_error(p.err, MOE_DEVERR_EXPERT_RANGE);
+    own = -1;
+  }
+  int id = threadIdx.x < p.T ? p.ids[threadIdx.x] : -2;
+  if (threadIdx.x < p.T && (id < -1 || id >= p.n)) id = -1;
+  const uint32_t m = __ballot_sync(0xffffffffu, id == own);
+  if ((threadIdx.x & 31) == 0) s.match[threadIdx.x >> 5] = m;
+  __syncthreads();
+  int before_me = 0, before_idx = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const uint32_t b = s.match[w];
+    const int me = static_cast<int>(threadIdx.x) - 32 * w, ix = idx - 32 * w;
+    before_me += me >= 32 ? __popc(b) : me > 0 ? __popc(b & ((1u << me) - 1u)) : 0;
+    before_idx += ix >= 32 ? __popc(b) : ix > 0 ? __popc(b & ((1u << ix) - 1u)) : 0;
+  }
+  if (before_idx % M) return -2;
+  const int at = before_me - before_idx;
+  if (id == own && at >= 0 && at < M) s.rows[at] = threadIdx.x;
+  __syncthreads();
+  return own;
+}
+
+template <int M, int R, bool kFp16>
+__global__ void __launch_bounds__(kThreads) adapter_kernel(const AdapterArgs p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Smem<M, R>& s = *reinterpret_cast<Smem<M, R>*>(smem_raw);
+  constexpr int MT = M / 16, NT = R / 8, RS = R / 16;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  pdl_trigger();
+  pdl_wait();
+  const int slot = find_tile(p, s);
+  if (slot == -2) return;
+  const int rank = slot >= 0 ? p.rank[slot] : 0;
+  const uint32_t cta = cluster_rank();
+  const int C = p.ctas;
+  const int nt = (rank + 7) / 8, rs = (rank + 15) / 16;
+  int row[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) row[m][0] = s.rows[16 * m + g], row[m][1] = s.rows[16 * m + g + 8];
+
+  if (rank > 0) {
+    // ---- shrink: this warp's chunks of 32 columns ---------------------------------------------------
+    const int nk = (p.K + 31) / 32, per = (nk + C * kWarps - 1) / (C * kWarps);
+    const int k0 = min((static_cast<int>(cta) * kWarps + warp) * per, nk), k1 = min(k0 + per, nk);
+    const uint4* wa = reinterpret_cast<const uint4*>(p.a + slot * p.a_slot) + lane;
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
+#pragma unroll 2
+    for (int k = k0; k < k1; ++k) {
+      uint4 w[NT], x[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[m][h] = make_uint4(0u, 0u, 0u, 0u);
+          if (row[m][h] >= 0) x[m][h] = load_x(p.x + row[m][h] * p.ldx, 32 * k + 8 * q, p.K, p.x_vec);
+        }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        if (j < nt) w[j] = wa[(static_cast<int64_t>(k) * NT + j) * 32];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (j < nt) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            mma<kFp16>(acc[m][j], x[m][0].x, x[m][1].x, x[m][0].y, x[m][1].y, w[j].x, w[j].y);
+            mma<kFp16>(acc[m][j], x[m][0].z, x[m][1].z, x[m][0].w, x[m][1].w, w[j].z, w[j].w);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        *reinterpret_cast<float2*>(&s.warp_part[warp][16 * m + g][8 * j + 2 * q]) = make_float2(acc[m][j][0], acc[m][j][1]);
+        *reinterpret_cast<float2*>(&s.warp_part[warp][16 * m + g + 8][8 * j + 2 * q]) =
+            make_float2(acc[m][j][2], acc[m][j][3]);
+      }
+    __syncthreads();
+    for (int i = threadIdx.x * 4; i < M * R; i += kThreads * 4) {
+      float4 v = *reinterpret_cast<const float4*>(&s.warp_part[0][0][0] + i);
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 o = *reinterpret_cast<const float4*>(&s.warp_part[w][0][0] + i);
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+      }
+      *reinterpret_cast<float4*>(&s.part[0][0] + i) = v;
+    }
+    cluster_barrier();
+    // ---- u of the tile, from the cluster's partial sums in order of rank; eight ranks a thread -------------
+    const float scale = p.scale[slot];
+    for (int i = threadIdx.x * 8; i < M * R; i += kThreads * 8) {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < C; ++c) {
+        const float4 o0 = ld_cluster_f32x4(&s.part[0][0] + i, c), o1 = ld_cluster_f32x4(&s.part[0][0] + i + 4, c);
+        v[0] += o0.x, v[1] += o0.y, v[2] += o0.z, v[3] += o0.w;
+        v[4] += o1.x, v[5] += o1.y, v[6] += o1.z, v[7] += o1.w;
+      }
+      const int r = i / R, c = i % R;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e >= rank) v[e] = 0.0f;  // (an infinite x makes NaN of the padding)
+      float mul = scale;
+      if (kFp16) {
+        float big = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(v[e] * scale));
+#pragma unroll
+        for (int o = 1; o < R / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        // 2^e with big in [2^e, 2^(e+1)); 1 for zero, infinity and NaN; 2^-126 .. 2^126
+        const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+        const int e2 = ex == -127 || ex == 128 ? 0 : max(-126, min(126, ex));
+        if (c == 0) s.row_scale[r] = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * scale * down;
+        mul = 1.0f;
+      }
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float a0 = v[e] * mul, a1 = v[e + 1] * mul;
+        float h0, h1;
+        if (kFp16) {
+          hi[e / 2] = pack_f16x2(a0, a1);
+          h0 = f16_bits_to_f32(hi[e / 2] & 0xffffu), h1 = f16_bits_to_f32(hi[e / 2] >> 16);
+        } else {
+          hi[e / 2] = pack_bf16x2(a0, a1);
+          h0 = bf16_bits_to_f32(hi[e / 2] & 0xffffu), h1 = bf16_bits_to_f32(hi[e / 2] >> 16);
+        }
+        // (an infinity has no rest)
+        const float l0 = isfinite(h0) ? a0 - h0 : 0.0f, l1 = isfinite(h1) ? a1 - h1 : 0.0f;
+        lo[e / 2] = kFp16 ? pack_f16x2(l0, l1) : pack_bf16x2(l0, l1);
+      }
+      *reinterpret_cast<uint4*>(&s.u[0][r][c]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(&s.u[1][r][c]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    cluster_barrier();  // u is written, and no CTA's partial sums are read any more
+  }
+
+  // ---- expand: this warp's chunks of 32 features -----------------------------------------------------
+  if (rank == 0 && p.base == p.out) return;
+  const int nc = (p.N + 31) / 32, per = (nc + C * kWarps - 1) / (C * kWarps);
+  const int c0 = min((static_cast<int>(cta) * kWarps + warp) * per, nc), c1 = min(c0 + per, nc);
+  const uint4* wb = reinterpret_cast<const uint4*>(p.b + (rank > 0 ? slot * p.b_slot : 0)) + lane;
+  for (int c = c0; c < c1; ++c) {
+    uint4 w[RS][2];
+#pragma unroll
+    for (int k = 0; k < RS; ++k)
+      if (k < rs) {
+        w[k][0] = wb[((static_cast<int64_t>(c) * RS + k) * 2 + 0) * 32];
+        w[k][1] = wb[((static_cast<int64_t>(c) * RS + k) * 2 + 1) * 32];
+      }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < RS; ++k)
+        if (k < rs) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {  // hi, lo
+            const uint2 lo = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g][16 * k + 4 * q]);
+            const uint2 up = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g + 8][16 * k + 4 * q]);
+            mma<kFp16>(acc[0], lo.x, up.x, lo.y, up.y, w[k][0].x, w[k][0].y);
+            mma<kFp16>(acc[1], lo.x, up.x, lo.y, up.y, w[k][0].z, w[k][0].w);
+            mma<kFp16>(acc[2], lo.x, up.x, lo.y, up.y, w[k][1].x, w[k][1].y);
+            mma<kFp16>(acc[3], lo.x, up.x, lo.y, up.y, w[k][1].z, w[k][1].w);
+          }
+        }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (row[m][h] < 0) continue;
+        float f = 1.0f;
+        if (kFp16 && rank > 0) f = s.row_scale[16 * m + g + 8 * h];
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[2 * j] = acc[j][2 * h] * f, v[2 * j + 1] = acc[j][2 * h + 1] * f;
+        add_store(p, row[m][h], 32 * c + 8 * q, v);
+      }
+    }
+  }
+}
+
+// ---- packing -------------------------------------------------------------------------------------------
+// A: for a chunk of 32 columns and 8 ranks, lane (g, q) holds rank 8 j + g, columns 8 q .. 8 q + 7.
+// B: for a chunk of 32 features and 16 ranks, lane (g, q) holds, for each of the four products t, feature
+// 8 (g / 2) + 2 t + g % 2, ranks 4 q .. 4 q + 3.
+__global__ void adapter_pack_kernel(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
+                                    int R, int64_t na, int64_t nb) {
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < na + nb;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    if (i < na) {
+      const int e = i % 8, lane = i / 8 % 32, j = i / 256 % (R / 8);
+      const int64_t chunk = i / 256 / (R / 8);
+      const int rank = 8 * j + lane / 4;
+      const int64_t col = 32 * chunk + 8 * (lane % 4) + e;
+      pa[i] = rank < r && col < K ? a[rank * static_cast<int64_t>(K) + col] : 0;
+    } else {
+      const int64_t o = i - na;
+      const int e = o % 4, t2 = o / 4 % 2, lane = o / 8 % 32, half = o / 256 % 2, k = o / 512 % (R / 16);
+      const int64_t chunk = o / 512 / (R / 16);
+      const int g = lane / 4, q = lane % 4, t = 2 * half + t2, rank = 16 * k + 4 * q + e;
+      const int64_t f = 32 * chunk + 8 * (g / 2) + 2 * t + g % 2;
+      pb[o] = rank < r && f < N ? b[f * r + rank] : 0;
+    }
+  }
+}
+
+// ---- grouping of larger steps -----------------------------------------------------------------------------
+// One block: histogram of the ids (no adapter counts as slot n), exclusive scans of rows and tiles, and the rows
+// in slot order.  The order of a slot's rows is not fixed; a row's result does not depend on its place.
+constexpr int kGroupThreads = 1024;
+__global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int32_t* ids, int T, int n, int M,
+                                                                      int32_t* order, AdapterTile* tiles,
+                                                                      int32_t* n_tiles, uint32_t* err) {
+  __shared__ int s_count[kAdaptersMax + 1], s_row[kAdaptersMax + 1];
+  __shared__ int s_warp[2][32];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i <= n; i += kGroupThreads) s_count[i] = 0;
+  __syncthreads();
+  bool bad_id = false;
+  for (int i0 = 0; i0 < T; i0 += kGroupThreads) {
+    const int i = i0 + tid;
+    int key = -1;
+    if (i < T) {
+      key = ids[i];
+      if (key < 0 || key >= n) bad_id |= key != -1, key = n;
+    }
+    const uint32_t same = __match_any_sync(0xffffffffu, key);
+    if (key >= 0 && lane == __ffs(same) - 1) atomicAdd(&s_count[key], __popc(same));
+  }
+  if (bad_id) set_error(err, MOE_DEVERR_EXPERT_RANGE);
+  __syncthreads();
+  // slot tid and, for the last thread, slot 1024: rows and tiles before it
+  int rows_before = 0, tiles_before = 0;
+  const int c = tid <= n ? s_count[tid] : 0;
+  int r = c, t = (c + M - 1) / M;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, r, o), b = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) r += a, t += b;
+  }
+  if (lane == 31) s_warp[0][warp] = r, s_warp[1][warp] = t;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) rows_before += s_warp[0][w], tiles_before += s_warp[1][w];
+  r += rows_before, t += tiles_before;  // inclusive
+  if (tid <= n) {
+    s_row[tid] = r - c;
+    for (int k = 0, at = t - (c + M - 1) / M; k * M < c; ++k)
+      tiles[at + k] = AdapterTile{tid < n ? tid : -1, r - c + k * M, min(M, c - k * M), 0};
+  }
+  if (tid == kGroupThreads - 1) {
+    int all = t;
+    if (n == kGroupThreads) {  // the slot behind the last thread's: the rows without an adapter
+      const int cc = s_count[n];
+      s_row[n] = r;
+      for (int k = 0; k * M < cc; ++k) tiles[all++] = AdapterTile{-1, r + k * M, min(M, cc - k * M), 0};
+    }
+    *n_tiles = all;
+  }
+  __syncthreads();
+  for (int i0 = 0; i0 < T; i0 += kGroupThreads) {
+    const int i = i0 + tid;
+    int key = -1;
+    if (i < T) {
+      key = ids[i];
+      if (key < 0 || key >= n) key = n;
+    }
+    const uint32_t same = __match_any_sync(0xffffffffu, key);
+    const int leader = __ffs(same) - 1;
+    int at = 0;
+    if (key >= 0 && lane == leader) at = atomicAdd(&s_row[key], __popc(same));
+    at = __shfl_sync(0xffffffffu, at, leader);
+    if (key >= 0) order[at + __popc(same & ((1u << lane) - 1u))] = i;
+  }
+}
+
+template <int M, int R, bool kFp16>
+cudaError_t launch(AdapterArgs p, int clusters, int C, cudaStream_t st) {
+  p.ctas = C;
+  auto kern = adapter_kernel<M, R, kFp16>;
+  const int smem = sizeof(Smem<M, R>);
+  cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_clusters(kern, dim3(C * clusters), dim3(kThreads), C, smem, st, p);
+}
+
+// Rows of a grouped tile: M R values of u, 64 accumulator registers a lane.
+constexpr int tile_rows(int rpad) { return rpad <= 32 ? 64 : 2048 / rpad; }
+
+template <int R, bool kFp16>
+cudaError_t launch_rank(const AdapterArgs& p, int num_sms, cudaStream_t st) {
+  if (!p.tiles) return launch<kAdapterRowsMin, R, kFp16>(p, p.T, 8, st);
+  constexpr int M = tile_rows(R);
+  return launch<M, R, kFp16>(p, (p.T + M - 1) / M + (p.n + 1 < p.T ? p.n + 1 : p.T), 2, st);
+}
+
+}  // namespace
+
+int adapter_tile_rows(int rpad) { return tile_rows(rpad); }
+
+cudaError_t launch_adapter_pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
+                                int rpad, cudaStream_t st) {
+  const int64_t na = adapter_a_elems(K, rpad), nb = adapter_b_elems(N, rpad);
+  const int64_t blocks = (na + nb + 255) / 256;
+  adapter_pack_kernel<<<static_cast<int>(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(a, b, pa, pb, r, K, N, rpad, na, nb);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, int32_t* order, AdapterTile* tiles,
+                                 int32_t* n_tiles, uint32_t* err, cudaStream_t st) {
+  return launch_pdl(adapter_group_kernel, dim3(1), dim3(kGroupThreads), 0, st, ids, T, n, rows, order, tiles, n_tiles, err);
+}
+
+cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, int num_sms, cudaStream_t st) {
+  switch (rpad) {
+    case 16: return fp16 ? launch_rank<16, true>(p, num_sms, st) : launch_rank<16, false>(p, num_sms, st);
+    case 32: return fp16 ? launch_rank<32, true>(p, num_sms, st) : launch_rank<32, false>(p, num_sms, st);
+    case 64: return fp16 ? launch_rank<64, true>(p, num_sms, st) : launch_rank<64, false>(p, num_sms, st);
+    default: return fp16 ? launch_rank<128, true>(p, num_sms, st) : launch_rank<128, false>(p, num_sms, st);
+  }
+}
+
+}  // namespace moe

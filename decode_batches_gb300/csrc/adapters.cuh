@@ -1,0 +1,54 @@
+// Low-rank adapters: interface between the C entry points (adapters_api.cu) and the kernels (adapters.cu).
+#pragma once
+
+#include "kernels.h"
+
+namespace moe {
+
+constexpr int kAdaptersMax = 1024;    // slots of a handle
+constexpr int kAdapterRankMax = 128;
+constexpr int kAdapterScan = 256;     // rows up to which a cluster finds its tile itself
+constexpr int kAdapterRowsMin = 16;   // rows of the smallest tile
+
+// Rows [start, start + rows) of `order` that share a slot (slot -1: rows without an adapter).
+struct AdapterTile {
+  int slot, start, rows, pad;
+};
+
+struct AdapterArgs {
+  const uint16_t* x = nullptr;      // [T][K]
+  int64_t ldx = 0;
+  const int32_t* ids = nullptr;     // [T]
+  const uint16_t* a = nullptr;      // packed A of all slots (adapter_pack)
+  const uint16_t* b = nullptr;      // packed B
+  const int32_t* rank = nullptr;    // [n] ranks, 0: empty slot
+  const float* scale = nullptr;     // [n]
+  const void* base = nullptr;       // [T][N] of out_type, or NULL (zero)
+  int64_t ld_base = 0;
+  void* out = nullptr;
+  int64_t ld_out = 0;
+  int out_type = MOE_BF16;
+  int x_vec = 0, out_vec = 0;       // rows of x / of base and out are 16-byte aligned, K / N a multiple of 8
+  int T = 0, n = 0, K = 0, N = 0;
+  int ctas = 1;                     // CTAs of a cluster, that share a tile (set at launch)
+  int64_t a_slot = 0, b_slot = 0;   // elements of a slot's packed A, B
+  const int32_t* order = nullptr;   // grouped rows and their tiles (larger T)
+  const AdapterTile* tiles = nullptr;
+  const int32_t* n_tiles = nullptr;
+  uint32_t* err = nullptr;
+};
+
+inline int adapter_rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+inline int64_t adapter_a_elems(int K, int rpad) { return static_cast<int64_t>((K + 31) / 32) * 32 * rpad; }
+inline int64_t adapter_b_elems(int N, int rpad) { return static_cast<int64_t>((N + 31) / 32) * 32 * rpad; }
+
+// One slot's A [r][K] and B [N][r] into the kernels' order.
+cudaError_t launch_adapter_pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
+                                int rpad, cudaStream_t st);
+int adapter_tile_rows(int rpad);  // rows of a tile of the grouped path
+// order [T], tiles (at most T / rows + n + 1), n_tiles from ids; ids outside [-1, n) set MOE_DEVERR_EXPERT_RANGE.
+cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, int32_t* order, AdapterTile* tiles,
+                                 int32_t* n_tiles, uint32_t* err, cudaStream_t st);
+cudaError_t launch_adapters(const AdapterArgs& a, int rpad, bool fp16, int num_sms, cudaStream_t st);
+
+}  // namespace moe

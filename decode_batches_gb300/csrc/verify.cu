@@ -15,6 +15,7 @@
 // fp64 throughout would take six times as long as the memory on this chip (2 additions a clock and SM);
 // the pair costs some 18 fp32 operations an element, half the memory's time.
 #include "abi_checks.h"
+#include "cluster.cuh"
 #include "elems.cuh"
 
 using namespace moe;
@@ -38,22 +39,6 @@ struct VerifyArgs {
   int32_t* accepted = nullptr;
   int R = 0, V = 0;
 };
-
-MOE_DEVICE uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-MOE_DEVICE void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-MOE_DEVICE double ld_cluster(const double* p, uint32_t rank) {
-  uint32_t addr;
-  double v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
-  return v;
-}
 
 // A probability as it counts: 0 unless 0 < v <= 2^64 (NaN, infinities and negative values count as 0; the
 // bound keeps every sum of 2^30 of them finite).
@@ -252,13 +237,12 @@ __global__ void __launch_bounds__(kWarps * 32) verify_kernel(const VerifyArgs a)
     const int v1 = min(v0 + per, total);
     const double mine = range_sum(r, v0, v1, lane);
     if (lane == 0) s_sum[warp] = mine;
-    __syncwarp();
-    cluster_sync();
+    cluster_barrier();
     // every warp: the ranges' sums in order, two a lane
     static_assert(kCluster * kWarps == 64, "two ranges a lane");
-    const double s0 = ld_cluster(&s_sum[(2 * lane) % kWarps], 2 * lane / kWarps);
-    const double s1 = ld_cluster(&s_sum[(2 * lane + 1) % kWarps], 2 * lane / kWarps);
-    cluster_sync();  // (the sums are read: the next round, or the exit, may follow)
+    const double s0 = ld_cluster_f64(&s_sum[(2 * lane) % kWarps], 2 * lane / kWarps);
+    const double s1 = ld_cluster_f64(&s_sum[(2 * lane + 1) % kWarps], 2 * lane / kWarps);
+    cluster_barrier();  // (the sums are read: the next round, or the exit, may follow)
     const double upto = warp_scan(s0 + s1, lane);
     const double sum = __shfl_sync(0xffffffffu, upto, 31);
     if (sum > 0.0) {
@@ -291,20 +275,7 @@ __global__ void __launch_bounds__(kWarps * 32) verify_kernel(const VerifyArgs a)
 
 template <typename E>
 cudaError_t launch(const VerifyArgs& a, int B, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster, B);
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<E>, a);
+  return launch_pdl_clusters(verify_kernel<E>, dim3(kCluster, B), dim3(kWarps * 32), kCluster, 0, st, a);
 }
 
 }  // namespace

@@ -501,6 +501,39 @@ moe_status moe_verify_drafts(const void* target, moe_dtype dtype, int64_t ldt, c
                              int R, int V, const int32_t* drafts, const int32_t* offsets, int B, const float* u,
                              const float* u_sample, int32_t* tokens, int32_t* accepted, moe_stream_t stream);
 
+/*
+ * Low-rank adapters of many requests beside a shared projection.  Source: the projections of "DeepSeek V4.1F Q4
+ * with native DSpark MTP on M3 Ultra", Decode and DSpark paragraphs; the adapters have no counterpart on the pages.
+ *   out[t] = base[t] + B_a (s_a A_a x[t]),  a = ids[t];  out[t] = base[t] where ids[t] == -1 or slot a is empty.
+ * A handle holds n slots of one shape: A_a [r_a][K], B_a [N][r_a], r_a <= r_max, s_a a number.
+ *   moe_adapters_create     1 <= n <= 1024, 1 <= N, K <= 2^20, 1 <= r_max <= 128; dtype (bf16 or fp16) is that of A,
+ *                           B and x.  Host only.  (Ranks are held padded to 16, 32, 64 or 128 of r_max.)
+ *   moe_adapters_set        contiguous A and B (device) copied into slot `slot` of the handle's memory in the kernel's
+ *                           layout; r = 0 empties the slot.  Synchronous (waits for the device); other slots' contents
+ *                           are kept, so that adapters come and go while the handle serves.
+ *   ..._workspace_bytes / set_workspace   caller-owned memory for grouping up to T_max rows, 256-byte aligned; one call
+ *                           at a time uses it (order them on a stream).
+ *   moe_adapters_forward    x [T][K] (pitch ldx), ids int32 [T], base [T][N] (pitch ldb; NULL: zero) and out [T][N]
+ *                           (pitch ldo) of out_dtype (bf16, fp16 or fp32).  base may be out (same pitch), else they do not
+ *                           overlap.  Rows may ask for any adapters in any order.  An id outside [-1, n) sets
+ *                           MOE_DEVERR_EXPERT_RANGE and counts as -1.
+ *   moe_adapters_get_device_error   as moe_plan_get_device_error, for the handle's calls.
+ * Both products accumulate in fp32; u = s_a A_a x is held as two terms of the 16-bit type (relative error 2^-16 of
+ * u in bf16, 2^-22 of a row's largest u in fp16); base is added in fp32 and the sum rounded once.
+ * The forward call only enqueues work; a NULL or not-ready handle, T < 0 or T > T_max, a pitch below the width or an
+ * unknown type is an error before any launch.
+ */
+typedef struct moe_adapters moe_adapters; /* opaque */
+
+moe_adapters* moe_adapters_create(int n, int N, int K, int r_max, moe_dtype dtype);
+void moe_adapters_destroy(moe_adapters* h);
+moe_status moe_adapters_set(moe_adapters* h, int slot, const void* a, const void* b, int r, float scale);
+size_t moe_adapters_workspace_bytes(const moe_adapters* h, int T_max);
+moe_status moe_adapters_set_workspace(moe_adapters* h, void* dev_ptr, size_t bytes, int T_max);
+moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64_t ldx, int T, const int32_t* ids, const void* base,
+                                int64_t ldb, void* out, moe_dtype out_dtype, int64_t ldo, moe_stream_t stream);
+moe_status moe_adapters_get_device_error(moe_adapters* h, uint32_t* code);
+
 #ifdef __cplusplus
 }
 #endif
