@@ -41,65 +41,39 @@ MOE_DEVICE void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight elements of a row of x from column c (zeros past K).
-MOE_DEVICE uint4 load_x(const uint16_t* row, int c, int K, bool vec) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (vec) {
-    if (c < K) v = *reinterpret_cast<const uint4*>(row + c);
-  } else {
-    uint32_t w[4];
+// Eight elements of a row of x from column c (zeros past K), at any alignment.
+MOE_DEVICE uint4 load_x(const uint16_t* row, int c, int K) {
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = c + 2 * i < K ? row[c + 2 * i] : 0u, hi = c + 2 * i + 1 < K ? row[c + 2 * i + 1] : 0u;
-      w[i] = lo | (hi << 16);
-    }
-    v = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = c + 2 * i < K ? row[c + 2 * i] : 0u, hi = c + 2 * i + 1 < K ? row[c + 2 * i + 1] : 0u;
+    w[i] = lo | (hi << 16);
   }
-  return v;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// out[c .. c + 7] = base + v, one rounding.
-template <typename E>
-MOE_DEVICE void add_store(const E* base, E* out, int c, int N, bool vec, const float (&v)[8]) {
-  if (vec) {
-    if (c >= N) return;
-    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (base) {
-      Raw8<E> r;
-      r.load(base + c);
-      r.to_f32(f);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] += v[i];
-    store8(out + c, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < N) out[c + i] = E::of((base ? base[c + i].f32() : 0.0f) + v[i]);
-  }
-}
-MOE_DEVICE void add_store(const AdapterArgs& p, int64_t row, int c, const float (&v)[8]) {
-  const bool vec = p.out_vec;
-  if (p.out_type == MOE_BF16)
-    add_store(p.base ? static_cast<const Bf16*>(p.base) + row * p.ld_base : nullptr,
-              static_cast<Bf16*>(p.out) + row * p.ld_out, c, p.N, vec, v);
-  else if (p.out_type == MOE_FP16)
-    add_store(p.base ? static_cast<const Fp16*>(p.base) + row * p.ld_base : nullptr,
-              static_cast<Fp16*>(p.out) + row * p.ld_out, c, p.N, vec, v);
-  else
-    add_store(p.base ? static_cast<const Fp32*>(p.base) + row * p.ld_base : nullptr,
-              static_cast<Fp32*>(p.out) + row * p.ld_out, c, p.N, vec, v);
-}
-
+// Shared memory of a CTA.  Each warp has a ring of stages that its loads go through (cp.async): a stage holds a
+// chunk of 32 columns of x and of A, or a chunk of 32 features of B.  A lane reads back exactly what it copied, so
+// the ring needs no barrier.  The first stage of all warps also holds the shrink's partial sums.
 template <int M, int R>
 struct Smem {
+  static constexpr int kStageBytes = (M + R) * 64;
+  // three warps' worth of bytes in flight hide the memory's latency; two CTAs fit an SM
+  static constexpr int kStages = kStageBytes <= 3072 ? 4 : 2;
   static constexpr int kPitch = R + (R % 32 == 0 ? 16 : 0);  // 16-bit elements: rows 8 apart share no bank
-  float warp_part[kWarps][M][R];
-  float part[M][R];
+  static constexpr int kSlots = kWarps / 2;                  // partial sums are joined in pairs first
+  union {
+    uint8_t ring[kStages][kWarps][kStageBytes];
+    struct {
+      float warp_part[kSlots][M][R];
+      float part[M][R];
+    };
+  };
   alignas(16) uint16_t u[2][M][kPitch];  // hi, lo
   float row_scale[M];                    // (fp16) the power of two that a row's u was divided by
   int rows[M];                           // the tile's rows, -1 past the last
   uint32_t match[kAdapterScan / 32];
+  static_assert((kSlots + 1) * M * R * 4 <= kWarps * kStageBytes, "the partial sums fit one stage");
 };
 
 // The tile of the cluster: small steps look for it in ids, larger ones read it from the list.  Returns the slot
@@ -142,141 +116,72 @@ MOE_DEVICE int find_tile(const AdapterArgs& p, Smem<M, R>& s) {
   return own;
 }
 
-template <int M, int R, bool kFp16>
-__global__ void __launch_bounds__(kThreads) adapter_kernel(const AdapterArgs p) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  Smem<M, R>& s = *reinterpret_cast<Smem<M, R>*>(smem_raw);
-  constexpr int MT = M / 16, NT = R / 8, RS = R / 16;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  pdl_trigger();
-  pdl_wait();
-  const int slot = find_tile(p, s);
-  if (slot == -2) return;
-  const int rank = slot >= 0 ? p.rank[slot] : 0;
-  const uint32_t cta = cluster_rank();
-  const int C = p.ctas;
-  const int nt = (rank + 7) / 8, rs = (rank + 15) / 16;
-  int row[MT][2];
+// One chunk of 32 columns of the tile's rows and of A into a stage: x pieces (row 16 m + 8 h + g, columns 8 q ..)
+// at ((2 m + h) * 32 + lane) * 16, A's fragments of 8 ranks j behind them.
+template <int M, int R>
+MOE_DEVICE void stage_shrink(const AdapterArgs& p, uint8_t* st, const int (&row)[M / 16][2], const uint4* wa, int k, int nt,
+                             int lane) {
+  const int col = 32 * k + 8 * (lane & 3);
+  uint4* x = reinterpret_cast<uint4*>(st) + lane;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) row[m][0] = s.rows[16 * m + g], row[m][1] = s.rows[16 * m + g + 8];
+  for (int m = 0; m < M / 16; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = row[m][h];
+      if (p.x_vec) {
+        const bool in = r >= 0 && col < p.K;  // (else zeros)
+        cp_async_16_part(smem_u32(x + (2 * m + h) * 32), in ? p.x + r * p.ldx + col : p.x, in ? 16u : 0u);
+      } else {
+        x[(2 * m + h) * 32] = r >= 0 ? load_x(p.x + r * p.ldx, col, p.K) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+#pragma unroll
+  for (int j = 0; j < R / 8; ++j)
+    if (j < nt) cp_async_16(smem_u32(x + (M / 8 + j) * 32), wa + (static_cast<int64_t>(k) * (R / 8) + j) * 32);
+}
 
-  if (rank > 0) {
-    // ---- shrink: this warp's chunks of 32 columns ---------------------------------------------------
-    const int nk = (p.K + 31) / 32, per = (nk + C * kWarps - 1) / (C * kWarps);
-    const int k0 = min((static_cast<int>(cta) * kWarps + warp) * per, nk), k1 = min(k0 + per, nk);
-    const uint4* wa = reinterpret_cast<const uint4*>(p.a + slot * p.a_slot) + lane;
-    float acc[MT][NT][4];
+// One chunk of 32 features of B into a stage.
+template <int R>
+MOE_DEVICE void stage_expand(uint8_t* st, const uint4* wb, int c, int rs, int lane) {
+  uint4* w = reinterpret_cast<uint4*>(st) + lane;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
-#pragma unroll 2
-    for (int k = k0; k < k1; ++k) {
-      uint4 w[NT], x[MT][2];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          x[m][h] = make_uint4(0u, 0u, 0u, 0u);
-          if (row[m][h] >= 0) x[m][h] = load_x(p.x + row[m][h] * p.ldx, 32 * k + 8 * q, p.K, p.x_vec);
-        }
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (j < nt) w[j] = wa[(static_cast<int64_t>(k) * NT + j) * 32];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if (j < nt) {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            mma<kFp16>(acc[m][j], x[m][0].x, x[m][1].x, x[m][0].y, x[m][1].y, w[j].x, w[j].y);
-            mma<kFp16>(acc[m][j], x[m][0].z, x[m][1].z, x[m][0].w, x[m][1].w, w[j].z, w[j].w);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        *reinterpret_cast<float2*>(&s.warp_part[warp][16 * m + g][8 * j + 2 * q]) = make_float2(acc[m][j][0], acc[m][j][1]);
-        *reinterpret_cast<float2*>(&s.warp_part[warp][16 * m + g + 8][8 * j + 2 * q]) =
-            make_float2(acc[m][j][2], acc[m][j][3]);
-      }
-    __syncthreads();
-    for (int i = threadIdx.x * 4; i < M * R; i += kThreads * 4) {
-      float4 v = *reinterpret_cast<const float4*>(&s.warp_part[0][0][0] + i);
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        const float4 o = *reinterpret_cast<const float4*>(&s.warp_part[w][0][0] + i);
-        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-      }
-      *reinterpret_cast<float4*>(&s.part[0][0] + i) = v;
-    }
-    cluster_barrier();
-    // ---- u of the tile, from the cluster's partial sums in order of rank; eight ranks a thread -------------
-    const float scale = p.scale[slot];
-    for (int i = threadIdx.x * 8; i < M * R; i += kThreads * 8) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int c = 0; c < C; ++c) {
-        const float4 o0 = ld_cluster_f32x4(&s.part[0][0] + i, c), o1 = ld_cluster_f32x4(&s.part[0][0] + i + 4, c);
-        v[0] += o0.x, v[1] += o0.y, v[2] += o0.z, v[3] += o0.w;
-        v[4] += o1.x, v[5] += o1.y, v[6] += o1.z, v[7] += o1.w;
-      }
-      const int r = i / R, c = i % R;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e >= rank) v[e] = 0.0f;  // (an infinite x makes NaN of the padding)
-      float mul = scale;
-      if (kFp16) {
-        float big = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(v[e] * scale));
-#pragma unroll
-        for (int o = 1; o < R / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        // 2^e with big in [2^e, 2^(e+1)); 1 for zero, infinity and NaN; 2^-126 .. 2^126
-        const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-        const int e2 = ex == -127 || ex == 128 ? 0 : max(-126, min(126, ex));
-        if (c == 0) s.row_scale[r] = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * scale * down;
-        mul = 1.0f;
-      }
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float a0 = v[e] * mul, a1 = v[e + 1] * mul;
-        float h0, h1;
-        if (kFp16) {
-          hi[e / 2] = pack_f16x2(a0, a1);
-          h0 = f16_bits_to_f32(hi[e / 2] & 0xffffu), h1 = f16_bits_to_f32(hi[e / 2] >> 16);
-        } else {
-          hi[e / 2] = pack_bf16x2(a0, a1);
-          h0 = bf16_bits_to_f32(hi[e / 2] & 0xffffu), h1 = bf16_bits_to_f32(hi[e / 2] >> 16);
-        }
-        // (an infinity has no rest)
-        const float l0 = isfinite(h0) ? a0 - h0 : 0.0f, l1 = isfinite(h1) ? a1 - h1 : 0.0f;
-        lo[e / 2] = kFp16 ? pack_f16x2(l0, l1) : pack_bf16x2(l0, l1);
-      }
-      *reinterpret_cast<uint4*>(&s.u[0][r][c]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(&s.u[1][r][c]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-    cluster_barrier();  // u is written, and no CTA's partial sums are read any more
-  }
+  for (int k = 0; k < R / 8; ++k)
+    if (k < 2 * rs) cp_async_16(smem_u32(w + k * 32), wb + (static_cast<int64_t>(c) * (R / 8) + k) * 32);
+}
 
-  // ---- expand: this warp's chunks of 32 features -----------------------------------------------------
-  if (rank == 0 && p.base == p.out) return;
-  const int nc = (p.N + 31) / 32, per = (nc + C * kWarps - 1) / (C * kWarps);
-  const int c0 = min((static_cast<int>(cta) * kWarps + warp) * per, nc), c1 = min(c0 + per, nc);
-  const uint4* wb = reinterpret_cast<const uint4*>(p.b + (rank > 0 ? slot * p.b_slot : 0)) + lane;
+// The expand's loop over the warp's chunks of features.  The first kStages - 1 chunks are on their way already, in
+// the stages from 1 on; the base's rows of the next chunk are requested before the products of this one.
+template <typename E, int M, int R, bool kFp16>
+MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const int (&row)[M / 16][2], const uint4* wb, int c0, int c1,
+                       int rank, int lane, int warp) {
+  constexpr int MT = M / 16, RS = R / 16, kStages = Smem<M, R>::kStages;
+  const int g = lane >> 2, q = lane & 3, rs = (rank + 15) / 16;
+  const E* base = static_cast<const E*>(p.base);
+  E* out = static_cast<E*>(p.out);
+  const bool ahead = base && p.out_vec;
+  Raw8<E> next[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      next[m][h].zero();
+      if (ahead && row[m][h] >= 0 && c0 < c1 && 32 * c0 + 8 * q < p.N) next[m][h].load(base + row[m][h] * p.ld_base + 32 * c0 + 8 * q);
+    }
+  int slot = 1 % kStages, fill = 0;
   for (int c = c0; c < c1; ++c) {
-    uint4 w[RS][2];
+    if (c + kStages - 1 < c1) stage_expand<R>(s.ring[fill][warp], wb, c + kStages - 1, rs, lane);
+    cp_async_commit();
+    Raw8<E> cur[MT][2];
 #pragma unroll
-    for (int k = 0; k < RS; ++k)
-      if (k < rs) {
-        w[k][0] = wb[((static_cast<int64_t>(c) * RS + k) * 2 + 0) * 32];
-        w[k][1] = wb[((static_cast<int64_t>(c) * RS + k) * 2 + 1) * 32];
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        cur[m][h] = next[m][h];
+        if (ahead && row[m][h] >= 0 && c + 1 < c1 && 32 * (c + 1) + 8 * q < p.N)
+          next[m][h].load(base + row[m][h] * p.ld_base + 32 * (c + 1) + 8 * q);
       }
+    cp_async_wait<kStages - 1>();
+    const uint4* w = reinterpret_cast<const uint4*>(s.ring[slot][warp]) + lane;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       float acc[4][4];
@@ -285,28 +190,197 @@ __global__ void __launch_bounds__(kThreads) adapter_kernel(const AdapterArgs p) 
 #pragma unroll
       for (int k = 0; k < RS; ++k)
         if (k < rs) {
+          const uint4 w0 = w[2 * k * 32], w1 = w[(2 * k + 1) * 32];
 #pragma unroll
           for (int t = 0; t < 2; ++t) {  // hi, lo
-            const uint2 lo = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g][16 * k + 4 * q]);
-            const uint2 up = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g + 8][16 * k + 4 * q]);
-            mma<kFp16>(acc[0], lo.x, up.x, lo.y, up.y, w[k][0].x, w[k][0].y);
-            mma<kFp16>(acc[1], lo.x, up.x, lo.y, up.y, w[k][0].z, w[k][0].w);
-            mma<kFp16>(acc[2], lo.x, up.x, lo.y, up.y, w[k][1].x, w[k][1].y);
-            mma<kFp16>(acc[3], lo.x, up.x, lo.y, up.y, w[k][1].z, w[k][1].w);
+            const uint2 a = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g][16 * k + 4 * q]);
+            const uint2 b = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g + 8][16 * k + 4 * q]);
+            mma<kFp16>(acc[0], a.x, b.x, a.y, b.y, w0.x, w0.y);
+            mma<kFp16>(acc[1], a.x, b.x, a.y, b.y, w0.z, w0.w);
+            mma<kFp16>(acc[2], a.x, b.x, a.y, b.y, w1.x, w1.y);
+            mma<kFp16>(acc[3], a.x, b.x, a.y, b.y, w1.z, w1.w);
           }
         }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (row[m][h] < 0) continue;
-        float f = 1.0f;
-        if (kFp16 && rank > 0) f = s.row_scale[16 * m + g + 8 * h];
+        const float f = kFp16 && rank > 0 ? s.row_scale[16 * m + g + 8 * h] : 1.0f;
         float v[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[2 * j] = acc[j][2 * h] * f, v[2 * j + 1] = acc[j][2 * h + 1] * f;
-        add_store(p, row[m][h], 32 * c + 8 * q, v);
+        const int col = 32 * c + 8 * q;
+        E* o = out + row[m][h] * p.ld_out;
+        if (p.out_vec) {
+          float b[8];
+          cur[m][h].to_f32(b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += b[i];
+          if (col < p.N) store8(o + col, v);
+        } else {
+          const E* bs = base + (base ? row[m][h] * p.ld_base : 0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (col + i < p.N) o[col + i] = E::of((base ? bs[col + i].f32() : 0.0f) + v[i]);
+        }
       }
     }
+    slot = slot + 1 == kStages ? 0 : slot + 1;
+    fill = fill + 1 == kStages ? 0 : fill + 1;
   }
+}
+
+template <int M, int R, bool kFp16>
+__global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Smem<M, R>& s = *reinterpret_cast<Smem<M, R>*>(smem_raw);
+  constexpr int MT = M / 16, NT = R / 8, kStages = Smem<M, R>::kStages, kSlots = Smem<M, R>::kSlots;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  pdl_trigger();
+  pdl_wait();
+  const int slot = find_tile(p, s);
+  if (slot == -2) return;
+  const int rank = slot >= 0 ? p.rank[slot] : 0;
+  if (rank == 0 && p.base == p.out) return;
+  const int cta = cluster_rank(), C = p.ctas;
+  int row[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) row[m][0] = s.rows[16 * m + g], row[m][1] = s.rows[16 * m + g + 8];
+  // this warp's chunks of 32 features
+  const int nc = (p.N + 31) / 32, per_n = (nc + C * kWarps - 1) / (C * kWarps);
+  const int c0 = min((cta * kWarps + warp) * per_n, nc), c1 = min(c0 + per_n, nc);
+  const uint4* wb = reinterpret_cast<const uint4*>(p.b + (rank > 0 ? slot * p.b_slot : 0)) + lane;
+
+  if (rank > 0) {
+    // ---- shrink: this warp's chunks of 32 columns ---------------------------------------------------
+    const int nt = (rank + 7) / 8;
+    const int nk = (p.K + 31) / 32, per = (nk + C * kWarps - 1) / (C * kWarps);
+    const int k0 = min((cta * kWarps + warp) * per, nk), k1 = min(k0 + per, nk);
+    const uint4* wa = reinterpret_cast<const uint4*>(p.a + slot * p.a_slot) + lane;
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (k0 + i < k1) stage_shrink<M, R>(p, s.ring[i][warp], row, wa, k0 + i, nt, lane);
+      cp_async_commit();
+    }
+    int from = 0, fill = kStages - 1;
+    for (int k = k0; k < k1; ++k) {
+      if (k + kStages - 1 < k1) stage_shrink<M, R>(p, s.ring[fill][warp], row, wa, k + kStages - 1, nt, lane);
+      cp_async_commit();
+      cp_async_wait<kStages - 1>();
+      const uint4* st = reinterpret_cast<const uint4*>(s.ring[from][warp]) + lane;
+      uint4 x[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) x[m][0] = st[2 * m * 32], x[m][1] = st[(2 * m + 1) * 32];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        if (j < nt) {
+          const uint4 w = st[(M / 8 + j) * 32];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            mma<kFp16>(acc[m][j], x[m][0].x, x[m][1].x, x[m][0].y, x[m][1].y, w.x, w.y);
+            mma<kFp16>(acc[m][j], x[m][0].z, x[m][1].z, x[m][0].w, x[m][1].w, w.z, w.w);
+          }
+        }
+      from = from + 1 == kStages ? 0 : from + 1;
+      fill = fill + 1 == kStages ? 0 : fill + 1;
+    }
+    __syncthreads();  // no warp reads its ring any more
+    // B's first chunks are on their way while u is put together (into the stages that hold no sums)
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (c0 + i < c1) stage_expand<R>(s.ring[i + 1][warp], wb, c0 + i, (rank + 15) / 16, lane);
+      cp_async_commit();
+    }
+    // ---- u: the warps' sums in pairs, then the pairs, then the CTAs, in order ---------------------------
+    if (warp >= kSlots) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float(*o)[R] = s.warp_part[warp - kSlots];
+          *reinterpret_cast<float2*>(&o[16 * m + g][8 * j + 2 * q]) = make_float2(acc[m][j][0], acc[m][j][1]);
+          *reinterpret_cast<float2*>(&o[16 * m + g + 8][8 * j + 2 * q]) = make_float2(acc[m][j][2], acc[m][j][3]);
+        }
+    }
+    __syncthreads();
+    if (warp < kSlots) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float(*o)[R] = s.warp_part[warp];
+          float2* lo = reinterpret_cast<float2*>(&o[16 * m + g][8 * j + 2 * q]);
+          float2* up = reinterpret_cast<float2*>(&o[16 * m + g + 8][8 * j + 2 * q]);
+          *lo = make_float2(acc[m][j][0] + lo->x, acc[m][j][1] + lo->y);
+          *up = make_float2(acc[m][j][2] + up->x, acc[m][j][3] + up->y);
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x * 4; i < M * R; i += kThreads * 4) {
+      float4 v = *reinterpret_cast<const float4*>(&s.warp_part[0][0][0] + i);
+#pragma unroll
+      for (int w = 1; w < kSlots; ++w) {
+        const float4 o = *reinterpret_cast<const float4*>(&s.warp_part[w][0][0] + i);
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+      }
+      *reinterpret_cast<float4*>(&s.part[0][0] + i) = v;
+    }
+    cluster_barrier();
+    const float scale = p.scale[slot];
+    for (int i = threadIdx.x * 8; i < M * R; i += kThreads * 8) {  // eight ranks a thread
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < C; ++c) {
+        const float4 o0 = ld_cluster_f32x4(&s.part[0][0] + i, c), o1 = ld_cluster_f32x4(&s.part[0][0] + i + 4, c);
+        v[0] += o0.x, v[1] += o0.y, v[2] += o0.z, v[3] += o0.w;
+        v[4] += o1.x, v[5] += o1.y, v[6] += o1.z, v[7] += o1.w;
+      }
+      const int r = i / R, c = i % R;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = c + e < rank ? v[e] * scale : 0.0f;  // (an infinite x makes NaN of the padding)
+      if (kFp16) {
+        float big = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(v[e]));
+#pragma unroll
+        for (int o = 1; o < R / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        // 2^e with big in [2^e, 2^(e+1)); 1 for zero, infinity and NaN; 2^-126 .. 2^126
+        const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+        const int e2 = ex == -127 || ex == 128 ? 0 : max(-126, min(126, ex));
+        if (c == 0) s.row_scale[r] = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= down;
+      }
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        float h0, h1;
+        if (kFp16) {
+          hi[e / 2] = pack_f16x2(v[e], v[e + 1]);
+          h0 = f16_bits_to_f32(hi[e / 2] & 0xffffu), h1 = f16_bits_to_f32(hi[e / 2] >> 16);
+        } else {
+          hi[e / 2] = pack_bf16x2(v[e], v[e + 1]);
+          h0 = bf16_bits_to_f32(hi[e / 2] & 0xffffu), h1 = bf16_bits_to_f32(hi[e / 2] >> 16);
+        }
+        // (an infinity has no rest)
+        const float l0 = isfinite(h0) ? v[e] - h0 : 0.0f, l1 = isfinite(h1) ? v[e + 1] - h1 : 0.0f;
+        lo[e / 2] = kFp16 ? pack_f16x2(l0, l1) : pack_bf16x2(l0, l1);
+      }
+      *reinterpret_cast<uint4*>(&s.u[0][r][c]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(&s.u[1][r][c]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    cluster_barrier();  // u is written, and no CTA's partial sums are read any more
+  }
+  if (p.out_type == MOE_BF16)
+    expand<Bf16, M, R, kFp16>(p, s, row, wb, c0, c1, rank, lane, warp);
+  else if (p.out_type == MOE_FP16)
+    expand<Fp16, M, R, kFp16>(p, s, row, wb, c0, c1, rank, lane, warp);
+  else
+    expand<Fp32, M, R, kFp16>(p, s, row, wb, c0, c1, rank, lane, warp);
 }
 
 // ---- packing -------------------------------------------------------------------------------------------
@@ -414,8 +488,8 @@ cudaError_t launch(AdapterArgs p, int clusters, int C, cudaStream_t st) {
   return launch_pdl_clusters(kern, dim3(C * clusters), dim3(kThreads), C, smem, st, p);
 }
 
-// Rows of a grouped tile: M R values of u, 64 accumulator registers a lane.
-constexpr int tile_rows(int rpad) { return rpad <= 32 ? 64 : 2048 / rpad; }
+// Rows of a grouped tile: M R / 32 accumulator registers a lane, and twice M / 2 for the fp32 base ahead.
+constexpr int tile_rows(int rpad) { return rpad <= 64 ? 32 : 16; }
 
 template <int R, bool kFp16>
 cudaError_t launch_rank(const AdapterArgs& p, int num_sms, cudaStream_t st) {
