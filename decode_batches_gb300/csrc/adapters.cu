@@ -28,13 +28,13 @@ constexpr int kWarps = kThreads / 32;
 template <bool kFp16>
 MOE_DEVICE void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if (kFp16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -58,7 +58,7 @@ MOE_DEVICE uint4 load_x(const uint16_t* row, int c, int K) {
 template <int M, int R>
 struct Smem {
   static constexpr int kStageBytes = (M + R) * 64;
-  // three warps' worth of bytes in flight hide the memory's latency; two CTAs fit an SM
+  // two CTAs fit an SM
   static constexpr int kStages = kStageBytes <= 3072 ? 4 : 2;
   static constexpr int kPitch = R + (R % 32 == 0 ? 16 : 0);  // 16-bit elements: rows 8 apart share no bank
   static constexpr int kSlots = kWarps / 2;                  // partial sums are joined in pairs first
@@ -76,26 +76,29 @@ struct Smem {
   static_assert((kSlots + 1) * M * R * 4 <= kWarps * kStageBytes, "the partial sums fit one stage");
 };
 
-// The tile of the cluster: small steps look for it in ids, larger ones read it from the list.  Returns the slot
-// (-1: no adapter), or -2: nothing to do.  The same for every thread of the cluster.
+// The tile of the cluster: its rows go to s.rows; small steps look for it in ids, larger ones read it from the list.
+// Returns whether there is one, with its slot (-1: no adapter) and rank.  The same for every thread of the cluster.
 template <int M, int R>
-MOE_DEVICE int find_tile(const AdapterArgs& p, Smem<M, R>& s) {
+MOE_DEVICE bool find_tile(const AdapterArgs& p, Smem<M, R>& s, int& slot, int& rank) {
   const int idx = blockIdx.x / p.ctas;
-  if (threadIdx.x < M) s.rows[threadIdx.x] = -1;
   if (p.tiles) {
-    if (idx >= *p.n_tiles) return -2;
-    const AdapterTile t = p.tiles[idx];
+    const int n = *p.n_tiles;
+    const AdapterTile t = p.tiles[idx];  // (the list has an entry for every cluster of the grid)
+    if (idx >= n) return false;
+    if (threadIdx.x < M) s.rows[threadIdx.x] = threadIdx.x < t.rows ? p.order[t.start + threadIdx.x] : -1;
     __syncthreads();
-    if (threadIdx.x < t.rows) s.rows[threadIdx.x] = p.order[t.start + threadIdx.x];
-    __syncthreads();
-    return t.slot;
+    slot = t.slot, rank = t.rank;
+    return true;
   }
   // Rows of equal id, 0, 1, 2, ... in order: row idx leads a tile when its number is a multiple of M.
+  if (threadIdx.x < M) s.rows[threadIdx.x] = -1;
   int own = p.ids[idx];
   if (own < -1 || own >= p.n) {
     if (threadIdx.x == 0) set_error(p.err, MOE_DEVERR_EXPERT_RANGE);
     own = -1;
   }
+  slot = own;
+  rank = own >= 0 ? p.rank[own] : 0;
   int id = threadIdx.x < p.T ? p.ids[threadIdx.x] : -2;
   if (threadIdx.x < p.T && (id < -1 || id >= p.n)) id = -1;
   const uint32_t m = __ballot_sync(0xffffffffu, id == own);
@@ -109,76 +112,91 @@ MOE_DEVICE int find_tile(const AdapterArgs& p, Smem<M, R>& s) {
     before_me += me >= 32 ? __popc(b) : me > 0 ? __popc(b & ((1u << me) - 1u)) : 0;
     before_idx += ix >= 32 ? __popc(b) : ix > 0 ? __popc(b & ((1u << ix) - 1u)) : 0;
   }
-  if (before_idx % M) return -2;
+  if (before_idx % M) return false;
   const int at = before_me - before_idx;
   if (id == own && at >= 0 && at < M) s.rows[at] = threadIdx.x;
   __syncthreads();
-  return own;
+  return true;
 }
 
 // One chunk of 32 columns of the tile's rows and of A into a stage: x pieces (row 16 m + 8 h + g, columns 8 q ..)
 // at ((2 m + h) * 32 + lane) * 16, A's fragments of 8 ranks j behind them.
-template <int M, int R>
-MOE_DEVICE void stage_shrink(const AdapterArgs& p, uint8_t* st, const int (&row)[M / 16][2], const uint4* wa, int k, int nt,
-                             int lane) {
+// kAll: the ranks are taken whole (zeros behind a slot's own); else those of the slot's rank alone.
+template <int M, int R, bool kAll>
+MOE_DEVICE void stage_shrink(const AdapterArgs& p, uint8_t* st, const uint16_t* const (&x_row)[M / 16][2], const uint4* wa,
+                             int k, int nt, int lane) {
   const int col = 32 * k + 8 * (lane & 3);
   uint4* x = reinterpret_cast<uint4*>(st) + lane;
+  if (p.x_vec && 32 * k + 32 <= p.K) {
 #pragma unroll
-  for (int m = 0; m < M / 16; ++m)
+    for (int i = 0; i < M / 8; ++i) cp_async_16(smem_u32(x + i * 32), x_row[i / 2][i % 2] + 32 * k);
+  } else if (p.x_vec) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = row[m][h];
-      if (p.x_vec) {
-        const bool in = r >= 0 && col < p.K;  // (else zeros)
-        cp_async_16_part(smem_u32(x + (2 * m + h) * 32), in ? p.x + r * p.ldx + col : p.x, in ? 16u : 0u);
-      } else {
-        x[(2 * m + h) * 32] = r >= 0 ? load_x(p.x + r * p.ldx, col, p.K) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
+    for (int i = 0; i < M / 8; ++i)
+      cp_async_16_part(smem_u32(x + i * 32), col < p.K ? x_row[i / 2][i % 2] + 32 * k : p.x, col < p.K ? 16u : 0u);
+  } else {
+    for (int i = 0; i < M / 8; ++i) x[i * 32] = load_x(x_row[i / 2][i % 2] - 8 * (lane & 3), col, p.K);
+  }
 #pragma unroll
   for (int j = 0; j < R / 8; ++j)
-    if (j < nt) cp_async_16(smem_u32(x + (M / 8 + j) * 32), wa + (static_cast<int64_t>(k) * (R / 8) + j) * 32);
+    if (kAll || j < nt) cp_async_16(smem_u32(x + (M / 8 + j) * 32), wa + (static_cast<int64_t>(k) * (R / 8) + j) * 32);
 }
 
 // One chunk of 32 features of B into a stage.
-template <int R>
+template <int R, bool kAll>
 MOE_DEVICE void stage_expand(uint8_t* st, const uint4* wb, int c, int rs, int lane) {
   uint4* w = reinterpret_cast<uint4*>(st) + lane;
 #pragma unroll
   for (int k = 0; k < R / 8; ++k)
-    if (k < 2 * rs) cp_async_16(smem_u32(w + k * 32), wb + (static_cast<int64_t>(c) * (R / 8) + k) * 32);
+    if (kAll || k < 2 * rs) cp_async_16(smem_u32(w + k * 32), wb + (static_cast<int64_t>(c) * (R / 8) + k) * 32);
 }
 
 // The expand's loop over the warp's chunks of features.  The first kStages - 1 chunks are on their way already, in
-// the stages from 1 on; the base's rows of the next chunk are requested before the products of this one.
-template <typename E, int M, int R, bool kFp16>
-MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const int (&row)[M / 16][2], const uint4* wb, int c0, int c1,
-                       int rank, int lane, int warp) {
+// the stages from 1 on; u's fragments stay in registers where there
+// are few, the base's rows are requested before the products.
+template <typename E, int M, int R, bool kFp16, bool kAll>
+MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const uint4* wb, int c0, int c1, int rank, int lane, int warp) {
   constexpr int MT = M / 16, RS = R / 16, kStages = Smem<M, R>::kStages;
   const int g = lane >> 2, q = lane & 3, rs = (rank + 15) / 16;
-  const E* base = static_cast<const E*>(p.base);
-  E* out = static_cast<E*>(p.out);
-  const bool ahead = base && p.out_vec;
-  Raw8<E> next[MT][2];
+  const E* base[MT][2];
+  E* out[MT][2];
+  float mul[MT][2];
+  uint32_t live = 0;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      next[m][h].zero();
-      if (ahead && row[m][h] >= 0 && c0 < c1 && 32 * c0 + 8 * q < p.N) next[m][h].load(base + row[m][h] * p.ld_base + 32 * c0 + 8 * q);
+      const int r = s.rows[16 * m + g + 8 * h];
+      if (r >= 0) live |= 1u << (2 * m + h);
+      base[m][h] = p.base ? static_cast<const E*>(p.base) + max(r, 0) * p.ld_base + 8 * q : nullptr;
+      out[m][h] = static_cast<E*>(p.out) + max(r, 0) * p.ld_out + 8 * q;
+      mul[m][h] = kFp16 && rank > 0 ? s.row_scale[16 * m + g + 8 * h] : 1.0f;
     }
+  constexpr bool kHold = MT * RS <= 4;
+  uint2 u[kHold ? MT : 1][kHold ? RS : 1][2][2];  // [.][.][hi, lo][row g, row g + 8]
+#pragma unroll
+  for (int m = 0; m < (kHold ? MT : 0); ++m)
+#pragma unroll
+    for (int k = 0; k < RS; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          u[m][k][t][h] = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g + 8 * h][16 * k + 4 * q]);
   int slot = 1 % kStages, fill = 0;
   for (int c = c0; c < c1; ++c) {
-    if (c + kStages - 1 < c1) stage_expand<R>(s.ring[fill][warp], wb, c + kStages - 1, rs, lane);
+    if (rank > 0 && c + kStages - 1 < c1) stage_expand<R, kAll>(s.ring[fill][warp], wb, c + kStages - 1, rs, lane);
     cp_async_commit();
-    Raw8<E> cur[MT][2];
+    const bool in = 32 * c + 8 * q < p.N;
+    Raw8<E> b[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        cur[m][h] = next[m][h];
-        if (ahead && row[m][h] >= 0 && c + 1 < c1 && 32 * (c + 1) + 8 * q < p.N)
-          next[m][h].load(base + row[m][h] * p.ld_base + 32 * (c + 1) + 8 * q);
+        if (p.base && p.out_vec && in && (live >> (2 * m + h) & 1u))
+          b[m][h].load(base[m][h] + 32 * c);
+        else
+          b[m][h].zero();
       }
     cp_async_wait<kStages - 1>();
     const uint4* w = reinterpret_cast<const uint4*>(s.ring[slot][warp]) + lane;
@@ -187,40 +205,43 @@ MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const int (&row)[M /
       float acc[4][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+      if (rank > 0) {
 #pragma unroll
-      for (int k = 0; k < RS; ++k)
-        if (k < rs) {
-          const uint4 w0 = w[2 * k * 32], w1 = w[(2 * k + 1) * 32];
+        for (int k = 0; k < RS; ++k)
+          if (kAll || k < rs) {
+            const uint4 w0 = w[2 * k * 32], w1 = w[(2 * k + 1) * 32];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {  // hi, lo
-            const uint2 a = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g][16 * k + 4 * q]);
-            const uint2 b = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g + 8][16 * k + 4 * q]);
-            mma<kFp16>(acc[0], a.x, b.x, a.y, b.y, w0.x, w0.y);
-            mma<kFp16>(acc[1], a.x, b.x, a.y, b.y, w0.z, w0.w);
-            mma<kFp16>(acc[2], a.x, b.x, a.y, b.y, w1.x, w1.y);
-            mma<kFp16>(acc[3], a.x, b.x, a.y, b.y, w1.z, w1.w);
+            for (int t = 0; t < 2; ++t) {
+              const uint2 a0 = kHold ? u[kHold ? m : 0][kHold ? k : 0][t][0]
+                                     : *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g][16 * k + 4 * q]);
+              const uint2 a1 = kHold ? u[kHold ? m : 0][kHold ? k : 0][t][1]
+                                     : *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g + 8][16 * k + 4 * q]);
+              mma<kFp16>(acc[0], a0.x, a1.x, a0.y, a1.y, w0.x, w0.y);
+              mma<kFp16>(acc[1], a0.x, a1.x, a0.y, a1.y, w0.z, w0.w);
+              mma<kFp16>(acc[2], a0.x, a1.x, a0.y, a1.y, w1.x, w1.y);
+              mma<kFp16>(acc[3], a0.x, a1.x, a0.y, a1.y, w1.z, w1.w);
+            }
           }
-        }
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (row[m][h] < 0) continue;
-        const float f = kFp16 && rank > 0 ? s.row_scale[16 * m + g + 8 * h] : 1.0f;
+        if (!(live >> (2 * m + h) & 1u)) continue;
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[2 * j] = acc[j][2 * h] * f, v[2 * j + 1] = acc[j][2 * h + 1] * f;
-        const int col = 32 * c + 8 * q;
-        E* o = out + row[m][h] * p.ld_out;
+        for (int j = 0; j < 4; ++j) v[2 * j] = acc[j][2 * h], v[2 * j + 1] = acc[j][2 * h + 1];
         if (p.out_vec) {
-          float b[8];
-          cur[m][h].to_f32(b);
+          float f[8];
+          b[m][h].to_f32(f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += b[i];
-          if (col < p.N) store8(o + col, v);
+          for (int i = 0; i < 8; ++i) v[i] = kFp16 ? fmaf(v[i], mul[m][h], f[i]) : v[i] + f[i];
+          if (in) store8(out[m][h] + 32 * c, v);
         } else {
-          const E* bs = base + (base ? row[m][h] * p.ld_base : 0);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (col + i < p.N) o[col + i] = E::of((base ? bs[col + i].f32() : 0.0f) + v[i]);
+            if (32 * c + 8 * q + i < p.N) {
+              const float f = p.base ? base[m][h][32 * c + i].f32() : 0.0f;
+              out[m][h][32 * c + i] = E::of(kFp16 ? fmaf(v[i], mul[m][h], f) : v[i] + f);
+            }
         }
       }
     }
@@ -229,7 +250,7 @@ MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const int (&row)[M /
   }
 }
 
-template <int M, int R, bool kFp16>
+template <int M, int R, bool kFp16, bool kAll>
 __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<M, R>& s = *reinterpret_cast<Smem<M, R>*>(smem_raw);
@@ -237,14 +258,10 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   pdl_trigger();
   pdl_wait();
-  const int slot = find_tile(p, s);
-  if (slot == -2) return;
-  const int rank = slot >= 0 ? p.rank[slot] : 0;
+  int slot, rank;
+  if (!find_tile(p, s, slot, rank)) return;
   if (rank == 0 && p.base == p.out) return;
   const int cta = cluster_rank(), C = p.ctas;
-  int row[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) row[m][0] = s.rows[16 * m + g], row[m][1] = s.rows[16 * m + g + 8];
   // this warp's chunks of 32 features
   const int nc = (p.N + 31) / 32, per_n = (nc + C * kWarps - 1) / (C * kWarps);
   const int c0 = min((cta * kWarps + warp) * per_n, nc), c1 = min(c0 + per_n, nc);
@@ -256,6 +273,14 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
     const int nk = (p.K + 31) / 32, per = (nk + C * kWarps - 1) / (C * kWarps);
     const int k0 = min((cta * kWarps + warp) * per, nk), k1 = min(k0 + per, nk);
     const uint4* wa = reinterpret_cast<const uint4*>(p.a + slot * p.a_slot) + lane;
+    const uint16_t* x_row[MT][2];  // (rows past the tile's last read its first: their results go nowhere)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = s.rows[16 * m + g + 8 * h];
+        x_row[m][h] = p.x + (r >= 0 ? r : s.rows[0]) * p.ldx + 8 * q;
+      }
     float acc[MT][NT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -263,12 +288,12 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
       for (int j = 0; j < NT; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-      if (k0 + i < k1) stage_shrink<M, R>(p, s.ring[i][warp], row, wa, k0 + i, nt, lane);
+      if (k0 + i < k1) stage_shrink<M, R, kAll>(p, s.ring[i][warp], x_row, wa, k0 + i, nt, lane);
       cp_async_commit();
     }
     int from = 0, fill = kStages - 1;
     for (int k = k0; k < k1; ++k) {
-      if (k + kStages - 1 < k1) stage_shrink<M, R>(p, s.ring[fill][warp], row, wa, k + kStages - 1, nt, lane);
+      if (k + kStages - 1 < k1) stage_shrink<M, R, kAll>(p, s.ring[fill][warp], x_row, wa, k + kStages - 1, nt, lane);
       cp_async_commit();
       cp_async_wait<kStages - 1>();
       const uint4* st = reinterpret_cast<const uint4*>(s.ring[from][warp]) + lane;
@@ -277,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
       for (int m = 0; m < MT; ++m) x[m][0] = st[2 * m * 32], x[m][1] = st[(2 * m + 1) * 32];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        if (j < nt) {
+        if (kAll || j < nt) {
           const uint4 w = st[(M / 8 + j) * 32];
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
@@ -292,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
     // B's first chunks are on their way while u is put together (into the stages that hold no sums)
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-      if (c0 + i < c1) stage_expand<R>(s.ring[i + 1][warp], wb, c0 + i, (rank + 15) / 16, lane);
+      if (c0 + i < c1) stage_expand<R, kAll>(s.ring[i + 1][warp], wb, c0 + i, (rank + 15) / 16, lane);
       cp_async_commit();
     }
     // ---- u: the warps' sums in pairs, then the pairs, then the CTAs, in order ---------------------------
@@ -376,11 +401,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
     cluster_barrier();  // u is written, and no CTA's partial sums are read any more
   }
   if (p.out_type == MOE_BF16)
-    expand<Bf16, M, R, kFp16>(p, s, row, wb, c0, c1, rank, lane, warp);
+    expand<Bf16, M, R, kFp16, kAll>(p, s, wb, c0, c1, rank, lane, warp);
   else if (p.out_type == MOE_FP16)
-    expand<Fp16, M, R, kFp16>(p, s, row, wb, c0, c1, rank, lane, warp);
+    expand<Fp16, M, R, kFp16, kAll>(p, s, wb, c0, c1, rank, lane, warp);
   else
-    expand<Fp32, M, R, kFp16>(p, s, row, wb, c0, c1, rank, lane, warp);
+    expand<Fp32, M, R, kFp16, kAll>(p, s, wb, c0, c1, rank, lane, warp);
 }
 
 // ---- packing -------------------------------------------------------------------------------------------
@@ -409,21 +434,25 @@ __global__ void adapter_pack_kernel(const uint16_t* a, const uint16_t* b, uint16
 }
 
 // ---- grouping of larger steps -----------------------------------------------------------------------------
-// One block: histogram of the ids (no adapter counts as slot n), exclusive scans of rows and tiles, and the rows
-// in slot order.  The order of a slot's rows is not fixed; a row's result does not depend on its place.
+// The rows in slot order and their tiles, from ids, by one cluster: each CTA counts the ids of its share of the rows
+// (no adapter counts as slot n), the counts meet in distributed shared memory, every CTA scans all slots' rows and
+// tiles, and places its rows.  The order of a slot's rows is not fixed; a row's result does not depend on its place.
 constexpr int kGroupThreads = 1024;
+constexpr int kGroupCtas = 8;
 __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int32_t* ids, int T, int n, int M,
-                                                                      int32_t* order, AdapterTile* tiles,
-                                                                      int32_t* n_tiles, uint32_t* err) {
-  __shared__ int s_count[kAdaptersMax + 1], s_row[kAdaptersMax + 1];
+                                                                      const int32_t* rank, int32_t* order,
+                                                                      AdapterTile* tiles, int32_t* n_tiles, uint32_t* err) {
+  __shared__ int s_count[kAdaptersMax + 1];                                             // of this CTA's rows
+  __shared__ int s_all[kAdaptersMax + 1], s_first[kAdaptersMax + 1], s_tile[kAdaptersMax + 1];  // of the slot
+  __shared__ int s_next[kAdaptersMax + 1];                                              // this CTA's next place
   __shared__ int s_warp[2][32];
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = cluster_rank();
   for (int i = tid; i <= n; i += kGroupThreads) s_count[i] = 0;
   __syncthreads();
   bool bad_id = false;
-  for (int i0 = 0; i0 < T; i0 += kGroupThreads) {
+  for (int i0 = cta * kGroupThreads; i0 < T; i0 += kGroupCtas * kGroupThreads) {
     const int i = i0 + tid;
     int key = -1;
     if (i < T) {
@@ -434,10 +463,15 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
     if (key >= 0 && lane == __ffs(same) - 1) atomicAdd(&s_count[key], __popc(same));
   }
   if (bad_id) set_error(err, MOE_DEVERR_EXPERT_RANGE);
-  __syncthreads();
-  // slot tid and, for the last thread, slot 1024: rows and tiles before it
-  int rows_before = 0, tiles_before = 0;
-  const int c = tid <= n ? s_count[tid] : 0;
+  cluster_barrier();
+  // slot tid: its rows in all CTAs, and in the CTAs before this one; inclusive scans of rows and tiles
+  int c = 0, before = 0;
+  if (tid <= n)
+    for (int k = 0; k < kGroupCtas; ++k) {
+      const int v = ld_cluster_s32(&s_count[tid], k);
+      c += v;
+      if (k < cta) before += v;
+    }
   int r = c, t = (c + M - 1) / M;
   for (int o = 1; o < 32; o <<= 1) {
     const int a = __shfl_up_sync(0xffffffffu, r, o), b = __shfl_up_sync(0xffffffffu, t, o);
@@ -445,24 +479,23 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
   }
   if (lane == 31) s_warp[0][warp] = r, s_warp[1][warp] = t;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) rows_before += s_warp[0][w], tiles_before += s_warp[1][w];
-  r += rows_before, t += tiles_before;  // inclusive
-  if (tid <= n) {
-    s_row[tid] = r - c;
-    for (int k = 0, at = t - (c + M - 1) / M; k * M < c; ++k)
-      tiles[at + k] = AdapterTile{tid < n ? tid : -1, r - c + k * M, min(M, c - k * M), 0};
-  }
+  for (int w = 0; w < warp; ++w) r += s_warp[0][w], t += s_warp[1][w];
+  if (tid <= n) s_all[tid] = c, s_first[tid] = r - c, s_tile[tid] = t - (c + M - 1) / M, s_next[tid] = r - c + before;
   if (tid == kGroupThreads - 1) {
-    int all = t;
     if (n == kGroupThreads) {  // the slot behind the last thread's: the rows without an adapter
-      const int cc = s_count[n];
-      s_row[n] = r;
-      for (int k = 0; k * M < cc; ++k) tiles[all++] = AdapterTile{-1, r + k * M, min(M, cc - k * M), 0};
+      int all = 0, mine = 0;
+      for (int k = 0; k < kGroupCtas; ++k) {
+        const int v = ld_cluster_s32(&s_count[n], k);
+        all += v;
+        if (k < cta) mine += v;
+      }
+      s_all[n] = all, s_first[n] = r, s_tile[n] = t, s_next[n] = r + mine;
+      t += (all + M - 1) / M;
     }
-    *n_tiles = all;
+    if (cta == 0) *n_tiles = t;
   }
-  __syncthreads();
-  for (int i0 = 0; i0 < T; i0 += kGroupThreads) {
+  cluster_barrier();  // (also: no CTA reads another's counts any more)
+  for (int i0 = cta * kGroupThreads; i0 < T; i0 += kGroupCtas * kGroupThreads) {
     const int i = i0 + tid;
     int key = -1;
     if (i < T) {
@@ -472,16 +505,21 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
     const uint32_t same = __match_any_sync(0xffffffffu, key);
     const int leader = __ffs(same) - 1;
     int at = 0;
-    if (key >= 0 && lane == leader) at = atomicAdd(&s_row[key], __popc(same));
-    at = __shfl_sync(0xffffffffu, at, leader);
-    if (key >= 0) order[at + __popc(same & ((1u << lane) - 1u))] = i;
+    if (key >= 0 && lane == leader) at = atomicAdd(&s_next[key], __popc(same));
+    at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
+    if (key < 0) continue;
+    order[at] = i;
+    const int in = at - s_first[key];
+    if (in % M == 0)  // the row that comes first in a tile writes the tile
+      tiles[s_tile[key] + in / M] =
+          AdapterTile{key < n ? key : -1, at, min(M, s_all[key] - in), key < n ? rank[key] : 0};
   }
 }
 
-template <int M, int R, bool kFp16>
+template <int M, int R, bool kFp16, bool kAll>
 cudaError_t launch(AdapterArgs p, int clusters, int C, cudaStream_t st) {
   p.ctas = C;
-  auto kern = adapter_kernel<M, R, kFp16>;
+  auto kern = adapter_kernel<M, R, kFp16, kAll>;
   const int smem = sizeof(Smem<M, R>);
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -493,9 +531,9 @@ constexpr int tile_rows(int rpad) { return rpad <= 64 ? 32 : 16; }
 
 template <int R, bool kFp16>
 cudaError_t launch_rank(const AdapterArgs& p, int num_sms, cudaStream_t st) {
-  if (!p.tiles) return launch<kAdapterRowsMin, R, kFp16>(p, p.T, 8, st);
+  if (!p.tiles) return launch<kAdapterRowsMin, R, kFp16, false>(p, p.T, 8, st);
   constexpr int M = tile_rows(R);
-  return launch<M, R, kFp16>(p, (p.T + M - 1) / M + (p.n + 1 < p.T ? p.n + 1 : p.T), 2, st);
+  return launch<M, R, kFp16, true>(p, (p.T + M - 1) / M + (p.n + 1 < p.T ? p.n + 1 : p.T), 2, st);
 }
 
 }  // namespace
@@ -510,9 +548,10 @@ cudaError_t launch_adapter_pack(const uint16_t* a, const uint16_t* b, uint16_t* 
   return cudaGetLastError();
 }
 
-cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, int32_t* order, AdapterTile* tiles,
-                                 int32_t* n_tiles, uint32_t* err, cudaStream_t st) {
-  return launch_pdl(adapter_group_kernel, dim3(1), dim3(kGroupThreads), 0, st, ids, T, n, rows, order, tiles, n_tiles, err);
+cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, const int32_t* rank, int32_t* order,
+                                 AdapterTile* tiles, int32_t* n_tiles, uint32_t* err, cudaStream_t st) {
+  return launch_pdl_clusters(adapter_group_kernel, dim3(kGroupCtas), dim3(kGroupThreads), kGroupCtas, 0, st, ids, T, n, rows,
+                             rank, order, tiles, n_tiles, err);
 }
 
 cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, int num_sms, cudaStream_t st) {

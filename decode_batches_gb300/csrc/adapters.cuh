@@ -12,7 +12,7 @@ constexpr int kAdapterRowsMin = 16;   // rows of the smallest tile
 
 // Rows [start, start + rows) of `order` that share a slot (slot -1: rows without an adapter).
 struct AdapterTile {
-  int slot, start, rows, pad;
+  int slot, start, rows, rank;
 };
 
 struct AdapterArgs {
@@ -47,8 +47,8 @@ cudaError_t launch_adapter_pack(const uint16_t* a, const uint16_t* b, uint16_t* 
                                 int rpad, cudaStream_t st);
 int adapter_tile_rows(int rpad);  // rows of a tile of the grouped path
 // order [T], tiles (at most T / rows + n + 1), n_tiles from ids; ids outside [-1, n) set MOE_DEVERR_EXPERT_RANGE.
-cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, int32_t* order, AdapterTile* tiles,
-                                 int32_t* n_tiles, uint32_t* err, cudaStream_t st);
+cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, const int32_t* rank, int32_t* order,
+                                 AdapterTile* tiles, int32_t* n_tiles, uint32_t* err, cudaStream_t st);
 cudaError_t launch_adapters(const AdapterArgs& a, int rpad, bool fp16, int num_sms, cudaStream_t st);
 
 }  // namespace moe

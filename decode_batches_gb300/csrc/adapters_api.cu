@@ -145,7 +145,7 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
     int32_t* n_tiles = reinterpret_cast<int32_t*>(h->ws);
     AdapterTile* tiles = reinterpret_cast<AdapterTile*>(h->ws + 256);
     int32_t* order = reinterpret_cast<int32_t*>(h->ws + 256 + tile_bytes(h, h->T_max));
-    LIN_TRY(launch_adapter_group(ids, T, h->n, adapter_tile_rows(h->rpad), order, tiles, n_tiles, h->err, st));
+    LIN_TRY(launch_adapter_group(ids, T, h->n, adapter_tile_rows(h->rpad), h->rank, order, tiles, n_tiles, h->err, st));
     a.order = order, a.tiles = tiles, a.n_tiles = n_tiles;
   }
   LIN_TRY(launch_adapters(a, h->rpad, h->type == MOE_FP16, h->num_sms, st));
