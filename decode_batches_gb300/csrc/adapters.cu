@@ -16,6 +16,7 @@
 // since one term's 2^-8 would dominate an fp32 result.  In fp16 a row's u is first brought to [1, 2) by a power
 // of two, so that neither term leaves the type's range.
 #include "adapters.cuh"
+#include "adapters_split.cuh"
 #include "cluster.cuh"
 #include "elems.cuh"
 
@@ -24,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kTileRows = 16;
 
 template <bool kFp16>
 MOE_DEVICE void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -39,17 +41,6 @@ MOE_DEVICE void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Eight elements of a row of x from column c (zeros past K), at any alignment.
-MOE_DEVICE uint4 load_x(const uint16_t* row, int c, int K) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = c + 2 * i < K ? row[c + 2 * i] : 0u, hi = c + 2 * i + 1 < K ? row[c + 2 * i + 1] : 0u;
-    w[i] = lo | (hi << 16);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Shared memory of a CTA.  Each warp has a ring of stages that its loads go through (cp.async): a stage holds a
@@ -76,20 +67,10 @@ struct Smem {
   static_assert((kSlots + 1) * M * R * 4 <= kWarps * kStageBytes, "the partial sums fit one stage");
 };
 
-// The tile of the cluster: its rows go to s.rows; small steps look for it in ids, larger ones read it from the list.
-// Returns whether there is one, with its slot (-1: no adapter) and rank.  The same for every thread of the cluster.
+// The tile of the cluster, found in ids: its rows go to s.rows.  Returns whether there is one, with its slot (-1: no adapter) and rank.  The same for every thread of the cluster.
 template <int M, int R>
 MOE_DEVICE bool find_tile(const AdapterArgs& p, Smem<M, R>& s, int& slot, int& rank) {
   const int idx = blockIdx.x / p.ctas;
-  if (p.tiles) {
-    const int n = *p.n_tiles;
-    const AdapterTile t = p.tiles[idx];  // (the list has an entry for every cluster of the grid)
-    if (idx >= n) return false;
-    if (threadIdx.x < M) s.rows[threadIdx.x] = threadIdx.x < t.rows ? p.order[t.start + threadIdx.x] : -1;
-    __syncthreads();
-    slot = t.slot, rank = t.rank;
-    return true;
-  }
   // Rows of equal id, 0, 1, 2, ... in order: row idx leads a tile when its number is a multiple of M.
   if (threadIdx.x < M) s.rows[threadIdx.x] = -1;
   int own = p.ids[idx];
@@ -121,8 +102,7 @@ MOE_DEVICE bool find_tile(const AdapterArgs& p, Smem<M, R>& s, int& slot, int& r
 
 // One chunk of 32 columns of the tile's rows and of A into a stage: x pieces (row 16 m + 8 h + g, columns 8 q ..)
 // at ((2 m + h) * 32 + lane) * 16, A's fragments of 8 ranks j behind them.
-// kAll: the ranks are taken whole (zeros behind a slot's own); else those of the slot's rank alone.
-template <int M, int R, bool kAll>
+template <int M, int R>
 MOE_DEVICE void stage_shrink(const AdapterArgs& p, uint8_t* st, const uint16_t* const (&x_row)[M / 16][2], const uint4* wa,
                              int k, int nt, int lane) {
   const int col = 32 * k + 8 * (lane & 3);
@@ -139,22 +119,22 @@ MOE_DEVICE void stage_shrink(const AdapterArgs& p, uint8_t* st, const uint16_t* 
   }
 #pragma unroll
   for (int j = 0; j < R / 8; ++j)
-    if (kAll || j < nt) cp_async_16(smem_u32(x + (M / 8 + j) * 32), wa + (static_cast<int64_t>(k) * (R / 8) + j) * 32);
+    if (j < nt) cp_async_16(smem_u32(x + (M / 8 + j) * 32), wa + (static_cast<int64_t>(k) * (R / 8) + j) * 32);
 }
 
 // One chunk of 32 features of B into a stage.
-template <int R, bool kAll>
+template <int R>
 MOE_DEVICE void stage_expand(uint8_t* st, const uint4* wb, int c, int rs, int lane) {
   uint4* w = reinterpret_cast<uint4*>(st) + lane;
 #pragma unroll
   for (int k = 0; k < R / 8; ++k)
-    if (kAll || k < 2 * rs) cp_async_16(smem_u32(w + k * 32), wb + (static_cast<int64_t>(c) * (R / 8) + k) * 32);
+    if (k < 2 * rs) cp_async_16(smem_u32(w + k * 32), wb + (static_cast<int64_t>(c) * (R / 8) + k) * 32);
 }
 
 // The expand's loop over the warp's chunks of features.  The first kStages - 1 chunks are on their way already, in
 // the stages from 1 on; u's fragments stay in registers where there
 // are few, the base's rows are requested before the products.
-template <typename E, int M, int R, bool kFp16, bool kAll>
+template <typename E, int M, int R, bool kFp16>
 MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const uint4* wb, int c0, int c1, int rank, int lane, int warp) {
   constexpr int MT = M / 16, RS = R / 16, kStages = Smem<M, R>::kStages;
   const int g = lane >> 2, q = lane & 3, rs = (rank + 15) / 16;
@@ -185,7 +165,7 @@ MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const uint4* wb, int
           u[m][k][t][h] = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g + 8 * h][16 * k + 4 * q]);
   int slot = 1 % kStages, fill = 0;
   for (int c = c0; c < c1; ++c) {
-    if (rank > 0 && c + kStages - 1 < c1) stage_expand<R, kAll>(s.ring[fill][warp], wb, c + kStages - 1, rs, lane);
+    if (rank > 0 && c + kStages - 1 < c1) stage_expand<R>(s.ring[fill][warp], wb, c + kStages - 1, rs, lane);
     cp_async_commit();
     const bool in = 32 * c + 8 * q < p.N;
     Raw8<E> b[MT][2];
@@ -208,7 +188,7 @@ MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const uint4* wb, int
       if (rank > 0) {
 #pragma unroll
         for (int k = 0; k < RS; ++k)
-          if (kAll || k < rs) {
+          if (k < rs) {
             const uint4 w0 = w[2 * k * 32], w1 = w[(2 * k + 1) * 32];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -250,7 +230,7 @@ MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const uint4* wb, int
   }
 }
 
-template <int M, int R, bool kFp16, bool kAll>
+template <int M, int R, bool kFp16>
 __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<M, R>& s = *reinterpret_cast<Smem<M, R>*>(smem_raw);
@@ -288,12 +268,12 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
       for (int j = 0; j < NT; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-      if (k0 + i < k1) stage_shrink<M, R, kAll>(p, s.ring[i][warp], x_row, wa, k0 + i, nt, lane);
+      if (k0 + i < k1) stage_shrink<M, R>(p, s.ring[i][warp], x_row, wa, k0 + i, nt, lane);
       cp_async_commit();
     }
     int from = 0, fill = kStages - 1;
     for (int k = k0; k < k1; ++k) {
-      if (k + kStages - 1 < k1) stage_shrink<M, R, kAll>(p, s.ring[fill][warp], x_row, wa, k + kStages - 1, nt, lane);
+      if (k + kStages - 1 < k1) stage_shrink<M, R>(p, s.ring[fill][warp], x_row, wa, k + kStages - 1, nt, lane);
       cp_async_commit();
       cp_async_wait<kStages - 1>();
       const uint4* st = reinterpret_cast<const uint4*>(s.ring[from][warp]) + lane;
@@ -302,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
       for (int m = 0; m < MT; ++m) x[m][0] = st[2 * m * 32], x[m][1] = st[(2 * m + 1) * 32];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        if (kAll || j < nt) {
+        if (j < nt) {
           const uint4 w = st[(M / 8 + j) * 32];
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
@@ -317,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
     // B's first chunks are on their way while u is put together (into the stages that hold no sums)
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-      if (c0 + i < c1) stage_expand<R, kAll>(s.ring[i + 1][warp], wb, c0 + i, (rank + 15) / 16, lane);
+      if (c0 + i < c1) stage_expand<R>(s.ring[i + 1][warp], wb, c0 + i, (rank + 15) / 16, lane);
       cp_async_commit();
     }
     // ---- u: the warps' sums in pairs, then the pairs, then the CTAs, in order ---------------------------
@@ -364,48 +344,20 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
         v[4] += o1.x, v[5] += o1.y, v[6] += o1.z, v[7] += o1.w;
       }
       const int r = i / R, c = i % R;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = c + e < rank ? v[e] * scale : 0.0f;  // (an infinite x makes NaN of the padding)
-      if (kFp16) {
-        float big = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(v[e]));
-#pragma unroll
-        for (int o = 1; o < R / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        // 2^e with big in [2^e, 2^(e+1)); 1 for zero, infinity and NaN; 2^-126 .. 2^126
-        const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-        const int e2 = ex == -127 || ex == 128 ? 0 : max(-126, min(126, ex));
-        if (c == 0) s.row_scale[r] = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= down;
-      }
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        float h0, h1;
-        if (kFp16) {
-          hi[e / 2] = pack_f16x2(v[e], v[e + 1]);
-          h0 = f16_bits_to_f32(hi[e / 2] & 0xffffu), h1 = f16_bits_to_f32(hi[e / 2] >> 16);
-        } else {
-          hi[e / 2] = pack_bf16x2(v[e], v[e + 1]);
-          h0 = bf16_bits_to_f32(hi[e / 2] & 0xffffu), h1 = bf16_bits_to_f32(hi[e / 2] >> 16);
-        }
-        // (an infinity has no rest)
-        const float l0 = isfinite(h0) ? v[e] - h0 : 0.0f, l1 = isfinite(h1) ? v[e + 1] - h1 : 0.0f;
-        lo[e / 2] = kFp16 ? pack_f16x2(l0, l1) : pack_bf16x2(l0, l1);
-      }
-      *reinterpret_cast<uint4*>(&s.u[0][r][c]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(&s.u[1][r][c]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      uint4 hi, lo;
+      const float mul = adapter_split<R, kFp16>(v, c, rank, scale, hi, lo);
+      if (kFp16 && c == 0) s.row_scale[r] = mul;
+      *reinterpret_cast<uint4*>(&s.u[0][r][c]) = hi;
+      *reinterpret_cast<uint4*>(&s.u[1][r][c]) = lo;
     }
     cluster_barrier();  // u is written, and no CTA's partial sums are read any more
   }
   if (p.out_type == MOE_BF16)
-    expand<Bf16, M, R, kFp16, kAll>(p, s, wb, c0, c1, rank, lane, warp);
+    expand<Bf16, M, R, kFp16>(p, s, wb, c0, c1, rank, lane, warp);
   else if (p.out_type == MOE_FP16)
-    expand<Fp16, M, R, kFp16, kAll>(p, s, wb, c0, c1, rank, lane, warp);
+    expand<Fp16, M, R, kFp16>(p, s, wb, c0, c1, rank, lane, warp);
   else
-    expand<Fp32, M, R, kFp16, kAll>(p, s, wb, c0, c1, rank, lane, warp);
+    expand<Fp32, M, R, kFp16>(p, s, wb, c0, c1, rank, lane, warp);
 }
 
 // ---- packing -------------------------------------------------------------------------------------------
@@ -439,9 +391,10 @@ __global__ void adapter_pack_kernel(const uint16_t* a, const uint16_t* b, uint16
 // tiles, and places its rows.  The order of a slot's rows is not fixed; a row's result does not depend on its place.
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupCtas = 8;
-__global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int32_t* ids, int T, int n, int M,
-                                                                      const int32_t* rank, int32_t* order,
-                                                                      AdapterTile* tiles, int32_t* n_tiles, uint32_t* err) {
+__global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int32_t* ids, int T, int n, const int32_t* rank,
+                                                                      int32_t* order, AdapterTile* tiles,
+                                                                      int32_t* n_tiles, uint32_t* err) {
+  constexpr int M = kAdapterTileRows;
   __shared__ int s_count[kAdaptersMax + 1];                                             // of this CTA's rows
   __shared__ int s_all[kAdaptersMax + 1], s_first[kAdaptersMax + 1], s_tile[kAdaptersMax + 1];  // of the slot
   __shared__ int s_next[kAdaptersMax + 1];                                              // this CTA's next place
@@ -510,35 +463,29 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
     if (key < 0) continue;
     order[at] = i;
     const int in = at - s_first[key];
-    if (in % M == 0)  // the row that comes first in a tile writes the tile
-      tiles[s_tile[key] + in / M] =
-          AdapterTile{key < n ? key : -1, at, min(M, s_all[key] - in), key < n ? rank[key] : 0};
+    // a slot's rows are cut evenly, in multiples of 16; the row that comes first in a tile writes the tile
+    const int all = s_all[key], parts = (all + M - 1) / M, per = ((all + parts - 1) / parts + 15) / 16 * 16;
+    if (in % per == 0)
+      tiles[s_tile[key] + in / per] = AdapterTile{key < n ? key : -1, at, min(per, all - in), key < n ? rank[key] : 0};
   }
 }
 
-template <int M, int R, bool kFp16, bool kAll>
-cudaError_t launch(AdapterArgs p, int clusters, int C, cudaStream_t st) {
-  p.ctas = C;
-  auto kern = adapter_kernel<M, R, kFp16, kAll>;
-  const int smem = sizeof(Smem<M, R>);
+template <int R, bool kFp16>
+cudaError_t launch(AdapterArgs p, cudaStream_t st) {
+  auto kern = adapter_kernel<kTileRows, R, kFp16>;
+  const int smem = sizeof(Smem<kTileRows, R>);
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_clusters(kern, dim3(C * clusters), dim3(kThreads), C, smem, st, p);
+  p.ctas = 8;
+  return launch_pdl_clusters(kern, dim3(p.T * p.ctas), dim3(kThreads), p.ctas, smem, st, p);
 }
 
-// Rows of a grouped tile: M R / 32 accumulator registers a lane, and twice M / 2 for the fp32 base ahead.
-constexpr int tile_rows(int rpad) { return rpad <= 64 ? 32 : 16; }
-
-template <int R, bool kFp16>
-cudaError_t launch_rank(const AdapterArgs& p, int num_sms, cudaStream_t st) {
-  if (!p.tiles) return launch<kAdapterRowsMin, R, kFp16, false>(p, p.T, 8, st);
-  constexpr int M = tile_rows(R);
-  return launch<M, R, kFp16, true>(p, (p.T + M - 1) / M + (p.n + 1 < p.T ? p.n + 1 : p.T), 2, st);
+template <int R>
+cudaError_t launch_rank(const AdapterArgs& p, bool fp16, cudaStream_t st) {
+  return fp16 ? launch<R, true>(p, st) : launch<R, false>(p, st);
 }
 
 }  // namespace
-
-int adapter_tile_rows(int rpad) { return tile_rows(rpad); }
 
 cudaError_t launch_adapter_pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
                                 int rpad, cudaStream_t st) {
@@ -548,18 +495,18 @@ cudaError_t launch_adapter_pack(const uint16_t* a, const uint16_t* b, uint16_t* 
   return cudaGetLastError();
 }
 
-cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, const int32_t* rank, int32_t* order,
-                                 AdapterTile* tiles, int32_t* n_tiles, uint32_t* err, cudaStream_t st) {
-  return launch_pdl_clusters(adapter_group_kernel, dim3(kGroupCtas), dim3(kGroupThreads), kGroupCtas, 0, st, ids, T, n, rows,
-                             rank, order, tiles, n_tiles, err);
+cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, const int32_t* rank, int32_t* order, AdapterTile* tiles,
+                                 int32_t* n_tiles, uint32_t* err, cudaStream_t st) {
+  return launch_pdl_clusters(adapter_group_kernel, dim3(kGroupCtas), dim3(kGroupThreads), kGroupCtas, 0, st, ids, T, n, rank,
+                             order, tiles, n_tiles, err);
 }
 
-cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, int num_sms, cudaStream_t st) {
+cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st) {
   switch (rpad) {
-    case 16: return fp16 ? launch_rank<16, true>(p, num_sms, st) : launch_rank<16, false>(p, num_sms, st);
-    case 32: return fp16 ? launch_rank<32, true>(p, num_sms, st) : launch_rank<32, false>(p, num_sms, st);
-    case 64: return fp16 ? launch_rank<64, true>(p, num_sms, st) : launch_rank<64, false>(p, num_sms, st);
-    default: return fp16 ? launch_rank<128, true>(p, num_sms, st) : launch_rank<128, false>(p, num_sms, st);
+    case 16: return launch_rank<16>(p, fp16, st);
+    case 32: return launch_rank<32>(p, fp16, st);
+    case 64: return launch_rank<64>(p, fp16, st);
+    default: return launch_rank<128>(p, fp16, st);
   }
 }
 

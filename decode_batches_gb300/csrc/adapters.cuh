@@ -8,7 +8,7 @@ namespace moe {
 constexpr int kAdaptersMax = 1024;    // slots of a handle
 constexpr int kAdapterRankMax = 128;
 constexpr int kAdapterScan = 256;     // rows up to which a cluster finds its tile itself
-constexpr int kAdapterRowsMin = 16;   // rows of the smallest tile
+constexpr int kAdapterTileRows = 128; // rows of a grouped tile
 
 // Rows [start, start + rows) of `order` that share a slot (slot -1: rows without an adapter).
 struct AdapterTile {
@@ -21,6 +21,9 @@ struct AdapterArgs {
   const int32_t* ids = nullptr;     // [T]
   const uint16_t* a = nullptr;      // packed A of all slots (adapter_pack)
   const uint16_t* b = nullptr;      // packed B
+  const uint16_t* a_tc = nullptr;   // the same as the tensor cores' operand tiles (adapter_tc_pack)
+  const uint16_t* b_tc = nullptr;
+  int64_t a_tc_slot = 0, b_tc_slot = 0;
   const int32_t* rank = nullptr;    // [n] ranks, 0: empty slot
   const float* scale = nullptr;     // [n]
   const void* base = nullptr;       // [T][N] of out_type, or NULL (zero)
@@ -42,13 +45,18 @@ inline int adapter_rank_pad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 6
 inline int64_t adapter_a_elems(int K, int rpad) { return static_cast<int64_t>((K + 31) / 32) * 32 * rpad; }
 inline int64_t adapter_b_elems(int N, int rpad) { return static_cast<int64_t>((N + 31) / 32) * 32 * rpad; }
 
+inline int64_t adapter_tc_a_elems(int K, int rpad) { return static_cast<int64_t>((K + 63) / 64) * 64 * rpad; }
+inline int64_t adapter_tc_b_elems(int N, int rpad) { return static_cast<int64_t>((N + 127) / 128) * 128 * rpad; }
+
 // One slot's A [r][K] and B [N][r] into the kernels' order.
 cudaError_t launch_adapter_pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
                                 int rpad, cudaStream_t st);
-int adapter_tile_rows(int rpad);  // rows of a tile of the grouped path
-// order [T], tiles (at most T / rows + n + 1), n_tiles from ids; ids outside [-1, n) set MOE_DEVERR_EXPERT_RANGE.
-cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, const int32_t* rank, int32_t* order,
-                                 AdapterTile* tiles, int32_t* n_tiles, uint32_t* err, cudaStream_t st);
-cudaError_t launch_adapters(const AdapterArgs& a, int rpad, bool fp16, int num_sms, cudaStream_t st);
+cudaError_t launch_adapter_tc_pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
+                                   int rpad, cudaStream_t st);
+// order [T], tiles (at most T / 128 + n + 1), n_tiles from ids; ids outside [-1, n) set MOE_DEVERR_EXPERT_RANGE.
+cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, const int32_t* rank, int32_t* order, AdapterTile* tiles,
+                                 int32_t* n_tiles, uint32_t* err, cudaStream_t st);
+cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st);     // T <= kAdapterScan
+cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, int num_sms, cudaStream_t st);  // from the tiles
 
 }  // namespace moe

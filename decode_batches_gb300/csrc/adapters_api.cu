@@ -10,7 +10,7 @@ struct moe_adapters {
   int n = 0, N = 0, K = 0, r = 0, rpad = 0;
   moe_dtype type = MOE_BF16;
   int num_sms = 1;
-  uint16_t* w = nullptr;     // packed A of all slots, then packed B
+  uint16_t* w = nullptr;     // packed weights: A of all slots, B, and both again as the tensor cores' tiles
   int32_t* rank = nullptr;   // [n]
   float* scale = nullptr;    // [n]
   uint32_t* err = nullptr;
@@ -18,12 +18,19 @@ struct moe_adapters {
   int T_max = 0;
   int64_t a_slot() const { return adapter_a_elems(K, rpad); }
   int64_t b_slot() const { return adapter_b_elems(N, rpad); }
+  int64_t a_tc_slot() const { return adapter_tc_a_elems(K, rpad); }
+  int64_t b_tc_slot() const { return adapter_tc_b_elems(N, rpad); }
+  int64_t slot_elems() const { return a_slot() + b_slot() + a_tc_slot() + b_tc_slot(); }
+  uint16_t* a() const { return w; }
+  uint16_t* b() const { return a() + n * a_slot(); }
+  uint16_t* a_tc() const { return b() + n * b_slot(); }
+  uint16_t* b_tc() const { return a_tc() + n * a_tc_slot(); }
 };
 
 constexpr int kMaxRows = 1 << 26;
 
 static size_t tile_bytes(const moe_adapters* h, int T) {
-  return (static_cast<size_t>(T / kAdapterRowsMin + h->n + 2) * sizeof(AdapterTile) + 255) & ~size_t(255);
+  return (static_cast<size_t>(T / kAdapterTileRows + h->n + 2) * sizeof(AdapterTile) + 255) & ~size_t(255);
 }
 
 extern "C" moe_adapters* moe_adapters_create(int n, int N, int K, int r_max, moe_dtype dtype) {
@@ -60,7 +67,7 @@ static moe_status allocate(moe_adapters* h) {
     LIN_TRY(cudaMemset(h->err, 0, sizeof(uint32_t)));
   }
   if (!h->scale) LIN_TRY(cudaMalloc(&h->scale, h->n * sizeof(float)));
-  if (!h->w) LIN_TRY(cudaMalloc(&h->w, static_cast<size_t>(h->n) * (h->a_slot() + h->b_slot()) * sizeof(uint16_t)));
+  if (!h->w) LIN_TRY(cudaMalloc(&h->w, static_cast<size_t>(h->n) * h->slot_elems() * sizeof(uint16_t)));
   if (!h->rank) {
     int32_t* p = nullptr;
     LIN_TRY(cudaMalloc(&p, h->n * sizeof(int32_t)));
@@ -88,8 +95,10 @@ extern "C" moe_status moe_adapters_set(moe_adapters* h, int slot, const void* a,
   // (the slot is empty until all of it is written)
   LIN_TRY(cudaMemset(h->rank + slot, 0, sizeof(int32_t)));
   if (r > 0) {
-    LIN_TRY(launch_adapter_pack(static_cast<const uint16_t*>(a), static_cast<const uint16_t*>(b), h->w + slot * h->a_slot(),
-                                h->w + h->n * h->a_slot() + slot * h->b_slot(), r, h->K, h->N, h->rpad, 0));
+    const uint16_t *pa = static_cast<const uint16_t*>(a), *pb = static_cast<const uint16_t*>(b);
+    LIN_TRY(launch_adapter_pack(pa, pb, h->a() + slot * h->a_slot(), h->b() + slot * h->b_slot(), r, h->K, h->N, h->rpad, 0));
+    LIN_TRY(launch_adapter_tc_pack(pa, pb, h->a_tc() + slot * h->a_tc_slot(), h->b_tc() + slot * h->b_tc_slot(), r, h->K,
+                                   h->N, h->rpad, 0));
     LIN_TRY(cudaMemcpy(h->scale + slot, &scale, sizeof scale, cudaMemcpyHostToDevice));
     LIN_TRY(cudaDeviceSynchronize());
     LIN_TRY(cudaMemcpy(h->rank + slot, &r, sizeof(int32_t), cudaMemcpyHostToDevice));
@@ -134,21 +143,24 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
   if (base == out && ldb != ldo) return bad(MOE_ERR_INVALID_ARG, "base and out are the same rows: their pitches must be equal");
   AdapterArgs a;
   a.x = static_cast<const uint16_t*>(x), a.ldx = ldx, a.ids = ids;
-  a.a = h->w, a.b = h->w + h->n * h->a_slot(), a.a_slot = h->a_slot(), a.b_slot = h->b_slot();
+  a.a = h->a(), a.b = h->b(), a.a_slot = h->a_slot(), a.b_slot = h->b_slot();
+  a.a_tc = h->a_tc(), a.b_tc = h->b_tc(), a.a_tc_slot = h->a_tc_slot(), a.b_tc_slot = h->b_tc_slot();
   a.rank = h->rank, a.scale = h->scale;
   a.base = base, a.ld_base = ldb, a.out = out, a.ld_out = ldo, a.out_type = out_dtype;
   a.x_vec = h->K % 8 == 0 && rows_aligned16(x, ldx, h->type, T);
   a.out_vec = h->N % 8 == 0 && rows_aligned16(out, ldo, out_dtype, T) && (!base || rows_aligned16(base, ldb, out_dtype, T));
   a.T = T, a.n = h->n, a.K = h->K, a.N = h->N, a.err = h->err;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (T > kAdapterScan) {
-    int32_t* n_tiles = reinterpret_cast<int32_t*>(h->ws);
-    AdapterTile* tiles = reinterpret_cast<AdapterTile*>(h->ws + 256);
-    int32_t* order = reinterpret_cast<int32_t*>(h->ws + 256 + tile_bytes(h, h->T_max));
-    LIN_TRY(launch_adapter_group(ids, T, h->n, adapter_tile_rows(h->rpad), h->rank, order, tiles, n_tiles, h->err, st));
-    a.order = order, a.tiles = tiles, a.n_tiles = n_tiles;
+  if (T <= kAdapterScan) {
+    LIN_TRY(launch_adapters(a, h->rpad, h->type == MOE_FP16, st));
+    return MOE_OK;
   }
-  LIN_TRY(launch_adapters(a, h->rpad, h->type == MOE_FP16, h->num_sms, st));
+  int32_t* n_tiles = reinterpret_cast<int32_t*>(h->ws);
+  AdapterTile* tiles = reinterpret_cast<AdapterTile*>(h->ws + 256);
+  int32_t* order = reinterpret_cast<int32_t*>(h->ws + 256 + tile_bytes(h, h->T_max));
+  LIN_TRY(launch_adapter_group(ids, T, h->n, h->rank, order, tiles, n_tiles, h->err, st));
+  a.order = order, a.tiles = tiles, a.n_tiles = n_tiles;
+  LIN_TRY(launch_adapters_tc(a, h->rpad, h->type == MOE_FP16, h->num_sms, st));
   return MOE_OK;
 }
 

@@ -1,0 +1,61 @@
+// Device helpers that both adapter kernels use.
+#pragma once
+
+#include "elems.cuh"
+
+namespace moe {
+
+// Eight elements of a row of x from column c (zeros past K), at any alignment.
+MOE_DEVICE uint4 load_x(const uint16_t* row, int c, int K) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = c + 2 * i < K ? row[c + 2 * i] : 0u, hi = c + 2 * i + 1 < K ? row[c + 2 * i + 1] : 0u;
+    w[i] = lo | (hi << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Ranks c .. c + 7 of a row's sums as two 16-bit terms of u = scale * v (0 behind the slot's rank, where an infinite x
+// makes NaN of the padding); R / 8 neighbouring lanes hold a row.  Returns what the terms were divided by: 1 in bf16;
+// in fp16 the power of two that brings the row's largest u to [1, 2), so that neither term leaves the type's range
+// (1 for a row that is zero, infinite or NaN).
+template <int R, bool kFp16>
+MOE_DEVICE float adapter_split(float (&v)[8], int c, int rank, float scale, uint4& hi, uint4& lo) {
+  float mul = 1.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = c + e < rank ? v[e] * scale : 0.0f;
+  if (kFp16) {
+    float big = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(v[e]));
+#pragma unroll
+    for (int o = 1; o < R / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;  // big in [2^ex, 2^(ex + 1))
+    const int e2 = ex == -127 || ex == 128 ? 0 : max(-126, min(126, ex));
+    mul = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= down;
+  }
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    float h0, h1;
+    if (kFp16) {
+      h[e / 2] = pack_f16x2(v[e], v[e + 1]);
+      h0 = f16_bits_to_f32(h[e / 2] & 0xffffu), h1 = f16_bits_to_f32(h[e / 2] >> 16);
+    } else {
+      h[e / 2] = pack_bf16x2(v[e], v[e + 1]);
+      h0 = bf16_bits_to_f32(h[e / 2] & 0xffffu), h1 = bf16_bits_to_f32(h[e / 2] >> 16);
+    }
+    // (an infinity has no rest)
+    const float l0 = isfinite(h0) ? v[e] - h0 : 0.0f, l1 = isfinite(h1) ? v[e + 1] - h1 : 0.0f;
+    l[e / 2] = kFp16 ? pack_f16x2(l0, l1) : pack_bf16x2(l0, l1);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  return mul;
+}
+
+}  // namespace moe

@@ -1,0 +1,504 @@
+// Low-rank adapters of larger steps on the tensor cores (adapters.cu has the formulas and the small steps' kernel).
+//
+// A tile is up to 128 rows of one adapter, a cluster of C CTAs computes it:
+//   shrink  D[128][R] = x A^T over this CTA's range of K: tcgen05 MMAs of 128 x R x 16, rows of x gathered with cp.async
+//           into the 128-byte-swizzled operand, A in tiles packed that way (bulk copies), a ring of 64-column stages;
+//   u       the CTAs' partial sums meet in distributed shared memory: each CTA adds up 128 / C rows, scales and splits
+//           them into two 16-bit terms (adapter_split) and writes those into every CTA's MMA operand;
+//   expand  128 features at a time, over this CTA's range of N: D[128][128] = (hi + lo) B^T, two MMAs a 16 ranks, D double
+//           buffered in TMEM; eight warps add the base and write.
+// Bound by memory: x, base and out pass once; the weights are read once a tile, from L2.  What the warp-level kernel's
+// fragments cost (24 M instructions for 8195 rows of 4096 x 4096, rank 64: 75 us) falls away: operands go from shared
+// memory to the tensor core without registers.
+//
+// The rows of a B tile are permuted within 32 features such that the 16x256b TMEM load hands a lane eight neighbouring
+// features of a row: base and out move as 16-byte vectors, 64 contiguous bytes a row, without a transposition.
+#include "adapters.cuh"
+#include "adapters_split.cuh"
+#include "cluster.cuh"
+#include "elems.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kRows = 128;             // rows of a tile (the MMA's M)
+constexpr int kMathWarps = 8;          // gather, reduction, epilogue
+constexpr int kThreads = 32 * (kMathWarps + 1);
+constexpr int kSlice = 128;            // features of an expand step
+
+template <int R>
+struct Cfg {
+  static constexpr int kXBytes = kRows * 128, kWBytes = R * 128, kStage = kXBytes + kWBytes;
+  static constexpr int kStages = R <= 16 ? 4 : R <= 64 ? 3 : 2;
+  static constexpr int kPart = kRows * R * 4;        // partial sums, after the shrink, at the ring's start
+  static constexpr int kBTile = kSlice * R * 2;
+  static constexpr int kRing = kStages * kStage > kPart + 2 * kBTile ? kStages * kStage : kPart + 2 * kBTile;
+  static constexpr int kBMax = (kRing - kPart) / kBTile;
+  static constexpr int kBSlots = kBMax < 4 ? kBMax : 4;  // behind the partial sums
+  static constexpr int kTerm = kRows * R * 2;        // u's hi or lo
+  static constexpr int kRowBytes = (R < 64 ? R : 64) * 2;  // a row of u or of a B tile within a block of 64 ranks
+  static constexpr int kTail = kRows * 8 + 256;
+  static constexpr int kBytes = kRing + 2 * kTerm + kTail + 1024;
+  static constexpr int kTmemCols = 256;              // two buffers of 128; the shrink's R are the first's
+};
+
+// Byte offset of 16-byte piece p of row r in a tile of kRowBytes-wide rows, swizzled over the row's own width.
+template <int kRowBytes>
+MOE_DEVICE constexpr uint32_t swizzled(uint32_t r, uint32_t p) {
+  const uint32_t at = r * kRowBytes + p * 16;
+  return at ^ ((at >> 3) & (kRowBytes - 16u));
+}
+
+// Descriptor of a K-major operand of kRowBytes-wide rows with the swizzle of that width: groups of 8 rows are
+// 8 kRowBytes apart; layout 2, 4 or 6 (128, 64 or 32 bytes).
+template <int kRowBytes>
+MOE_DEVICE uint64_t operand_desc(uint32_t addr) {
+  constexpr uint64_t layout = kRowBytes == 128 ? 2 : kRowBytes == 64 ? 4 : 6;
+  return (static_cast<uint64_t>((addr >> 4) & 0x3FFFu)) | (1ull << 16) | (static_cast<uint64_t>(8 * kRowBytes >> 4) << 32) |
+         (1ull << 46) | (layout << 61);
+}
+
+// 16 lanes x 32 columns: lane (g, q) gets rows g and g + 8 (of the 16 at taddr's lane), and of each 8 columns i the
+// columns 8 i + 2 q, 8 i + 2 q + 1: r[4 i], r[4 i + 1] of row g, r[4 i + 2], r[4 i + 3] of row g + 8.
+MOE_DEVICE void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+MOE_DEVICE void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+MOE_DEVICE void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+// Generic writes (also to another CTA's shared memory) before the tensor core's reads.
+MOE_DEVICE void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+template <int R>
+struct Smem {
+  uint8_t* ring;
+  uint8_t* u;
+  int* rows;         // [128] row numbers, -1 past the last
+  float* row_scale;  // [128] (fp16)
+  uint64_t* full;    // [kStages] x's eight warps and A's copy
+  uint64_t* empty;   // [kStages]
+  uint64_t* b_full;  // [4]
+  uint64_t* b_empty;
+  uint64_t* o_full;  // [2] D of an expand step
+  uint64_t* o_empty;
+  uint64_t* d_full;  // the shrink's D
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
+  MOE_DEVICE explicit Smem(uint8_t* raw) {
+    uint8_t* p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    ring = p, p += Cfg<R>::kRing;
+    u = p, p += 2 * Cfg<R>::kTerm;
+    rows = reinterpret_cast<int*>(p), p += kRows * 4;
+    row_scale = reinterpret_cast<float*>(p), p += kRows * 4;
+    full = reinterpret_cast<uint64_t*>(p);
+    empty = full + 4, b_full = empty + 4, b_empty = b_full + 4, o_full = b_empty + 4, o_empty = o_full + 2;
+    d_full = o_empty + 2;
+    tmem_slot = reinterpret_cast<uint32_t*>(d_full + 1);
+    abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  }
+};
+
+// ---- the issuing lane ----------------------------------------------------------------------------------
+template <int R, bool kFp16>
+MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R>& s, int slot, int rs, int k0, int n, uint32_t tmem) {
+  using C = Cfg<R>;
+  const uint8_t* w = reinterpret_cast<const uint8_t*>(p.a_tc + slot * p.a_tc_slot) + static_cast<int64_t>(k0) * C::kWBytes;
+  const uint32_t wbytes = rs * 16 * 128, idesc = kFp16 ? idesc_f16_f32(kRows, 16 * rs) : idesc_bf16_f32(kRows, 16 * rs);
+  const uint64_t pol = l2_policy_evict_last();
+  const auto load = [&](int i) {
+    const int st = i % C::kStages;
+    mbar_arrive_expect_tx(&s.full[st], wbytes);
+    bulk_load(s.ring + st * C::kStage + C::kXBytes, w + static_cast<int64_t>(i) * C::kWBytes, wbytes, &s.full[st], pol);
+  };
+  for (int i = 0; i < n && i < C::kStages; ++i) load(i);
+  for (int i = 0; i < n; ++i) {
+    const int st = i % C::kStages;
+    if (!mbar_wait(&s.full[st], (i / C::kStages) & 1, s.abort_flag, p.err)) return;
+    tc_fence_after();
+    const uint32_t at = smem_u32(s.ring + st * C::kStage);
+    const uint64_t xd = operand_desc<128>(at), wd = operand_desc<128>(at + C::kXBytes);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mma_f16_ss(tmem, xd + 2 * k, wd + 2 * k, idesc, i > 0 || k > 0);
+    mma_commit(&s.empty[st]);
+    // the stage of the step before is about to be free: its next A tile (x is asked for by the other warps)
+    if (i >= 1 && i - 1 + C::kStages < n) {
+      if (!mbar_wait(&s.empty[(i - 1) % C::kStages], ((i - 1) / C::kStages) & 1, s.abort_flag, p.err)) return;
+      load(i - 1 + C::kStages);
+    }
+  }
+  mma_commit(s.d_full);
+}
+
+template <int R>
+MOE_DEVICE void load_b(const AdapterArgs& p, const Smem<R>& s, const uint8_t* w, int j) {
+  using C = Cfg<R>;
+  const int at = j % C::kBSlots;
+  mbar_arrive_expect_tx(&s.b_full[at], C::kBTile);
+  bulk_load(s.ring + C::kPart + at * C::kBTile, w + static_cast<int64_t>(j) * C::kBTile, C::kBTile, &s.b_full[at],
+            l2_policy_evict_last());
+}
+
+template <int R, bool kFp16>
+MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
+  using C = Cfg<R>;
+  const uint32_t idesc = kFp16 ? idesc_f16_f32(kRows, kSlice) : idesc_bf16_f32(kRows, kSlice);
+  const uint32_t u0 = smem_u32(s.u), b0 = smem_u32(s.ring + C::kPart);
+  for (int j = 0; j < n; ++j) {
+    const int at = j % C::kBSlots, buf = j & 1;
+    if (!mbar_wait(&s.b_full[at], (j / C::kBSlots) & 1, s.abort_flag, p.err)) return;
+    if (!mbar_wait(&s.o_empty[buf], ((j >> 1) & 1) ^ 1, s.abort_flag, p.err)) return;
+    tc_fence_after();
+    for (int t = 0; t < 2; ++t)
+      for (int k = 0; k < rs; ++k) {  // 16 ranks: 32 bytes of a row, four to a block of 64 ranks
+        const uint32_t in = (k / 4) * kRows * 128 + (k % 4) * 32;
+        mma_f16_ss(tmem + buf * kSlice, operand_desc<C::kRowBytes>(u0 + t * C::kTerm + in),
+                   operand_desc<C::kRowBytes>(b0 + at * C::kBTile + in), idesc, t > 0 || k > 0);
+      }
+    mma_commit(&s.b_empty[at]);
+    mma_commit(&s.o_full[buf]);
+    if (j >= 1 && j - 1 + C::kBSlots < n) {
+      if (!mbar_wait(&s.b_empty[(j - 1) % C::kBSlots], ((j - 1) / C::kBSlots) & 1, s.abort_flag, p.err)) return;
+      load_b<R>(p, s, w, j - 1 + C::kBSlots);
+    }
+  }
+}
+
+// ---- the other warps ---------------------------------------------------------------------------------------
+// x's rows into the stages: eight lanes a row's 128 bytes, four rows a lane.  A stage is announced kStages - 1 steps
+// after its copies were asked for.
+template <int R>
+MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R>& s, int k0, int n) {
+  using C = Cfg<R>;
+  const int piece = threadIdx.x & 7, lane = threadIdx.x & 31;
+  const uint16_t* row[4];
+  uint32_t dst[4];
+  bool live[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (threadIdx.x >> 3) + 32 * i, t = s.rows[r];
+    live[i] = t >= 0;  // (rows past the tile's last keep what the stage holds: their results go nowhere)
+    row[i] = p.x + max(t, 0) * p.ldx + 64 * static_cast<int64_t>(k0);
+    dst[i] = swizzled<128>(r, piece);
+  }
+  const auto announce = [&](int i) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.full[i % C::kStages]);
+  };
+  for (int i = 0; i < n; ++i) {
+    const int st = i % C::kStages;
+    if (!mbar_wait_warp(&s.empty[st], ((i / C::kStages) & 1) ^ 1, s.abort_flag, p.err)) return;
+    uint8_t* at = s.ring + st * C::kStage;
+    const int col = 64 * (k0 + i) + 8 * piece;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (!live[j]) continue;
+      if (p.x_vec)
+        cp_async_16_part(smem_u32(at + dst[j]), col < p.K ? row[j] + 64 * i + 8 * piece : p.x, col < p.K ? 16u : 0u);
+      else
+        *reinterpret_cast<uint4*>(at + dst[j]) = load_x(row[j] - 64 * static_cast<int64_t>(k0), col, p.K);
+    }
+    cp_async_commit();
+    if (i >= C::kStages - 1) {
+      cp_async_wait<C::kStages - 1>();
+      announce(i - (C::kStages - 1));
+    }
+  }
+  cp_async_wait<0>();
+  for (int i = max(0, n - (C::kStages - 1)); i < n; ++i) announce(i);
+}
+
+// This CTA's partial sums from TMEM into shared memory (16-byte units swizzled by the row).
+template <int R>
+MOE_DEVICE uint32_t part_at(int row, int unit) {
+  constexpr int kMask = R / 4 < 8 ? R / 4 - 1 : 7;
+  return (row * (R / 4) + (unit ^ (row & kMask))) * 16;
+}
+template <int R>
+MOE_DEVICE void write_part(const Smem<R>& s, uint32_t tmem, bool any) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = 32 * (warp & 3) + lane;
+  for (int c = 16 * (warp >> 2); c < R; c += 32) {
+    uint32_t v[16];
+    if (any) {
+      tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(s.ring + part_at<R>(row, c / 4 + i)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+}
+
+// u of this CTA's share of the rows, into every CTA of the cluster.
+template <int R, bool kFp16>
+MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R>& s, float scale, int rank, int cta) {
+  using C = Cfg<R>;
+  const int share = kRows / p.ctas;
+  for (int i = threadIdx.x * 8; i < share * R; i += 32 * kMathWarps * 8) {
+    const int r = cta * share + i / R, c = i % R;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < p.ctas; ++k) {
+      const float4 a = ld_cluster_f32x4(reinterpret_cast<const float*>(s.ring + part_at<R>(r, c / 4)), k);
+      const float4 b = ld_cluster_f32x4(reinterpret_cast<const float*>(s.ring + part_at<R>(r, c / 4 + 1)), k);
+      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+      v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
+    uint4 hi, lo;
+    const float mul = adapter_split<R, kFp16>(v, c, rank, scale, hi, lo);
+    const uint32_t at = smem_u32(s.u) + (c / 64) * kRows * 128 + swizzled<C::kRowBytes>(r, c % 64 / 8);
+    for (int k = 0; k < p.ctas; ++k) {
+      const uint32_t to = cluster_addr_u32(at, k);
+      st_cluster_v4(to, hi.x, hi.y, hi.z, hi.w);
+      st_cluster_v4(to + C::kTerm, lo.x, lo.y, lo.z, lo.w);
+      if (kFp16 && c == 0) st_cluster_f32(cluster_addr(&s.row_scale[r], k), mul);
+    }
+  }
+}
+
+// The expand's steps: warp w has the rows of lane quarter w % 4 and half w / 4 of the step's features.
+template <typename E, int R, bool kFp16>
+MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R>& s, int s0, int n, int rank, uint32_t tmem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int quarter = warp & 3, half = warp >> 2;
+  const E* base[2][2];
+  E* out[2][2];
+  float mul[2][2];
+  bool live[2][2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = 32 * quarter + 16 * m + 8 * h + g, r = s.rows[at];
+      live[m][h] = r >= 0;
+      base[m][h] = p.base ? static_cast<const E*>(p.base) + max(r, 0) * p.ld_base : nullptr;
+      out[m][h] = static_cast<E*>(p.out) + max(r, 0) * p.ld_out;
+      mul[m][h] = kFp16 && rank > 0 ? s.row_scale[at] : 1.0f;
+    }
+  const bool some[2] = {s.rows[32 * quarter] >= 0, s.rows[32 * quarter + 16] >= 0};  // (rows come first, gaps last)
+  for (int j = 0; j < n; ++j) {
+    const int buf = j & 1, col0 = (s0 + j) * kSlice + 64 * half + 8 * q;
+    bool ready = rank == 0;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (!some[m]) continue;
+      Raw8<E> b[2][2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (p.base && p.out_vec && live[m][h] && col0 + 32 * c < p.N)
+            b[c][h].load(base[m][h] + col0 + 32 * c);
+          else
+            b[c][h].zero();
+        }
+      uint32_t d[2][16];
+      if (rank > 0) {
+        if (!ready) {
+          if (!mbar_wait_warp(&s.o_full[buf], (j >> 1) & 1, s.abort_flag, p.err)) return;
+          tc_fence_after();
+          ready = true;
+        }
+        const uint32_t at = tmem + (static_cast<uint32_t>(32 * quarter + 16 * m) << 16) + buf * kSlice + 64 * half;
+        tmem_ld_16x256b_x4(at, d[0]);
+        tmem_ld_16x256b_x4(at + 32, d[1]);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d[0][i] = d[1][i] = 0u;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!live[m][h]) continue;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[2 * i] = __uint_as_float(d[c][4 * i + 2 * h]), v[2 * i + 1] = __uint_as_float(d[c][4 * i + 2 * h + 1]);
+          const int col = col0 + 32 * c;
+          if (p.out_vec) {
+            float f[8];
+            b[c][h].to_f32(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = kFp16 ? fmaf(v[i], mul[m][h], f[i]) : v[i] + f[i];
+            if (col < p.N) store8(out[m][h] + col, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (col + i < p.N) {
+                const float f = p.base ? base[m][h][col + i].f32() : 0.0f;
+                out[m][h][col + i] = E::of(kFp16 ? fmaf(v[i], mul[m][h], f) : v[i] + f);
+              }
+          }
+        }
+    }
+    if (rank > 0) {
+      if (!ready && !mbar_wait_warp(&s.o_full[buf], (j >> 1) & 1, s.abort_flag, p.err)) return;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.o_empty[buf]);
+    }
+  }
+}
+
+template <int R, bool kFp16>
+__global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(const AdapterArgs p) {
+  using C = Cfg<R>;
+  extern __shared__ uint8_t smem_raw[];
+  const Smem<R> s(smem_raw);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&s.full[i], kMathWarps + 1), mbar_init(&s.empty[i], 1);
+    for (int i = 0; i < C::kBSlots; ++i) mbar_init(&s.b_full[i], 1), mbar_init(&s.b_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.o_full[i], 1), mbar_init(&s.o_empty[i], kMathWarps);
+    mbar_init(s.d_full, 1);
+    *s.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMathWarps) {
+    tmem_alloc(s.tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s.tmem_slot;
+  pdl_trigger();  // (with its TMEM in hand: a dependent that came first would hold it while it waits for this grid)
+  pdl_wait();
+  const int idx = blockIdx.x / p.ctas, cta = cluster_rank();
+  const int n_tiles = *p.n_tiles;
+  const AdapterTile t = p.tiles[idx];  // (the list has an entry for every cluster of the grid)
+  const int rank = t.rank, rs = (rank + 15) / 16;
+  if (idx < n_tiles && !(rank == 0 && p.base == p.out)) {  // (the same for the whole cluster)
+    if (threadIdx.x < kRows) s.rows[threadIdx.x] = threadIdx.x < t.rows ? p.order[t.start + threadIdx.x] : -1;
+    __syncthreads();
+    const int nk = (p.K + 63) / 64, per_k = (nk + p.ctas - 1) / p.ctas, k0 = min(cta * per_k, nk), kn = min(per_k, nk - k0);
+    const int ns = (p.N + kSlice - 1) / kSlice, per_n = (ns + p.ctas - 1) / p.ctas;
+    const int s0 = min(cta * per_n, ns), sn = min(per_n, ns - s0);
+    const uint8_t* wb = reinterpret_cast<const uint8_t*>(p.b_tc + (rank > 0 ? t.slot * p.b_tc_slot : 0)) +
+                        static_cast<int64_t>(s0) * C::kBTile;
+    if (rank > 0) {
+      if (warp == kMathWarps) {
+        if (elect_one() && kn > 0) {
+          issue_shrink<R, kFp16>(p, s, t.slot, rs, k0, kn, tmem);
+          // the ring is free once the shrink's MMAs are done: B's first tiles, behind the partial sums' place
+          if (mbar_wait(s.d_full, 0, s.abort_flag, p.err))
+            for (int j = 0; j < sn && j < C::kBSlots; ++j) load_b<R>(p, s, wb, j);
+        }
+        __syncwarp();
+        if (kn == 0 && elect_one())
+          for (int j = 0; j < sn && j < C::kBSlots; ++j) load_b<R>(p, s, wb, j);
+        __syncwarp();
+      } else {
+        gather_x<R>(p, s, k0, kn);
+        const bool done = kn > 0 && mbar_wait_warp(s.d_full, 0, s.abort_flag, p.err);
+        tc_fence_after();
+        write_part<R>(s, tmem, done);
+        tc_fence_before();
+      }
+      cluster_barrier();
+      if (warp < kMathWarps) share_u<R, kFp16>(p, s, p.scale[t.slot], rank, cta);
+      fence_proxy_async_all();
+      cluster_barrier();  // u is whole, and no CTA's partial sums are read any more
+      tc_fence_after();
+      fence_proxy_async_all();
+    }
+    if (warp == kMathWarps) {
+      if (rank > 0 && elect_one()) issue_expand<R, kFp16>(p, s, wb, rs, sn, tmem);
+      __syncwarp();
+    } else if (p.out_type == MOE_BF16) {
+      write_out<Bf16, R, kFp16>(p, s, s0, sn, rank, tmem);
+    } else if (p.out_type == MOE_FP16) {
+      write_out<Fp16, R, kFp16>(p, s, s0, sn, rank, tmem);
+    } else {
+      write_out<Fp32, R, kFp16>(p, s, s0, sn, rank, tmem);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  abort_quiesce(s.abort_flag);
+  if (warp == kMathWarps) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// ---- packing -------------------------------------------------------------------------------------------
+// A: 64 columns at a time, [R rows][128 bytes] swizzled.  B: 128 features at a time, blocks of 64 ranks
+// [128 rows][kRowBytes] swizzled; row 8 i + 2 q + b of each 32 is feature 8 q + 2 i + b.
+template <int R>
+__global__ void adapter_tc_pack_kernel(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
+                                       int64_t na, int64_t nb) {
+  using C = Cfg<R>;
+  constexpr int W = C::kRowBytes / 2;  // elements of a row
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < na + nb;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    if (i < na) {
+      const int64_t chunk = i / (64 * R);
+      const int row = i / 64 % R, e = i % 64;
+      const int64_t col = 64 * chunk + e;
+      pa[chunk * (64 * R) + swizzled<128>(row, e / 8) / 2 + e % 8] =
+          row < r && col < K ? a[row * static_cast<int64_t>(K) + col] : 0;
+    } else {
+      const int64_t o = i - na, tile = o / (kSlice * R);
+      const int in = o % (kSlice * R), block = in / (kSlice * W), row = in / W % kSlice, e = in % W;
+      const int x = row % 32, rank = 64 * block + e;
+      const int64_t f = kSlice * tile + 32 * (row / 32) + 8 * (x / 2 % 4) + 2 * (x / 8) + x % 2;
+      pb[tile * (kSlice * R) + block * (kSlice * W) + swizzled<C::kRowBytes>(row, e / 8) / 2 + e % 8] =
+          rank < r && f < N ? b[f * r + rank] : 0;
+    }
+  }
+}
+
+template <int R>
+cudaError_t pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N, cudaStream_t st) {
+  const int64_t na = adapter_tc_a_elems(K, R), nb = adapter_tc_b_elems(N, R), blocks = (na + nb + 255) / 256;
+  adapter_tc_pack_kernel<R><<<static_cast<int>(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(a, b, pa, pb, r, K, N, na, nb);
+  return cudaGetLastError();
+}
+
+template <int R, bool kFp16>
+cudaError_t launch(AdapterArgs p, int num_sms, cudaStream_t st) {
+  auto kern = adapter_tc_kernel<R, kFp16>;
+  cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), Cfg<R>::kBytes);
+  if (e != cudaSuccess) return e;
+  // CTAs of a cluster: as many (1 to 8) as keep T / 128 whole tiles within two CTAs an SM
+  const int tiles = (p.T + kRows - 1) / kRows;
+  p.ctas = 8;
+  while (p.ctas > 1 && static_cast<int64_t>(tiles) * p.ctas > 2 * num_sms) p.ctas /= 2;
+  const int clusters = tiles + (p.n + 1 < p.T ? p.n + 1 : p.T);
+  return launch_pdl_clusters(kern, dim3(clusters * p.ctas), dim3(kThreads), p.ctas, Cfg<R>::kBytes, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_adapter_tc_pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
+                                   int rpad, cudaStream_t st) {
+  switch (rpad) {
+    case 16: return pack<16>(a, b, pa, pb, r, K, N, st);
+    case 32: return pack<32>(a, b, pa, pb, r, K, N, st);
+    case 64: return pack<64>(a, b, pa, pb, r, K, N, st);
+    default: return pack<128>(a, b, pa, pb, r, K, N, st);
+  }
+}
+
+cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, int num_sms, cudaStream_t st) {
+  switch (rpad) {
+    case 16: return fp16 ? launch<16, true>(p, num_sms, st) : launch<16, false>(p, num_sms, st);
+    case 32: return fp16 ? launch<32, true>(p, num_sms, st) : launch<32, false>(p, num_sms, st);
+    case 64: return fp16 ? launch<64, true>(p, num_sms, st) : launch<64, false>(p, num_sms, st);
+    default: return fp16 ? launch<128, true>(p, num_sms, st) : launch<128, false>(p, num_sms, st);
+  }
+}
+
+}  // namespace moe
