@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTileRows = 16;
+constexpr int kCtas = 8;  // of a cluster
 
 template <bool kFp16>
 MOE_DEVICE void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -70,7 +71,7 @@ struct Smem {
 // The tile of the cluster, found in ids: its rows go to s.rows.  Returns whether there is one, with its slot (-1: no adapter) and rank.  The same for every thread of the cluster.
 template <int M, int R>
 MOE_DEVICE bool find_tile(const AdapterArgs& p, Smem<M, R>& s, int& slot, int& rank) {
-  const int idx = blockIdx.x / p.ctas;
+  const int idx = blockIdx.x / kCtas;
   // Rows of equal id, 0, 1, 2, ... in order: row idx leads a tile when its number is a multiple of M.
   if (threadIdx.x < M) s.rows[threadIdx.x] = -1;
   int own = p.ids[idx];
@@ -79,7 +80,7 @@ MOE_DEVICE bool find_tile(const AdapterArgs& p, Smem<M, R>& s, int& slot, int& r
     own = -1;
   }
   slot = own;
-  rank = own >= 0 ? p.rank[own] : 0;
+  rank = own >= 0 ? p.slots.rank[own] : 0;
   int id = threadIdx.x < p.T ? p.ids[threadIdx.x] : -2;
   if (threadIdx.x < p.T && (id < -1 || id >= p.n)) id = -1;
   const uint32_t m = __ballot_sync(0xffffffffu, id == own);
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
   int slot, rank;
   if (!find_tile(p, s, slot, rank)) return;
   if (rank == 0 && p.base == p.out) return;
-  const int cta = cluster_rank(), C = p.ctas;
+  const int cta = cluster_rank(), C = kCtas;
   // this warp's chunks of 32 features
   const int nc = (p.N + 31) / 32, per_n = (nc + C * kWarps - 1) / (C * kWarps);
   const int c0 = min((cta * kWarps + warp) * per_n, nc), c1 = min(c0 + per_n, nc);
@@ -335,13 +336,20 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
       *reinterpret_cast<float4*>(&s.part[0][0] + i) = v;
     }
     cluster_barrier();
-    const float scale = p.scale[slot];
+    const float scale = p.slots.scale[slot];
     for (int i = threadIdx.x * 8; i < M * R; i += kThreads * 8) {  // eight ranks a thread
       float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int c = 0; c < C; ++c) {
-        const float4 o0 = ld_cluster_f32x4(&s.part[0][0] + i, c), o1 = ld_cluster_f32x4(&s.part[0][0] + i + 4, c);
-        v[0] += o0.x, v[1] += o0.y, v[2] += o0.z, v[3] += o0.w;
-        v[4] += o1.x, v[5] += o1.y, v[6] += o1.z, v[7] += o1.w;
+      const uint32_t at = smem_u32(&s.part[0][0] + i);
+      for (int c = 0; c < C; c += 4) {  // four CTAs' sums in flight
+        float4 o[4][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e][0] = ld_cluster_f32x4(cluster_addr_u32(at, c + e)), o[e][1] = ld_cluster_f32x4(cluster_addr_u32(at + 16, c + e));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[0] += o[e][0].x, v[1] += o[e][0].y, v[2] += o[e][0].z, v[3] += o[e][0].w;
+          v[4] += o[e][1].x, v[5] += o[e][1].y, v[6] += o[e][1].z, v[7] += o[e][1].w;
+        }
       }
       const int r = i / R, c = i % R;
       uint4 hi, lo;
@@ -391,10 +399,9 @@ __global__ void adapter_pack_kernel(const uint16_t* a, const uint16_t* b, uint16
 // tiles, and places its rows.  The order of a slot's rows is not fixed; a row's result does not depend on its place.
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupCtas = 8;
-__global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int32_t* ids, int T, int n, const int32_t* rank,
-                                                                      int32_t* order, AdapterTile* tiles,
-                                                                      int32_t* n_tiles, uint32_t* err) {
-  constexpr int M = kAdapterTileRows;
+__global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int32_t* ids, int T, int n, int M,
+                                                                      const AdapterSlots slots, int32_t* order,
+                                                                      AdapterTile* tiles, int32_t* n_tiles, uint32_t* err) {
   __shared__ int s_count[kAdaptersMax + 1];                                             // of this CTA's rows
   __shared__ int s_all[kAdaptersMax + 1], s_first[kAdaptersMax + 1], s_tile[kAdaptersMax + 1];  // of the slot
   __shared__ int s_next[kAdaptersMax + 1];                                              // this CTA's next place
@@ -419,12 +426,16 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
   cluster_barrier();
   // slot tid: its rows in all CTAs, and in the CTAs before this one; inclusive scans of rows and tiles
   int c = 0, before = 0;
-  if (tid <= n)
+  if (tid <= n) {
+    int v[kGroupCtas];
+#pragma unroll
+    for (int k = 0; k < kGroupCtas; ++k) v[k] = ld_cluster_s32(cluster_addr(&s_count[tid], k));
+#pragma unroll
     for (int k = 0; k < kGroupCtas; ++k) {
-      const int v = ld_cluster_s32(&s_count[tid], k);
-      c += v;
-      if (k < cta) before += v;
+      c += v[k];
+      if (k < cta) before += v[k];
     }
+  }
   int r = c, t = (c + M - 1) / M;
   for (int o = 1; o < 32; o <<= 1) {
     const int a = __shfl_up_sync(0xffffffffu, r, o), b = __shfl_up_sync(0xffffffffu, t, o);
@@ -438,7 +449,7 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
     if (n == kGroupThreads) {  // the slot behind the last thread's: the rows without an adapter
       int all = 0, mine = 0;
       for (int k = 0; k < kGroupCtas; ++k) {
-        const int v = ld_cluster_s32(&s_count[n], k);
+        const int v = ld_cluster_s32(cluster_addr(&s_count[n], k));
         all += v;
         if (k < cta) mine += v;
       }
@@ -465,19 +476,21 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
     const int in = at - s_first[key];
     // a slot's rows are cut evenly, in multiples of 16; the row that comes first in a tile writes the tile
     const int all = s_all[key], parts = (all + M - 1) / M, per = ((all + parts - 1) / parts + 15) / 16 * 16;
-    if (in % per == 0)
-      tiles[s_tile[key] + in / per] = AdapterTile{key < n ? key : -1, at, min(per, all - in), key < n ? rank[key] : 0};
+    if (in % per == 0) {
+      AdapterTile t{-1, at, static_cast<uint16_t>(min(per, all - in)), 0, 0.0f};
+      if (key < n) t.slot = key, t.rank = static_cast<uint16_t>(slots.rank[key]), t.scale = slots.scale[key];
+      tiles[s_tile[key] + in / per] = t;
+    }
   }
 }
 
 template <int R, bool kFp16>
-cudaError_t launch(AdapterArgs p, cudaStream_t st) {
+cudaError_t launch(const AdapterArgs& p, cudaStream_t st) {
   auto kern = adapter_kernel<kTileRows, R, kFp16>;
   const int smem = sizeof(Smem<kTileRows, R>);
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  p.ctas = 8;
-  return launch_pdl_clusters(kern, dim3(p.T * p.ctas), dim3(kThreads), p.ctas, smem, st, p);
+  return launch_pdl_clusters(kern, dim3(p.T * kCtas), dim3(kThreads), kCtas, smem, st, p);
 }
 
 template <int R>
@@ -495,10 +508,10 @@ cudaError_t launch_adapter_pack(const uint16_t* a, const uint16_t* b, uint16_t* 
   return cudaGetLastError();
 }
 
-cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, const int32_t* rank, int32_t* order, AdapterTile* tiles,
-                                 int32_t* n_tiles, uint32_t* err, cudaStream_t st) {
-  return launch_pdl_clusters(adapter_group_kernel, dim3(kGroupCtas), dim3(kGroupThreads), kGroupCtas, 0, st, ids, T, n, rank,
-                             order, tiles, n_tiles, err);
+cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, const AdapterSlots& slots, int32_t* order,
+                                 AdapterTile* tiles, int32_t* n_tiles, uint32_t* err, cudaStream_t st) {
+  return launch_pdl_clusters(adapter_group_kernel, dim3(kGroupCtas), dim3(kGroupThreads), kGroupCtas, 0, st, ids, T, n, rows,
+                             slots, order, tiles, n_tiles, err);
 }
 
 cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st) {

@@ -8,12 +8,24 @@ namespace moe {
 constexpr int kAdaptersMax = 1024;    // slots of a handle
 constexpr int kAdapterRankMax = 128;
 constexpr int kAdapterScan = 256;     // rows up to which a cluster finds its tile itself
-constexpr int kAdapterTileRows = 128; // rows of a grouped tile
+constexpr int kAdapterTileMin = 64;   // rows of a grouped tile at most, in steps of fewer rows (128 else)
 
-// Rows [start, start + rows) of `order` that share a slot (slot -1: rows without an adapter).
-struct AdapterTile {
-  int slot, start, rows, rank;
+// Rows [start, start + rows) of `order` that share a slot (slot -1: rows without an adapter), with what a tile needs to
+// know of it.
+struct alignas(16) AdapterTile {
+  int slot, start;
+  uint16_t rows, rank;
+  float scale;
 };
+struct AdapterSlots {
+  const int32_t* rank = nullptr;    // [n] ranks, 0: empty slot
+  const float* scale = nullptr;     // [n]
+};
+// How a step of T rows is cut: rows of a tile at most, CTAs that share a tile.
+struct AdapterCut {
+  int rows, ctas;
+};
+AdapterCut adapter_cut(int T, int n, int num_sms);
 
 struct AdapterArgs {
   const uint16_t* x = nullptr;      // [T][K]
@@ -24,8 +36,7 @@ struct AdapterArgs {
   const uint16_t* a_tc = nullptr;   // the same as the tensor cores' operand tiles (adapter_tc_pack)
   const uint16_t* b_tc = nullptr;
   int64_t a_tc_slot = 0, b_tc_slot = 0;
-  const int32_t* rank = nullptr;    // [n] ranks, 0: empty slot
-  const float* scale = nullptr;     // [n]
+  AdapterSlots slots;
   const void* base = nullptr;       // [T][N] of out_type, or NULL (zero)
   int64_t ld_base = 0;
   void* out = nullptr;
@@ -33,7 +44,7 @@ struct AdapterArgs {
   int out_type = MOE_BF16;
   int x_vec = 0, out_vec = 0;       // rows of x / of base and out are 16-byte aligned, K / N a multiple of 8
   int T = 0, n = 0, K = 0, N = 0;
-  int ctas = 1;                     // CTAs of a cluster, that share a tile (set at launch)
+  AdapterCut cut = {128, 1};        // tensor-core path
   int64_t a_slot = 0, b_slot = 0;   // elements of a slot's packed A, B
   const int32_t* order = nullptr;   // grouped rows and their tiles (larger T)
   const AdapterTile* tiles = nullptr;
@@ -53,10 +64,10 @@ cudaError_t launch_adapter_pack(const uint16_t* a, const uint16_t* b, uint16_t* 
                                 int rpad, cudaStream_t st);
 cudaError_t launch_adapter_tc_pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
                                    int rpad, cudaStream_t st);
-// order [T], tiles (at most T / 128 + n + 1), n_tiles from ids; ids outside [-1, n) set MOE_DEVERR_EXPERT_RANGE.
-cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, const int32_t* rank, int32_t* order, AdapterTile* tiles,
-                                 int32_t* n_tiles, uint32_t* err, cudaStream_t st);
+// order [T], tiles of at most `rows` rows (T / rows + n + 1 of them at most), n_tiles from ids; ids outside [-1, n) set MOE_DEVERR_EXPERT_RANGE.
+cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, const AdapterSlots& slots, int32_t* order,
+                                 AdapterTile* tiles, int32_t* n_tiles, uint32_t* err, cudaStream_t st);
 cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st);     // T <= kAdapterScan
-cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, int num_sms, cudaStream_t st);  // from the tiles
+cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st);  // from the tiles
 
 }  // namespace moe

@@ -30,7 +30,7 @@ struct moe_adapters {
 constexpr int kMaxRows = 1 << 26;
 
 static size_t tile_bytes(const moe_adapters* h, int T) {
-  return (static_cast<size_t>(T / kAdapterTileRows + h->n + 2) * sizeof(AdapterTile) + 255) & ~size_t(255);
+  return (static_cast<size_t>(T / kAdapterTileMin + h->n + 2) * sizeof(AdapterTile) + 255) & ~size_t(255);
 }
 
 extern "C" moe_adapters* moe_adapters_create(int n, int N, int K, int r_max, moe_dtype dtype) {
@@ -145,7 +145,7 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
   a.x = static_cast<const uint16_t*>(x), a.ldx = ldx, a.ids = ids;
   a.a = h->a(), a.b = h->b(), a.a_slot = h->a_slot(), a.b_slot = h->b_slot();
   a.a_tc = h->a_tc(), a.b_tc = h->b_tc(), a.a_tc_slot = h->a_tc_slot(), a.b_tc_slot = h->b_tc_slot();
-  a.rank = h->rank, a.scale = h->scale;
+  a.slots = AdapterSlots{h->rank, h->scale};
   a.base = base, a.ld_base = ldb, a.out = out, a.ld_out = ldo, a.out_type = out_dtype;
   a.x_vec = h->K % 8 == 0 && rows_aligned16(x, ldx, h->type, T);
   a.out_vec = h->N % 8 == 0 && rows_aligned16(out, ldo, out_dtype, T) && (!base || rows_aligned16(base, ldb, out_dtype, T));
@@ -158,9 +158,10 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
   int32_t* n_tiles = reinterpret_cast<int32_t*>(h->ws);
   AdapterTile* tiles = reinterpret_cast<AdapterTile*>(h->ws + 256);
   int32_t* order = reinterpret_cast<int32_t*>(h->ws + 256 + tile_bytes(h, h->T_max));
-  LIN_TRY(launch_adapter_group(ids, T, h->n, h->rank, order, tiles, n_tiles, h->err, st));
+  a.cut = adapter_cut(T, h->n, h->num_sms);
+  LIN_TRY(launch_adapter_group(ids, T, h->n, a.cut.rows, a.slots, order, tiles, n_tiles, h->err, st));
   a.order = order, a.tiles = tiles, a.n_tiles = n_tiles;
-  LIN_TRY(launch_adapters_tc(a, h->rpad, h->type == MOE_FP16, h->num_sms, st));
+  LIN_TRY(launch_adapters_tc(a, h->rpad, h->type == MOE_FP16, st));
   return MOE_OK;
 }
 

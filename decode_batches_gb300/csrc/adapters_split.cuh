@@ -46,12 +46,12 @@ MOE_DEVICE float adapter_split(float (&v)[8], int c, int rank, float scale, uint
       h[e / 2] = pack_f16x2(v[e], v[e + 1]);
       h0 = f16_bits_to_f32(h[e / 2] & 0xffffu), h1 = f16_bits_to_f32(h[e / 2] >> 16);
     } else {
-      h[e / 2] = pack_bf16x2(v[e], v[e + 1]);
+      h[e / 2] = cvt_bf16x2(v[e], v[e + 1]);
       h0 = bf16_bits_to_f32(h[e / 2] & 0xffffu), h1 = bf16_bits_to_f32(h[e / 2] >> 16);
     }
     // (an infinity has no rest)
     const float l0 = isfinite(h0) ? v[e] - h0 : 0.0f, l1 = isfinite(h1) ? v[e + 1] - h1 : 0.0f;
-    l[e / 2] = kFp16 ? pack_f16x2(l0, l1) : pack_bf16x2(l0, l1);
+    l[e / 2] = kFp16 ? pack_f16x2(l0, l1) : cvt_bf16x2(l0, l1);
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);

@@ -109,9 +109,8 @@ struct Smem {
 
 // ---- the issuing lane ----------------------------------------------------------------------------------
 template <int R, bool kFp16>
-MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R>& s, int slot, int rs, int k0, int n, uint32_t tmem) {
+MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
   using C = Cfg<R>;
-  const uint8_t* w = reinterpret_cast<const uint8_t*>(p.a_tc + slot * p.a_tc_slot) + static_cast<int64_t>(k0) * C::kWBytes;
   const uint32_t wbytes = rs * 16 * 128, idesc = kFp16 ? idesc_f16_f32(kRows, 16 * rs) : idesc_bf16_f32(kRows, 16 * rs);
   const uint64_t pol = l2_policy_evict_last();
   const auto load = [&](int i) {
@@ -245,20 +244,36 @@ MOE_DEVICE void write_part(const Smem<R>& s, uint32_t tmem, bool any) {
 template <int R, bool kFp16>
 MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R>& s, float scale, int rank, int cta) {
   using C = Cfg<R>;
-  const int share = kRows / p.ctas;
+  const int share = kRows / p.cut.ctas;
   for (int i = threadIdx.x * 8; i < share * R; i += 32 * kMathWarps * 8) {
     const int r = cta * share + i / R, c = i % R;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < p.ctas; ++k) {
-      const float4 a = ld_cluster_f32x4(reinterpret_cast<const float*>(s.ring + part_at<R>(r, c / 4)), k);
-      const float4 b = ld_cluster_f32x4(reinterpret_cast<const float*>(s.ring + part_at<R>(r, c / 4 + 1)), k);
-      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-      v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    // (rows of 256 bytes and more: half of eight lanes take their second unit first, so that they meet no bank twice)
+    const int swap = R >= 64 ? threadIdx.x >> 2 & 1 : 0;
+    const uint32_t p0 = smem_u32(s.ring + part_at<R>(r, c / 4 + swap)), p1 = smem_u32(s.ring + part_at<R>(r, c / 4 + 1 - swap));
+    for (int k = 0; k < p.cut.ctas; k += 4) {  // four CTAs' sums in flight
+      float4 a[4], b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (k + e < p.cut.ctas) a[e] = ld_cluster_f32x4(cluster_addr_u32(p0, k + e)), b[e] = ld_cluster_f32x4(cluster_addr_u32(p1, k + e));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (k + e < p.cut.ctas) {
+          v[0] += a[e].x, v[1] += a[e].y, v[2] += a[e].z, v[3] += a[e].w;
+          v[4] += b[e].x, v[5] += b[e].y, v[6] += b[e].z, v[7] += b[e].w;
+        }
+    }
+    if (swap) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = v[e];
+        v[e] = v[e + 4], v[e + 4] = x;
+      }
     }
     uint4 hi, lo;
     const float mul = adapter_split<R, kFp16>(v, c, rank, scale, hi, lo);
     const uint32_t at = smem_u32(s.u) + (c / 64) * kRows * 128 + swizzled<C::kRowBytes>(r, c % 64 / 8);
-    for (int k = 0; k < p.ctas; ++k) {
+    for (int k = 0; k < p.cut.ctas; ++k) {
       const uint32_t to = cluster_addr_u32(at, k);
       st_cluster_v4(to, hi.x, hi.y, hi.z, hi.w);
       st_cluster_v4(to + C::kTerm, lo.x, lo.y, lo.z, lo.w);
@@ -267,11 +282,16 @@ MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R>& s, float scale, int
   }
 }
 
-// The expand's steps: warp w has the rows of lane quarter w % 4 and half w / 4 of the step's features.
-template <typename E, int R, bool kFp16>
+// The expand's steps: warp w has the rows of lane quarter w % 4 and half w / 4 of the step's features.  A step is four
+// units of 16 rows and 32 features.  The base of a unit is asked for kAhead units before it is used: with two units of
+// 16-bit rows in flight a warp, 32 KB an SM, the memory's latency held the writes at 4.5 TB/s.
+// kWhole: rows are 16-byte aligned and N is a multiple of 128: no column is checked.
+template <typename E, int R, bool kFp16, bool kWhole>
 MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R>& s, int s0, int n, int rank, uint32_t tmem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int quarter = warp & 3, half = warp >> 2;
+  const bool has_base = p.base != nullptr;
+  const int first = s0 * kSlice + 64 * half + 8 * q;  // this lane's column of a step's first units
   const E* base[2][2];
   E* out[2][2];
   float mul[2][2];
@@ -282,75 +302,97 @@ MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R>& s, int s0, int n,
     for (int h = 0; h < 2; ++h) {
       const int at = 32 * quarter + 16 * m + 8 * h + g, r = s.rows[at];
       live[m][h] = r >= 0;
-      base[m][h] = p.base ? static_cast<const E*>(p.base) + max(r, 0) * p.ld_base : nullptr;
-      out[m][h] = static_cast<E*>(p.out) + max(r, 0) * p.ld_out;
+      base[m][h] = static_cast<const E*>(has_base ? p.base : p.out) + max(r, 0) * (has_base ? p.ld_base : p.ld_out) + first;
+      out[m][h] = static_cast<E*>(p.out) + max(r, 0) * p.ld_out + first;
       mul[m][h] = kFp16 && rank > 0 ? s.row_scale[at] : 1.0f;
     }
   const bool some[2] = {s.rows[32 * quarter] >= 0, s.rows[32 * quarter + 16] >= 0};  // (rows come first, gaps last)
+  constexpr int kAhead = sizeof(E) == 2 ? 4 : 2;
+  Raw8<E> b[kAhead][2];
+  // unit `unit` of the step `next` steps on
+  const auto ask = [&](int j, int next, int unit, Raw8<E> (&to)[2]) {
+    const int m = unit >> 1, off = next * kSlice + 32 * (unit & 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = kWhole || (p.out_vec && first + j * kSlice + off < p.N);
+      if (has_base && live[m][h] && j + next < n && in)
+        to[h].load(base[m][h] + off);
+      else
+        to[h].zero();
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) ask(0, 0, i, b[i]);
   for (int j = 0; j < n; ++j) {
-    const int buf = j & 1, col0 = (s0 + j) * kSlice + 64 * half + 8 * q;
-    bool ready = rank == 0;
+    const int buf = j & 1;
+    if (rank > 0) {
+      if (!mbar_wait_warp(&s.o_full[buf], (j >> 1) & 1, s.abort_flag, p.err)) return;
+      tc_fence_after();
+    }
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + buf * kSlice + 64 * half;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      if (!some[m]) continue;
-      Raw8<E> b[2][2];
+    for (int unit = 0; unit < 4; ++unit) {
+      const int m = unit >> 1, c = unit & 1;
+      if (some[m]) {
+        uint32_t d[16];
+        if (rank > 0) {
+          tmem_ld_16x256b_x4(at + (static_cast<uint32_t>(16 * m) << 16) + 32 * c, d);
+          tmem_wait_ld();
+        } else {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (p.base && p.out_vec && live[m][h] && col0 + 32 * c < p.N)
-            b[c][h].load(base[m][h] + col0 + 32 * c);
-          else
-            b[c][h].zero();
+          for (int i = 0; i < 16; ++i) d[i] = 0u;
         }
-      uint32_t d[2][16];
-      if (rank > 0) {
-        if (!ready) {
-          if (!mbar_wait_warp(&s.o_full[buf], (j >> 1) & 1, s.abort_flag, p.err)) return;
-          tc_fence_after();
-          ready = true;
-        }
-        const uint32_t at = tmem + (static_cast<uint32_t>(32 * quarter + 16 * m) << 16) + buf * kSlice + 64 * half;
-        tmem_ld_16x256b_x4(at, d[0]);
-        tmem_ld_16x256b_x4(at + 32, d[1]);
-        tmem_wait_ld();
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) d[0][i] = d[1][i] = 0u;
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!live[m][h]) continue;
           float v[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            v[2 * i] = __uint_as_float(d[c][4 * i + 2 * h]), v[2 * i + 1] = __uint_as_float(d[c][4 * i + 2 * h + 1]);
-          const int col = col0 + 32 * c;
-          if (p.out_vec) {
+            v[2 * i] = __uint_as_float(d[4 * i + 2 * h]), v[2 * i + 1] = __uint_as_float(d[4 * i + 2 * h + 1]);
+          if (kWhole || p.out_vec) {
             float f[8];
-            b[c][h].to_f32(f);
+            b[unit % kAhead][h].to_f32(f);
+            if (kFp16) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = kFp16 ? fmaf(v[i], mul[m][h], f[i]) : v[i] + f[i];
-            if (col < p.N) store8(out[m][h] + col, v);
+              for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], mul[m][h], f[i]);
+            } else {
+              add8(v, f);
+            }
+            if (kWhole || first + j * kSlice + 32 * c < p.N) store8(out[m][h] + 32 * c, v);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (col + i < p.N) {
-                const float f = p.base ? base[m][h][col + i].f32() : 0.0f;
-                out[m][h][col + i] = E::of(kFp16 ? fmaf(v[i], mul[m][h], f) : v[i] + f);
+              if (first + j * kSlice + 32 * c + i < p.N) {
+                const float f = has_base ? base[m][h][32 * c + i].f32() : 0.0f;
+                out[m][h][32 * c + i] = E::of(kFp16 ? fmaf(v[i], mul[m][h], f) : v[i] + f);
               }
           }
         }
+      }
+      ask(j, unit + kAhead < 4 ? 0 : 1, (unit + kAhead) % 4, b[unit % kAhead]);
     }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) base[m][h] += kSlice, out[m][h] += kSlice;
     if (rank > 0) {
-      if (!ready && !mbar_wait_warp(&s.o_full[buf], (j >> 1) & 1, s.abort_flag, p.err)) return;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.o_empty[buf]);
     }
   }
+}
+template <typename E, int R, bool kFp16>
+MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R>& s, int s0, int n, int rank, uint32_t tmem) {
+  if (p.out_vec && p.N % kSlice == 0)
+    write_out<E, R, kFp16, true>(p, s, s0, n, rank, tmem);
+  else
+    write_out<E, R, kFp16, false>(p, s, s0, n, rank, tmem);
+}
+
+// Asks L2 for `bytes` from p (16-byte aligned, a multiple of 16).
+MOE_DEVICE void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 template <int R, bool kFp16>
@@ -377,22 +419,31 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(c
   const uint32_t tmem = *s.tmem_slot;
   pdl_trigger();  // (with its TMEM in hand: a dependent that came first would hold it while it waits for this grid)
   pdl_wait();
-  const int idx = blockIdx.x / p.ctas, cta = cluster_rank();
+  const int idx = blockIdx.x / p.cut.ctas, cta = cluster_rank();
   const int n_tiles = *p.n_tiles;
   const AdapterTile t = p.tiles[idx];  // (the list has an entry for every cluster of the grid)
   const int rank = t.rank, rs = (rank + 15) / 16;
   if (idx < n_tiles && !(rank == 0 && p.base == p.out)) {  // (the same for the whole cluster)
     if (threadIdx.x < kRows) s.rows[threadIdx.x] = threadIdx.x < t.rows ? p.order[t.start + threadIdx.x] : -1;
     __syncthreads();
-    const int nk = (p.K + 63) / 64, per_k = (nk + p.ctas - 1) / p.ctas, k0 = min(cta * per_k, nk), kn = min(per_k, nk - k0);
-    const int ns = (p.N + kSlice - 1) / kSlice, per_n = (ns + p.ctas - 1) / p.ctas;
+    const int nk = (p.K + 63) / 64, per_k = (nk + p.cut.ctas - 1) / p.cut.ctas, k0 = min(cta * per_k, nk), kn = min(per_k, nk - k0);
+    const int ns = (p.N + kSlice - 1) / kSlice, per_n = (ns + p.cut.ctas - 1) / p.cut.ctas;
     const int s0 = min(cta * per_n, ns), sn = min(per_n, ns - s0);
+    const uint8_t* wa = reinterpret_cast<const uint8_t*>(p.a_tc + (rank > 0 ? t.slot * p.a_tc_slot : 0)) +
+                        static_cast<int64_t>(k0) * C::kWBytes;
     const uint8_t* wb = reinterpret_cast<const uint8_t*>(p.b_tc + (rank > 0 ? t.slot * p.b_tc_slot : 0)) +
                         static_cast<int64_t>(s0) * C::kBTile;
     if (rank > 0) {
       if (warp == kMathWarps) {
+        // Few rows: the weights are most of what the tile reads, and come from memory: all of them are asked for now.
+        // (With many rows an adapter's weights are in L2 already, and the requests cost 2 us of 15.)
+        if (t.rows <= 32) {
+          for (int j = threadIdx.x & 31; j < kn; j += 32) prefetch_l2(wa + static_cast<int64_t>(j) * C::kWBytes, rs * 16 * 128);
+          for (int j = threadIdx.x & 31; j < sn; j += 32) prefetch_l2(wb + static_cast<int64_t>(j) * C::kBTile, C::kBTile);
+        }
+        __syncwarp();
         if (elect_one() && kn > 0) {
-          issue_shrink<R, kFp16>(p, s, t.slot, rs, k0, kn, tmem);
+          issue_shrink<R, kFp16>(p, s, wa, rs, kn, tmem);
           // the ring is free once the shrink's MMAs are done: B's first tiles, behind the partial sums' place
           if (mbar_wait(s.d_full, 0, s.abort_flag, p.err))
             for (int j = 0; j < sn && j < C::kBSlots; ++j) load_b<R>(p, s, wb, j);
@@ -409,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(c
         tc_fence_before();
       }
       cluster_barrier();
-      if (warp < kMathWarps) share_u<R, kFp16>(p, s, p.scale[t.slot], rank, cta);
+      if (warp < kMathWarps) share_u<R, kFp16>(p, s, t.scale, rank, cta);
       fence_proxy_async_all();
       cluster_barrier();  // u is whole, and no CTA's partial sums are read any more
       tc_fence_after();
@@ -468,16 +519,12 @@ cudaError_t pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* p
 }
 
 template <int R, bool kFp16>
-cudaError_t launch(AdapterArgs p, int num_sms, cudaStream_t st) {
+cudaError_t launch(const AdapterArgs& p, cudaStream_t st) {
   auto kern = adapter_tc_kernel<R, kFp16>;
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), Cfg<R>::kBytes);
   if (e != cudaSuccess) return e;
-  // CTAs of a cluster: as many (1 to 8) as keep T / 128 whole tiles within two CTAs an SM
-  const int tiles = (p.T + kRows - 1) / kRows;
-  p.ctas = 8;
-  while (p.ctas > 1 && static_cast<int64_t>(tiles) * p.ctas > 2 * num_sms) p.ctas /= 2;
-  const int clusters = tiles + (p.n + 1 < p.T ? p.n + 1 : p.T);
-  return launch_pdl_clusters(kern, dim3(clusters * p.ctas), dim3(kThreads), p.ctas, Cfg<R>::kBytes, st, p);
+  const int clusters = (p.T + p.cut.rows - 1) / p.cut.rows + (p.n + 1 < p.T ? p.n + 1 : p.T);
+  return launch_pdl_clusters(kern, dim3(clusters * p.cut.ctas), dim3(kThreads), p.cut.ctas, Cfg<R>::kBytes, st, p);
 }
 
 }  // namespace
@@ -492,12 +539,19 @@ cudaError_t launch_adapter_tc_pack(const uint16_t* a, const uint16_t* b, uint16_
   }
 }
 
-cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, int num_sms, cudaStream_t st) {
+AdapterCut adapter_cut(int T, int n, int num_sms) {
+  const int tiles = (T + kRows - 1) / kRows;
+  AdapterCut c{kRows, 8};
+  while (c.ctas > 1 && static_cast<int64_t>(tiles) * c.ctas > 2 * num_sms) c.ctas /= 2;
+  return c;
+}
+
+cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st) {
   switch (rpad) {
-    case 16: return fp16 ? launch<16, true>(p, num_sms, st) : launch<16, false>(p, num_sms, st);
-    case 32: return fp16 ? launch<32, true>(p, num_sms, st) : launch<32, false>(p, num_sms, st);
-    case 64: return fp16 ? launch<64, true>(p, num_sms, st) : launch<64, false>(p, num_sms, st);
-    default: return fp16 ? launch<128, true>(p, num_sms, st) : launch<128, false>(p, num_sms, st);
+    case 16: return fp16 ? launch<16, true>(p, st) : launch<16, false>(p, st);
+    case 32: return fp16 ? launch<32, true>(p, st) : launch<32, false>(p, st);
+    case 64: return fp16 ? launch<64, true>(p, st) : launch<64, false>(p, st);
+    default: return fp16 ? launch<128, true>(p, st) : launch<128, false>(p, st);
   }
 }
 

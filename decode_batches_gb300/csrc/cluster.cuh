@@ -15,32 +15,28 @@ MOE_DEVICE void cluster_barrier() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// CTA `rank`'s copy of the shared-memory object at this CTA's address p.
-MOE_DEVICE uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
-}
+// The shared memory of CTA `rank` at this CTA's address p.
 MOE_DEVICE uint32_t cluster_addr_u32(uint32_t addr, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
   return a;
 }
-MOE_DEVICE double ld_cluster_f64(const double* p, uint32_t rank) {
+MOE_DEVICE uint32_t cluster_addr(const void* p, uint32_t rank) { return cluster_addr_u32(smem_u32(p), rank); }
+MOE_DEVICE double ld_cluster_f64(uint32_t addr) {
   double v;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
   return v;
 }
-MOE_DEVICE int ld_cluster_s32(const int* p, uint32_t rank) {
+MOE_DEVICE int ld_cluster_s32(uint32_t addr) {
   int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-MOE_DEVICE float4 ld_cluster_f32x4(const float* p, uint32_t rank) {
+MOE_DEVICE float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_addr(p, rank))
+               : "r"(addr)
                : "memory");
   return v;
 }

@@ -58,9 +58,15 @@ struct Raw8<Fp32> {
   }
 };
 
+// (cvt.rn.bf16x2 takes the upper half first)
+MOE_DEVICE uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 MOE_DEVICE void store8(Bf16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                            pack_bf16x2(v[6], v[7]));
+  *reinterpret_cast<uint4*>(p) = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
+                                            cvt_bf16x2(v[6], v[7]));
 }
 MOE_DEVICE void store8(Fp16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
@@ -69,6 +75,15 @@ MOE_DEVICE void store8(Fp16* p, const float (&v)[8]) {
 MOE_DEVICE void store8(Fp32* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// v += f, in pairs (each sum rounded as by itself)
+MOE_DEVICE void add8(float (&v)[8], const float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(v[i]), "+f"(v[i + 1])
+        : "f"(f[i]), "f"(f[i + 1]));
 }
 
 }  // namespace moe

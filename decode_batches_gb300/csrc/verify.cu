@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(kWarps * 32) verify_kernel(const VerifyArgs a)
     cluster_barrier();
     // every warp: the ranges' sums in order, two a lane
     static_assert(kCluster * kWarps == 64, "two ranges a lane");
-    const double s0 = ld_cluster_f64(&s_sum[(2 * lane) % kWarps], 2 * lane / kWarps);
-    const double s1 = ld_cluster_f64(&s_sum[(2 * lane + 1) % kWarps], 2 * lane / kWarps);
+    const double s0 = ld_cluster_f64(cluster_addr(&s_sum[(2 * lane) % kWarps], 2 * lane / kWarps));
+    const double s1 = ld_cluster_f64(cluster_addr(&s_sum[(2 * lane + 1) % kWarps], 2 * lane / kWarps));
     cluster_barrier();  // (the sums are read: the next round, or the exit, may follow)
     const double upto = warp_scan(s0 + s1, lane);
     const double sum = __shfl_sync(0xffffffffu, upto, 31);
