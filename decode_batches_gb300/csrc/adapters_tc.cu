@@ -26,20 +26,24 @@ constexpr int kMathWarps = 8;          // gather, reduction, epilogue
 constexpr int kThreads = 32 * (kMathWarps + 1);
 constexpr int kSlice = 128;            // features of an expand step
 
+// Shared memory: the ring, then u.  During the shrink its stages run on into u's place; after it the ring's start holds
+// the partial sums, B's first tiles come behind them and the later ones, once the sums are read, also in their place.
 template <int R>
 struct Cfg {
   static constexpr int kXBytes = kRows * 128, kWBytes = R * 128, kStage = kXBytes + kWBytes;
-  static constexpr int kStages = R <= 16 ? 4 : R <= 64 ? 3 : 2;
-  static constexpr int kPart = kRows * R * 4;        // partial sums, after the shrink, at the ring's start
-  static constexpr int kBTile = kSlice * R * 2;
-  static constexpr int kRing = kStages * kStage > kPart + 2 * kBTile ? kStages * kStage : kPart + 2 * kBTile;
-  static constexpr int kBMax = (kRing - kPart) / kBTile;
-  static constexpr int kBSlots = kBMax < 4 ? kBMax : 4;  // behind the partial sums
   static constexpr int kTerm = kRows * R * 2;        // u's hi or lo
+  static constexpr int kPart = kRows * R * 4;        // partial sums
+  static constexpr int kBTile = kSlice * R * 2;
+  static constexpr int kRing = R <= 64 ? 72 * 1024 : 128 * 1024;  // (two CTAs an SM up to rank 64)
+  static constexpr int kStagesMax = (kRing + 2 * kTerm) / kStage, kStages = kStagesMax < 4 ? kStagesMax : 4;
+  static constexpr int kBEarly = (kRing - kPart) / kBTile < 4 ? (kRing - kPart) / kBTile : 4;
+  static constexpr int kBSlots = kBEarly + kPart / kBTile;
   static constexpr int kRowBytes = (R < 64 ? R : 64) * 2;  // a row of u or of a B tile within a block of 64 ranks
   static constexpr int kTail = kRows * 8 + 256;
   static constexpr int kBytes = kRing + 2 * kTerm + kTail + 1024;
   static constexpr int kTmemCols = 256;              // two buffers of 128; the shrink's R are the first's
+  static constexpr int b_at(int slot) { return slot < kBEarly ? kPart + slot * kBTile : (slot - kBEarly) * kBTile; }
+  static_assert(kBEarly >= 2 && kBSlots <= 6 && kStages >= 3, "");
 };
 
 // Byte offset of 16-byte piece p of row r in a tile of kRowBytes-wide rows, swizzled over the row's own width.
@@ -84,9 +88,9 @@ struct Smem {
   uint8_t* u;
   int* rows;         // [128] row numbers, -1 past the last
   float* row_scale;  // [128] (fp16)
-  uint64_t* full;    // [kStages] x's eight warps and A's copy
+  uint64_t* full;    // [kStages] x's 256 threads and A's copy
   uint64_t* empty;   // [kStages]
-  uint64_t* b_full;  // [4]
+  uint64_t* b_full;  // [kBSlots]
   uint64_t* b_empty;
   uint64_t* o_full;  // [2] D of an expand step
   uint64_t* o_empty;
@@ -100,7 +104,7 @@ struct Smem {
     rows = reinterpret_cast<int*>(p), p += kRows * 4;
     row_scale = reinterpret_cast<float*>(p), p += kRows * 4;
     full = reinterpret_cast<uint64_t*>(p);
-    empty = full + 4, b_full = empty + 4, b_empty = b_full + 4, o_full = b_empty + 4, o_empty = o_full + 2;
+    empty = full + 4, b_full = empty + 4, b_empty = b_full + 6, o_full = b_empty + 6, o_empty = o_full + 2;
     d_full = o_empty + 2;
     tmem_slot = reinterpret_cast<uint32_t*>(d_full + 1);
     abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -122,6 +126,7 @@ MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R>& s, const uint8
   for (int i = 0; i < n; ++i) {
     const int st = i % C::kStages;
     if (!mbar_wait(&s.full[st], (i / C::kStages) & 1, s.abort_flag, p.err)) return;
+    fence_proxy_async_smem();  // (x was written by the generic proxy)
     tc_fence_after();
     const uint32_t at = smem_u32(s.ring + st * C::kStage);
     const uint64_t xd = operand_desc<128>(at), wd = operand_desc<128>(at + C::kXBytes);
@@ -142,7 +147,7 @@ MOE_DEVICE void load_b(const AdapterArgs& p, const Smem<R>& s, const uint8_t* w,
   using C = Cfg<R>;
   const int at = j % C::kBSlots;
   mbar_arrive_expect_tx(&s.b_full[at], C::kBTile);
-  bulk_load(s.ring + C::kPart + at * C::kBTile, w + static_cast<int64_t>(j) * C::kBTile, C::kBTile, &s.b_full[at],
+  bulk_load(s.ring + C::b_at(at), w + static_cast<int64_t>(j) * C::kBTile, C::kBTile, &s.b_full[at],
             l2_policy_evict_last());
 }
 
@@ -150,7 +155,8 @@ template <int R, bool kFp16>
 MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
   using C = Cfg<R>;
   const uint32_t idesc = kFp16 ? idesc_f16_f32(kRows, kSlice) : idesc_bf16_f32(kRows, kSlice);
-  const uint32_t u0 = smem_u32(s.u), b0 = smem_u32(s.ring + C::kPart);
+  const uint32_t u0 = smem_u32(s.u), b0 = smem_u32(s.ring);
+  for (int j = C::kBEarly; j < n && j < C::kBSlots; ++j) load_b<R>(p, s, w, j);  // (the partial sums' place is free now)
   for (int j = 0; j < n; ++j) {
     const int at = j % C::kBSlots, buf = j & 1;
     if (!mbar_wait(&s.b_full[at], (j / C::kBSlots) & 1, s.abort_flag, p.err)) return;
@@ -160,7 +166,7 @@ MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R>& s, const uint8
       for (int k = 0; k < rs; ++k) {  // 16 ranks: 32 bytes of a row, four to a block of 64 ranks
         const uint32_t in = (k / 4) * kRows * 128 + (k % 4) * 32;
         mma_f16_ss(tmem + buf * kSlice, operand_desc<C::kRowBytes>(u0 + t * C::kTerm + in),
-                   operand_desc<C::kRowBytes>(b0 + at * C::kBTile + in), idesc, t > 0 || k > 0);
+                   operand_desc<C::kRowBytes>(b0 + C::b_at(at) + in), idesc, t > 0 || k > 0);
       }
     mma_commit(&s.b_empty[at]);
     mma_commit(&s.o_full[buf]);
@@ -171,13 +177,24 @@ MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R>& s, const uint8
   }
 }
 
+// Asks L2 for `bytes` from p (16-byte aligned, a multiple of 16).
+MOE_DEVICE void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // ---- the other warps ---------------------------------------------------------------------------------------
-// x's rows into the stages: eight lanes a row's 128 bytes, four rows a lane.  A stage is announced kStages - 1 steps
-// after its copies were asked for.
+// Arrives on the mbarrier (one of its expected arrivals) once this thread's copies so far have landed.
+MOE_DEVICE void cp_async_mbar_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// x's rows into the stages: eight lanes a row's 128 bytes, four rows a lane.  The copies announce themselves; a proxy
+// fence here, before each announcement, waited for every copy in flight and made the stages take turns (0.8 us each),
+// so the issuing lane has it.
 template <int R>
 MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R>& s, int k0, int n) {
   using C = Cfg<R>;
-  const int piece = threadIdx.x & 7, lane = threadIdx.x & 31;
+  const int piece = threadIdx.x & 7;
   const uint16_t* row[4];
   uint32_t dst[4];
   bool live[4];
@@ -188,32 +205,23 @@ MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R>& s, int k0, int n) 
     row[i] = p.x + max(t, 0) * p.ldx + 64 * static_cast<int64_t>(k0);
     dst[i] = swizzled<128>(r, piece);
   }
-  const auto announce = [&](int i) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.full[i % C::kStages]);
-  };
   for (int i = 0; i < n; ++i) {
     const int st = i % C::kStages;
     if (!mbar_wait_warp(&s.empty[st], ((i / C::kStages) & 1) ^ 1, s.abort_flag, p.err)) return;
     uint8_t* at = s.ring + st * C::kStage;
     const int col = 64 * (k0 + i) + 8 * piece;
+    if (p.x_vec) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (!live[j]) continue;
-      if (p.x_vec)
-        cp_async_16_part(smem_u32(at + dst[j]), col < p.K ? row[j] + 64 * i + 8 * piece : p.x, col < p.K ? 16u : 0u);
-      else
-        *reinterpret_cast<uint4*>(at + dst[j]) = load_x(row[j] - 64 * static_cast<int64_t>(k0), col, p.K);
-    }
-    cp_async_commit();
-    if (i >= C::kStages - 1) {
-      cp_async_wait<C::kStages - 1>();
-      announce(i - (C::kStages - 1));
+      for (int j = 0; j < 4; ++j)
+        if (live[j]) cp_async_16_part(smem_u32(at + dst[j]), col < p.K ? row[j] + 64 * i + 8 * piece : p.x, col < p.K ? 16u : 0u);
+      cp_async_mbar_arrive(&s.full[st]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (live[j]) *reinterpret_cast<uint4*>(at + dst[j]) = load_x(row[j] - 64 * static_cast<int64_t>(k0), col, p.K);
+      mbar_arrive(&s.full[st]);
     }
   }
-  cp_async_wait<0>();
-  for (int i = max(0, n - (C::kStages - 1)); i < n; ++i) announce(i);
 }
 
 // This CTA's partial sums from TMEM into shared memory (16-byte units swizzled by the row).
@@ -242,11 +250,12 @@ MOE_DEVICE void write_part(const Smem<R>& s, uint32_t tmem, bool any) {
 
 // u of this CTA's share of the rows, into every CTA of the cluster.
 template <int R, bool kFp16>
-MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R>& s, float scale, int rank, int cta) {
+MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R>& s, float scale, int rank, int rows, int cta) {
   using C = Cfg<R>;
-  const int share = kRows / p.cut.ctas;
-  for (int i = threadIdx.x * 8; i < share * R; i += 32 * kMathWarps * 8) {
-    const int r = cta * share + i / R, c = i % R;
+  // (whole warps take part, 256 / R rows each; those past the tile's last repeat it)
+  const int share = (rows + p.cut.ctas - 1) / p.cut.ctas;
+  for (int i = threadIdx.x * 8; (i & ~255) < share * R; i += 32 * kMathWarps * 8) {
+    const int r = min(min(i / R, share - 1) + cta * share, rows - 1), c = i % R;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     // (rows of 256 bytes and more: half of eight lanes take their second unit first, so that they meet no bank twice)
     const int swap = R >= 64 ? threadIdx.x >> 2 & 1 : 0;
@@ -390,11 +399,6 @@ MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R>& s, int s0, int n,
     write_out<E, R, kFp16, false>(p, s, s0, n, rank, tmem);
 }
 
-// Asks L2 for `bytes` from p (16-byte aligned, a multiple of 16).
-MOE_DEVICE void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 template <int R, bool kFp16>
 __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(const AdapterArgs p) {
   using C = Cfg<R>;
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(c
   const Smem<R> s(smem_raw);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) mbar_init(&s.full[i], kMathWarps + 1), mbar_init(&s.empty[i], 1);
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&s.full[i], 32 * kMathWarps + 1), mbar_init(&s.empty[i], 1);
     for (int i = 0; i < C::kBSlots; ++i) mbar_init(&s.b_full[i], 1), mbar_init(&s.b_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&s.o_full[i], 1), mbar_init(&s.o_empty[i], kMathWarps);
     mbar_init(s.d_full, 1);
@@ -446,11 +450,11 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(c
           issue_shrink<R, kFp16>(p, s, wa, rs, kn, tmem);
           // the ring is free once the shrink's MMAs are done: B's first tiles, behind the partial sums' place
           if (mbar_wait(s.d_full, 0, s.abort_flag, p.err))
-            for (int j = 0; j < sn && j < C::kBSlots; ++j) load_b<R>(p, s, wb, j);
+            for (int j = 0; j < sn && j < C::kBEarly; ++j) load_b<R>(p, s, wb, j);
         }
         __syncwarp();
         if (kn == 0 && elect_one())
-          for (int j = 0; j < sn && j < C::kBSlots; ++j) load_b<R>(p, s, wb, j);
+          for (int j = 0; j < sn && j < C::kBEarly; ++j) load_b<R>(p, s, wb, j);
         __syncwarp();
       } else {
         gather_x<R>(p, s, k0, kn);
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(c
         tc_fence_before();
       }
       cluster_barrier();
-      if (warp < kMathWarps) share_u<R, kFp16>(p, s, t.scale, rank, cta);
+      if (warp < kMathWarps) share_u<R, kFp16>(p, s, t.scale, rank, t.rows, cta);
       fence_proxy_async_all();
       cluster_barrier();  // u is whole, and no CTA's partial sums are read any more
       tc_fence_after();
@@ -539,11 +543,19 @@ cudaError_t launch_adapter_tc_pack(const uint16_t* a, const uint16_t* b, uint16_
   }
 }
 
+// The most CTAs, up to two an SM (all that run at a time: a cluster more waits for the first to end, 96 us instead of 63 at
+// 8195 rows), from tiles of 128 or 64 rows and clusters of 8 to 1.  The slots' rows are unknown here: half a tile is
+// lost to each slot, and a slot that is used has one at least.
 AdapterCut adapter_cut(int T, int n, int num_sms) {
-  const int tiles = (T + kRows - 1) / kRows;
-  AdapterCut c{kRows, 8};
-  while (c.ctas > 1 && static_cast<int64_t>(tiles) * c.ctas > 2 * num_sms) c.ctas /= 2;
-  return c;
+  const int used = n < T ? n : T;
+  AdapterCut best{kRows, 1};
+  int64_t most = 0;
+  for (int rows = kRows; rows >= kAdapterTileMin; rows /= 2) {
+    const int64_t cut = static_cast<int64_t>(T) / rows + used / 2 + 1, tiles = cut > used ? cut : used;
+    for (int c = 8; c >= 1; c /= 2)
+      if (tiles * c <= 2 * num_sms && tiles * c > most) most = tiles * c, best = AdapterCut{rows, c};
+  }
+  return best;
 }
 
 cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st) {
