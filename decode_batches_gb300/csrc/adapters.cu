@@ -26,7 +26,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTileRows = 16;
-constexpr int kCtas = 8;  // of a cluster
 
 template <bool kFp16>
 MOE_DEVICE void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -64,39 +63,70 @@ struct Smem {
   alignas(16) uint16_t u[2][M][kPitch];  // hi, lo
   float row_scale[M];                    // (fp16) the power of two that a row's u was divided by
   int rows[M];                           // the tile's rows, -1 past the last
-  uint32_t match[kAdapterScan / 32];
+  alignas(16) int ids[kThreads];
+  uint32_t leads[kWarps];
+  int tile[4];                           // slot, number of its first row, rank, is there one
+  static_assert(kAdapterScan <= kThreads, "a thread a row");
   static_assert((kSlots + 1) * M * R * 4 <= kWarps * kStageBytes, "the partial sums fit one stage");
 };
 
-// The tile of the cluster, found in ids: its rows go to s.rows.  Returns whether there is one, with its slot (-1: no adapter) and rank.  The same for every thread of the cluster.
+// The tile of the cluster, found in ids by every CTA for itself (a step has 256 rows at most): a row whose number among
+// the rows of its id is a multiple of M leads a tile, and cluster i takes the i-th leader's, whose rows go to s.rows.
+// Returns whether there is one, with its slot (-1: no adapter) and rank.  The same for every thread of the cluster.
 template <int M, int R>
 MOE_DEVICE bool find_tile(const AdapterArgs& p, Smem<M, R>& s, int& slot, int& rank) {
-  const int idx = blockIdx.x / kCtas;
-  // Rows of equal id, 0, 1, 2, ... in order: row idx leads a tile when its number is a multiple of M.
-  if (threadIdx.x < M) s.rows[threadIdx.x] = -1;
-  int own = p.ids[idx];
-  if (own < -1 || own >= p.n) {
-    if (threadIdx.x == 0) set_error(p.err, MOE_DEVERR_EXPERT_RANGE);
-    own = -1;
+  const int idx = blockIdx.x / p.cut.ctas, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  int id = -2;
+  if (t < p.T) {
+    id = p.ids[t];
+    if (id < -1 || id >= p.n) {
+      if (blockIdx.x == 0) set_error(p.err, MOE_DEVERR_EXPERT_RANGE);
+      id = -1;
+    }
   }
-  slot = own;
-  rank = own >= 0 ? p.slots.rank[own] : 0;
-  int id = threadIdx.x < p.T ? p.ids[threadIdx.x] : -2;
-  if (threadIdx.x < p.T && (id < -1 || id >= p.n)) id = -1;
-  const uint32_t m = __ballot_sync(0xffffffffu, id == own);
-  if ((threadIdx.x & 31) == 0) s.match[threadIdx.x >> 5] = m;
+  const int own_rank = id >= 0 ? p.slots.rank[id] : 0;
+  if (p.T <= 32) {  // one warp's ids: the first warp finds the tile without a barrier (1 us of 6 less for one row)
+    if (warp == 0) {
+      const uint32_t same = __match_any_sync(0xffffffffu, id);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      const bool lead = t < p.T && before % M == 0;
+      const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+      if (lane == 0) s.tile[3] = idx < __popc(leads);
+      if (lead && __popc(leads & ((1u << lane) - 1u)) == idx) {
+        s.tile[0] = id, s.tile[2] = own_rank;
+        uint32_t left = same & ~((1u << lane) - 1u);  // the tile's rows: the leader's and the next M - 1 of its id
+#pragma unroll
+        for (int i = 0; i < M; ++i) s.rows[i] = left ? __ffs(left) - 1 : -1, left &= left - 1;
+      }
+    }
+    __syncthreads();
+    slot = s.tile[0], rank = s.tile[2];
+    return s.tile[3];
+  }
+  if (t < M) s.rows[t] = -1;
+  s.ids[t] = id;
   __syncthreads();
-  int before_me = 0, before_idx = 0;
+  int before = __popc(__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1u));  // earlier rows of this id
+  for (int i = 0; i < 32 * warp; i += 4) {
+    const int4 v = *reinterpret_cast<const int4*>(&s.ids[i]);
+    before += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
+  }
+  const bool lead = t < p.T && before % M == 0;
+  const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+  if (lane == 0) s.leads[warp] = leads;
+  __syncthreads();
+  int number = __popc(leads & ((1u << lane) - 1u)), all = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const uint32_t b = s.match[w];
-    const int me = static_cast<int>(threadIdx.x) - 32 * w, ix = idx - 32 * w;
-    before_me += me >= 32 ? __popc(b) : me > 0 ? __popc(b & ((1u << me) - 1u)) : 0;
-    before_idx += ix >= 32 ? __popc(b) : ix > 0 ? __popc(b & ((1u << ix) - 1u)) : 0;
+    if (w == warp) number += all;
+    all += __popc(s.leads[w]);
   }
-  if (before_idx % M) return false;
-  const int at = before_me - before_idx;
-  if (id == own && at >= 0 && at < M) s.rows[at] = threadIdx.x;
+  if (idx >= all) return false;
+  if (lead && number == idx) s.tile[0] = id, s.tile[1] = before, s.tile[2] = own_rank;
+  __syncthreads();
+  slot = s.tile[0], rank = s.tile[2];
+  const int at = before - s.tile[1];
+  if (t < p.T && id == slot && at >= 0 && at < M) s.rows[at] = t;
   __syncthreads();
   return true;
 }
@@ -242,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
   int slot, rank;
   if (!find_tile(p, s, slot, rank)) return;
   if (rank == 0 && p.base == p.out) return;
-  const int cta = cluster_rank(), C = kCtas;
+  const int cta = cluster_rank(), C = p.cut.ctas;
   // this warp's chunks of 32 features
   const int nc = (p.N + 31) / 32, per_n = (nc + C * kWarps - 1) / (C * kWarps);
   const int c0 = min((cta * kWarps + warp) * per_n, nc), c1 = min(c0 + per_n, nc);
@@ -343,8 +373,13 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
       for (int c = 0; c < C; c += 4) {  // four CTAs' sums in flight
         float4 o[4][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e][0] = ld_cluster_f32x4(cluster_addr_u32(at, c + e)), o[e][1] = ld_cluster_f32x4(cluster_addr_u32(at + 16, c + e));
+        for (int e = 0; e < 4; ++e) {
+          o[e][0] = o[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c + e < C) {
+            const uint32_t from = cluster_addr_u32(at, c + e);
+            o[e][0] = ld_cluster_f32x4(from), o[e][1] = ld_cluster_f32x4(from + 16);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           v[0] += o[e][0].x, v[1] += o[e][0].y, v[2] += o[e][0].z, v[3] += o[e][0].w;
@@ -484,18 +519,22 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
   }
 }
 
+// One cluster for each tile that there may be, of as many CTAs (1 to 8) as run at the same time.
 template <int R, bool kFp16>
-cudaError_t launch(const AdapterArgs& p, cudaStream_t st) {
+cudaError_t launch(AdapterArgs p, int num_sms, cudaStream_t st) {
   auto kern = adapter_kernel<kTileRows, R, kFp16>;
   const int smem = sizeof(Smem<kTileRows, R>);
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_clusters(kern, dim3(p.T * kCtas), dim3(kThreads), kCtas, smem, st, p);
+  const int most = (p.n + 1 < p.T ? p.n + 1 : p.T) + p.T / kTileRows, tiles = most < p.T ? most : p.T;
+  const int fit = (R <= 64 ? 2 : 1) * num_sms / tiles;
+  p.cut.ctas = fit < 1 ? 1 : fit > 8 ? 8 : fit;
+  return launch_pdl_clusters(kern, dim3(tiles * p.cut.ctas), dim3(kThreads), p.cut.ctas, smem, st, p);
 }
 
 template <int R>
-cudaError_t launch_rank(const AdapterArgs& p, bool fp16, cudaStream_t st) {
-  return fp16 ? launch<R, true>(p, st) : launch<R, false>(p, st);
+cudaError_t launch_rank(const AdapterArgs& p, bool fp16, int num_sms, cudaStream_t st) {
+  return fp16 ? launch<R, true>(p, num_sms, st) : launch<R, false>(p, num_sms, st);
 }
 
 }  // namespace
@@ -514,12 +553,12 @@ cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, con
                              slots, order, tiles, n_tiles, err);
 }
 
-cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st) {
+cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, int num_sms, cudaStream_t st) {
   switch (rpad) {
-    case 16: return launch_rank<16>(p, fp16, st);
-    case 32: return launch_rank<32>(p, fp16, st);
-    case 64: return launch_rank<64>(p, fp16, st);
-    default: return launch_rank<128>(p, fp16, st);
+    case 16: return launch_rank<16>(p, fp16, num_sms, st);
+    case 32: return launch_rank<32>(p, fp16, num_sms, st);
+    case 64: return launch_rank<64>(p, fp16, num_sms, st);
+    default: return launch_rank<128>(p, fp16, num_sms, st);
   }
 }
 

@@ -44,7 +44,7 @@ struct AdapterArgs {
   int out_type = MOE_BF16;
   int x_vec = 0, out_vec = 0;       // rows of x / of base and out are 16-byte aligned, K / N a multiple of 8
   int T = 0, n = 0, K = 0, N = 0;
-  AdapterCut cut = {128, 1};        // tensor-core path
+  AdapterCut cut = {128, 1};        // (the small steps' is set at launch)
   int64_t a_slot = 0, b_slot = 0;   // elements of a slot's packed A, B
   const int32_t* order = nullptr;   // grouped rows and their tiles (larger T)
   const AdapterTile* tiles = nullptr;
@@ -67,7 +67,8 @@ cudaError_t launch_adapter_tc_pack(const uint16_t* a, const uint16_t* b, uint16_
 // order [T], tiles of at most `rows` rows (T / rows + n + 1 of them at most), n_tiles from ids; ids outside [-1, n) set MOE_DEVERR_EXPERT_RANGE.
 cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, const AdapterSlots& slots, int32_t* order,
                                  AdapterTile* tiles, int32_t* n_tiles, uint32_t* err, cudaStream_t st);
-cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st);     // T <= kAdapterScan
+cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, int num_sms,
+                            cudaStream_t st);                        // T <= kAdapterScan
 cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st);  // from the tiles
 
 }  // namespace moe

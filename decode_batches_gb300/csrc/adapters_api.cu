@@ -152,7 +152,7 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
   a.T = T, a.n = h->n, a.K = h->K, a.N = h->N, a.err = h->err;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (T <= kAdapterScan) {
-    LIN_TRY(launch_adapters(a, h->rpad, h->type == MOE_FP16, st));
+    LIN_TRY(launch_adapters(a, h->rpad, h->type == MOE_FP16, h->num_sms, st));
     return MOE_OK;
   }
   int32_t* n_tiles = reinterpret_cast<int32_t*>(h->ws);

@@ -263,14 +263,15 @@ MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R>& s, float scale, int
     for (int k = 0; k < p.cut.ctas; k += 4) {  // four CTAs' sums in flight
       float4 a[4], b[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < 4; ++e) {
+        a[e] = b[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k + e < p.cut.ctas) a[e] = ld_cluster_f32x4(cluster_addr_u32(p0, k + e)), b[e] = ld_cluster_f32x4(cluster_addr_u32(p1, k + e));
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (k + e < p.cut.ctas) {
-          v[0] += a[e].x, v[1] += a[e].y, v[2] += a[e].z, v[3] += a[e].w;
-          v[4] += b[e].x, v[5] += b[e].y, v[6] += b[e].z, v[7] += b[e].w;
-        }
+      for (int e = 0; e < 4; ++e) {
+        v[0] += a[e].x, v[1] += a[e].y, v[2] += a[e].z, v[3] += a[e].w;
+        v[4] += b[e].x, v[5] += b[e].y, v[6] += b[e].z, v[7] += b[e].w;
+      }
     }
     if (swap) {
 #pragma unroll
@@ -552,7 +553,7 @@ AdapterCut adapter_cut(int T, int n, int num_sms) {
   int64_t most = 0;
   for (int rows = kRows; rows >= kAdapterTileMin; rows /= 2) {
     const int64_t cut = static_cast<int64_t>(T) / rows + used / 2 + 1, tiles = cut > used ? cut : used;
-    for (int c = 8; c >= 1; c /= 2)
+    for (int c = 8; c >= 1; --c)
       if (tiles * c <= 2 * num_sms && tiles * c > most) most = tiles * c, best = AdapterCut{rows, c};
   }
   return best;
