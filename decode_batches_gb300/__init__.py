@@ -251,30 +251,47 @@ def quantize_fp8_weight(w: torch.Tensor, stream=None):
 
 
 def _here(*tensors):
-    """The tensors' device, which has to be the current one (launches go to its current stream)."""
-    dev = torch.cuda.current_device()
+    """The current device, which has to be the tensors' (launches go to its current stream)."""
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors must be on the current CUDA device ({dev}), got {t.device}")
+
+
+def _row_args(t: torch.Tensor, name: str, dtypes, rows: Optional[int], width: int):
+    """``_rows`` for a tensor whose device is known, with a number of rows (None: any)."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} must have shape ({'rows' if rows is None else rows}, {width}), got {tuple(shape)}")
+    pitch, step = t.stride()
+    if step != 1 and shape[0] and width > 1:
+        raise ValueError(f"{name} must have dense rows")
+    if shape[0] <= 1 and pitch < width:  # with one row (or none) the pitch is never used to step; keep it valid
+        pitch = width
+    return t.data_ptr(), pitch
 
 
 def _assignments(inv: torch.Tensor, weights: Optional[torch.Tensor]):
     """(T, k, inv's pointer, weights' pointer) of the assignments' rows."""
-    if inv.dim() != 2:
-        raise ValueError(f"inv must have shape (T, k), got {tuple(inv.shape)}")
-    T, k = inv.shape
-    return T, k, _dev(inv, "inv", torch.int32), _dev(weights, "weights", torch.float32, (T, k))
+    shape = inv.shape
+    if len(shape) != 2:
+        raise ValueError(f"inv must have shape (T, k), got {tuple(shape)}")
+    if inv.dtype != torch.int32:
+        raise ValueError(f"inv must be torch.int32, got {inv.dtype}")
+    return *shape, _ptr(inv), None if weights is None else _dev(weights, "weights", torch.float32, shape)
 
 
 def _outside(out: torch.Tensor, *inputs):
     """out must not share memory with an input (the extents of their rows are compared)."""
     def extent(t):
-        n = t.numel() and 1 + sum((s - 1) * st for s, st in zip(t.shape, t.stride()))
+        n = 1 + sum((s - 1) * st for s, st in zip(t.shape, t.stride()))
         return t.data_ptr(), t.data_ptr() + n * t.element_size()
-    lo, hi = extent(out)
+    base = out.untyped_storage().data_ptr()
     for t in inputs:
-        if t is not None:
-            a, b = extent(t)
+        if t is not None and t.untyped_storage().data_ptr() == base and t.numel() and out.numel():
+            (lo, hi), (a, b) = extent(out), extent(t)
             if a < hi and lo < b:
                 raise ValueError("an output overlaps an input")
 
@@ -290,14 +307,12 @@ def sort_rows(x: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Tensor
     _here(x, inv, weights, out)
     T, k, pi, pw = _assignments(inv, weights)
     d = x.shape[-1]
-    px, ldx = _rows(x, "x", DTYPES, d)
-    if x.shape[0] != T:
-        raise ValueError(f"x must have {T} rows, got {x.shape[0]}")
+    px, ldx = _row_args(x, "x", DTYPES, T, d)
     if out is None:
         out = torch.empty((T * k, d), dtype=x.dtype, device=x.device)
     else:
         _outside(out, x, inv, weights)
-    po, ldo = _rows(out, "out", (x.dtype,), d)
+    po, ldo = _row_args(out, "out", (x.dtype,), None, d)
     _check(load_library().moe_sort_rows(px, DTYPES[x.dtype], ldx, T, k, d, pi, pw, po, ldo, out.shape[0], _stream()))
     return out
 
@@ -312,20 +327,16 @@ def sort_rows_backward(grad: torch.Tensor, inv: torch.Tensor, weights: Optional[
     _here(grad, inv, weights, x, out)
     T, k, pi, pw = _assignments(inv, weights)
     d = grad.shape[-1]
-    pg, ldg = _rows(grad, "grad", DTYPES, d)
+    pg, ldg = _row_args(grad, "grad", DTYPES, None, d)
     px = ldx = dw = None
     if x is not None:
-        px, ldx = _rows(x, "x", (grad.dtype,), d)
-        if x.shape[0] != T:
-            raise ValueError(f"x must have {T} rows, got {x.shape[0]}")
+        px, ldx = _row_args(x, "x", (grad.dtype,), T, d)
         dw = torch.empty((T, k), dtype=torch.float32, device=grad.device)
     if out is None:
         out = torch.empty((T, d), dtype=grad.dtype, device=grad.device)
     else:
         _outside(out, grad, inv, weights, x)
-    po, ldo = _rows(out, "out", (grad.dtype,), d)
-    if out.shape[0] != T:
-        raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
+    po, ldo = _row_args(out, "out", (grad.dtype,), T, d)
     _check(load_library().moe_sort_rows_backward(pg, DTYPES[grad.dtype], ldg, grad.shape[0], T, k, d, pi, pw, px, ldx or 0,
                                                  po, ldo, _ptr(dw), _stream()))
     return out if dw is None else (out, dw)
@@ -341,22 +352,18 @@ def combine_rows(y: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Ten
     _here(y, inv, weights, shared, out)
     T, k, pi, pw = _assignments(inv, weights)
     d = y.shape[-1]
-    py, ldy = _rows(y, "y", DTYPES, d)
+    py, ldy = _row_args(y, "y", DTYPES, None, d)
     ps, lds, sdt = None, 0, 0
     if shared is not None:
-        ps, lds = _rows(shared, "shared", DTYPES, d)
+        ps, lds = _row_args(shared, "shared", DTYPES, T, d)
         sdt = DTYPES[shared.dtype]
-        if shared.shape[0] != T:
-            raise ValueError(f"shared must have {T} rows, got {shared.shape[0]}")
     if out is None:
         out = torch.empty((T, d), dtype=out_dtype or y.dtype, device=y.device)
     else:
         _outside(out, y, inv, weights, shared)
-    po, ldo = _rows(out, "out", DTYPES if out_dtype is None else (out_dtype,), d)
-    if out.shape[0] != T:
-        raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
-    if out.dtype not in DTYPES:
-        raise ValueError(f"out must be bf16, fp16 or fp32, got {out.dtype}")
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
+    po, ldo = _row_args(out, "out", DTYPES, T, d)
     _check(load_library().moe_combine_rows(py, DTYPES[y.dtype], ldy, y.shape[0], T, k, d, pi, pw, ps, sdt, lds, po,
                                            DTYPES[out.dtype], ldo, _stream()))
     return out
@@ -374,20 +381,16 @@ def combine_rows_backward(grad: torch.Tensor, inv: torch.Tensor, weights: Option
     _here(grad, inv, weights, y, out)
     T, k, pi, pw = _assignments(inv, weights)
     d = grad.shape[-1]
-    pg, ldg = _rows(grad, "grad", DTYPES, d)
-    if grad.shape[0] != T:
-        raise ValueError(f"grad must have {T} rows, got {grad.shape[0]}")
+    pg, ldg = _row_args(grad, "grad", DTYPES, T, d)
     py = ldy = dw = None
     if y is not None:
-        py, ldy = _rows(y, "y", DTYPES, d)
+        py, ldy = _row_args(y, "y", DTYPES, None, d)
         dw = torch.empty((T, k), dtype=torch.float32, device=grad.device)
     if out is None:
         out = torch.empty((T * k if y is None else y.shape[0], d), dtype=(grad if y is None else y).dtype, device=grad.device)
     else:
         _outside(out, grad, inv, weights, y)
-    po, ldo = _rows(out, "out", DTYPES if y is None else (y.dtype,), d)
-    if y is not None and out.shape[0] != y.shape[0]:
-        raise ValueError(f"out must have {y.shape[0]} rows, got {out.shape[0]}")
+    po, ldo = _row_args(out, "out", DTYPES if y is None else (y.dtype,), None if y is None else y.shape[0], d)
     _check(load_library().moe_combine_rows_backward(pg, DTYPES[grad.dtype], ldg, T, k, d, pi, pw, py, ldy or 0, po,
                                                     DTYPES[out.dtype], ldo, out.shape[0], _ptr(dw), _stream()))
     return out if dw is None else (out, dw)
@@ -411,12 +414,10 @@ def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, offsets: torch.Ten
     if target.dim() != 2 or u_sample.dim() != 1:
         raise ValueError(f"target must be 2-D and u_sample 1-D, got {tuple(target.shape)} and {tuple(u_sample.shape)}")
     (R, V), B = target.shape, u_sample.shape[0]
-    pt, ldt = _rows(target, "target", DTYPES, V)
+    pt, ldt = _row_args(target, "target", DTYPES, R, V)
     pd = ldd = None
     if draft_probs is not None:
-        pd, ldd = _rows(draft_probs, "draft_probs", (target.dtype,), V)
-        if draft_probs.shape[0] != R:
-            raise ValueError(f"draft_probs must have {R} rows, got {draft_probs.shape[0]}")
+        pd, ldd = _row_args(draft_probs, "draft_probs", (target.dtype,), R, V)
     if tokens is None:
         tokens = torch.empty((R,), dtype=torch.int32, device=target.device)
     else:
@@ -595,7 +596,7 @@ class LowRankAdapters:
         if (lin.N, lin.K) != (self.N, self.K):
             raise ValueError(f"adapters of {self.N} x {self.K} beside a projection of {lin.N} x {lin.K}")
         _here(x, ids)
-        _rows(x, "x", (self.dtype,), self.K)
+        _row_args(x, "x", (self.dtype,), None, self.K)
         _dev(ids, "adapter_ids", torch.int32, (x.shape[0],))
         if x.shape[0] > self.T_max:
             raise ValueError(f"the adapters' workspace holds {self.T_max} rows, got {x.shape[0]}")
@@ -608,25 +609,21 @@ class LowRankAdapters:
             with torch.cuda.stream(stream):
                 return self.forward(x, ids, base, out, out_dtype)
         _here(x, ids, base, out)
-        px, ldx = _rows(x, "x", (self.dtype,), self.K)
+        px, ldx = _row_args(x, "x", (self.dtype,), None, self.K)
         T = x.shape[0]
         pb, ldb = None, 0
         if base is not None:
             if out_dtype is not None and out_dtype != base.dtype:
                 raise ValueError(f"out has base's type {base.dtype}, got {out_dtype}")
             out_dtype = base.dtype
-            pb, ldb = _rows(base, "base", DTYPES, self.N)
-            if base.shape[0] != T:
-                raise ValueError(f"base must have {T} rows, got {base.shape[0]}")
+            pb, ldb = _row_args(base, "base", DTYPES, T, self.N)
         if out is None:
             out = torch.empty((T, self.N), dtype=out_dtype or self.dtype, device=x.device)
             if out.dtype not in DTYPES:
                 raise ValueError(f"out must be bf16, fp16 or fp32, got {out.dtype}")
             po, ldo = out.data_ptr(), self.N
         else:
-            po, ldo = _rows(out, "out", DTYPES if out_dtype is None else (out_dtype,), self.N)
-            if out.shape[0] != T:
-                raise ValueError(f"out must have {T} rows, got {out.shape[0]}")
+            po, ldo = _row_args(out, "out", DTYPES if out_dtype is None else (out_dtype,), T, self.N)
             _outside(out, x, ids, base if pb != po or ldb != ldo else None)
         _check(self.lib.moe_adapters_forward(self._h, px, ldx, T, _dev(ids, "ids", torch.int32, (T,)), pb, ldb, po,
                                              DTYPES[out.dtype], ldo, _stream()))

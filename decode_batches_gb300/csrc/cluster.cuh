@@ -22,9 +22,9 @@ MOE_DEVICE uint32_t cluster_addr_u32(uint32_t addr, uint32_t rank) {
   return a;
 }
 MOE_DEVICE uint32_t cluster_addr(const void* p, uint32_t rank) { return cluster_addr_u32(smem_u32(p), rank); }
-MOE_DEVICE double ld_cluster_f64(uint32_t addr) {
-  double v;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+MOE_DEVICE float2 ld_cluster_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 MOE_DEVICE int ld_cluster_s32(uint32_t addr) {

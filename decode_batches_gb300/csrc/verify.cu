@@ -11,9 +11,10 @@
 // owns it goes through its range again (from L2) and writes the token.
 //
 // The answer is an index, so the sums are held far below the rows' resolution: p - q as an unevaluated
-// pair of fp32 values (its rounding error is kept), a lane's sum likewise (some 48 bits), joined in fp64.
-// fp64 throughout would take six times as long as the memory on this chip (2 additions a clock and SM);
-// the pair costs some 18 fp32 operations an element, half the memory's time.
+// pair of fp32 values (its rounding error is kept), every sum likewise (some 47 bits).
+// fp64 would take six times as long as the memory on this chip (2 additions a clock and SM), and even its use in the
+// reductions alone took a third of the time (24 warps an SM, 30 operations each); only the warp that writes the token
+// uses it.  The elements' pairs go two elements an instruction (f32x2): some 10 instructions an element.
 #include "abi_checks.h"
 #include "cluster.cuh"
 #include "elems.cuh"
@@ -23,9 +24,10 @@ using namespace moe;
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kCluster = 8;   // CTAs of a request
-constexpr int kGroups = 4;    // groups of 32 vectors whose loads are in flight together
+constexpr int kClusterMax = 8;  // CTAs of a request
+constexpr int kRing = 8;        // vector pairs a lane has in flight
+constexpr int kMarks = 4;       // partial sums of a range that are kept
+constexpr int kGroups = 4;      // vectors whose loads are in flight together in the search
 
 struct VerifyArgs {
   const void* p = nullptr;
@@ -38,12 +40,14 @@ struct VerifyArgs {
   int32_t* tokens = nullptr;
   int32_t* accepted = nullptr;
   int R = 0, V = 0;
+  int ctas = 1;  // of a cluster
 };
 
 // A probability as it counts: 0 unless 0 < v <= 2^64 (NaN, infinities and negative values count as 0; the
 // bound keeps every sum of 2^30 of them finite).
+constexpr uint32_t kLargest = 0x5f800000u;
 MOE_DEVICE float clean(float v) {
-  return __float_as_uint(v) - 1u < 0x5f800000u ? v : 0.0f;
+  return __float_as_uint(v) - 1u < kLargest ? v : 0.0f;
 }
 
 // One row pair as the sums read it: vectors of 16 bytes from the first aligned address at or below the
@@ -65,63 +69,124 @@ struct RowPair {
     together = mp == mq;
   }
   MOE_DEVICE int vectors() const { return (V + skip + kVec - 1) / kVec; }
-  static MOE_DEVICE void load(const E* row, int first, int V, bool whole, float (&o)[kVec]) {
-    if (whole) {
-      alignas(16) E e[kVec];
-      *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(row + first);
+  static MOE_DEVICE uint4 load(const E* row, int first, int V, bool whole) {
+    if (whole) return *reinterpret_cast<const uint4*>(row + first);
+    alignas(16) E e[kVec];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) o[i] = e[i].f32();
-    } else {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) o[i] = first + i >= 0 && first + i < V ? row[first + i].f32() : 0.0f;
-    }
+    for (int i = 0; i < kVec; ++i) e[i] = first + i >= 0 && first + i < V ? row[first + i] : E{};
+    return *reinterpret_cast<const uint4*>(e);
   }
-  // the cleaned values of vector v (zeros for v at or past `end`)
-  MOE_DEVICE void get(int v, int end, float (&a)[kVec], float (&b)[kVec]) const {
+  // vector v as it lies in memory (zeros at or past `end`)
+  MOE_DEVICE void get(int v, int end, uint4& a, uint4& b) const {
     const int first = v * kVec - skip;
-    const bool in = v < end, whole = in && together && first >= 0 && first + kVec <= V;
-    if (in) {
-      load(p, first, V, whole, a);
-    } else {
+    const bool in = v < end, whole = together && first >= 0 && first + kVec <= V;
+    a = in ? load(p, first, V, whole) : make_uint4(0u, 0u, 0u, 0u);
+    b = in && q ? load(q, first, V, whole) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  // its values as they count, with p raised to q where it is below: p - q is then max(p - q, 0)
+  MOE_DEVICE void values(int v, const uint4& ra, const uint4& rb, float (&a)[kVec], float (&b)[kVec]) const {
+    to_floats(ra, a);
+    to_floats(rb, b);
+    uint32_t most = 0;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) a[i] = 0.0f;
-    }
-    if (in && q) {
-      load(q, first, V, whole, b);
-    } else {
+    for (int i = 0; i < kVec; ++i) most = max(most, max(__float_as_uint(a[i]), __float_as_uint(b[i])));
+    if (most > kLargest) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) b[i] = 0.0f;
+      for (int i = 0; i < kVec; ++i) a[i] = clean(a[i]), b[i] = clean(b[i]);
     }
-    if (static_cast<uint32_t>(drop - first) < kVec && drop >= 0) {
+    const int first = v * kVec - skip;
+    if (drop >= first && drop < first + kVec) {
 #pragma unroll
       for (int i = 0; i < kVec; ++i)
         if (first + i == drop) a[i] = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) a[i] = clean(a[i]), b[i] = clean(b[i]);
+    for (int i = 0; i < kVec; ++i) a[i] = fmaxf(a[i], b[i]);
+  }
+  static MOE_DEVICE void to_floats(const uint4& r, float (&o)[kVec]) {
+    if constexpr (kVec == 8) {
+      Raw8<E> x;
+      x.a = r;
+      x.to_f32(o);
+    } else {
+      o[0] = __uint_as_float(r.x), o[1] = __uint_as_float(r.y), o[2] = __uint_as_float(r.z), o[3] = __uint_as_float(r.w);
+    }
   }
 };
 
-// hi + lo += max(p - q, 0), the rounding errors of the difference and of the sum kept in lo
-MOE_DEVICE void add_rest(float p, float q, float& hi, float& lo) {
-  const float d = p - q;
-  const float bb = p - d;                       // (Knuth's two-sum of p and -q)
-  const float ed = (p - (d + bb)) + (bb - q);
-  const bool pos = d > 0.0f;
-  const float v = pos ? d : 0.0f, e = pos ? ed : 0.0f;
-  const float s = hi + v;
-  const float t = s - hi;
-  const float es = (hi - (s - t)) + (v - t);
-  hi = s;
-  lo += e + es;
+// Two fp32 values an instruction, each rounded as by itself.
+struct Pair {
+  uint64_t v;
+  MOE_DEVICE Pair() {}
+  MOE_DEVICE Pair(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+  MOE_DEVICE void get(float& x, float& y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+};
+MOE_DEVICE Pair operator+(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+MOE_DEVICE Pair operator-(Pair a, Pair b) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(b.v), "l"(Pair(-1.0f, -1.0f).v), "l"(a.v));
+  return r;
 }
 
-MOE_DEVICE double warp_sum(double v) {
+// hi + lo += p - q for two elements with p >= q, the rounding errors of the difference and of the sum kept in lo
+// (Knuth's two-sum, twice)
+MOE_DEVICE void add_rest(Pair p, Pair q, Pair& hi, Pair& lo) {
+  const Pair d = p - q, bb = p - d;
+  const Pair ed = (p - (d + bb)) + (bb - q);
+  const Pair s = hi + d, t = s - hi;
+  const Pair es = (hi - (s - t)) + (d - t);
+  hi = s;
+  lo = lo + (ed + es);
+}
+
+// hi + lo += v
+MOE_DEVICE void add_value(Pair v, Pair& hi, Pair& lo) {
+  const Pair s = hi + v, t = s - hi;
+  lo = lo + ((hi - (s - t)) + (v - t));
+  hi = s;
+}
+
+// hi + lo, |lo| <= half a step of hi: sums with some 47 bits at fp32's rate.
+struct alignas(8) Wide {
+  float hi, lo;
+  MOE_DEVICE double f64() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+};
+MOE_DEVICE Wide renormalised(float hi, float lo) {  // |hi| >= |lo|, or hi == 0
+  const float s = hi + lo;
+  return Wide{s, lo - (s - hi)};
+}
+MOE_DEVICE Wide operator+(Wide a, Wide b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  return renormalised(s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo));
+}
+MOE_DEVICE Wide operator*(float u, Wide a) {
+  const float p = u * a.hi;
+  return renormalised(p, fmaf(u, a.hi, -p) + u * a.lo);
+}
+MOE_DEVICE bool operator>(Wide a, Wide b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+
+MOE_DEVICE Wide shfl(Wide v, int lane) {
+  return Wide{__shfl_sync(0xffffffffu, v.hi, lane), __shfl_sync(0xffffffffu, v.lo, lane)};
+}
+MOE_DEVICE Wide warp_sum(Wide v) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o >= 1; o >>= 1)
+    v = v + Wide{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)};
   return v;
 }
-MOE_DEVICE double warp_scan(double v, int lane) {  // inclusive
+MOE_DEVICE Wide warp_scan(Wide v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Wide n{__shfl_up_sync(0xffffffffu, v.hi, o), __shfl_up_sync(0xffffffffu, v.lo, o)};
+    if (lane >= o) v = n + v;
+  }
+  return v;
+}
+MOE_DEVICE double warp_scan(double v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const double n = __shfl_up_sync(0xffffffffu, v, o);
@@ -130,33 +195,173 @@ MOE_DEVICE double warp_scan(double v, int lane) {  // inclusive
   return v;
 }
 
-// The sum of the warp's range [v0, v1) of vectors.
-template <typename E>
-MOE_DEVICE double range_sum(const RowPair<E>& r, int v0, int v1, int lane) {
-  constexpr int n = RowPair<E>::kVec;
-  float hi = 0.0f, lo = 0.0f;
-  for (int v = v0; v < v1; v += 32 * kGroups) {
-    float a[kGroups][n], b[kGroups][n];
+// A lane's sum of rests.
+struct Rest {
+  Pair hi, lo;
+  MOE_DEVICE Rest() : hi(0.0f, 0.0f), lo(0.0f, 0.0f) {}
+  template <typename E>
+  MOE_DEVICE void add(const RowPair<E>& r, int v, const uint4& a, const uint4& b) {
+    constexpr int n = RowPair<E>::kVec;
+    float x[n], y[n];
+    r.values(v, a, b, x, y);
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) r.get(v + 32 * g + lane, v1, a[g], b[g]);
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-      for (int i = 0; i < n; ++i) add_rest(a[g][i], b[g][i], hi, lo);
+    for (int i = 0; i < n; i += 2) add_rest(Pair(x[i], x[i + 1]), Pair(y[i], y[i + 1]), hi, lo);
   }
-  return warp_sum(static_cast<double>(hi) + static_cast<double>(lo));
+  MOE_DEVICE Wide sum() const {
+    float h0, h1, l0, l1;
+    hi.get(h0, h1);
+    lo.get(l0, l1);
+    return renormalised(h0, l0) + renormalised(h1, l1);
+  }
+};
+
+// The range's sum, the vectors v0 + lane, v0 + lane + 32, ... below v1 a lane.  The vectors come through a ring in shared
+// memory (cp.async; a lane reads back what it copied, so no barrier): with loads into registers the warps waited for
+// memory and for each other in turns, 20 GB/s a CTA.  marks[k][lane] is the lane's sum up to its vector (k + 1) * per_mark.
+template <typename E>
+MOE_DEVICE Wide range_sum(const RowPair<E>& r, int v0, int v1, int lane, uint4* ring, Wide (*marks)[32], int per_mark) {
+  const int n = (max(v1 - v0, 0) + 31) / 32;
+  const auto ask = [&](int i) {
+    const int v = v0 + 32 * i + lane, first = v * RowPair<E>::kVec - r.skip;
+    uint4* at = ring + (i % kRing) * 64 + lane;
+    if (v < v1 && r.together && first >= 0 && first + RowPair<E>::kVec <= r.V) {
+      cp_async_16(smem_u32(at), r.p + first);
+      if (r.q) cp_async_16(smem_u32(at + 32), r.q + first);
+    } else {
+      uint4 a, b;
+      r.get(v, v1, a, b);
+      at[0] = a, at[32] = b;
+    }
+    if (!r.q) at[32] = make_uint4(0u, 0u, 0u, 0u);
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) {
+    if (i < n) ask(i);
+    cp_async_commit();
+  }
+  Rest sum;
+  int mark = per_mark, k = 0;
+  for (int i = 0; i < n; ++i) {
+    if (i + kRing - 1 < n) ask(i + kRing - 1);
+    cp_async_commit();
+    cp_async_wait<kRing - 1>();
+    const uint4* at = ring + (i % kRing) * 64 + lane;
+    sum.add(r, v0 + 32 * i + lane, at[0], at[32]);
+    if (i + 1 == mark && k < kMarks) marks[k++][lane] = sum.sum(), mark += per_mark;
+  }
+  cp_async_wait<0>();
+  return sum.sum();
 }
 
-// The lowest index of the range whose cumulative sum exceeds `at`; the last with a value above 0 where
-// rounding leaves none.
+// The same for a range of whole vectors whose values are all in [0, 2) (plain probabilities) and that has no dropped
+// index: no vector and no value is checked, which leaves some 11 instructions an element (of 36).  Returns whether the
+// values were that, seen from the bits of all of them: a sign, or the exponents of 2 and more, NaN and infinity.
+template <typename E, bool kQ>
+MOE_DEVICE bool range_sum_plain(const RowPair<E>& r, int v0, int n, int lane, uint4* ring, Wide (*marks)[32], int per_mark,
+                                Wide& result) {
+  constexpr int m = RowPair<E>::kVec;
+  const E* p = r.p + (static_cast<int64_t>(v0 + lane) * m - r.skip);
+  const E* q = kQ ? r.q + (static_cast<int64_t>(v0 + lane) * m - r.skip) : nullptr;
+  const uint32_t base = smem_u32(ring + lane);
+  uint32_t fill = 0, from = 0, bits = 0;
+  const auto ask = [&] {
+    cp_async_16(base + fill, p);
+    if (kQ) cp_async_16(base + fill + 512, q);
+    p += 32 * m;
+    if (kQ) q += 32 * m;
+    fill = (fill + 1024) & (1024 * kRing - 1);
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) {
+    if (i < n) ask();
+    cp_async_commit();
+  }
+  Rest sum;
+  int mark = per_mark, k = 0;
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    if (i + kRing - 1 < n) ask();
+    cp_async_commit();
+    cp_async_wait<kRing - 1>();
+    const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(ring + lane) + from);
+    from = (from + 1024) & (1024 * kRing - 1);
+    float x[m], y[m];
+    RowPair<E>::to_floats(at[0], x);
+    if (kQ) RowPair<E>::to_floats(at[32], y);
+#pragma unroll
+    for (int j = 0; j < m; ++j) {
+      bits |= __float_as_uint(x[j]);
+      if (kQ) bits |= __float_as_uint(y[j]), x[j] = fmaxf(x[j], y[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < m; j += 2) {
+      if (kQ)
+        add_rest(Pair(x[j], x[j + 1]), Pair(y[j], y[j + 1]), sum.hi, sum.lo);
+      else
+        add_value(Pair(x[j], x[j + 1]), sum.hi, sum.lo);
+    }
+    if (i + 1 == mark && k < kMarks) marks[k++][lane] = sum.sum(), mark += per_mark;
+  }
+  cp_async_wait<0>();
+  result = sum.sum();
+  return !__any_sync(0xffffffffu, bits >> 30);
+}
+
+// The vectors [v0, v1) narrowed to the marked part whose cumulative sum exceeds `at` first (lowered by what lies before).
 template <typename E>
-MOE_DEVICE int range_find(const RowPair<E>& r, int v0, int v1, int lane, double at) {
+MOE_DEVICE void narrow(const RowPair<E>&, int& v0, int& v1, double& at, const Wide (*marks)[32], int per_mark, int lane) {
+  const int n = (v1 - v0 + 31) / 32, full = min(n / per_mark, kMarks);  // marks that were written
+  double before = 0.0;
+  int k = 0;
+  for (; k < full; ++k) {  // (the part behind the last mark is what is left)
+    const double upto = warp_sum(marks[k][lane]).f64();
+    if (upto > at) break;
+    before = upto;
+  }
+  const int first = v0 + 32 * per_mark * k;
+  if (first >= v1) return;  // rounding left none: the whole range is searched for its last
+  v1 = k < full ? min(first + 32 * per_mark, v1) : v1;
+  v0 = first;
+  at -= before;
+}
+
+// The sum of the vectors [v0, v1), one lane's.
+template <typename E>
+MOE_DEVICE Wide lane_sum(const RowPair<E>& r, int v0, int v1) {
+  Rest sum;
+  for (int v = v0; v < v1; v += kGroups) {
+    uint4 a[kGroups], b[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) r.get(v + g, v1, a[g], b[g]);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) sum.add(r, v + g, a[g], b[g]);
+  }
+  return sum.sum();
+}
+
+// The lowest index of the vectors [v0, v1) whose cumulative sum exceeds `at`; the last with a value above 0 where
+// rounding leaves none.  Longer ranges are narrowed to a lane's contiguous 32nd first.
+template <typename E>
+__device__ __noinline__ int range_find(const RowPair<E>& r, int v0, int v1, int lane, double at) {
   constexpr int n = RowPair<E>::kVec;
+  if (v1 - v0 > 32) {
+    const int per = (v1 - v0 + 31) / 32, l0 = min(v0 + lane * per, v1), l1 = min(l0 + per, v1);
+    const double own = lane_sum(r, l0, l1).f64(), upto = warp_scan(own, lane);
+    const uint32_t some = __ballot_sync(0xffffffffu, own > 0.0);
+    const uint32_t over = __ballot_sync(0xffffffffu, own > 0.0 && upto > at);
+    if (!some) return -1;
+    const int l = over ? __ffs(over) - 1 : 31 - __clz(some);
+    const double before = __shfl_sync(0xffffffffu, upto - own, l);
+    at = over ? at - before : __longlong_as_double(0x7ff0000000000000ll);
+    v0 = __shfl_sync(0xffffffffu, l0, l), v1 = __shfl_sync(0xffffffffu, l1, l);
+  }
   double before = 0.0;
   int last = -1;
   for (int v = v0; v < v1; v += 32) {
+    uint4 ra, rb;
     float a[n], b[n];
-    r.get(v + lane, v1, a, b);
+    r.get(v + lane, v1, ra, rb);
+    r.values(v + lane, ra, rb, a, b);
     double own = 0.0;
     int mine = -1;
 #pragma unroll
@@ -168,13 +373,11 @@ MOE_DEVICE int range_find(const RowPair<E>& r, int v0, int v1, int lane, double 
       const int l = __ffs(over) - 1;
       double c = upto - own;
       int found = mine;
+      bool open = true;
 #pragma unroll
-      for (int i = n - 1; i >= 0; --i) {  // (from the back: the lowest index stays)
-        double s = c;
-#pragma unroll
-        for (int j = 0; j <= i; ++j)
-          if (a[j] > b[j]) s += static_cast<double>(a[j]) - static_cast<double>(b[j]);
-        if (a[i] > b[i] && s > at) found = i;
+      for (int i = 0; i < n; ++i) {
+        if (a[i] > b[i]) c += static_cast<double>(a[i]) - static_cast<double>(b[i]);
+        if (open && a[i] > b[i] && c > at) found = i, open = false;
       }
       return __shfl_sync(0xffffffffu, (v + lane) * n - r.skip + found, l);
     }
@@ -185,10 +388,13 @@ MOE_DEVICE int range_find(const RowPair<E>& r, int v0, int v1, int lane, double 
   return last;
 }
 
-template <typename E>
-__global__ void __launch_bounds__(kWarps * 32) verify_kernel(const VerifyArgs a) {
+template <typename E, int W>
+__global__ void __launch_bounds__(W * 32, 24 / W > 0 ? 24 / W : 1) verify_kernel(const VerifyArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  uint4* ring = reinterpret_cast<uint4*>(smem_raw) + (threadIdx.x >> 5) * (kRing * 64);
+  Wide (*marks)[32] = reinterpret_cast<Wide (*)[32]>(smem_raw + W * kRing * 64 * 16) + (threadIdx.x >> 5) * kMarks;
   __shared__ int s_refused;
-  __shared__ double s_sum[kWarps];
+  __shared__ Wide s_sum[W];
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -230,39 +436,61 @@ __global__ void __launch_bounds__(kWarps * 32) verify_kernel(const VerifyArgs a)
   r.open(prow, refused && a.q ? static_cast<const E*>(a.q) + row * a.ldq : nullptr, a.V,
          refused && !a.q ? a.drafts[row] : -1);
   for (int round = 0;; ++round) {
-    const int total = r.vectors(), parts = kCluster * kWarps;
+    const int total = r.vectors(), parts = a.ctas * W;
     const int per = ((total + parts - 1) / parts + 31) / 32 * 32;
-    const int part = rank * kWarps + warp;
+    const int part = rank * W + warp;
     const int v0 = static_cast<int>(min(static_cast<int64_t>(part) * per, static_cast<int64_t>(total)));
     const int v1 = min(v0 + per, total);
-    const double mine = range_sum(r, v0, v1, lane);
+    const int per_mark = (per / 32 + kMarks) / (kMarks + 1);
+    Wide mine;
+    const int e0 = v0 * RowPair<E>::kVec - r.skip, e1 = v1 * RowPair<E>::kVec - r.skip;  // elements [e0, e1)
+    bool done = false;
+    if (r.together && e0 >= 0 && e1 <= a.V && (v1 - v0) % 32 == 0 && !(r.drop >= e0 && r.drop < e1))
+      done = r.q ? range_sum_plain<E, true>(r, v0, (v1 - v0) / 32, lane, ring, marks, per_mark, mine)
+                 : range_sum_plain<E, false>(r, v0, (v1 - v0) / 32, lane, ring, marks, per_mark, mine);
+    if (!done) mine = range_sum(r, v0, v1, lane, ring, marks, per_mark);
+    mine = warp_sum(mine);
     if (lane == 0) s_sum[warp] = mine;
     cluster_barrier();
-    // every warp: the ranges' sums in order, two a lane
-    static_assert(kCluster * kWarps == 64, "two ranges a lane");
-    const double s0 = ld_cluster_f64(cluster_addr(&s_sum[(2 * lane) % kWarps], 2 * lane / kWarps));
-    const double s1 = ld_cluster_f64(cluster_addr(&s_sum[(2 * lane + 1) % kWarps], 2 * lane / kWarps));
-    cluster_barrier();  // (the sums are read: the next round, or the exit, may follow)
-    const double upto = warp_scan(s0 + s1, lane);
-    const double sum = __shfl_sync(0xffffffffu, upto, 31);
-    if (sum > 0.0) {
-      const double at = us > 0.0f ? static_cast<double>(us) * sum : 0.0;
-      // the first range that reaches past `at`, else the last that holds anything
-      const double c0 = upto - s1, c1 = upto;
-      uint32_t h0 = __ballot_sync(0xffffffffu, s0 > 0.0 && c0 > at), h1 = __ballot_sync(0xffffffffu, s1 > 0.0 && c1 > at);
-      int found;
-      if (h0 | h1) {
-        const int l = __ffs(h0 | h1) - 1;
-        found = 2 * l + ((h0 >> l) & 1u ? 0 : 1);
-      } else {
-        h0 = __ballot_sync(0xffffffffu, s0 > 0.0), h1 = __ballot_sync(0xffffffffu, s1 > 0.0);
-        const int l = 31 - __clz(h0 | h1);
-        found = 2 * l + ((h1 >> l) & 1u);
+    // every warp: the ranges' sums in order, kPer neighbours a lane
+    constexpr int kPer = kClusterMax * W / 32;
+    static_assert(kPer >= 1 && W % kPer == 0, "a lane's ranges are one CTA's");
+    Wide c[kPer], own{0.0f, 0.0f};  // c: cumulative within the lane
+    uint32_t some = 0;
+    if (kPer * lane < parts) {
+      const uint32_t from = cluster_addr(&s_sum[kPer * lane % W], kPer * lane / W);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float2 v = ld_cluster_f32x2(from + i * sizeof(Wide));
+        c[i] = Wide{v.x, v.y};
       }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) some |= c[i].hi > 0.0f ? 1u << i : 0u, own = own + c[i], c[i] = own;
+    }
+    cluster_barrier();  // (the sums are read: the next round, or the exit, may follow)
+    const Wide upto = warp_scan(own, lane), sum = shfl(upto, 31);
+    if (sum.hi > 0.0f) {
+      const Wide at = us > 0.0f ? us * sum : Wide{0.0f, 0.0f}, before = upto + Wide{-own.hi, -own.lo};
+      // the first range that reaches past `at`, else the last that holds anything
+      uint32_t over = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if ((some >> i & 1u) && before + c[i] > at) over |= 1u << i;
+      const uint32_t lanes_over = __ballot_sync(0xffffffffu, over != 0), lanes_some = __ballot_sync(0xffffffffu, some != 0);
+      const int l = lanes_over ? __ffs(lanes_over) - 1 : 31 - __clz(lanes_some);
+      const int in = __shfl_sync(0xffffffffu, lanes_over ? __ffs(over) - 1 : 31 - __clz(some), l);
+      const int found = kPer * l + in;
       if (found == part) {
-        const double x0 = __shfl_sync(0xffffffffu, upto - s1 - s0, found / 2);
-        const double x1 = __shfl_sync(0xffffffffu, upto - s1, found / 2);
-        const int tok = range_find(r, v0, v1, lane, at - (found & 1 ? x1 : x0));
+        Wide skipped{0.0f, 0.0f};  // what lies before this range within the lane's
+#pragma unroll
+        for (int i = 0; i + 1 < kPer; ++i)
+          if (i < in) skipped = c[i];
+        double left = at.f64() - shfl(before + skipped, l).f64();
+        int w0 = v0, w1 = v1;
+        __syncwarp();
+        narrow(r, w0, w1, left, marks, per_mark, lane);
+        int tok = range_find(r, w0, w1, lane, left);
+        if (tok < 0) tok = range_find(r, v0, v1, lane, __longlong_as_double(0x7ff0000000000000ll));  // (by rounding)
         if (lane == 0) a.tokens[row] = tok;
       }
       return;
@@ -273,9 +501,25 @@ __global__ void __launch_bounds__(kWarps * 32) verify_kernel(const VerifyArgs a)
   if (rank == 0 && threadIdx.x == 0) a.tokens[row] = -1;  // p holds nothing either
 }
 
+template <typename E, int W>
+cudaError_t launch_warps(VerifyArgs a, int B, int ctas, cudaStream_t st) {
+  constexpr int smem = W * (kRing * 64 * 16 + kMarks * 32 * sizeof(Wide));
+  cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(verify_kernel<E, W>), smem);
+  if (e != cudaSuccess) return e;
+  a.ctas = ctas;
+  return launch_pdl_clusters(verify_kernel<E, W>, dim3(ctas, B), dim3(W * 32), ctas, smem, st, a);
+}
+
 template <typename E>
-cudaError_t launch(const VerifyArgs& a, int B, cudaStream_t st) {
-  return launch_pdl_clusters(verify_kernel<E>, dim3(kCluster, B), dim3(kWarps * 32), kCluster, 0, st, a);
+cudaError_t launch(const VerifyArgs& a, int B, int num_sms, cudaStream_t st) {
+  // Few requests: the most threads a request, two CTAs of 8 warps an SM (five requests of 32003: 8.3 us, 9.9 with 4).  Many:
+  // CTAs of 4 warps, whose acceptance, reading and search overlap better (192 requests of 131072: 42 us, 51 with 8), as
+  // long as a warp's range has eight groups of 32 vectors (192 requests of 32003: 4 CTAs 18.8 us, 8 22.1).
+  if (B * kClusterMax <= 2 * num_sms) return launch_warps<E, 8>(a, B, kClusterMax, st);
+  const int groups = a.V / (32 * RowPair<E>::kVec);
+  int ctas = kClusterMax;
+  while (ctas > 1 && groups < 8 * 4 * ctas) ctas /= 2;
+  return launch_warps<E, 4>(a, B, ctas, st);
 }
 
 }  // namespace
@@ -301,6 +545,7 @@ extern "C" moe_status moe_verify_drafts(const void* target, moe_dtype dtype, int
   a.p = target, a.ldp = ldt, a.q = draft_probs, a.ldq = ldd, a.R = R, a.V = V;
   a.drafts = drafts, a.offsets = offsets, a.u = u, a.u_sample = u_sample, a.tokens = tokens, a.accepted = accepted;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  LIN_TRY(dtype == MOE_BF16 ? launch<Bf16>(a, B, st) : dtype == MOE_FP16 ? launch<Fp16>(a, B, st) : launch<Fp32>(a, B, st));
+  LIN_TRY(dtype == MOE_BF16 ? launch<Bf16>(a, B, current_sms(), st) : dtype == MOE_FP16 ? launch<Fp16>(a, B, current_sms(), st)
+                                                                     : launch<Fp32>(a, B, current_sms(), st));
   return MOE_OK;
 }
