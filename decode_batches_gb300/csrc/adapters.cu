@@ -432,6 +432,18 @@ __global__ void adapter_pack_kernel(const uint16_t* a, const uint16_t* b, uint16
 // The rows in slot order and their tiles, from ids, by one cluster: each CTA counts the ids of its share of the rows
 // (no adapter counts as slot n), the counts meet in distributed shared memory, every CTA scans all slots' rows and
 // tiles, and places its rows.  The order of a slot's rows is not fixed; a row's result does not depend on its place.
+// counts[key] += 1 for every lane with a key >= 0, and what was there before this lane's: a run of one key (a prompt's
+// rows) with one addition, else a lane's each, whose few collisions take less time than to find them (10 us of 22 at
+// 30000 rows).
+MOE_DEVICE int count_key(int* counts, int key, int lane) {
+  if (__all_sync(0xffffffffu, key == __shfl_sync(0xffffffffu, key, 0)) && key >= 0) {
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&counts[key], 32);
+    return __shfl_sync(0xffffffffu, at, 0) + lane;
+  }
+  return key >= 0 ? atomicAdd(&counts[key], 1) : 0;
+}
+
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupCtas = 8;
 __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int32_t* ids, int T, int n, int M,
@@ -454,8 +466,7 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
       key = ids[i];
       if (key < 0 || key >= n) bad_id |= key != -1, key = n;
     }
-    const uint32_t same = __match_any_sync(0xffffffffu, key);
-    if (key >= 0 && lane == __ffs(same) - 1) atomicAdd(&s_count[key], __popc(same));
+    count_key(s_count, key, lane);
   }
   if (bad_id) set_error(err, MOE_DEVERR_EXPERT_RANGE);
   cluster_barrier();
@@ -501,11 +512,7 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
       key = ids[i];
       if (key < 0 || key >= n) key = n;
     }
-    const uint32_t same = __match_any_sync(0xffffffffu, key);
-    const int leader = __ffs(same) - 1;
-    int at = 0;
-    if (key >= 0 && lane == leader) at = atomicAdd(&s_next[key], __popc(same));
-    at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1u));
+    const int at = count_key(s_next, key, lane);
     if (key < 0) continue;
     order[at] = i;
     const int in = at - s_first[key];
