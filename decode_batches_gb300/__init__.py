@@ -284,7 +284,8 @@ def _assignments(inv: torch.Tensor, weights: Optional[torch.Tensor]):
 
 
 def _outside(out: torch.Tensor, *inputs):
-    """out must not share memory with an input (the extents of their rows are compared)."""
+    """out must not share memory with an input: their extents are compared, and where both are rows of one pitch (parts of
+    one wide buffer) their columns."""
     def extent(t):
         n = 1 + sum((s - 1) * st for s, st in zip(t.shape, t.stride()))
         return t.data_ptr(), t.data_ptr() + n * t.element_size()
@@ -292,8 +293,13 @@ def _outside(out: torch.Tensor, *inputs):
     for t in inputs:
         if t is not None and t.untyped_storage().data_ptr() == base and t.numel() and out.numel():
             (lo, hi), (a, b) = extent(out), extent(t)
-            if a < hi and lo < b:
-                raise ValueError("an output overlaps an input")
+            if not (a < hi and lo < b):
+                continue
+            if t.dim() == out.dim() == 2 and t.stride() == out.stride() and t.element_size() == out.element_size():
+                pitch, off = out.stride(0), (a - lo) // out.element_size() % max(1, out.stride(0))
+                if out.shape[1] <= off and off + t.shape[1] <= pitch:
+                    continue
+            raise ValueError("an output overlaps an input")
 
 
 def sort_rows(x: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -500,7 +506,7 @@ class Fp8Linear:
         if (adapters is None) != (adapter_ids is None):
             raise ValueError("adapters and adapter_ids go together")
         if adapters is not None:
-            adapters._beside(self, x, adapter_ids)
+            adapters._beside(self, x, adapter_ids, out)
         px, ldx = _rows(x, "x", DTYPES, self.K)
         T = x.shape[0]
         out, po, ldo = self._out(T, out, out_dtype, x.device)
@@ -591,7 +597,7 @@ class LowRankAdapters:
         self.set_workspace(buf, T_max)
         return buf
 
-    def _beside(self, lin, x, ids):
+    def _beside(self, lin, x, ids, out):
         """The checks of a projection's call with these adapters, before anything of it is queued."""
         if (lin.N, lin.K) != (self.N, self.K):
             raise ValueError(f"adapters of {self.N} x {self.K} beside a projection of {lin.N} x {lin.K}")
@@ -600,6 +606,9 @@ class LowRankAdapters:
         _dev(ids, "adapter_ids", torch.int32, (x.shape[0],))
         if x.shape[0] > self.T_max:
             raise ValueError(f"the adapters' workspace holds {self.T_max} rows, got {x.shape[0]}")
+        if out is not None:
+            _here(out)
+            _outside(out, x, ids)
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, base: Optional[torch.Tensor] = None,
                 out: Optional[torch.Tensor] = None, out_dtype=None, stream=None):

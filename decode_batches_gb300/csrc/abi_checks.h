@@ -15,6 +15,7 @@ inline moe_status bad(moe_status s, const char* msg) { return fail_message(s, ms
 inline moe_status cuda_fail(const char* what, cudaError_t e) {
   char buf[256];
   snprintf(buf, sizeof buf, "%s: %s", what, cudaGetErrorString(e));
+  cudaGetLastError();  // reported here: a later check of the caller's own launches does not find it again
   return fail_message(MOE_ERR_CUDA, buf);
 }
 #define LIN_TRY(expr)                                         \
@@ -31,9 +32,14 @@ inline bool rows_aligned16(const void* p, int64_t ld, moe_dtype t, int64_t rows)
   return aligned(p, 16) && (rows <= 1 || ld * static_cast<int64_t>(elem_bytes(t)) % 16 == 0);
 }
 
-inline int current_sms() {
-  int dev = 0, n = 0;
+inline int current_device() {
+  int dev = 0;
   cudaGetDevice(&dev);
+  return dev;
+}
+inline int current_sms() {
+  int n = 0;
+  const int dev = current_device();
   cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
   return n > 0 ? n : 1;
 }

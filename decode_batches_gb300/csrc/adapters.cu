@@ -432,18 +432,6 @@ __global__ void adapter_pack_kernel(const uint16_t* a, const uint16_t* b, uint16
 // The rows in slot order and their tiles, from ids, by one cluster: each CTA counts the ids of its share of the rows
 // (no adapter counts as slot n), the counts meet in distributed shared memory, every CTA scans all slots' rows and
 // tiles, and places its rows.  The order of a slot's rows is not fixed; a row's result does not depend on its place.
-// counts[key] += 1 for every lane with a key >= 0, and what was there before this lane's: a run of one key (a prompt's
-// rows) with one addition, else a lane's each, whose few collisions take less time than to find them (10 us of 22 at
-// 30000 rows).
-MOE_DEVICE int count_key(int* counts, int key, int lane) {
-  if (__all_sync(0xffffffffu, key == __shfl_sync(0xffffffffu, key, 0)) && key >= 0) {
-    int at = 0;
-    if (lane == 0) at = atomicAdd(&counts[key], 32);
-    return __shfl_sync(0xffffffffu, at, 0) + lane;
-  }
-  return key >= 0 ? atomicAdd(&counts[key], 1) : 0;
-}
-
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupCtas = 8;
 __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int32_t* ids, int T, int n, int M,
@@ -516,8 +504,7 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
     if (key < 0) continue;
     order[at] = i;
     const int in = at - s_first[key];
-    // a slot's rows are cut evenly, in multiples of 16; the row that comes first in a tile writes the tile
-    const int all = s_all[key], parts = (all + M - 1) / M, per = ((all + parts - 1) / parts + 15) / 16 * 16;
+    const int all = s_all[key], per = adapter_tile_rows(all, M);  // the row that comes first in a tile writes the tile
     if (in % per == 0) {
       AdapterTile t{-1, at, static_cast<uint16_t>(min(per, all - in)), 0, 0.0f};
       if (key < n) t.slot = key, t.rank = static_cast<uint16_t>(slots.rank[key]), t.scale = slots.scale[key];

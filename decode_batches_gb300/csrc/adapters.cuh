@@ -8,6 +8,7 @@ namespace moe {
 constexpr int kAdaptersMax = 1024;    // slots of a handle
 constexpr int kAdapterRankMax = 128;
 constexpr int kAdapterScan = 256;     // rows up to which a cluster finds its tile itself
+constexpr int kAdapterCount = 1024;   // rows up to which the larger steps' clusters count the ids themselves
 constexpr int kAdapterTileMin = 64;   // rows of a grouped tile at most, in steps of fewer rows (128 else)
 
 // Rows [start, start + rows) of `order` that share a slot (slot -1: rows without an adapter), with what a tile needs to
@@ -25,6 +26,11 @@ struct AdapterSlots {
 struct AdapterCut {
   int rows, ctas;
 };
+// A slot's `all` rows are cut evenly, in multiples of 16: rows of each of its tiles but the last.
+__host__ __device__ inline int adapter_tile_rows(int all, int most) {
+  const int parts = (all + most - 1) / most;
+  return ((all + parts - 1) / parts + 15) / 16 * 16;
+}
 AdapterCut adapter_cut(int T, int n, int num_sms);
 
 struct AdapterArgs {
@@ -69,6 +75,6 @@ cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, con
                                  AdapterTile* tiles, int32_t* n_tiles, uint32_t* err, cudaStream_t st);
 cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, int num_sms,
                             cudaStream_t st);                        // T <= kAdapterScan
-cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st);  // from the tiles
+cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st);  // p.tiles: T > kAdapterCount
 
 }  // namespace moe

@@ -10,6 +10,7 @@ struct moe_adapters {
   int n = 0, N = 0, K = 0, r = 0, rpad = 0;
   moe_dtype type = MOE_BF16;
   int num_sms = 1;
+  int device = -1;           // of the handle's memory, once there is any
   uint16_t* w = nullptr;     // packed weights: A of all slots, B, and both again as the tensor cores' tiles
   int32_t* rank = nullptr;   // [n]
   float* scale = nullptr;    // [n]
@@ -62,6 +63,10 @@ extern "C" void moe_adapters_destroy(moe_adapters* h) {
 
 // The slots' memory, all empty, on the first slot that is set or the workspace, whichever comes first.
 static moe_status allocate(moe_adapters* h) {
+  const int dev = current_device();
+  if (h->device >= 0 && h->device != dev)
+    return bad(MOE_ERR_INVALID_ARG, "the handle's memory is on another device than the current one");
+  h->device = dev;
   if (!h->err) {
     LIN_TRY(cudaMalloc(&h->err, sizeof(uint32_t)));
     LIN_TRY(cudaMemset(h->err, 0, sizeof(uint32_t)));
@@ -135,6 +140,8 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
   if (!h->ws) return bad(MOE_ERR_NOT_READY, "workspace not set");
   if (T > h->T_max) return bad(MOE_ERR_WORKSPACE, "T exceeds the workspace's T_max");
   if (T == 0) return MOE_OK;
+  if (h->device != current_device())
+    return bad(MOE_ERR_INVALID_ARG, "the handle's memory is on another device than the current one");
   if (!x || !ids || !out) return bad(MOE_ERR_INVALID_ARG, "x, ids and out are required");
   if (ldx < h->K || ldo < h->N || (base && ldb < h->N)) return bad(MOE_ERR_INVALID_ARG, "a row pitch is below the width");
   const size_t e = elem_bytes(out_dtype);
@@ -155,12 +162,14 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
     LIN_TRY(launch_adapters(a, h->rpad, h->type == MOE_FP16, h->num_sms, st));
     return MOE_OK;
   }
-  int32_t* n_tiles = reinterpret_cast<int32_t*>(h->ws);
-  AdapterTile* tiles = reinterpret_cast<AdapterTile*>(h->ws + 256);
-  int32_t* order = reinterpret_cast<int32_t*>(h->ws + 256 + tile_bytes(h, h->T_max));
   a.cut = adapter_cut(T, h->n, h->num_sms);
-  LIN_TRY(launch_adapter_group(ids, T, h->n, a.cut.rows, a.slots, order, tiles, n_tiles, h->err, st));
-  a.order = order, a.tiles = tiles, a.n_tiles = n_tiles;
+  if (T > kAdapterCount) {
+    int32_t* n_tiles = reinterpret_cast<int32_t*>(h->ws);
+    AdapterTile* tiles = reinterpret_cast<AdapterTile*>(h->ws + 256);
+    int32_t* order = reinterpret_cast<int32_t*>(h->ws + 256 + tile_bytes(h, h->T_max));
+    LIN_TRY(launch_adapter_group(ids, T, h->n, a.cut.rows, a.slots, order, tiles, n_tiles, h->err, st));
+    a.order = order, a.tiles = tiles, a.n_tiles = n_tiles;
+  }
   LIN_TRY(launch_adapters_tc(a, h->rpad, h->type == MOE_FP16, st));
   return MOE_OK;
 }

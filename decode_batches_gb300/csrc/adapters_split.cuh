@@ -5,6 +5,18 @@
 
 namespace moe {
 
+// counts[key] += 1 for every lane with a key >= 0, and what was there before this lane's: a run of one key (a prompt's
+// rows) with one addition, else a lane's each, whose few collisions take less time than to find them (10 us of 22 at
+// 30000 rows).
+MOE_DEVICE int count_key(int* counts, int key, int lane) {
+  if (__all_sync(0xffffffffu, key == __shfl_sync(0xffffffffu, key, 0)) && key >= 0) {
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&counts[key], 32);
+    return __shfl_sync(0xffffffffu, at, 0) + lane;
+  }
+  return key >= 0 ? atomicAdd(&counts[key], 1) : 0;
+}
+
 // Eight elements of a row of x from column c (zeros past K), at any alignment.
 MOE_DEVICE uint4 load_x(const uint16_t* row, int c, int K) {
   uint32_t w[4];

@@ -240,3 +240,9 @@ def test_no_rows_and_refusals():
     with pytest.raises(ValueError):
         ad.forward(x, ids, buf[:4], out=buf[1:])
     ad.forward(x, ids, buf[:4], out=buf[:4])
+    # parts of one wide buffer: other columns of the same rows are no overlap, shared ones are
+    wide = torch.zeros((4, 160), dtype=torch.float32, device="cuda")
+    wide[:, :64] = base
+    assert torch.equal(ad.forward(x, ids, wide[:, :64], out=wide[:, 64:128]), ad.forward(x, ids, base))
+    with pytest.raises(ValueError):
+        ad.forward(x, ids, wide[:, :64], out=wide[:, 60:124])
