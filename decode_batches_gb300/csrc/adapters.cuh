@@ -31,7 +31,7 @@ __host__ __device__ inline int adapter_tile_rows(int all, int most) {
   const int parts = (all + most - 1) / most;
   return ((all + parts - 1) / parts + 15) / 16 * 16;
 }
-AdapterCut adapter_cut(int T, int n, int num_sms);
+AdapterCut adapter_cut(int T, int n, int rpad, int num_sms);
 
 struct AdapterArgs {
   const uint16_t* x = nullptr;      // [T][K]

@@ -162,7 +162,7 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
     LIN_TRY(launch_adapters(a, h->rpad, h->type == MOE_FP16, h->num_sms, st));
     return MOE_OK;
   }
-  a.cut = adapter_cut(T, h->n, h->num_sms);
+  a.cut = adapter_cut(T, h->n, h->rpad, h->num_sms);
   if (T > kAdapterCount) {
     int32_t* n_tiles = reinterpret_cast<int32_t*>(h->ws);
     AdapterTile* tiles = reinterpret_cast<AdapterTile*>(h->ws + 256);

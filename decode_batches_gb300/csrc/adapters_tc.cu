@@ -25,25 +25,33 @@ constexpr int kRows = 128;             // rows of a tile (the MMA's M)
 constexpr int kMathWarps = 8;          // gather, reduction, epilogue
 constexpr int kThreads = 32 * (kMathWarps + 1);
 constexpr int kSlice = 128;            // features of an expand step
+constexpr int kStagesMax = 8;
 
 // Shared memory: the ring, then u.  During the shrink its stages run on into u's place; after it the ring's start holds
 // the partial sums, B's first tiles come behind them and the later ones, once the sums are read, also in their place.
 template <int R>
 struct Cfg {
-  static constexpr int kXBytes = kRows * 128, kWBytes = R * 128, kStage = kXBytes + kWBytes;
+  static constexpr int kWBytes = R * 128;
   static constexpr int kTerm = kRows * R * 2;        // u's hi or lo
   static constexpr int kPart = kRows * R * 4;        // partial sums
   static constexpr int kBTile = kSlice * R * 2;
   static constexpr int kRing = R <= 64 ? 72 * 1024 : 128 * 1024;  // (two CTAs an SM up to rank 64)
-  static constexpr int kStagesMax = (kRing + 2 * kTerm) / kStage, kStages = kStagesMax < 4 ? kStagesMax : 4;
   static constexpr int kBEarly = (kRing - kPart) / kBTile < 4 ? (kRing - kPart) / kBTile : 4;
   static constexpr int kBSlots = kBEarly + kPart / kBTile;
   static constexpr int kRowBytes = (R < 64 ? R : 64) * 2;  // a row of u or of a B tile within a block of 64 ranks
-  static constexpr int kTail = kRows * 8 + 256;
+  static constexpr int kTail = kRows * 8 + 320;
   static constexpr int kBytes = kRing + 2 * kTerm + kTail + 1024;
   static constexpr int kTmemCols = 256;              // two buffers of 128; the shrink's R are the first's
   static constexpr int b_at(int slot) { return slot < kBEarly ? kPart + slot * kBTile : (slot - kBEarly) * kBTile; }
-  static_assert(kBEarly >= 2 && kBSlots <= 6 && kStages >= 3, "");
+  static_assert(kBEarly >= 2 && kBSlots <= 6, "");
+  // Stages for tiles of `rows` rows (64 or 128).  With 64 the MMA's other 64 rows are whatever follows, so that the last
+  // stage's 16 KB have to end within the memory: 6 stages of 16 KB instead of 4 of 24 at rank 64, the same bytes of x in
+  // flight as with whole tiles and half as many again as with half-empty stages.
+  static constexpr int stage_bytes(int rows) { return rows * 128 + kWBytes; }
+  static constexpr int stages(int rows) {
+    const int n = (kRing + 2 * kTerm - kRows * 128) / stage_bytes(rows) + 1, m = (kRing + 2 * kTerm) / stage_bytes(rows);
+    return n < m ? (n < kStagesMax ? n : kStagesMax) : (m < kStagesMax ? m : kStagesMax);
+  }
 };
 
 // Byte offset of 16-byte piece p of row r in a tile of kRowBytes-wide rows, swizzled over the row's own width.
@@ -88,8 +96,8 @@ struct Smem {
   uint8_t* u;
   int* rows;         // [128] row numbers, -1 past the last
   float* row_scale;  // [128] (fp16)
-  uint64_t* full;    // [kStages] x's 256 threads and A's copy
-  uint64_t* empty;   // [kStages]
+  uint64_t* full;    // [kStagesMax] x's 256 threads and A's copy
+  uint64_t* empty;   // [kStagesMax]
   uint64_t* b_full;  // [kBSlots]
   uint64_t* b_empty;
   uint64_t* o_full;  // [2] D of an expand step
@@ -104,7 +112,7 @@ struct Smem {
     rows = reinterpret_cast<int*>(p), p += kRows * 4;
     row_scale = reinterpret_cast<float*>(p), p += kRows * 4;
     full = reinterpret_cast<uint64_t*>(p);
-    empty = full + 4, b_full = empty + 4, b_empty = b_full + 6, o_full = b_empty + 6, o_empty = o_full + 2;
+    empty = full + kStagesMax, b_full = empty + kStagesMax, b_empty = b_full + 6, o_full = b_empty + 6, o_empty = o_full + 2;
     d_full = o_empty + 2;
     tmem_slot = reinterpret_cast<uint32_t*>(d_full + 1);
     abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -112,32 +120,44 @@ struct Smem {
 };
 
 // ---- the issuing lane ----------------------------------------------------------------------------------
+// The stages' ring, turn by turn.
+struct Turn {
+  int st = 0;
+  uint32_t phase = 0;
+  MOE_DEVICE void next(int stages) {
+    if (++st == stages) st = 0, phase ^= 1u;
+  }
+};
+
 template <int R, bool kFp16>
 MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
   using C = Cfg<R>;
   const uint32_t wbytes = rs * 16 * 128, idesc = kFp16 ? idesc_f16_f32(kRows, 16 * rs) : idesc_bf16_f32(kRows, 16 * rs);
   const uint64_t pol = l2_policy_evict_last();
-  const auto load = [&](int i) {
-    const int st = i % C::kStages;
+  const int xbytes = p.cut.rows * 128, stage = C::stage_bytes(p.cut.rows), stages = C::stages(p.cut.rows);
+  const auto load = [&](int i, int st) {
     mbar_arrive_expect_tx(&s.full[st], wbytes);
-    bulk_load(s.ring + st * C::kStage + C::kXBytes, w + static_cast<int64_t>(i) * C::kWBytes, wbytes, &s.full[st], pol);
+    bulk_load(s.ring + st * stage + xbytes, w + static_cast<int64_t>(i) * C::kWBytes, wbytes, &s.full[st], pol);
   };
-  for (int i = 0; i < n && i < C::kStages; ++i) load(i);
-  for (int i = 0; i < n; ++i) {
-    const int st = i % C::kStages;
-    if (!mbar_wait(&s.full[st], (i / C::kStages) & 1, s.abort_flag, p.err)) return;
+  fence_proxy_async_smem();  // (the ring was the tile search's memory)
+  for (int i = 0; i < n && i < stages; ++i) load(i, i);
+  Turn t, before;
+  for (int i = 0; i < n; ++i, t.next(stages)) {
+    if (!mbar_wait(&s.full[t.st], t.phase, s.abort_flag, p.err)) return;
     fence_proxy_async_smem();  // (x was written by the generic proxy)
     tc_fence_after();
-    const uint32_t at = smem_u32(s.ring + st * C::kStage);
-    const uint64_t xd = operand_desc<128>(at), wd = operand_desc<128>(at + C::kXBytes);
+    const uint32_t at = smem_u32(s.ring + t.st * stage);
+    const uint64_t xd = operand_desc<128>(at), wd = operand_desc<128>(at + xbytes);
 #pragma unroll
     for (int k = 0; k < 4; ++k) mma_f16_ss(tmem, xd + 2 * k, wd + 2 * k, idesc, i > 0 || k > 0);
-    mma_commit(&s.empty[st]);
+    mma_commit(&s.empty[t.st]);
+    if (i == 0) continue;
     // the stage of the step before is about to be free: its next A tile (x is asked for by the other warps)
-    if (i >= 1 && i - 1 + C::kStages < n) {
-      if (!mbar_wait(&s.empty[(i - 1) % C::kStages], ((i - 1) / C::kStages) & 1, s.abort_flag, p.err)) return;
-      load(i - 1 + C::kStages);
+    if (i - 1 + stages < n) {
+      if (!mbar_wait(&s.empty[before.st], before.phase, s.abort_flag, p.err)) return;
+      load(i - 1 + stages, before.st);
     }
+    before.next(stages);
   }
   mma_commit(s.d_full);
 }
@@ -205,10 +225,12 @@ MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R>& s, int k0, int n) 
     row[i] = p.x + max(t, 0) * p.ldx + 64 * static_cast<int64_t>(k0);
     dst[i] = swizzled<128>(r, piece);
   }
-  for (int i = 0; i < n; ++i) {
-    const int st = i % C::kStages;
-    if (!mbar_wait_warp(&s.empty[st], ((i / C::kStages) & 1) ^ 1, s.abort_flag, p.err)) return;
-    uint8_t* at = s.ring + st * C::kStage;
+  const int stage = C::stage_bytes(p.cut.rows), stages = C::stages(p.cut.rows);
+  Turn t;
+  for (int i = 0; i < n; ++i, t.next(stages)) {
+    const int st = t.st;
+    if (!mbar_wait_warp(&s.empty[st], t.phase ^ 1u, s.abort_flag, p.err)) return;
+    uint8_t* at = s.ring + st * stage;
     const int col = 64 * (k0 + i) + 8 * piece;
     if (p.x_vec) {
 #pragma unroll
@@ -511,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(c
   const Smem<R> s(smem_raw);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) mbar_init(&s.full[i], 32 * kMathWarps + 1), mbar_init(&s.empty[i], 1);
+    for (int i = 0; i < kStagesMax; ++i) mbar_init(&s.full[i], 32 * kMathWarps + 1), mbar_init(&s.empty[i], 1);
     for (int i = 0; i < C::kBSlots; ++i) mbar_init(&s.b_full[i], 1), mbar_init(&s.b_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&s.o_full[i], 1), mbar_init(&s.o_empty[i], kMathWarps);
     mbar_init(s.d_full, 1);
@@ -646,17 +668,18 @@ cudaError_t launch_adapter_tc_pack(const uint16_t* a, const uint16_t* b, uint16_
   }
 }
 
-// The most CTAs, up to two an SM (all that run at a time: a cluster more waits for the first to end, 96 us instead of 63 at
+// The most CTAs, up to two an SM (one above rank 64: all that run at a time; a cluster more waits for the first to end, 96 us instead of 63 at
 // 8195 rows), from tiles of 128 or 64 rows and clusters of 8 to 1.  The slots' rows are unknown here: half a tile is
 // lost to each slot, and a slot that is used has one at least.
-AdapterCut adapter_cut(int T, int n, int num_sms) {
+AdapterCut adapter_cut(int T, int n, int rpad, int num_sms) {
+  const int64_t fit = (rpad <= 64 ? 2 : 1) * num_sms;
   const int used = n < T ? n : T;
   AdapterCut best{kRows, 1};
   int64_t most = 0;
   for (int rows = kRows; rows >= kAdapterTileMin; rows /= 2) {
     const int64_t cut = static_cast<int64_t>(T) / rows + used / 2 + 1, tiles = cut > used ? cut : used;
     for (int c = 8; c >= 1; --c)
-      if (tiles * c <= 2 * num_sms && tiles * c > most) most = tiles * c, best = AdapterCut{rows, c};
+      if (tiles * c <= fit && tiles * c > most) most = tiles * c, best = AdapterCut{rows, c};
   }
   return best;
 }
