@@ -434,17 +434,19 @@ __global__ void adapter_pack_kernel(const uint16_t* a, const uint16_t* b, uint16
 // tiles, and places its rows.  The order of a slot's rows is not fixed; a row's result does not depend on its place.
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupCtas = 8;
-__global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int32_t* ids, int T, int n, int M,
-                                                                      const AdapterSlots slots, int32_t* order,
-                                                                      AdapterTile* tiles, int32_t* n_tiles, uint32_t* err) {
+__global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int32_t* ids, int T, int n, int ctas,
+                                                                      int fit, const AdapterSlots slots,
+                                                                      int32_t* order, AdapterTile* tiles,
+                                                                      int32_t* n_tiles, uint32_t* err) {
   __shared__ int s_count[kAdaptersMax + 1];                                             // of this CTA's rows
   __shared__ int s_all[kAdaptersMax + 1], s_first[kAdaptersMax + 1], s_tile[kAdaptersMax + 1];  // of the slot
   __shared__ int s_next[kAdaptersMax + 1];                                              // this CTA's next place
-  __shared__ int s_warp[2][32];
+  __shared__ int s_warp[2][32], s_tiles[kAdapterTileRows / 16];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = cluster_rank();
   for (int i = tid; i <= n; i += kGroupThreads) s_count[i] = 0;
+  if (tid < kAdapterTileRows / 16) s_tiles[tid] = 0;
   __syncthreads();
   bool bad_id = false;
   for (int i0 = cta * kGroupThreads; i0 < T; i0 += kGroupCtas * kGroupThreads) {
@@ -470,7 +472,21 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
       if (k < cta) before += v[k];
     }
   }
-  int r = c, t = (c + M - 1) / M;
+  // Rows of a tile: as few (64 to 128, in steps of 16) as leave the number of waves that 128 would need
+  constexpr int kSizes = kAdapterTileRows / 16;
+  const int of_slot = tid < n ? c : 0;
+#pragma unroll
+  for (int m = 3; m < kSizes; ++m) {
+    int v = (of_slot + 16 * m + 15) / (16 * m + 16);
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && v) atomicAdd(&s_tiles[m], v);
+  }
+  __syncthreads();
+  int M = kAdapterTileRows;
+  const int64_t waves = (static_cast<int64_t>(s_tiles[kSizes - 1]) * ctas + fit - 1) / fit;
+  for (int m = kSizes - 2; m >= 3; --m)
+    if (static_cast<int64_t>(s_tiles[m]) * ctas <= waves * fit) M = 16 * m + 16;
+  int r = c, t = (of_slot + M - 1) / M;
   for (int o = 1; o < 32; o <<= 1) {
     const int a = __shfl_up_sync(0xffffffffu, r, o), b = __shfl_up_sync(0xffffffffu, t, o);
     if (lane >= o) r += a, t += b;
@@ -478,20 +494,14 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
   if (lane == 31) s_warp[0][warp] = r, s_warp[1][warp] = t;
   __syncthreads();
   for (int w = 0; w < warp; ++w) r += s_warp[0][w], t += s_warp[1][w];
-  if (tid <= n) s_all[tid] = c, s_first[tid] = r - c, s_tile[tid] = t - (c + M - 1) / M, s_next[tid] = r - c + before;
-  if (tid == kGroupThreads - 1) {
-    if (n == kGroupThreads) {  // the slot behind the last thread's: the rows without an adapter
-      int all = 0, mine = 0;
-      for (int k = 0; k < kGroupCtas; ++k) {
-        const int v = ld_cluster_s32(cluster_addr(&s_count[n], k));
-        all += v;
-        if (k < cta) mine += v;
-      }
-      s_all[n] = all, s_first[n] = r, s_tile[n] = t, s_next[n] = r + mine;
-      t += (all + M - 1) / M;
-    }
-    if (cta == 0) *n_tiles = t;
+  if (tid <= n) s_all[tid] = c, s_first[tid] = r - c, s_tile[tid] = t - (of_slot + M - 1) / M, s_next[tid] = r - c + before;
+  if (n == kGroupThreads && tid == kGroupThreads - 1) {  // the rows without an adapter, behind the last thread's slot
+    int mine = 0;
+    for (int k = 0; k < cta; ++k) mine += ld_cluster_s32(cluster_addr(&s_count[n], k));
+    s_first[n] = r, s_next[n] = r + mine;
   }
+  __syncthreads();
+  if (cta == 0 && tid == kGroupThreads - 1) n_tiles[0] = t, n_tiles[1] = s_first[n], n_tiles[2] = M;
   cluster_barrier();  // (also: no CTA reads another's counts any more)
   for (int i0 = cta * kGroupThreads; i0 < T; i0 += kGroupCtas * kGroupThreads) {
     const int i = i0 + tid;
@@ -503,11 +513,12 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
     const int at = count_key(s_next, key, lane);
     if (key < 0) continue;
     order[at] = i;
+    if (key == n) continue;
     const int in = at - s_first[key];
     const int all = s_all[key], per = adapter_tile_rows(all, M);  // the row that comes first in a tile writes the tile
     if (in % per == 0) {
-      AdapterTile t{-1, at, static_cast<uint16_t>(min(per, all - in)), 0, 0.0f};
-      if (key < n) t.slot = key, t.rank = static_cast<uint16_t>(slots.rank[key]), t.scale = slots.scale[key];
+      const AdapterTile t{key, at, static_cast<uint16_t>(min(per, all - in)), static_cast<uint16_t>(slots.rank[key]),
+                          slots.scale[key]};
       tiles[s_tile[key] + in / per] = t;
     }
   }
@@ -541,10 +552,10 @@ cudaError_t launch_adapter_pack(const uint16_t* a, const uint16_t* b, uint16_t* 
   return cudaGetLastError();
 }
 
-cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, int rows, const AdapterSlots& slots, int32_t* order,
+cudaError_t launch_adapter_group(const int32_t* ids, int T, int n, const AdapterCut& cut, const AdapterSlots& slots, int32_t* order,
                                  AdapterTile* tiles, int32_t* n_tiles, uint32_t* err, cudaStream_t st) {
-  return launch_pdl_clusters(adapter_group_kernel, dim3(kGroupCtas), dim3(kGroupThreads), kGroupCtas, 0, st, ids, T, n, rows,
-                             slots, order, tiles, n_tiles, err);
+  return launch_pdl_clusters(adapter_group_kernel, dim3(kGroupCtas), dim3(kGroupThreads), kGroupCtas, 0, st, ids, T, n,
+                             cut.ctas, cut.slots, slots, order, tiles, n_tiles, err);
 }
 
 cudaError_t launch_adapters(const AdapterArgs& p, int rpad, bool fp16, int num_sms, cudaStream_t st) {

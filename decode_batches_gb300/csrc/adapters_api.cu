@@ -31,7 +31,8 @@ struct moe_adapters {
 constexpr int kMaxRows = 1 << 26;
 
 static size_t tile_bytes(const moe_adapters* h, int T) {
-  return (static_cast<size_t>(T / kAdapterTileMin + h->n + 2) * sizeof(AdapterTile) + 255) & ~size_t(255);
+  // an entry for every cluster of a grid: whole waves beside T / 128 + n tiles, and those that copy
+  return (static_cast<size_t>(T / kAdapterTileRows + h->n + 4 + 4 * h->num_sms) * sizeof(AdapterTile) + 255) & ~size_t(255);
 }
 
 extern "C" moe_adapters* moe_adapters_create(int n, int N, int K, int r_max, moe_dtype dtype) {
@@ -164,10 +165,11 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
   }
   a.cut = adapter_cut(T, h->n, h->rpad, h->num_sms);
   if (T > kAdapterCount) {
+    a.cut.rows = kAdapterTileRows;  // (the grouping lowers it)
     int32_t* n_tiles = reinterpret_cast<int32_t*>(h->ws);
     AdapterTile* tiles = reinterpret_cast<AdapterTile*>(h->ws + 256);
     int32_t* order = reinterpret_cast<int32_t*>(h->ws + 256 + tile_bytes(h, h->T_max));
-    LIN_TRY(launch_adapter_group(ids, T, h->n, a.cut.rows, a.slots, order, tiles, n_tiles, h->err, st));
+    LIN_TRY(launch_adapter_group(ids, T, h->n, a.cut, a.slots, order, tiles, n_tiles, h->err, st));
     a.order = order, a.tiles = tiles, a.n_tiles = n_tiles;
   }
   LIN_TRY(launch_adapters_tc(a, h->rpad, h->type == MOE_FP16, st));

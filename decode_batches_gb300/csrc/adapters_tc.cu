@@ -22,22 +22,24 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 128;             // rows of a tile (the MMA's M)
-constexpr int kMathWarps = 8;          // gather, reduction, epilogue
-constexpr int kThreads = 32 * (kMathWarps + 1);
 constexpr int kSlice = 128;            // features of an expand step
 constexpr int kStagesMax = 8;
 
 // Shared memory: the ring, then u.  During the shrink its stages run on into u's place; after it the ring's start holds
 // the partial sums, B's first tiles come behind them and the later ones, once the sums are read, also in their place.
-template <int R>
+template <int R, int W>
 struct Cfg {
+  static constexpr int kThreads = 32 * (W + 1);      // W warps gather, add up and write, one lane issues
+  static constexpr int kCtas = W == 8 ? 2 : 1;       // an SM
+
   static constexpr int kWBytes = R * 128;
   static constexpr int kTerm = kRows * R * 2;        // u's hi or lo
   static constexpr int kPart = kRows * R * 4;        // partial sums
   static constexpr int kBTile = kSlice * R * 2;
-  static constexpr int kRing = R <= 64 ? 72 * 1024 : 128 * 1024;  // (two CTAs an SM up to rank 64)
+  static constexpr int kRing = W == 8 ? 72 * 1024 : R <= 64 ? 160 * 1024 : 128 * 1024;
   static constexpr int kBEarly = (kRing - kPart) / kBTile < 4 ? (kRing - kPart) / kBTile : 4;
   static constexpr int kBSlots = kBEarly + kPart / kBTile;
+  static_assert(W == 16 || R <= 64, "");
   static constexpr int kRowBytes = (R < 64 ? R : 64) * 2;  // a row of u or of a B tile within a block of 64 ranks
   static constexpr int kTail = kRows * 8 + 320;
   static constexpr int kBytes = kRing + 2 * kTerm + kTail + 1024;
@@ -90,25 +92,27 @@ MOE_DEVICE void st_cluster_f32(uint32_t addr, float v) {
 // Generic writes (also to another CTA's shared memory) before the tensor core's reads.
 MOE_DEVICE void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-template <int R>
+template <int R, int W>
 struct Smem {
   uint8_t* ring;
   uint8_t* u;
   int* rows;         // [128] row numbers, -1 past the last
   float* row_scale;  // [128] (fp16)
-  uint64_t* full;    // [kStagesMax] x's 256 threads and A's copy
+  uint64_t* full;    // [kStagesMax] the threads that copy x, and A's copy
   uint64_t* empty;   // [kStagesMax]
   uint64_t* b_full;  // [kBSlots]
   uint64_t* b_empty;
   uint64_t* o_full;  // [2] D of an expand step
   uint64_t* o_empty;
   uint64_t* d_full;  // the shrink's D
+  int tile_rows;     // 64 or 128: rows that the stages and the MMAs are made for
+  int spare;         // rows without an adapter that this cluster copies
   uint32_t* tmem_slot;
   volatile int* abort_flag;
   MOE_DEVICE explicit Smem(uint8_t* raw) {
     uint8_t* p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    ring = p, p += Cfg<R>::kRing;
-    u = p, p += 2 * Cfg<R>::kTerm;
+    ring = p, p += Cfg<R, W>::kRing;
+    u = p, p += 2 * Cfg<R, W>::kTerm;
     rows = reinterpret_cast<int*>(p), p += kRows * 4;
     row_scale = reinterpret_cast<float*>(p), p += kRows * 4;
     full = reinterpret_cast<uint64_t*>(p);
@@ -129,12 +133,12 @@ struct Turn {
   }
 };
 
-template <int R, bool kFp16>
-MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
-  using C = Cfg<R>;
-  const uint32_t wbytes = rs * 16 * 128, idesc = kFp16 ? idesc_f16_f32(kRows, 16 * rs) : idesc_bf16_f32(kRows, 16 * rs);
+template <int R, int W, bool kFp16>
+MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R, W>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
+  using C = Cfg<R, W>;
+  const uint32_t wbytes = rs * 16 * 128, idesc = kFp16 ? idesc_f16_f32(s.tile_rows, 16 * rs) : idesc_bf16_f32(s.tile_rows, 16 * rs);
   const uint64_t pol = l2_policy_evict_last();
-  const int xbytes = p.cut.rows * 128, stage = C::stage_bytes(p.cut.rows), stages = C::stages(p.cut.rows);
+  const int xbytes = s.tile_rows * 128, stage = C::stage_bytes(s.tile_rows), stages = C::stages(s.tile_rows);
   const auto load = [&](int i, int st) {
     mbar_arrive_expect_tx(&s.full[st], wbytes);
     bulk_load(s.ring + st * stage + xbytes, w + static_cast<int64_t>(i) * C::kWBytes, wbytes, &s.full[st], pol);
@@ -162,21 +166,21 @@ MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R>& s, const uint8
   mma_commit(s.d_full);
 }
 
-template <int R>
-MOE_DEVICE void load_b(const AdapterArgs& p, const Smem<R>& s, const uint8_t* w, int j) {
-  using C = Cfg<R>;
+template <int R, int W>
+MOE_DEVICE void load_b(const AdapterArgs& p, const Smem<R, W>& s, const uint8_t* w, int j) {
+  using C = Cfg<R, W>;
   const int at = j % C::kBSlots;
   mbar_arrive_expect_tx(&s.b_full[at], C::kBTile);
   bulk_load(s.ring + C::b_at(at), w + static_cast<int64_t>(j) * C::kBTile, C::kBTile, &s.b_full[at],
             l2_policy_evict_last());
 }
 
-template <int R, bool kFp16>
-MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
-  using C = Cfg<R>;
-  const uint32_t idesc = kFp16 ? idesc_f16_f32(kRows, kSlice) : idesc_bf16_f32(kRows, kSlice);
+template <int R, int W, bool kFp16>
+MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R, W>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
+  using C = Cfg<R, W>;
+  const uint32_t idesc = kFp16 ? idesc_f16_f32(s.tile_rows, kSlice) : idesc_bf16_f32(s.tile_rows, kSlice);
   const uint32_t u0 = smem_u32(s.u), b0 = smem_u32(s.ring);
-  for (int j = C::kBEarly; j < n && j < C::kBSlots; ++j) load_b<R>(p, s, w, j);  // (the partial sums' place is free now)
+  for (int j = C::kBEarly; j < n && j < C::kBSlots; ++j) load_b<R, W>(p, s, w, j);  // (the partial sums' place is free now)
   for (int j = 0; j < n; ++j) {
     const int at = j % C::kBSlots, buf = j & 1;
     if (!mbar_wait(&s.b_full[at], (j / C::kBSlots) & 1, s.abort_flag, p.err)) return;
@@ -192,7 +196,7 @@ MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R>& s, const uint8
     mma_commit(&s.o_full[buf]);
     if (j >= 1 && j - 1 + C::kBSlots < n) {
       if (!mbar_wait(&s.b_empty[(j - 1) % C::kBSlots], ((j - 1) / C::kBSlots) & 1, s.abort_flag, p.err)) return;
-      load_b<R>(p, s, w, j - 1 + C::kBSlots);
+      load_b<R, W>(p, s, w, j - 1 + C::kBSlots);
     }
   }
 }
@@ -208,24 +212,25 @@ MOE_DEVICE void cp_async_mbar_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// x's rows into the stages: eight lanes a row's 128 bytes, four rows a lane.  The copies announce themselves; a proxy
+// x's rows into the stages: eight lanes a row's 128 bytes, 32 / W rows a lane.  The copies announce themselves; a proxy
 // fence here, before each announcement, waited for every copy in flight and made the stages take turns (0.8 us each),
 // so the issuing lane has it.
-template <int R>
-MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R>& s, int k0, int n) {
-  using C = Cfg<R>;
+template <int R, int W>
+MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R, W>& s, int k0, int n) {
+  using C = Cfg<R, W>;
   const int piece = threadIdx.x & 7;
-  const uint16_t* row[4];
-  uint32_t dst[4];
-  bool live[4];
+  constexpr int kPer = kRows / (4 * W);
+  const uint16_t* row[kPer];
+  uint32_t dst[kPer];
+  bool live[kPer];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (threadIdx.x >> 3) + 32 * i, t = s.rows[r];
+  for (int i = 0; i < kPer; ++i) {
+    const int r = (threadIdx.x >> 3) + 4 * W * i, t = s.rows[r];
     live[i] = t >= 0;  // (rows past the tile's last keep what the stage holds: their results go nowhere)
     row[i] = p.x + max(t, 0) * p.ldx + 64 * static_cast<int64_t>(k0);
     dst[i] = swizzled<128>(r, piece);
   }
-  const int stage = C::stage_bytes(p.cut.rows), stages = C::stages(p.cut.rows);
+  const int stage = C::stage_bytes(s.tile_rows), stages = C::stages(s.tile_rows);
   Turn t;
   for (int i = 0; i < n; ++i, t.next(stages)) {
     const int st = t.st;
@@ -234,12 +239,12 @@ MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R>& s, int k0, int n) 
     const int col = 64 * (k0 + i) + 8 * piece;
     if (p.x_vec) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < kPer; ++j)
         if (live[j]) cp_async_16_part(smem_u32(at + dst[j]), col < p.K ? row[j] + 64 * i + 8 * piece : p.x, col < p.K ? 16u : 0u);
       cp_async_mbar_arrive(&s.full[st]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < kPer; ++j)
         if (live[j]) *reinterpret_cast<uint4*>(at + dst[j]) = load_x(row[j] - 64 * static_cast<int64_t>(k0), col, p.K);
       mbar_arrive(&s.full[st]);
     }
@@ -252,10 +257,10 @@ MOE_DEVICE uint32_t part_at(int row, int unit) {
   constexpr int kMask = R / 4 < 8 ? R / 4 - 1 : 7;
   return (row * (R / 4) + (unit ^ (row & kMask))) * 16;
 }
-template <int R>
-MOE_DEVICE void write_part(const Smem<R>& s, uint32_t tmem, bool any) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = 32 * (warp & 3) + lane;
-  for (int c = 16 * (warp >> 2); c < R; c += 32) {
+template <int R, int W>
+MOE_DEVICE void write_part(const Smem<R, W>& s, uint32_t tmem, bool any) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = s.tile_rows / 4, row = per * (warp & 3) + lane;
+  for (int c = 16 * (warp >> 2); c < R; c += 4 * W) {
     uint32_t v[16];
     if (any) {
       tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
@@ -264,6 +269,7 @@ MOE_DEVICE void write_part(const Smem<R>& s, uint32_t tmem, bool any) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = 0u;
     }
+    if (lane >= per) continue;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<uint4*>(s.ring + part_at<R>(row, c / 4 + i)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -271,12 +277,12 @@ MOE_DEVICE void write_part(const Smem<R>& s, uint32_t tmem, bool any) {
 }
 
 // u of this CTA's share of the rows, into every CTA of the cluster.
-template <int R, bool kFp16>
-MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R>& s, float scale, int rank, int rows, int cta) {
-  using C = Cfg<R>;
+template <int R, int W, bool kFp16>
+MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R, W>& s, float scale, int rank, int rows, int cta) {
+  using C = Cfg<R, W>;
   // (whole warps take part, 256 / R rows each; those past the tile's last repeat it)
   const int share = (rows + p.cut.ctas - 1) / p.cut.ctas;
-  for (int i = threadIdx.x * 8; (i & ~255) < share * R; i += 32 * kMathWarps * 8) {
+  for (int i = threadIdx.x * 8; (i & ~255) < share * R; i += 32 * W * 8) {
     const int r = min(min(i / R, share - 1) + cta * share, rows - 1), c = i % R;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     // (rows of 256 bytes and more: half of eight lanes take their second unit first, so that they meet no bank twice)
@@ -314,16 +320,17 @@ MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R>& s, float scale, int
   }
 }
 
-// The expand's steps: warp w has the rows of lane quarter w % 4 and half w / 4 of the step's features.  A step is four
-// units of 16 rows and 32 features.  The base of a unit is asked for kAhead units before it is used: with two units of
-// 16-bit rows in flight a warp, 32 KB an SM, the memory's latency held the writes at 4.5 TB/s.
+// The expand's steps: warp w has the rows of lane quarter w % 4 (32, or 16 of a 64-row tile) and the w / 4-th 32 (8 warps:
+// 64) of the step's features, in units of 16 rows and 32 features.  The base of a unit is asked for four units (32-bit
+// rows: two) before it is used: with two of 16-bit rows, 32 KB an SM, the memory's latency held the writes at 4.5 TB/s.
 // kWhole: rows are 16-byte aligned and N is a multiple of 128: no column is checked.
-template <typename E, int R, bool kFp16, bool kWhole>
-MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R>& s, int s0, int n, int rank, uint32_t tmem) {
+template <typename E, int R, int W, bool kFp16, bool kWhole>
+MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R, W>& s, int s0, int n, uint32_t tmem) {
+  constexpr int kCols = 512 / W, kChunks = kCols / 32, kUnits = 2 * kChunks;  // of a warp in a step
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int quarter = warp & 3, half = warp >> 2;
+  const int quarter = warp & 3, part = warp >> 2, per = s.tile_rows / 4;
   const bool has_base = p.base != nullptr;
-  const int first = s0 * kSlice + 64 * half + 8 * q;  // this lane's column of a step's first units
+  const int first = s0 * kSlice + kCols * part + 8 * q;  // this lane's column of the first step
   const E* base[2][2];
   E* out[2][2];
   float mul[2][2];
@@ -332,120 +339,149 @@ MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R>& s, int s0, int n,
   for (int m = 0; m < 2; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int at = 32 * quarter + 16 * m + 8 * h + g, r = s.rows[at];
+      const int at = per * quarter + 16 * m + 8 * h + g, r = 16 * m < per ? s.rows[at] : -1;
       live[m][h] = r >= 0;
       base[m][h] = static_cast<const E*>(has_base ? p.base : p.out) + max(r, 0) * (has_base ? p.ld_base : p.ld_out) + first;
       out[m][h] = static_cast<E*>(p.out) + max(r, 0) * p.ld_out + first;
-      mul[m][h] = kFp16 && rank > 0 ? s.row_scale[at] : 1.0f;
+      mul[m][h] = kFp16 && r >= 0 ? s.row_scale[at] : 1.0f;
     }
-  const bool some[2] = {s.rows[32 * quarter] >= 0, s.rows[32 * quarter + 16] >= 0};  // (rows come first, gaps last)
-  constexpr int kAhead = sizeof(E) == 2 ? 4 : 2;
+  const bool some[2] = {s.rows[per * quarter] >= 0, per > 16 && s.rows[per * quarter + 16] >= 0};  // (gaps come last)
+  constexpr int kAhead = sizeof(E) == 2 ? 4 : 2;  // units, whole steps' or half a step's
+  constexpr int kTurn = kAhead > kUnits ? kAhead / kUnits : 1;  // steps after which the units' places repeat
   Raw8<E> b[kAhead][2];
-  // unit `unit` of the step `next` steps on
-  const auto ask = [&](int j, int next, int unit, Raw8<E> (&to)[2]) {
-    const int m = unit >> 1, off = next * kSlice + 32 * (unit & 1);
+  // unit u (m = u / kChunks, chunk u % kChunks) of step j + ahead
+  const auto ask = [&](int j, int ahead, int u, Raw8<E> (&to)[2]) {
+    const int m = u / kChunks, off = ahead * kSlice + 32 * (u % kChunks);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const bool in = kWhole || (p.out_vec && first + j * kSlice + off < p.N);
-      if (has_base && live[m][h] && j + next < n && in)
+      if (has_base && live[m][h] && j + ahead < n && in)
         to[h].load(base[m][h] + off);
       else
         to[h].zero();
     }
   };
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) ask(0, 0, i, b[i]);
-  for (int j = 0; j < n; ++j) {
-    const int buf = j & 1;
-    if (rank > 0) {
+  for (int i = 0; i < kAhead; ++i) ask(0, i / kUnits, i % kUnits, b[i]);
+  for (int j0 = 0; j0 < n; j0 += kTurn) {
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i) {
+      const int j = j0 + i, buf = j & 1;
+      if (j >= n) break;
       if (!mbar_wait_warp(&s.o_full[buf], (j >> 1) & 1, s.abort_flag, p.err)) return;
       tc_fence_after();
-    }
-    const uint32_t at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + buf * kSlice + 64 * half;
+      const uint32_t at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + buf * kSlice + kCols * part;
 #pragma unroll
-    for (int unit = 0; unit < 4; ++unit) {
-      const int m = unit >> 1, c = unit & 1;
-      if (some[m]) {
-        uint32_t d[16];
-        if (rank > 0) {
+      for (int u = 0; u < kUnits; ++u) {
+        const int m = u / kChunks, c = u % kChunks, place = (i * kUnits + u) % kAhead;
+        if (some[m]) {
+          uint32_t d[16];
           tmem_ld_16x256b_x4(at + (static_cast<uint32_t>(16 * m) << 16) + 32 * c, d);
           tmem_wait_ld();
-        } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) d[i] = 0u;
-        }
+          for (int h = 0; h < 2; ++h) {
+            if (!live[m][h]) continue;
+            float v[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!live[m][h]) continue;
-          float v[8];
+            for (int e = 0; e < 4; ++e)
+              v[2 * e] = __uint_as_float(d[4 * e + 2 * h]), v[2 * e + 1] = __uint_as_float(d[4 * e + 2 * h + 1]);
+            const int col = first + j * kSlice + 32 * c;
+            if (kWhole || p.out_vec) {
+              float f[8];
+              b[place][h].to_f32(f);
+              if (kFp16) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[2 * i] = __uint_as_float(d[4 * i + 2 * h]), v[2 * i + 1] = __uint_as_float(d[4 * i + 2 * h + 1]);
-          if (kWhole || p.out_vec) {
-            float f[8];
-            b[unit % kAhead][h].to_f32(f);
-            if (kFp16) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], mul[m][h], f[i]);
-            } else {
-              add8(v, f);
-            }
-            if (kWhole || first + j * kSlice + 32 * c < p.N) store8(out[m][h] + 32 * c, v);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (first + j * kSlice + 32 * c + i < p.N) {
-                const float f = has_base ? base[m][h][32 * c + i].f32() : 0.0f;
-                out[m][h][32 * c + i] = E::of(kFp16 ? fmaf(v[i], mul[m][h], f) : v[i] + f);
+                for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], mul[m][h], f[e]);
+              } else {
+                add8(v, f);
               }
+              if (kWhole || col < p.N) store8(out[m][h] + 32 * c, v);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (col + e < p.N) {
+                  const float f = has_base ? base[m][h][32 * c + e].f32() : 0.0f;
+                  out[m][h][32 * c + e] = E::of(kFp16 ? fmaf(v[e], mul[m][h], f) : v[e] + f);
+                }
+            }
           }
         }
+        ask(j, (u + kAhead) / kUnits, (u + kAhead) % kUnits, b[place]);
       }
-      ask(j, unit + kAhead < 4 ? 0 : 1, (unit + kAhead) % 4, b[unit % kAhead]);
-    }
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) base[m][h] += kSlice, out[m][h] += kSlice;
-    if (rank > 0) {
+        for (int h = 0; h < 2; ++h) base[m][h] += kSlice, out[m][h] += kSlice;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.o_empty[buf]);
     }
   }
 }
-template <typename E, int R, bool kFp16>
-MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R>& s, int s0, int n, int rank, uint32_t tmem) {
+template <typename E, int R, int W, bool kFp16>
+MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R, W>& s, int s0, int n, uint32_t tmem) {
   if (p.out_vec && p.N % kSlice == 0)
-    write_out<E, R, kFp16, true>(p, s, s0, n, rank, tmem);
+    write_out<E, R, W, kFp16, true>(p, s, s0, n, tmem);
   else
-    write_out<E, R, kFp16, false>(p, s, s0, n, rank, tmem);
+    write_out<E, R, W, kFp16, false>(p, s, s0, n, tmem);
 }
 
-// The cluster's tile and its rows (to s.rows) from the grouping's list.  Every thread of the CTA calls it.
-template <int R>
-MOE_DEVICE bool read_tile(const AdapterArgs& p, const Smem<R>& s, AdapterTile& t) {
-  const int idx = blockIdx.x / p.cut.ctas, n = *p.n_tiles;
+// out = base (or zero) for a row: the bits, a warp a row.
+MOE_DEVICE void copy_row(const AdapterArgs& p, int64_t row, int lane) {
+  const int64_t e = p.out_type == MOE_FP32 ? 4 : 2, bytes = p.N * e;
+  const uint8_t* from = p.base ? static_cast<const uint8_t*>(p.base) + row * p.ld_base * e : nullptr;
+  uint8_t* to = static_cast<uint8_t*>(p.out) + row * p.ld_out * e;
+  if (p.out_vec) {
+    constexpr int kAhead = 8;
+    for (int64_t i = lane * 16; i < bytes; i += 512 * kAhead) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        v[k] = from && i + 512 * k < bytes ? *reinterpret_cast<const uint4*>(from + i + 512 * k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (i + 512 * k < bytes) *reinterpret_cast<uint4*>(to + i + 512 * k) = v[k];
+    }
+  } else {
+    for (int64_t i = lane * 2; i < bytes; i += 64)
+      *reinterpret_cast<uint16_t*>(to + i) = from ? *reinterpret_cast<const uint16_t*>(from + i) : static_cast<uint16_t>(0);
+  }
+}
+
+// What the cluster does: a tile (its rows in s.rows), or, behind the last tile, its share of the rows without an adapter
+// (rank 0, t.rows of them from p.order[t.start], or in s.rows).  Every thread of the CTA calls it.
+// From the grouping's list:
+template <int R, int W>
+MOE_DEVICE void read_tile(const AdapterArgs& p, Smem<R, W>& s, AdapterTile& t) {
+  const int idx = blockIdx.x / p.cut.ctas;
   t = p.tiles[idx];  // (the list has an entry for every cluster of the grid)
-  if (idx >= n) return false;
-  if (threadIdx.x < kRows) s.rows[threadIdx.x] = threadIdx.x < t.rows ? p.order[t.start + threadIdx.x] : -1;
+  const int n = p.n_tiles[0], rest = p.n_tiles[1];
+  s.tile_rows = p.n_tiles[2] <= 64 ? 64 : kRows;
+  if (idx < n) {
+    if (threadIdx.x < kRows) s.rows[threadIdx.x] = threadIdx.x < t.rows ? p.order[t.start + threadIdx.x] : -1;
+  } else {
+    const int clusters = gridDim.x / p.cut.ctas - n, share = (p.T - rest + clusters - 1) / clusters;
+    t.start = min(rest + (idx - n) * share, p.T);
+    s.spare = min(share, p.T - t.start);
+    t.rank = 0;
+  }
   __syncthreads();
-  return true;
 }
 
-// The same from the ids, by every CTA for itself: counts of all slots (no adapter counts as slot n), their tiles' scan,
-// the slot that holds the cluster's tile, and that slot's rows in order.  Beside 64 x 64 products, 300 rows: 9.8 us, with
-// the grouping's launch 12.0; 2051 rows: 13.6 and 13.4; 4096: 17.7 and 18.6, but 19.9 and 19.8 with two slots.
-template <int R>
-MOE_DEVICE bool count_tile(const AdapterArgs& p, const Smem<R>& s, AdapterTile& t) {
-  constexpr int kCounters = 32 * kMathWarps;
+// From the ids, by every CTA for itself: counts of all slots (no adapter counts as slot n), their tiles' scan, the slot
+// that holds the cluster's tile, and that slot's rows in order.  Beside 64 x 64 products, 300 rows: 9.8 us, with the
+// grouping's launch 12.0; 2051 rows: 13.6 and 13.4; 4096: 17.7 and 18.6, but 19.9 and 19.8 with two slots.
+template <int R, int W>
+MOE_DEVICE void count_tile(const AdapterArgs& p, Smem<R, W>& s, AdapterTile& t) {
+  constexpr int kCounters = 32 * W;
   int* counts = reinterpret_cast<int*>(s.ring);     // [n + 1]
-  int* warp_sum = counts + kAdaptersMax + 8;        // [8]
-  int* pick = warp_sum + kMathWarps;                // slot, rows of the slot, tile within the slot
-  const int idx = blockIdx.x / p.cut.ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int* warp_sum = counts + kAdaptersMax + 8;        // [W]
+  int* pick = warp_sum + W;                // slot, tile within the slot, all tiles
+  const int idx = blockIdx.x / p.cut.ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, most = p.cut.rows;
   const bool counter = tid < kCounters;
-  for (int i = tid; i <= p.n; i += kThreads) counts[i] = 0;
-  if (tid == 0) pick[0] = -1;
+  s.tile_rows = most <= 64 ? 64 : kRows;
+  for (int i = tid; i <= p.n; i += Cfg<R, W>::kThreads) counts[i] = 0;
+  if (tid == 0) pick[0] = p.n, pick[1] = 0;
   if (tid < kRows) s.rows[tid] = -1;
   __syncthreads();
   // a warp has a stretch of the step, whose ids stay in its lanes' registers
@@ -455,26 +491,25 @@ MOE_DEVICE bool count_tile(const AdapterArgs& p, const Smem<R>& s, AdapterTile& 
 #pragma unroll
   for (int j = 0; j < kIds; ++j) {
     const int i = i0 + 32 * j + lane;
-    key[j] = counter && j < stretch && i < p.T ? p.ids[i] : -2;
+    key[j] = -2;
+    if (counter && j < stretch && i < p.T) {
+      key[j] = p.ids[i];
+      if (key[j] < 0 || key[j] >= p.n) {
+        if (key[j] != -1 && blockIdx.x == 0) set_error(p.err, MOE_DEVERR_EXPERT_RANGE);
+        key[j] = p.n;
+      }
+    }
   }
   if (counter) {
-    bool bad_id = false;
 #pragma unroll
-    for (int j = 0; j < kIds; ++j) {
-      if (j >= stretch) break;
-      if (key[j] != -2 || i0 + 32 * j + lane < p.T) {
-        if (key[j] < 0 || key[j] >= p.n) bad_id |= key[j] != -1, key[j] = p.n;
-      }
-      count_key(counts, key[j], lane);
-    }
-    if (bad_id && blockIdx.x == 0) set_error(p.err, MOE_DEVERR_EXPERT_RANGE);
+    for (int j = 0; j < kIds; ++j) count_key(counts, key[j], lane);
   }
   __syncthreads();
   // a counter's share of consecutive slots: its tiles, and those before it
-  const int share = (p.n + 1 + kCounters - 1) / kCounters, first = tid * share, last = min(first + share, p.n + 1);
+  const int share = (p.n + kCounters - 1) / kCounters, first = min(tid * share, p.n), last = min(first + share, p.n);
   int mine = 0, upto = 0;
   if (counter) {
-    for (int k = first; k < last; ++k) mine += (counts[k] + p.cut.rows - 1) / p.cut.rows;
+    for (int k = first; k < last; ++k) mine += (counts[k] + most - 1) / most;
     upto = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -488,22 +523,30 @@ MOE_DEVICE bool count_tile(const AdapterArgs& p, const Smem<R>& s, AdapterTile& 
     int at = upto - mine;
     if (idx >= at && idx < upto)
       for (int k = first; k < last; ++k) {
-        const int tiles = (counts[k] + p.cut.rows - 1) / p.cut.rows;
+        const int tiles = (counts[k] + most - 1) / most;
         if (idx < at + tiles) {
-          pick[0] = k, pick[1] = counts[k], pick[2] = idx - at;
+          pick[0] = k, pick[1] = idx - at;
           break;
         }
         at += tiles;
       }
+    if (tid == kCounters - 1) pick[2] = upto;
   }
   __syncthreads();
-  const int slot = pick[0], all = pick[1];
-  if (slot < 0) return false;
-  const int per = adapter_tile_rows(all, p.cut.rows), from = pick[2] * per;
-  t.slot = slot < p.n ? slot : -1, t.start = 0, t.rows = static_cast<uint16_t>(min(per, all - from));
-  t.rank = slot < p.n ? static_cast<uint16_t>(p.slots.rank[slot]) : 0;
-  t.scale = slot < p.n ? p.slots.scale[slot] : 0.0f;
-  // each warp numbers the slot's rows of its stretch
+  // the rows of `slot` whose number lies in [from, from + rows)
+  const int slot = pick[0], all = counts[slot];
+  int from, rows;
+  if (slot < p.n) {
+    const int per = adapter_tile_rows(all, most);
+    from = pick[1] * per, rows = min(per, all - from);
+    t.rank = static_cast<uint16_t>(p.slots.rank[slot]), t.scale = p.slots.scale[slot];
+  } else {  // behind the last tile: a share of the rows without an adapter, 128 at most (there are clusters enough)
+    const int clusters = gridDim.x / p.cut.ctas - pick[2], per = (all + clusters - 1) / clusters;
+    from = min((idx - pick[2]) * per, all), rows = min(per, all - from);
+    t.rank = 0, t.scale = 0.0f;
+  }
+  t.slot = slot, t.start = -1, t.rows = static_cast<uint16_t>(rows);
+  s.spare = rows;
   int number = 0;
   if (counter) {
 #pragma unroll
@@ -518,29 +561,28 @@ MOE_DEVICE bool count_tile(const AdapterArgs& p, const Smem<R>& s, AdapterTile& 
     for (int j = 0; j < kIds; ++j) {
       const uint32_t b = __ballot_sync(0xffffffffu, key[j] == slot);
       const int at = number + __popc(b & ((1u << lane) - 1u));
-      if (key[j] == slot && at >= 0 && at < t.rows) s.rows[at] = i0 + 32 * j + lane;
+      if (key[j] == slot && at >= 0 && at < rows) s.rows[at] = i0 + 32 * j + lane;
       number += __popc(b);
     }
   }
   __syncthreads();  // (the ring's memory is free again, too)
-  return true;
 }
 
-template <int R, bool kFp16>
-__global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(const AdapterArgs p) {
-  using C = Cfg<R>;
+template <int R, int W, bool kFp16>
+__global__ void __launch_bounds__(Cfg<R, W>::kThreads, Cfg<R, W>::kCtas) adapter_tc_kernel(const AdapterArgs p) {
+  using C = Cfg<R, W>;
   extern __shared__ uint8_t smem_raw[];
-  const Smem<R> s(smem_raw);
+  Smem<R, W> s(smem_raw);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStagesMax; ++i) mbar_init(&s.full[i], 32 * kMathWarps + 1), mbar_init(&s.empty[i], 1);
+    for (int i = 0; i < kStagesMax; ++i) mbar_init(&s.full[i], 32 * W + 1), mbar_init(&s.empty[i], 1);
     for (int i = 0; i < C::kBSlots; ++i) mbar_init(&s.b_full[i], 1), mbar_init(&s.b_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&s.o_full[i], 1), mbar_init(&s.o_empty[i], kMathWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.o_full[i], 1), mbar_init(&s.o_empty[i], W);
     mbar_init(s.d_full, 1);
     *s.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMathWarps) {
+  if (warp == W) {
     tmem_alloc(s.tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
@@ -552,65 +594,74 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(c
   pdl_wait();
   const int cta = cluster_rank();
   AdapterTile t;
-  const bool found = p.tiles ? read_tile(p, s, t) : count_tile(p, s, t);
-  const int rank = t.rank, rs = (rank + 15) / 16;
-  if (found && !(rank == 0 && p.base == p.out)) {  // (the same for the whole cluster)
+  if (p.tiles)
+    read_tile(p, s, t);
+  else
+    count_tile(p, s, t);
+  const int rank = t.rank, rs = (rank + 15) / 16;  // (the same for the whole cluster)
+  if (rank == 0) {  // rows without an adapter, or of an empty slot: a warp a row, the cluster's warps in turn
+    if (p.base != p.out) {
+      const bool listed = t.start >= 0;
+      const int rows = listed && blockIdx.x / p.cut.ctas < p.n_tiles[0] ? t.rows : s.spare;
+      const int step = (W + 1) * p.cut.ctas;
+      for (int i = warp * p.cut.ctas + cta; i < rows; i += step)
+        copy_row(p, listed ? p.order[t.start + i] : s.rows[i], threadIdx.x & 31);
+    }
+  } else {
     const int nk = (p.K + 63) / 64, per_k = (nk + p.cut.ctas - 1) / p.cut.ctas, k0 = min(cta * per_k, nk), kn = min(per_k, nk - k0);
     const int ns = (p.N + kSlice - 1) / kSlice, per_n = (ns + p.cut.ctas - 1) / p.cut.ctas;
     const int s0 = min(cta * per_n, ns), sn = min(per_n, ns - s0);
-    const uint8_t* wa = reinterpret_cast<const uint8_t*>(p.a_tc + (rank > 0 ? t.slot * p.a_tc_slot : 0)) +
+    const uint8_t* wa = reinterpret_cast<const uint8_t*>(p.a_tc + t.slot * p.a_tc_slot) +
                         static_cast<int64_t>(k0) * C::kWBytes;
-    const uint8_t* wb = reinterpret_cast<const uint8_t*>(p.b_tc + (rank > 0 ? t.slot * p.b_tc_slot : 0)) +
+    const uint8_t* wb = reinterpret_cast<const uint8_t*>(p.b_tc + t.slot * p.b_tc_slot) +
                         static_cast<int64_t>(s0) * C::kBTile;
-    if (rank > 0) {
-      if (warp == kMathWarps) {
-        // Few rows: the weights are most of what the tile reads, and come from memory: all of them are asked for now.
-        // (With many rows an adapter's weights are in L2 already, and the requests cost 2 us of 15.)
-        if (t.rows <= 32) {
-          for (int j = threadIdx.x & 31; j < kn; j += 32) prefetch_l2(wa + static_cast<int64_t>(j) * C::kWBytes, rs * 16 * 128);
-          for (int j = threadIdx.x & 31; j < sn; j += 32) prefetch_l2(wb + static_cast<int64_t>(j) * C::kBTile, C::kBTile);
-        }
-        __syncwarp();
-        if (elect_one() && kn > 0) {
-          issue_shrink<R, kFp16>(p, s, wa, rs, kn, tmem);
-          // the ring is free once the shrink's MMAs are done: B's first tiles, behind the partial sums' place
-          if (mbar_wait(s.d_full, 0, s.abort_flag, p.err))
-            for (int j = 0; j < sn && j < C::kBEarly; ++j) load_b<R>(p, s, wb, j);
-        }
-        __syncwarp();
-        if (kn == 0 && elect_one())
-          for (int j = 0; j < sn && j < C::kBEarly; ++j) load_b<R>(p, s, wb, j);
-        __syncwarp();
-      } else {
-        gather_x<R>(p, s, k0, kn);
-        const bool done = kn > 0 && mbar_wait_warp(s.d_full, 0, s.abort_flag, p.err);
-        tc_fence_after();
-        write_part<R>(s, tmem, done);
-        tc_fence_before();
+    if (warp == W) {
+      // Few rows: the weights are most of what the tile reads, and come from memory: all of them are asked for now.
+      // (With many rows an adapter's weights are in L2 already, and the requests cost 2 us of 15.)
+      if (t.rows <= 32) {
+        for (int j = threadIdx.x & 31; j < kn; j += 32) prefetch_l2(wa + static_cast<int64_t>(j) * C::kWBytes, rs * 16 * 128);
+        for (int j = threadIdx.x & 31; j < sn; j += 32) prefetch_l2(wb + static_cast<int64_t>(j) * C::kBTile, C::kBTile);
       }
-      cluster_barrier();
-      if (warp < kMathWarps) share_u<R, kFp16>(p, s, t.scale, rank, t.rows, cta);
-      fence_proxy_async_all();
-      cluster_barrier();  // u is whole, and no CTA's partial sums are read any more
+      __syncwarp();
+      if (elect_one() && kn > 0) {
+        issue_shrink<R, W, kFp16>(p, s, wa, rs, kn, tmem);
+        // the ring is free once the shrink's MMAs are done: B's first tiles, behind the partial sums' place
+        if (mbar_wait(s.d_full, 0, s.abort_flag, p.err))
+          for (int j = 0; j < sn && j < C::kBEarly; ++j) load_b<R, W>(p, s, wb, j);
+      }
+      __syncwarp();
+      if (kn == 0 && elect_one())
+        for (int j = 0; j < sn && j < C::kBEarly; ++j) load_b<R, W>(p, s, wb, j);
+      __syncwarp();
+    } else {
+      gather_x<R, W>(p, s, k0, kn);
+      const bool done = kn > 0 && mbar_wait_warp(s.d_full, 0, s.abort_flag, p.err);
       tc_fence_after();
-      fence_proxy_async_all();
+      write_part<R, W>(s, tmem, done);
+      tc_fence_before();
     }
-    if (warp == kMathWarps) {
-      if (rank > 0 && elect_one()) issue_expand<R, kFp16>(p, s, wb, rs, sn, tmem);
+    cluster_barrier();
+    if (warp < W) share_u<R, W, kFp16>(p, s, t.scale, rank, t.rows, cta);
+    fence_proxy_async_all();
+    cluster_barrier();  // u is whole, and no CTA's partial sums are read any more
+    tc_fence_after();
+    fence_proxy_async_all();
+    if (warp == W) {
+      if (elect_one()) issue_expand<R, W, kFp16>(p, s, wb, rs, sn, tmem);
       __syncwarp();
     } else if (p.out_type == MOE_BF16) {
-      write_out<Bf16, R, kFp16>(p, s, s0, sn, rank, tmem);
+      write_out<Bf16, R, W, kFp16>(p, s, s0, sn, tmem);
     } else if (p.out_type == MOE_FP16) {
-      write_out<Fp16, R, kFp16>(p, s, s0, sn, rank, tmem);
+      write_out<Fp16, R, W, kFp16>(p, s, s0, sn, tmem);
     } else {
-      write_out<Fp32, R, kFp16>(p, s, s0, sn, rank, tmem);
+      write_out<Fp32, R, W, kFp16>(p, s, s0, sn, tmem);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   abort_quiesce(s.abort_flag);
-  if (warp == kMathWarps) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == W) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 // ---- packing -------------------------------------------------------------------------------------------
@@ -619,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, R <= 64 ? 2 : 1) adapter_tc_kernel(c
 template <int R>
 __global__ void adapter_tc_pack_kernel(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
                                        int64_t na, int64_t nb) {
-  using C = Cfg<R>;
+  using C = Cfg<R, 16>;
   constexpr int W = C::kRowBytes / 2;  // elements of a row
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < na + nb;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -647,13 +698,22 @@ cudaError_t pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* p
   return cudaGetLastError();
 }
 
+template <int R, int W, bool kFp16>
+cudaError_t launch_warps(const AdapterArgs& p, cudaStream_t st) {
+  auto kern = adapter_tc_kernel<R, W, kFp16>;
+  using C = Cfg<R, W>;
+  cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::kBytes);
+  if (e != cudaSuccess) return e;
+  const int clusters = adapter_clusters(p.T, p.n, p.cut, p.base != p.out);
+  return launch_pdl_clusters(kern, dim3(clusters * p.cut.ctas), dim3(C::kThreads), p.cut.ctas, C::kBytes, st, p);
+}
+
 template <int R, bool kFp16>
 cudaError_t launch(const AdapterArgs& p, cudaStream_t st) {
-  auto kern = adapter_tc_kernel<R, kFp16>;
-  cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), Cfg<R>::kBytes);
-  if (e != cudaSuccess) return e;
-  const int clusters = (p.T + p.cut.rows - 1) / p.cut.rows + (p.n + 1 < p.T ? p.n + 1 : p.T);
-  return launch_pdl_clusters(kern, dim3(clusters * p.cut.ctas), dim3(kThreads), p.cut.ctas, Cfg<R>::kBytes, st, p);
+  if constexpr (R <= 64) {
+    if (p.cut.small) return launch_warps<R, 8, kFp16>(p, st);
+  }
+  return launch_warps<R, 16, kFp16>(p, st);
 }
 
 }  // namespace
@@ -668,20 +728,31 @@ cudaError_t launch_adapter_tc_pack(const uint16_t* a, const uint16_t* b, uint16_
   }
 }
 
-// The most CTAs, up to two an SM (one above rank 64: all that run at a time; a cluster more waits for the first to end, 96 us instead of 63 at
-// 8195 rows), from tiles of 128 or 64 rows and clusters of 8 to 1.  The slots' rows are unknown here: half a tile is
-// lost to each slot, and a slot that is used has one at least.
+// Up to 3500 rows two CTAs of 8 warps run on an SM, whose waits fill each other, above one of 16 with a deep ring (rank 64,
+// 4096 x 4096; 4096 rows: 39.4 and 36.7 us, 2051: 25.6 and 27.4, 20000: 116 and 96).  CTAs that share a tile: a power of
+// two that should leave all tiles running at once.  How many there will be is unknown here: a slot that has rows has a
+// tile at least, and loses part of one.  (8195 rows in 32 slots, one of 16 warps: 52 us with 2 CTAs a tile and 60 with 1
+// where 64 tiles come out, 67 and 60 where 80 do.)
 AdapterCut adapter_cut(int T, int n, int rpad, int num_sms) {
-  const int64_t fit = (rpad <= 64 ? 2 : 1) * num_sms;
   const int used = n < T ? n : T;
-  AdapterCut best{kRows, 1};
-  int64_t most = 0;
-  for (int rows = kRows; rows >= kAdapterTileMin; rows /= 2) {
-    const int64_t cut = static_cast<int64_t>(T) / rows + used / 2 + 1, tiles = cut > used ? cut : used;
-    for (int c = 8; c >= 1; --c)
-      if (tiles * c <= fit && tiles * c > most) most = tiles * c, best = AdapterCut{rows, c};
-  }
-  return best;
+  AdapterCut c;
+  c.small = rpad <= 64 && T <= 3500;
+  c.slots = c.small ? 2 * num_sms : num_sms;
+  const int about = c.small ? T / 64 + used / 2 + 1 : T / kRows + used / 4 + 1, tiles = about > used ? about : used;
+  c.ctas = 8;
+  while (c.ctas > 1 && tiles * c.ctas > c.slots) c.ctas /= 2;
+  // (steps with a grouping launch: it chooses the rows)
+  c.rows = static_cast<int64_t>(T / 64 + used / 2 + 1) * c.ctas <= c.slots ? 64 : kRows;
+  return c;
+}
+
+// Clusters of the grid: for all tiles that there may be, of the rows that the grouping may choose to fill whole waves (64 at
+// least), and a few more where there may be rows to be copied.  (A cluster with nothing to do costs its CTAs' start.)
+int adapter_clusters(int T, int n, const AdapterCut& cut, bool copies) {
+  const int64_t used = n < T ? n : T, most = (T + cut.rows - 1) / cut.rows + used;
+  const int64_t waves = (most * cut.ctas + cut.slots - 1) / cut.slots, whole = waves * cut.slots / cut.ctas;
+  const int64_t fine = (T + 63) / 64 + used, tiles = most > whole ? most : whole < fine ? whole : fine;
+  return static_cast<int>((most > tiles ? most : tiles) + (copies ? cut.slots / (8 * cut.ctas) + 1 : 0));
 }
 
 cudaError_t launch_adapters_tc(const AdapterArgs& p, int rpad, bool fp16, cudaStream_t st) {
