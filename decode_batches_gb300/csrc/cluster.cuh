@@ -15,6 +15,15 @@ MOE_DEVICE void cluster_barrier() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The barrier in halves.
+MOE_DEVICE void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+MOE_DEVICE void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // The shared memory of CTA `rank` at this CTA's address p.
 MOE_DEVICE uint32_t cluster_addr_u32(uint32_t addr, uint32_t rank) {
   uint32_t a;

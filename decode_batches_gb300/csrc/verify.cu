@@ -25,9 +25,10 @@ namespace moe {
 namespace {
 
 constexpr int kClusterMax = 8;  // CTAs of a request
-constexpr int kRing = 8;        // vector pairs a lane has in flight
 constexpr int kMarks = 4;       // partial sums of a range that are kept
 constexpr int kGroups = 4;      // vectors whose loads are in flight together in the search
+// vector pairs that a lane has in flight: with 8 warps (few requests) a range of 131072 / 64 values stays there whole
+constexpr int ring_of(int warps) { return warps == 8 ? 16 : 8; }
 
 struct VerifyArgs {
   const void* p = nullptr;
@@ -153,7 +154,6 @@ MOE_DEVICE void add_value(Pair v, Pair& hi, Pair& lo) {
 // hi + lo, |lo| <= half a step of hi: sums with some 47 bits at fp32's rate.
 struct alignas(8) Wide {
   float hi, lo;
-  MOE_DEVICE double f64() const { return static_cast<double>(hi) + static_cast<double>(lo); }
 };
 MOE_DEVICE Wide renormalised(float hi, float lo) {  // |hi| >= |lo|, or hi == 0
   const float s = hi + lo;
@@ -179,20 +179,18 @@ MOE_DEVICE Wide warp_sum(Wide v) {
   return v;
 }
 MOE_DEVICE Wide warp_scan(Wide v, int lane) {  // inclusive
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const Wide n{__shfl_up_sync(0xffffffffu, v.hi, o), __shfl_up_sync(0xffffffffu, v.lo, o)};
     if (lane >= o) v = n + v;
   }
   return v;
 }
-MOE_DEVICE double warp_scan(double v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double n = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += n;
-  }
-  return v;
+MOE_DEVICE Wide operator-(Wide a, Wide b) { return a + Wide{-b.hi, -b.lo}; }
+// p - q where p >= q, exactly
+MOE_DEVICE Wide rest(float p, float q) {
+  const float d = p - q, bb = p - d;
+  return Wide{d, (p - (d + bb)) + (bb - q)};
 }
 
 // A lane's sum of rests.
@@ -218,7 +216,7 @@ struct Rest {
 // The range's sum, the vectors v0 + lane, v0 + lane + 32, ... below v1 a lane.  The vectors come through a ring in shared
 // memory (cp.async; a lane reads back what it copied, so no barrier): with loads into registers the warps waited for
 // memory and for each other in turns, 20 GB/s a CTA.  marks[k][lane] is the lane's sum up to its vector (k + 1) * per_mark.
-template <typename E>
+template <typename E, int kRing>
 MOE_DEVICE Wide range_sum(const RowPair<E>& r, int v0, int v1, int lane, uint4* ring, Wide (*marks)[32], int per_mark) {
   const int n = (max(v1 - v0, 0) + 31) / 32;
   const auto ask = [&](int i) {
@@ -234,7 +232,7 @@ MOE_DEVICE Wide range_sum(const RowPair<E>& r, int v0, int v1, int lane, uint4* 
     }
     if (!r.q) at[32] = make_uint4(0u, 0u, 0u, 0u);
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kRing - 1; ++i) {
     if (i < n) ask(i);
     cp_async_commit();
@@ -256,7 +254,7 @@ MOE_DEVICE Wide range_sum(const RowPair<E>& r, int v0, int v1, int lane, uint4* 
 // The same for a range of whole vectors whose values are all in [0, 2) (plain probabilities) and that has no dropped
 // index: no vector and no value is checked, which leaves some 11 instructions an element (of 36).  Returns whether the
 // values were that, seen from the bits of all of them: a sign, or the exponents of 2 and more, NaN and infinity.
-template <typename E, bool kQ>
+template <typename E, bool kQ, int kRing>
 MOE_DEVICE bool range_sum_plain(const RowPair<E>& r, int v0, int n, int lane, uint4* ring, Wide (*marks)[32], int per_mark,
                                 Wide& result) {
   constexpr int m = RowPair<E>::kVec;
@@ -271,7 +269,7 @@ MOE_DEVICE bool range_sum_plain(const RowPair<E>& r, int v0, int n, int lane, ui
     if (kQ) q += 32 * m;
     fill = (fill + 1024) & (1024 * kRing - 1);
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kRing - 1; ++i) {
     if (i < n) ask();
     cp_async_commit();
@@ -307,24 +305,6 @@ MOE_DEVICE bool range_sum_plain(const RowPair<E>& r, int v0, int n, int lane, ui
   return !__any_sync(0xffffffffu, bits >> 30);
 }
 
-// The vectors [v0, v1) narrowed to the marked part whose cumulative sum exceeds `at` first (lowered by what lies before).
-template <typename E>
-MOE_DEVICE void narrow(const RowPair<E>&, int& v0, int& v1, double& at, const Wide (*marks)[32], int per_mark, int lane) {
-  const int n = (v1 - v0 + 31) / 32, full = min(n / per_mark, kMarks);  // marks that were written
-  double before = 0.0;
-  int k = 0;
-  for (; k < full; ++k) {  // (the part behind the last mark is what is left)
-    const double upto = warp_sum(marks[k][lane]).f64();
-    if (upto > at) break;
-    before = upto;
-  }
-  const int first = v0 + 32 * per_mark * k;
-  if (first >= v1) return;  // rounding left none: the whole range is searched for its last
-  v1 = k < full ? min(first + 32 * per_mark, v1) : v1;
-  v0 = first;
-  at -= before;
-}
-
 // The sum of the vectors [v0, v1), one lane's.
 template <typename E>
 MOE_DEVICE Wide lane_sum(const RowPair<E>& r, int v0, int v1) {
@@ -339,58 +319,91 @@ MOE_DEVICE Wide lane_sum(const RowPair<E>& r, int v0, int v1) {
   return sum.sum();
 }
 
-// The lowest index of the vectors [v0, v1) whose cumulative sum exceeds `at`; the last with a value above 0 where
-// rounding leaves none.  Longer ranges are narrowed to a lane's contiguous 32nd first.
+// The lowest index of the range [v0, v1) whose cumulative sum exceeds `at`; the last with a value above 0 where rounding
+// leaves none.  ring: the range's vectors, group i of 32 at 64 i, or nullptr.
 template <typename E>
-__device__ __noinline__ int range_find(const RowPair<E>& r, int v0, int v1, int lane, double at) {
+MOE_DEVICE int range_find(const RowPair<E>& r, int v0, int v1, Wide at, const uint4* ring,
+                                       const Wide (*marks)[32], int per_mark) {
   constexpr int n = RowPair<E>::kVec;
-  if (v1 - v0 > 32) {
-    const int per = (v1 - v0 + 31) / 32, l0 = min(v0 + lane * per, v1), l1 = min(l0 + per, v1);
-    const double own = lane_sum(r, l0, l1).f64(), upto = warp_scan(own, lane);
-    const uint32_t some = __ballot_sync(0xffffffffu, own > 0.0);
-    const uint32_t over = __ballot_sync(0xffffffffu, own > 0.0 && upto > at);
-    if (!some) return -1;
-    const int l = over ? __ffs(over) - 1 : 31 - __clz(some);
-    const double before = __shfl_sync(0xffffffffu, upto - own, l);
-    at = over ? at - before : __longlong_as_double(0x7ff0000000000000ll);
-    v0 = __shfl_sync(0xffffffffu, l0, l), v1 = __shfl_sync(0xffffffffu, l1, l);
+  const int lane = threadIdx.x & 31, start = v0, whole_end = v1;
+  // the marked part that it lies in
+  const int written = min((v1 - v0 + 31) / 32 / per_mark, kMarks);
+  Wide before{0.0f, 0.0f};
+  int k = 0;
+#pragma unroll 1
+  for (; k < written; ++k) {
+    const Wide part = warp_sum(marks[k][lane]);
+    if (part > at) break;
+    before = part;
   }
-  double before = 0.0;
-  int last = -1;
-  for (int v = v0; v < v1; v += 32) {
-    uint4 ra, rb;
-    float a[n], b[n];
-    r.get(v + lane, v1, ra, rb);
-    r.values(v + lane, ra, rb, a, b);
-    double own = 0.0;
-    int mine = -1;
-#pragma unroll
-    for (int i = 0; i < n; ++i)
-      if (a[i] > b[i]) own += static_cast<double>(a[i]) - static_cast<double>(b[i]), mine = i;
-    const double upto = before + warp_scan(own, lane);
-    const uint32_t over = __ballot_sync(0xffffffffu, mine >= 0 && upto > at);
+  if (v0 + 32 * per_mark * k < v1) {
+    v0 += 32 * per_mark * k;
+    if (k < written) v1 = min(v0 + 32 * per_mark, v1);
+    at = at - before;
+  }
+  // a long part: a lane's contiguous 32nd of it
+  if (v1 - v0 > 32 * 16) {
+    const int per = (v1 - v0 + 31) / 32, l0 = min(v0 + lane * per, v1), l1 = min(l0 + per, v1);
+    const Wide own = lane_sum(r, l0, l1), upto = warp_scan(own, lane);
+    const uint32_t over = __ballot_sync(0xffffffffu, own.hi > 0.0f && upto > at);
     if (over) {
       const int l = __ffs(over) - 1;
-      double c = upto - own;
-      int found = mine;
-      bool open = true;
+      at = at - shfl(upto - own, l);
+      v0 = __shfl_sync(0xffffffffu, l0, l), v1 = __shfl_sync(0xffffffffu, l1, l);
+      ring = nullptr;
+    }
+  }
+#pragma unroll 1
+  for (int v = v0; v < v1; v += 32) {
+    uint4 ra, rb;
+    if (ring)
+      ra = ring[(v - start) * 2 + lane], rb = r.q ? ring[(v - start) * 2 + 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
+    else
+      r.get(v + lane, v1, ra, rb);
+    float a[n], b[n];
+    r.values(v + lane, ra, rb, a, b);
+    Wide own{0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < n; ++i) own = own + rest(a[i], b[i]);
+    const Wide upto = warp_scan(own, lane);
+    const uint32_t over = __ballot_sync(0xffffffffu, own.hi > 0.0f && upto > at);
+    if (over) {
+      Wide c = upto - own;
+      int found = -1, last = 0;
 #pragma unroll
       for (int i = 0; i < n; ++i) {
-        if (a[i] > b[i]) c += static_cast<double>(a[i]) - static_cast<double>(b[i]);
-        if (open && a[i] > b[i] && c > at) found = i, open = false;
+        c = c + rest(a[i], b[i]);
+        if (a[i] > b[i]) {
+          last = i;
+          if (found < 0 && c > at) found = i;
+        }
       }
-      return __shfl_sync(0xffffffffu, (v + lane) * n - r.skip + found, l);
+      return __shfl_sync(0xffffffffu, (v + lane) * n - r.skip + (found < 0 ? last : found), __ffs(over) - 1);
     }
-    const uint32_t some = __ballot_sync(0xffffffffu, mine >= 0);
-    if (some) last = __shfl_sync(0xffffffffu, (v + lane) * n - r.skip + mine, 31 - __clz(some));
-    before = __shfl_sync(0xffffffffu, upto, 31);
+    at = at - shfl(upto, 31);
   }
-  return last;
+  // none by rounding: the last value above 0 of the part, else of the range
+  for (int again = 0;; ++again) {
+    int last = -1;
+    for (int v = v0; v < v1; v += 32) {
+      uint4 ra, rb;
+      float a[n], b[n];
+      r.get(v + lane, v1, ra, rb);
+      r.values(v + lane, ra, rb, a, b);
+#pragma unroll
+      for (int i = 0; i < n; ++i)
+        if (a[i] > b[i]) last = (v + lane) * n - r.skip + i;
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (last >= 0 || again) return last;
+    v0 = start, v1 = whole_end;
+  }
 }
 
 template <typename E, int W>
-__global__ void __launch_bounds__(W * 32, 24 / W > 0 ? 24 / W : 1) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(W * 32, W == 8 ? 1 : 6) verify_kernel(const VerifyArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
+  constexpr int kRing = ring_of(W);
   uint4* ring = reinterpret_cast<uint4*>(smem_raw) + (threadIdx.x >> 5) * (kRing * 64);
   Wide (*marks)[32] = reinterpret_cast<Wide (*)[32]>(smem_raw + W * kRing * 64 * 16) + (threadIdx.x >> 5) * kMarks;
   __shared__ int s_refused;
@@ -446,9 +459,9 @@ __global__ void __launch_bounds__(W * 32, 24 / W > 0 ? 24 / W : 1) verify_kernel
     const int e0 = v0 * RowPair<E>::kVec - r.skip, e1 = v1 * RowPair<E>::kVec - r.skip;  // elements [e0, e1)
     bool done = false;
     if (r.together && e0 >= 0 && e1 <= a.V && (v1 - v0) % 32 == 0 && !(r.drop >= e0 && r.drop < e1))
-      done = r.q ? range_sum_plain<E, true>(r, v0, (v1 - v0) / 32, lane, ring, marks, per_mark, mine)
-                 : range_sum_plain<E, false>(r, v0, (v1 - v0) / 32, lane, ring, marks, per_mark, mine);
-    if (!done) mine = range_sum(r, v0, v1, lane, ring, marks, per_mark);
+      done = r.q ? range_sum_plain<E, true, kRing>(r, v0, (v1 - v0) / 32, lane, ring, marks, per_mark, mine)
+                 : range_sum_plain<E, false, kRing>(r, v0, (v1 - v0) / 32, lane, ring, marks, per_mark, mine);
+    if (!done) mine = range_sum<E, kRing>(r, v0, v1, lane, ring, marks, per_mark);
     mine = warp_sum(mine);
     if (lane == 0) s_sum[warp] = mine;
     cluster_barrier();
@@ -467,10 +480,10 @@ __global__ void __launch_bounds__(W * 32, 24 / W > 0 ? 24 / W : 1) verify_kernel
 #pragma unroll
       for (int i = 0; i < kPer; ++i) some |= c[i].hi > 0.0f ? 1u << i : 0u, own = own + c[i], c[i] = own;
     }
-    cluster_barrier();  // (the sums are read: the next round, or the exit, may follow)
+    cluster_arrive();  // the sums are read: the next round, or the exit, waits for all of that
     const Wide upto = warp_scan(own, lane), sum = shfl(upto, 31);
     if (sum.hi > 0.0f) {
-      const Wide at = us > 0.0f ? us * sum : Wide{0.0f, 0.0f}, before = upto + Wide{-own.hi, -own.lo};
+      const Wide at = us > 0.0f ? us * sum : Wide{0.0f, 0.0f}, before = upto - own;
       // the first range that reaches past `at`, else the last that holds anything
       uint32_t over = 0;
 #pragma unroll
@@ -485,16 +498,15 @@ __global__ void __launch_bounds__(W * 32, 24 / W > 0 ? 24 / W : 1) verify_kernel
 #pragma unroll
         for (int i = 0; i + 1 < kPer; ++i)
           if (i < in) skipped = c[i];
-        double left = at.f64() - shfl(before + skipped, l).f64();
-        int w0 = v0, w1 = v1;
+        const Wide left = at - shfl(before + skipped, l);
         __syncwarp();
-        narrow(r, w0, w1, left, marks, per_mark, lane);
-        int tok = range_find(r, w0, w1, lane, left);
-        if (tok < 0) tok = range_find(r, v0, v1, lane, __longlong_as_double(0x7ff0000000000000ll));  // (by rounding)
+        const int tok = range_find(r, v0, v1, left, (v1 - v0 + 31) / 32 <= kRing ? ring : nullptr, marks, per_mark);
         if (lane == 0) a.tokens[row] = tok;
       }
+      cluster_wait();
       return;
     }
+    cluster_wait();
     if (!refused || round) break;
     r.open(prow, nullptr, a.V, -1);  // nothing is left of p - q: from p itself
   }
@@ -503,7 +515,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W > 0 ? 24 / W : 1) verify_kernel
 
 template <typename E, int W>
 cudaError_t launch_warps(VerifyArgs a, int B, int ctas, cudaStream_t st) {
-  constexpr int smem = W * (kRing * 64 * 16 + kMarks * 32 * sizeof(Wide));
+  constexpr int smem = W * (ring_of(W) * 64 * 16 + kMarks * 32 * sizeof(Wide));
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(verify_kernel<E, W>), smem);
   if (e != cudaSuccess) return e;
   a.ctas = ctas;
@@ -512,10 +524,10 @@ cudaError_t launch_warps(VerifyArgs a, int B, int ctas, cudaStream_t st) {
 
 template <typename E>
 cudaError_t launch(const VerifyArgs& a, int B, int num_sms, cudaStream_t st) {
-  // Few requests: the most threads a request, two CTAs of 8 warps an SM (five requests of 32003: 8.3 us, 9.9 with 4).  Many:
+  // Few requests: the most threads a request, a CTA of 8 warps an SM.  Many:
   // CTAs of 4 warps, whose acceptance, reading and search overlap better (192 requests of 131072: 42 us, 51 with 8), as
   // long as a warp's range has eight groups of 32 vectors (192 requests of 32003: 4 CTAs 18.8 us, 8 22.1).
-  if (B * kClusterMax <= 2 * num_sms) return launch_warps<E, 8>(a, B, kClusterMax, st);
+  if (B * kClusterMax <= num_sms) return launch_warps<E, 8>(a, B, kClusterMax, st);
   const int groups = a.V / (32 * RowPair<E>::kVec);
   int ctas = kClusterMax;
   while (ctas > 1 && groups < 8 * 4 * ctas) ctas /= 2;
