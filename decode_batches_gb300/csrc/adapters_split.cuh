@@ -5,6 +5,11 @@
 
 namespace moe {
 
+// Asks L2 for `bytes` from p (16-byte aligned, a multiple of 16).
+MOE_DEVICE void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // counts[key] += 1 for every lane with a key >= 0, and what was there before this lane's: a run of one key (a prompt's
 // rows) with one addition, else a lane's each, whose few collisions take less time than to find them (10 us of 22 at
 // 30000 rows).

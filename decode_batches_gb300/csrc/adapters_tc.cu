@@ -1,15 +1,18 @@
 // Low-rank adapters of larger steps on the tensor cores (adapters.cu has the formulas and the small steps' kernel).
 //
 // A tile is up to 128 rows of one adapter, a cluster of C CTAs computes it:
-//   shrink  D[128][R] = x A^T over this CTA's range of K: tcgen05 MMAs of 128 x R x 16, rows of x gathered with cp.async
-//           into the 128-byte-swizzled operand, A in tiles packed that way (bulk copies), a ring of 64-column stages;
-//   u       the CTAs' partial sums meet in distributed shared memory: each CTA adds up 128 / C rows, scales and splits
-//           them into two 16-bit terms (adapter_split) and writes those into every CTA's MMA operand;
-//   expand  128 features at a time, over this CTA's range of N: D[128][128] = (hi + lo) B^T, two MMAs a 16 ranks, D double
-//           buffered in TMEM; eight warps add the base and write.
-// Bound by memory: x, base and out pass once; the weights are read once a tile, from L2.  What the warp-level kernel's
-// fragments cost (24 M instructions for 8195 rows of 4096 x 4096, rank 64: 75 us) falls away: operands go from shared
-// memory to the tensor core without registers.
+//   shrink  D[rows][R] = x A^T over this CTA's range of K: tcgen05 MMAs of 128 (or 64) x R x 16, rows of x gathered with
+//           cp.async into the 128-byte-swizzled operand, A in tiles packed that way (bulk copies), a ring of 64-column
+//           stages;
+//   u       the CTAs' partial sums meet in distributed shared memory: each CTA adds up its share of the rows, scales and
+//           splits them into two 16-bit terms (adapter_split) and writes those into every CTA's MMA operand;
+//   expand  128 features at a time, over this CTA's range of N: D[rows][128] = (hi + lo) B^T, two MMAs a 16 ranks, D
+//           double buffered in TMEM; W warps add the base and write.
+// Bound by memory: x, base and out pass once; the weights are read once a tile, from L2, whose way to an SM is as tight
+// (64 bytes a ns and SM in either phase): so tiles are as large as still leave every SM one.  8195 rows of 4096 x 4096 in
+// 32 adapters of rank 64: 52 us, of which 12 the gather (83 MB), 23 the expand (150 MB), 6 u's way through the cluster, 9
+// the grouping's launch and the two starts; the floor is 33.  Warp-level fragments in the small steps' manner took 85 us
+// and 24 M instructions there (14 M here).
 //
 // The rows of a B tile are permuted within 32 features such that the 16x256b TMEM load hands a lane eight neighbouring
 // features of a row: base and out move as 16-byte vectors, 64 contiguous bytes a row, without a transposition.
@@ -21,7 +24,7 @@
 namespace moe {
 namespace {
 
-constexpr int kRows = 128;             // rows of a tile (the MMA's M)
+constexpr int kRows = 128;             // rows of a tile at most (the MMA's M; 64 where all tiles have that many at most)
 constexpr int kSlice = 128;            // features of an expand step
 constexpr int kStagesMax = 8;
 
@@ -31,7 +34,6 @@ template <int R, int W>
 struct Cfg {
   static constexpr int kThreads = 32 * (W + 1);      // W warps gather, add up and write, one lane issues
   static constexpr int kCtas = W == 8 ? 2 : 1;       // an SM
-
   static constexpr int kWBytes = R * 128;
   static constexpr int kTerm = kRows * R * 2;        // u's hi or lo
   static constexpr int kPart = kRows * R * 4;        // partial sums
@@ -39,20 +41,18 @@ struct Cfg {
   static constexpr int kRing = W == 8 ? 72 * 1024 : R <= 64 ? 160 * 1024 : 128 * 1024;
   static constexpr int kBEarly = (kRing - kPart) / kBTile < 4 ? (kRing - kPart) / kBTile : 4;
   static constexpr int kBSlots = kBEarly + kPart / kBTile;
-  static_assert(W == 16 || R <= 64, "");
+  static_assert(W == 16 || (W == 8 && R <= 64), "");
   static constexpr int kRowBytes = (R < 64 ? R : 64) * 2;  // a row of u or of a B tile within a block of 64 ranks
   static constexpr int kTail = kRows * 8 + 320;
   static constexpr int kBytes = kRing + 2 * kTerm + kTail + 1024;
   static constexpr int kTmemCols = 256;              // two buffers of 128; the shrink's R are the first's
   static constexpr int b_at(int slot) { return slot < kBEarly ? kPart + slot * kBTile : (slot - kBEarly) * kBTile; }
   static_assert(kBEarly >= 2 && kBSlots <= 6, "");
-  // Stages for tiles of `rows` rows (64 or 128).  With 64 the MMA's other 64 rows are whatever follows, so that the last
-  // stage's 16 KB have to end within the memory: 6 stages of 16 KB instead of 4 of 24 at rank 64, the same bytes of x in
-  // flight as with whole tiles and half as many again as with half-empty stages.
+  // Stages for tiles of `rows` rows (64 or 128): 6 of 16 KB or 4 of 24 at rank 64 with two CTAs an SM.
   static constexpr int stage_bytes(int rows) { return rows * 128 + kWBytes; }
   static constexpr int stages(int rows) {
-    const int n = (kRing + 2 * kTerm - kRows * 128) / stage_bytes(rows) + 1, m = (kRing + 2 * kTerm) / stage_bytes(rows);
-    return n < m ? (n < kStagesMax ? n : kStagesMax) : (m < kStagesMax ? m : kStagesMax);
+    const int n = (kRing + 2 * kTerm) / stage_bytes(rows);
+    return n < kStagesMax ? n : kStagesMax;
   }
 };
 
@@ -201,11 +201,6 @@ MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R, W>& s, const ui
   }
 }
 
-// Asks L2 for `bytes` from p (16-byte aligned, a multiple of 16).
-MOE_DEVICE void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 // ---- the other warps ---------------------------------------------------------------------------------------
 // Arrives on the mbarrier (one of its expected arrivals) once this thread's copies so far have landed.
 MOE_DEVICE void cp_async_mbar_arrive(uint64_t* bar) {
@@ -251,7 +246,8 @@ MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R, W>& s, int k0, int 
   }
 }
 
-// This CTA's partial sums from TMEM into shared memory (16-byte units swizzled by the row).
+// This CTA's partial sums from TMEM into shared memory (16-byte units swizzled by the row).  D's rows lie a quarter in each
+// warp's 32 TMEM lanes: 32, or the first 16 of them where M is 64.
 template <int R>
 MOE_DEVICE uint32_t part_at(int row, int unit) {
   constexpr int kMask = R / 4 < 8 ? R / 4 - 1 : 7;

@@ -524,9 +524,9 @@ cudaError_t launch_warps(VerifyArgs a, int B, int ctas, cudaStream_t st) {
 
 template <typename E>
 cudaError_t launch(const VerifyArgs& a, int B, int num_sms, cudaStream_t st) {
-  // Few requests: the most threads a request, a CTA of 8 warps an SM.  Many:
-  // CTAs of 4 warps, whose acceptance, reading and search overlap better (192 requests of 131072: 42 us, 51 with 8), as
-  // long as a warp's range has eight groups of 32 vectors (192 requests of 32003: 4 CTAs 18.8 us, 8 22.1).
+  // Few requests: the most threads a request, a CTA of 8 warps an SM (8 requests of 131072: 10.8 us, 12.8 with 4 warps).
+  // Many: CTAs of 4 warps, six an SM, whose acceptance, reading and search overlap (192 requests of 131072: 39 us, 95 with
+  // 8), as long as a warp's range has eight groups of 32 vectors (192 requests of 32003: 4 CTAs 16.7 us, 8 18.2).
   if (B * kClusterMax <= num_sms) return launch_warps<E, 8>(a, B, kClusterMax, st);
   const int groups = a.V / (32 * RowPair<E>::kVec);
   int ctas = kClusterMax;

@@ -507,7 +507,8 @@ moe_status moe_verify_drafts(const void* target, moe_dtype dtype, int64_t ldt, c
  *   out[t] = base[t] + B_a (s_a A_a x[t]),  a = ids[t];  out[t] = base[t] where ids[t] == -1 or slot a is empty.
  * A handle holds n slots of one shape: A_a [r_a][K], B_a [N][r_a], r_a <= r_max, s_a a number.
  *   moe_adapters_create     1 <= n <= 1024, 1 <= N, K <= 2^20, 1 <= r_max <= 128; dtype (bf16 or fp16) is that of A,
- *                           B and x.  Host only.  (Ranks are held padded to 16, 32, 64 or 128 of r_max.)
+ *                           B and x.  Host only.  (Slots are held padded to rank 16, 32, 64 or 128 of r_max, and twice:
+ *                           as small and as large steps read them.)
  *   moe_adapters_set        contiguous A and B (device) copied into slot `slot` of the handle's memory in the kernel's
  *                           layout; r = 0 empties the slot.  Synchronous (waits for the device); other slots' contents
  *                           are kept, so that adapters come and go while the handle serves.
@@ -519,7 +520,8 @@ moe_status moe_verify_drafts(const void* target, moe_dtype dtype, int64_t ldt, c
  *                           MOE_DEVERR_EXPERT_RANGE and counts as -1.
  *   moe_adapters_get_device_error   as moe_plan_get_device_error, for the handle's calls.
  * Both products accumulate in fp32; u = s_a A_a x is held as two terms of the 16-bit type (relative error 2^-16 of
- * u in bf16, 2^-22 of a row's largest u in fp16); base is added in fp32 and the sum rounded once.
+ * u in bf16, 2^-22 of a row's largest u in fp16); base is added in fp32 and the sum rounded once.  A row's result does
+ * not depend on its place or on the other rows; steps of another T may split the sums otherwise.  T_max <= 2^26.
  * The forward call only enqueues work; a NULL or not-ready handle, T < 0 or T > T_max, a pitch below the width or an
  * unknown type is an error before any launch.
  */
