@@ -263,7 +263,7 @@ def _row_args(t: torch.Tensor, name: str, dtypes, rows: Optional[int], width: in
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
     shape = t.shape
-    if len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows):
+    if len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows) or shape[0] > 0x7fffffff:
         raise ValueError(f"{name} must have shape ({'rows' if rows is None else rows}, {width}), got {tuple(shape)}")
     pitch, step = t.stride()
     if step != 1 and shape[0] and width > 1:
@@ -278,8 +278,8 @@ def _assignments(inv: torch.Tensor, weights: Optional[torch.Tensor]):
     shape = inv.shape
     if len(shape) != 2:
         raise ValueError(f"inv must have shape (T, k), got {tuple(shape)}")
-    if inv.dtype != torch.int32:
-        raise ValueError(f"inv must be torch.int32, got {inv.dtype}")
+    if inv.dtype != torch.int32 or shape[0] > 0x7fffffff:
+        raise ValueError(f"inv must be torch.int32 with fewer than 2^31 rows, got {inv.dtype} {tuple(shape)}")
     return *shape, _ptr(inv), None if weights is None else _dev(weights, "weights", torch.float32, shape)
 
 
