@@ -278,9 +278,21 @@ def _assignments(inv: torch.Tensor, weights: Optional[torch.Tensor]):
     shape = inv.shape
     if len(shape) != 2:
         raise ValueError(f"inv must have shape (T, k), got {tuple(shape)}")
-    if inv.dtype != torch.int32 or shape[0] > 0x7fffffff:
+    T, k = shape
+    if inv.dtype is not torch.int32 or T > 0x7fffffff:
         raise ValueError(f"inv must be torch.int32 with fewer than 2^31 rows, got {inv.dtype} {tuple(shape)}")
-    return *shape, _ptr(inv), None if weights is None else _dev(weights, "weights", torch.float32, shape)
+    if weights is None:
+        return T, k, _ptr(inv), None
+    if weights.dtype is not torch.float32 or weights.shape != shape:
+        raise ValueError(f"weights must be torch.float32 of shape {tuple(shape)}, got {weights.dtype} {tuple(weights.shape)}")
+    return T, k, _ptr(inv), _ptr(weights)
+
+
+def _vector(t: torch.Tensor, name: str, dtype, n: int):
+    """The pointer of a dense vector of n elements whose device is known."""
+    if t.dtype is not dtype or t.shape != (n,):
+        raise ValueError(f"{name} must be {dtype} of shape ({n},), got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
 
 
 def _outside(out: torch.Tensor, *inputs):
@@ -316,9 +328,10 @@ def sort_rows(x: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Tensor
     px, ldx = _row_args(x, "x", DTYPES, T, d)
     if out is None:
         out = torch.empty((T * k, d), dtype=x.dtype, device=x.device)
+        po, ldo = out.data_ptr(), d
     else:
         _outside(out, x, inv, weights)
-    po, ldo = _row_args(out, "out", (x.dtype,), None, d)
+        po, ldo = _row_args(out, "out", (x.dtype,), None, d)
     _check(load_library().moe_sort_rows(px, DTYPES[x.dtype], ldx, T, k, d, pi, pw, po, ldo, out.shape[0], _stream()))
     return out
 
@@ -340,9 +353,10 @@ def sort_rows_backward(grad: torch.Tensor, inv: torch.Tensor, weights: Optional[
         dw = torch.empty((T, k), dtype=torch.float32, device=grad.device)
     if out is None:
         out = torch.empty((T, d), dtype=grad.dtype, device=grad.device)
+        po, ldo = out.data_ptr(), d
     else:
         _outside(out, grad, inv, weights, x)
-    po, ldo = _row_args(out, "out", (grad.dtype,), T, d)
+        po, ldo = _row_args(out, "out", (grad.dtype,), T, d)
     _check(load_library().moe_sort_rows_backward(pg, DTYPES[grad.dtype], ldg, grad.shape[0], T, k, d, pi, pw, px, ldx or 0,
                                                  po, ldo, _ptr(dw), _stream()))
     return out if dw is None else (out, dw)
@@ -364,12 +378,15 @@ def combine_rows(y: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Ten
         ps, lds = _row_args(shared, "shared", DTYPES, T, d)
         sdt = DTYPES[shared.dtype]
     if out is None:
+        if out_dtype is not None and out_dtype not in DTYPES:
+            raise ValueError(f"out must be bf16, fp16 or fp32, got {out_dtype}")
         out = torch.empty((T, d), dtype=out_dtype or y.dtype, device=y.device)
+        po, ldo = out.data_ptr(), d
     else:
         _outside(out, y, inv, weights, shared)
-    if out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
-    po, ldo = _row_args(out, "out", DTYPES, T, d)
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
+        po, ldo = _row_args(out, "out", DTYPES, T, d)
     _check(load_library().moe_combine_rows(py, DTYPES[y.dtype], ldy, y.shape[0], T, k, d, pi, pw, ps, sdt, lds, po,
                                            DTYPES[out.dtype], ldo, _stream()))
     return out
@@ -394,9 +411,10 @@ def combine_rows_backward(grad: torch.Tensor, inv: torch.Tensor, weights: Option
         dw = torch.empty((T, k), dtype=torch.float32, device=grad.device)
     if out is None:
         out = torch.empty((T * k if y is None else y.shape[0], d), dtype=(grad if y is None else y).dtype, device=grad.device)
+        po, ldo = out.data_ptr(), d
     else:
         _outside(out, grad, inv, weights, y)
-    po, ldo = _row_args(out, "out", DTYPES if y is None else (y.dtype,), None if y is None else y.shape[0], d)
+        po, ldo = _row_args(out, "out", DTYPES if y is None else (y.dtype,), None if y is None else y.shape[0], d)
     _check(load_library().moe_combine_rows_backward(pg, DTYPES[grad.dtype], ldg, T, k, d, pi, pw, py, ldy or 0, po,
                                                     DTYPES[out.dtype], ldo, out.shape[0], _ptr(dw), _stream()))
     return out if dw is None else (out, dw)
@@ -424,20 +442,19 @@ def verify_drafts(target: torch.Tensor, drafts: torch.Tensor, offsets: torch.Ten
     pd = ldd = None
     if draft_probs is not None:
         pd, ldd = _row_args(draft_probs, "draft_probs", (target.dtype,), R, V)
+    i32, f32, dev = torch.int32, torch.float32, target.device
     if tokens is None:
-        tokens = torch.empty((R,), dtype=torch.int32, device=target.device)
+        tokens = torch.empty((R,), dtype=i32, device=dev)
     else:
         _outside(tokens, target, drafts, offsets, u, u_sample, draft_probs)
     if accepted is None:
-        accepted = torch.empty((B,), dtype=torch.int32, device=target.device)
+        accepted = torch.empty((B,), dtype=i32, device=dev)
     else:
         _outside(accepted, target, drafts, offsets, u, u_sample, draft_probs, tokens)
-    i32 = torch.int32
     _check(load_library().moe_verify_drafts(
-        pt, DTYPES[target.dtype], ldt, pd, ldd or 0, R, V, _dev(drafts, "drafts", i32, (R,)),
-        _dev(offsets, "offsets", i32, (B + 1,)), B, _dev(u, "u", torch.float32, (R,)),
-        _dev(u_sample, "u_sample", torch.float32, (B,)), _dev(tokens, "tokens", i32, (R,)),
-        _dev(accepted, "accepted", i32, (B,)), _stream()))
+        pt, DTYPES[target.dtype], ldt, pd, ldd or 0, R, V, _vector(drafts, "drafts", i32, R),
+        _vector(offsets, "offsets", i32, B + 1), B, _vector(u, "u", f32, R), _vector(u_sample, "u_sample", f32, B),
+        _vector(tokens, "tokens", i32, R), _vector(accepted, "accepted", i32, B), _stream()))
     return tokens, accepted
 
 
@@ -576,13 +593,19 @@ class LowRankAdapters:
         _here(A, B)
         if A.dim() != 2:
             raise ValueError(f"A must be 2-D, got {tuple(A.shape)}")
+        self._slot(slot)
         r = A.shape[0]
         _check(self.lib.moe_adapters_set(self._h, slot, _dev(A, "A", self.dtype, (r, self.K)),
                                          _dev(B, "B", self.dtype, (self.N, r)), r, scale))
 
     def clear(self, slot: int):
         """Empty slot `slot`: rows that ask for it get the base alone."""
+        self._slot(slot)
         _check(self.lib.moe_adapters_set(self._h, slot, None, None, 0, 1.0))
+
+    def _slot(self, slot: int):
+        if not 0 <= slot < self.n:
+            raise ValueError(f"slot must be in [0, {self.n}), got {slot}")
 
     def workspace_bytes(self, T_max: int) -> int:
         return int(self.lib.moe_adapters_workspace_bytes(self._h, T_max))
@@ -634,7 +657,7 @@ class LowRankAdapters:
         else:
             po, ldo = _row_args(out, "out", DTYPES if out_dtype is None else (out_dtype,), T, self.N)
             _outside(out, x, ids, base if pb != po or ldb != ldo else None)
-        _check(self.lib.moe_adapters_forward(self._h, px, ldx, T, _dev(ids, "ids", torch.int32, (T,)), pb, ldb, po,
+        _check(self.lib.moe_adapters_forward(self._h, px, ldx, T, _vector(ids, "ids", torch.int32, T), pb, ldb, po,
                                              DTYPES[out.dtype], ldo, _stream()))
         return out
 

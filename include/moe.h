@@ -478,7 +478,7 @@ moe_status moe_combine_rows_backward(const void* grad, moe_dtype grad_dtype, int
  * Verification of drafted tokens.  Source: "DeepSeek V4.1F Q4 with native DSpark MTP on M3 Ultra", DSpark
  * paragraph (a block of 6 rows verifies drafted tokens); the acceptance rule has no counterpart on the pages.
  * B requests own consecutive rows of the step's R verify rows: request b the rows offsets[b] .. offsets[b+1] - 1
- * (int32 [B+1], device), one for each of its n = rows - 1 drafts and one behind the last.  Row r of target [R][V]
+ * (int32 [B+1], device; requests share no row), one for each of its n = rows - 1 drafts and one behind the last.  Row r of target [R][V]
  * holds the probabilities of the token that follows; drafts[r] (int32 [R]; not read in a request's last row) is the
  * token that row r verifies, and row r of draft_probs [R][V] the distribution q it was drawn from (not read in a
  * request's last row; NULL: the draft was certain, q = 1 at the drafted token and 0 elsewhere).  u fp32 [R] and

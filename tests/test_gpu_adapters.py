@@ -230,7 +230,8 @@ def test_no_rows_and_refusals():
                  lambda: ad.forward(x, ids, out_dtype=torch.float64), lambda: ad.forward(x, ids.cpu(), base),
                  lambda: ad.forward(x, ids, base[:1].expand(4, 64)), lambda: ad.forward(x, ids, base[:3], out=base[1:]),
                  lambda: ad.forward(big, torch.zeros(9, dtype=torch.int32, device="cuda")),
-                 lambda: ad.set(2, x[:, :32], base[:, :4].bfloat16()), lambda: ad.set(0, x, base.bfloat16()),
+                 lambda: ad.set(2, x[:, :32], base[:, :4].bfloat16()), lambda: ad.set(2**32, x[:2], x[:2].t().contiguous()),
+                 lambda: ad.clear(-1), lambda: ad.clear(2), lambda: ad.set(0, x, base.bfloat16()),
                  lambda: ad.set(0, x.half(), base[:, :4].half()), lambda: p.LowRankAdapters(2, 8, 8, 8, torch.float32),
                  lambda: p.LowRankAdapters(2, 8, 8, 200), lambda: p.LowRankAdapters(2, 8, 8, 8).forward(x[:, :8], ids)):
         with pytest.raises((ValueError, p.MoeError)):
@@ -246,3 +247,28 @@ def test_no_rows_and_refusals():
     assert torch.equal(ad.forward(x, ids, wide[:, :64], out=wide[:, 64:128]), ad.forward(x, ids, base))
     with pytest.raises(ValueError):
         ad.forward(x, ids, wide[:, :64], out=wide[:, 60:124])
+
+
+def test_two_handles_on_two_streams():
+    """Calls of two handles, and of verify_drafts, at the same time: nothing of a call is shared."""
+    a, b = make(4, 256, 512, 16, torch.bfloat16, 71)[0], make(7, 192, 384, 40, torch.float16, 72)[0]
+    xa, xb = tensor(700, 512, torch.bfloat16, 73), tensor(1100, 384, torch.float16, 74)
+    ia, ib = ids_of("mixed", 700, 4, 75).cuda(), ids_of("holes", 1100, 7, 76).cuda()
+    p = torch.softmax(tensor(96, 5000, torch.float32, 77), 1)
+    off = torch.arange(0, 97, 4, dtype=torch.int32, device="cuda")
+    d = torch.zeros(96, dtype=torch.int32, device="cuda")
+    u, us = torch.rand(96, device="cuda"), torch.rand(24, device="cuda")
+    calls = [lambda: a.forward(xa, ia), lambda: b.forward(xb, ib, out_dtype=torch.float32),
+             lambda: pkg().verify_drafts(p, d, off, u, us)[0]]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for _ in range(20):
+        for i, (c, st) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(st):
+                got[i].append(c())
+    torch.cuda.synchronize()
+    for w, results in zip(want, got):
+        assert all(torch.equal(w, r) for r in results)
+    assert a.device_error() == b.device_error() == 0

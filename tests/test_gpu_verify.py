@@ -186,6 +186,22 @@ def test_graph_replay_another_stream_and_repeats():
     assert got[0].tolist() == ref and got[1].tolist() == acc
 
 
+@pytest.mark.parametrize("dt", sorted(TYPES))
+@pytest.mark.parametrize("V,B", [(2000003, 2), (2000003, 60), (300000, 40)])
+def test_vocabularies_of_many_groups(V, B, dt):
+    """Ranges too long for the ring and for one part of the search; against 64-bit cumulative sums (whose own rounding is
+    1e-10 of a probability here)."""
+    g = torch.Generator(device="cuda").manual_seed(V + B)
+    p = torch.rand((B, V), device="cuda", generator=g).to(TYPES[dt])
+    p[0, : V // 2] = 0.0
+    us = torch.rand(B, device="cuda", generator=g)
+    off = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    tokens, accepted = pkg().verify_drafts(p, torch.zeros(B, dtype=torch.int32, device="cuda"), off, us, us)
+    c = p.double().cumsum(1)
+    want = torch.searchsorted(c, us.double()[:, None] * c[:, -1:], right=True)[:, 0]
+    assert torch.equal(tokens.long(), want) and not accepted.any()
+
+
 def test_refusals():
     p, q, d, off, u, us = inputs([3, 2], 40, torch.float32, 12)
     off = torch.tensor(off, dtype=torch.int32)
