@@ -7,8 +7,12 @@
 
 namespace moe {
 
+// Three blocks of aligned 16-bit rows an SM, two of all others, so that enough loads are under way.
+// Spreading with dots and weights, 8195 tokens of 4096, top 6: bf16 148 us with no bound, 133 with
+// three; fp16 rows of fp32 tokens 236 and 140.  4095 columns, not aligned: 517 us with one block, 300
+// with two, 396 with three.
 template <typename ET, typename ER, bool kVec, bool kDots>
-__global__ void __launch_bounds__(kRowWarps * 32) spread_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kRowWarps * 32, kVec && sizeof(ER) == 2 ? 3 : 2) spread_kernel(const RowsArgs a) {
   __shared__ float part[kDots ? kRowWarps : 1][kSlots];
   pdl_trigger();
   pdl_wait();
