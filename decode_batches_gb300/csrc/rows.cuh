@@ -7,6 +7,7 @@
 // each, so neither needs the forward permutation and nothing is read twice.
 #pragma once
 
+#include "abi_checks.h"
 #include "elems.cuh"
 
 namespace moe {
@@ -129,30 +130,40 @@ MOE_DEVICE void sum_dots(const RowsArgs& a, int64_t t, int j0, const int (&r)[kS
 
 // Grid and block: with dots, a block holds a token's whole row (its sums meet in shared memory);
 // without, a token's spans are spread over blocks of four warps, so that few tokens still fill SMs.
-inline void rows_grid(const RowsArgs& a, dim3* grid, dim3* block) {
+// A kernel whose blocks go on to further tokens (kBlocks of kRowWarps warps an SM, else 0) gets as many
+// as fit at once, above four times as many tokens; below, the last tokens would wait for whole turns
+// (517 tokens of 8 rows with dots: 4.6 us with a block a token, 5.0 in turns).
+inline void rows_grid(const RowsArgs& a, int blocks, dim3* grid, dim3* block) {
   const int spans = (a.d + kSpan - 1) / kSpan;
   const int per = a.dots ? kRowWarps : 4, warps = spans < per ? spans : per;
   *block = dim3(32 * warps);
   *grid = dim3(a.T, a.dots ? 1 : (spans + warps - 1) / warps);
+  if (blocks == 0) return;
+  const int64_t need = static_cast<int64_t>(warps) * grid->y, fit = static_cast<int64_t>(current_sms()) * blocks * kRowWarps;
+  const int64_t at_once = fit > need ? fit / need : 1;
+  if (a.T > 4 * at_once) grid->x = static_cast<unsigned>(at_once);
+}
+
+template <template <typename, typename, bool, bool> class K, typename ET, typename ER, bool kVec, bool kDots>
+cudaError_t launch_rows_as(const RowsArgs& a, cudaStream_t st) {
+  dim3 grid, block;
+  rows_grid(a, K<ET, ER, kVec, kDots>::kBlocks, &grid, &block);
+  return launch_pdl(K<ET, ER, kVec, kDots>::fn(), grid, block, 0, st, a);
 }
 
 template <template <typename, typename, bool, bool> class K, bool kVec, bool kDots>
 cudaError_t launch_rows_typed(const RowsArgs& a, moe_dtype tok, moe_dtype rows, cudaStream_t st) {
-  dim3 grid, block;
-  rows_grid(a, &grid, &block);
-  void (*fn)(RowsArgs) = nullptr;
   switch (tok * 3 + rows) {
-    case 0: fn = K<Bf16, Bf16, kVec, kDots>::fn(); break;
-    case 1: fn = K<Bf16, Fp16, kVec, kDots>::fn(); break;
-    case 2: fn = K<Bf16, Fp32, kVec, kDots>::fn(); break;
-    case 3: fn = K<Fp16, Bf16, kVec, kDots>::fn(); break;
-    case 4: fn = K<Fp16, Fp16, kVec, kDots>::fn(); break;
-    case 5: fn = K<Fp16, Fp32, kVec, kDots>::fn(); break;
-    case 6: fn = K<Fp32, Bf16, kVec, kDots>::fn(); break;
-    case 7: fn = K<Fp32, Fp16, kVec, kDots>::fn(); break;
-    default: fn = K<Fp32, Fp32, kVec, kDots>::fn(); break;
+    case 0: return launch_rows_as<K, Bf16, Bf16, kVec, kDots>(a, st);
+    case 1: return launch_rows_as<K, Bf16, Fp16, kVec, kDots>(a, st);
+    case 2: return launch_rows_as<K, Bf16, Fp32, kVec, kDots>(a, st);
+    case 3: return launch_rows_as<K, Fp16, Bf16, kVec, kDots>(a, st);
+    case 4: return launch_rows_as<K, Fp16, Fp16, kVec, kDots>(a, st);
+    case 5: return launch_rows_as<K, Fp16, Fp32, kVec, kDots>(a, st);
+    case 6: return launch_rows_as<K, Fp32, Bf16, kVec, kDots>(a, st);
+    case 7: return launch_rows_as<K, Fp32, Fp16, kVec, kDots>(a, st);
+    default: return launch_rows_as<K, Fp32, Fp32, kVec, kDots>(a, st);
   }
-  return launch_pdl(fn, grid, block, 0, st, a);
 }
 
 template <template <typename, typename, bool, bool> class K>

@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, kVec && sizeof(ER) == 2 ? 3 : 
 
 template <typename ET, typename ER, bool kVec, bool kDots>
 struct Spread {
+  static constexpr int kBlocks = 0;  // a block a token
   static void (*fn())(RowsArgs) { return spread_kernel<ET, ER, kVec, kDots>; }
 };
 
