@@ -27,8 +27,8 @@ namespace {
 constexpr int kClusterMax = 8;  // CTAs of a request
 constexpr int kMarks = 4;       // partial sums of a range that are kept
 constexpr int kGroups = 4;      // vectors whose loads are in flight together in the search
-// vector pairs that a lane has in flight: with 8 warps (few requests) a range of 131072 / 64 values stays there whole
-constexpr int ring_of(int warps) { return warps == 8 ? 16 : 8; }
+// vector pairs that a lane has in flight: with one CTA an SM (few requests) a range of 131072 / 64 values stays there whole
+constexpr int ring_of(int blocks) { return blocks == 1 ? 16 : 8; }
 
 struct VerifyArgs {
   const void* p = nullptr;
@@ -400,10 +400,10 @@ MOE_DEVICE int range_find(const RowPair<E>& r, int v0, int v1, Wide at, const ui
   }
 }
 
-template <typename E, int W>
-__global__ void __launch_bounds__(W * 32, W == 8 ? 1 : 6) verify_kernel(const VerifyArgs a) {
+template <typename E, int W, int kBlocks>
+__global__ void __launch_bounds__(W * 32, kBlocks) verify_kernel(const VerifyArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  constexpr int kRing = ring_of(W);
+  constexpr int kRing = ring_of(kBlocks);
   uint4* ring = reinterpret_cast<uint4*>(smem_raw) + (threadIdx.x >> 5) * (kRing * 64);
   Wide (*marks)[32] = reinterpret_cast<Wide (*)[32]>(smem_raw + W * kRing * 64 * 16) + (threadIdx.x >> 5) * kMarks;
   __shared__ int s_refused;
@@ -513,25 +513,29 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 1 : 6) verify_kernel(const Ve
   if (rank == 0 && threadIdx.x == 0) a.tokens[row] = -1;  // p holds nothing either
 }
 
-template <typename E, int W>
+template <typename E, int W, int kBlocks>
 cudaError_t launch_warps(VerifyArgs a, int B, int ctas, cudaStream_t st) {
-  constexpr int smem = W * (ring_of(W) * 64 * 16 + kMarks * 32 * sizeof(Wide));
-  cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(verify_kernel<E, W>), smem);
+  constexpr int smem = W * (ring_of(kBlocks) * 64 * 16 + kMarks * 32 * sizeof(Wide));
+  cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(verify_kernel<E, W, kBlocks>), smem);
   if (e != cudaSuccess) return e;
   a.ctas = ctas;
-  return launch_pdl_clusters(verify_kernel<E, W>, dim3(ctas, B), dim3(W * 32), ctas, smem, st, a);
+  return launch_pdl_clusters(verify_kernel<E, W, kBlocks>, dim3(ctas, B), dim3(W * 32), ctas, smem, st, a);
 }
 
 template <typename E>
 cudaError_t launch(const VerifyArgs& a, int B, int num_sms, cudaStream_t st) {
   // Few requests: the most threads a request, a CTA of 8 warps an SM (8 requests of 131072: 10.8 us, 12.8 with 4 warps).
-  // Many: CTAs of 4 warps, six an SM, whose acceptance, reading and search overlap (192 requests of 131072: 39 us, 95 with
-  // 8), as long as a warp's range has eight groups of 32 vectors (192 requests of 32003: 4 CTAs 16.7 us, 8 18.2).
-  if (B * kClusterMax <= num_sms) return launch_warps<E, 8>(a, B, kClusterMax, st);
+  // Up to three such CTAs an SM, where a warp's range has three groups of 32 vectors at least (48 requests of 131072:
+  // 17.0 us, with CTAs of 4 warps 19.6; of 32003: 9.1 and 12.1; of 16384, two groups: 7.6 and 7.3; 64 of 131072, which do
+  // not all run at once: 23.5 and 23.1).
+  // Many: CTAs of 4 warps, six an SM, whose acceptance, reading and search overlap (192 requests of 131072: 39 us, 46 with
+  // 8), as long as a warp's range has eight groups (192 requests of 32003: 4 CTAs 16.7 us, 8 18.2).
   const int groups = a.V / (32 * RowPair<E>::kVec);
+  if (B * kClusterMax <= num_sms) return launch_warps<E, 8, 1>(a, B, kClusterMax, st);
+  if (B * kClusterMax <= 3 * num_sms && groups >= 3 * 8 * kClusterMax) return launch_warps<E, 8, 3>(a, B, kClusterMax, st);
   int ctas = kClusterMax;
   while (ctas > 1 && groups < 8 * 4 * ctas) ctas /= 2;
-  return launch_warps<E, 4>(a, B, ctas, st);
+  return launch_warps<E, 4, 6>(a, B, ctas, st);
 }
 
 }  // namespace
