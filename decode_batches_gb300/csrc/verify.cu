@@ -529,12 +529,14 @@ cudaError_t launch(const VerifyArgs& a, int B, int num_sms, cudaStream_t st) {
   // 17.0 us, with CTAs of 4 warps 19.6; of 32003: 9.1 and 12.1; of 16384, two groups: 7.6 and 7.3; 64 of 131072, which do
   // not all run at once: 23.5 and 23.1).
   // Many: CTAs of 4 warps, six an SM, whose acceptance, reading and search overlap (192 requests of 131072: 39 us, 46 with
-  // 8), as long as a warp's range has eight groups (192 requests of 32003: 4 CTAs 16.7 us, 8 18.2).
+  // 8), as long as a warp's range has three groups where all CTAs run at once (100 requests of 32003: 8 CTAs 10.4 us, 4
+  // 13.5; six an SM do not always fit in clusters, so five and a half are counted: 114 of 16384, 4 CTAs 10.3, 2 9.6), eight
+  // where they do not (192 requests of 32003: 4 CTAs 16.7 us, 8 18.2).
   const int groups = a.V / (32 * RowPair<E>::kVec);
   if (B * kClusterMax <= num_sms) return launch_warps<E, 8, 1>(a, B, kClusterMax, st);
   if (B * kClusterMax <= 3 * num_sms && groups >= 3 * 8 * kClusterMax) return launch_warps<E, 8, 3>(a, B, kClusterMax, st);
   int ctas = kClusterMax;
-  while (ctas > 1 && groups < 8 * 4 * ctas) ctas /= 2;
+  while (ctas > 1 && groups < (B * ctas <= 11 * num_sms / 2 ? 3 : 8) * 4 * ctas) ctas /= 2;
   return launch_warps<E, 4, 6>(a, B, ctas, st);
 }
 

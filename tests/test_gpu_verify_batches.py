@@ -1,4 +1,4 @@
-"""Batches of 20 to 57 requests over long vocabularies, whose requests have fewer threads each than those of small calls:
+"""Batches of 20 to 110 requests, whose requests have fewer threads each than those of small calls:
 the same answers as in calls of a few requests, and the exact ones.  (A sum is off by some 2^-40 of itself at most, so two
 right kernels differ where u falls that near to a border: no number here does, or the exact form would show it.)"""
 import pytest
@@ -12,7 +12,8 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("B,V,dt,pad,shift", [(20, 24576, "fp32", 0, 0), (57, 24575, "fp32", 0, 1), (58, 24576, "fp32", 0, 0),
                                               (33, 32003, "fp32", 0, 0), (57, 49153, "bf16", 7, 0), (40, 65536, "fp16", 0, 0),
-                                              (24, 131072, "bf16", 0, 0)])
+                                              (24, 131072, "bf16", 0, 0), (100, 12289, "fp32", 0, 3), (110, 12288, "bf16", 0, 0),
+                                              (90, 6151, "fp16", 1, 0)])
 def test_batches_as_in_small_calls(B, V, dt, pad, shift):
     counts = [(3 * b) % 4 for b in range(B)]                        # (a request without rows among them)
     p, q, d, off, u, us = inputs(counts, V, TYPES[dt], B + V, sharp=2.0)
