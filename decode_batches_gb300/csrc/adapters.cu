@@ -211,6 +211,7 @@ MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const uint4* wb, int
           b[m][h].zero();
       }
     cp_async_wait<kStages - 1>();
+    __syncwarp();  // (the products are the whole warp's, and lanes without a row skipped the stores before them)
     const uint4* w = reinterpret_cast<const uint4*>(s.ring[slot][warp]) + lane;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -308,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
       if (k + kStages - 1 < k1) stage_shrink<M, R>(p, s.ring[fill][warp], x_row, wa, k + kStages - 1, nt, lane);
       cp_async_commit();
       cp_async_wait<kStages - 1>();
+      __syncwarp();
       const uint4* st = reinterpret_cast<const uint4*>(s.ring[from][warp]) + lane;
       uint4 x[MT][2];
 #pragma unroll

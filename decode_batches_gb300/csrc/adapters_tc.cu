@@ -259,16 +259,18 @@ MOE_DEVICE void write_part(const Smem<R, W>& s, uint32_t tmem, bool any) {
   for (int c = 16 * (warp >> 2); c < R; c += 4 * W) {
     uint32_t v[16];
     if (any) {
+      __syncwarp();  // (the load is the whole warp's, and lanes without a row skipped the stores before it)
       tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
       tmem_wait_ld();
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = 0u;
     }
-    if (lane >= per) continue;
+    if (lane < per) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4*>(s.ring + part_at<R>(row, c / 4 + i)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(s.ring + part_at<R>(row, c / 4 + i)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
   }
 }
 
@@ -372,6 +374,7 @@ MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R, W>& s, int s0, int
         const int m = u / kChunks, c = u % kChunks, place = (i * kUnits + u) % kAhead;
         if (some[m]) {
           uint32_t d[16];
+          __syncwarp();  // (the load is the whole warp's, and lanes without a row skipped the stores before it)
           tmem_ld_16x256b_x4(at + (static_cast<uint32_t>(16 * m) << 16) + 32 * c, d);
           tmem_wait_ld();
 #pragma unroll
