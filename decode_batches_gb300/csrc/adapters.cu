@@ -14,9 +14,9 @@
 // barriers, 4.8 us for one row (rank 16, 4096 x 4096) of which a launch is 2; 48 rows of 35 adapters of rank 64 16.5 us,
 // 2.2 TB/s of weights.
 //
-// u is split in two 16-bit terms, u = hi + lo (relative error 2^-16 or less of it in bf16, 2^-22 in fp16),
-// since one term's 2^-8 would dominate an fp32 result.  In fp16 a row's u is first brought to [1, 2) by a power
-// of two, so that neither term leaves the type's range.
+// u is split in 16-bit terms, three in bf16 (all of its 24 bits) and two in fp16 (2^-22 of a row's largest), since
+// one term's 2^-8 would dominate the result.  In fp16 a row's u is first brought to [1, 2) by a power of two, so
+// that neither term leaves the type's range.
 #include "adapters.cuh"
 #include "adapters_split.cuh"
 #include "cluster.cuh"
@@ -48,8 +48,9 @@ MOE_DEVICE void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32
 // Shared memory of a CTA.  Each warp has a ring of stages that its loads go through (cp.async): a stage holds a
 // chunk of 32 columns of x and of A, or a chunk of 32 features of B.  A lane reads back exactly what it copied, so
 // the ring needs no barrier.  The first stage of all warps also holds the shrink's partial sums.
-template <int M, int R>
+template <int M, int R, bool kFp16>
 struct Smem {
+  static constexpr int kTerms = kAdapterTerms<kFp16>;
   static constexpr int kStageBytes = (M + R) * 64;
   static constexpr int kStages = kStageBytes <= 3072 ? 4 : 2;  // (two CTAs fit an SM up to rank 64)
   static constexpr int kPitch = R + (R % 32 == 0 ? 16 : 0);  // 16-bit elements: rows 8 apart share no bank
@@ -61,7 +62,7 @@ struct Smem {
       float part[M][R];
     };
   };
-  alignas(16) uint16_t u[2][M][kPitch];  // hi, lo
+  alignas(16) uint16_t u[kTerms][M][kPitch];
   float row_scale[M];                    // (fp16) the power of two that a row's u was divided by
   int rows[M];                           // the tile's rows, -1 past the last
   alignas(16) int ids[kThreads];
@@ -74,8 +75,8 @@ struct Smem {
 // The tile of the cluster, found in ids by every CTA for itself (a step has 256 rows at most): a row whose number among
 // the rows of its id is a multiple of M leads a tile, and cluster i takes the i-th leader's, whose rows go to s.rows.
 // Returns whether there is one, with its slot (-1: no adapter) and rank.  The same for every thread of the cluster.
-template <int M, int R>
-MOE_DEVICE bool find_tile(const AdapterArgs& p, Smem<M, R>& s, int& slot, int& rank) {
+template <int M, int R, bool kFp16>
+MOE_DEVICE bool find_tile(const AdapterArgs& p, Smem<M, R, kFp16>& s, int& slot, int& rank) {
   const int idx = blockIdx.x / p.cut.ctas, t = threadIdx.x, lane = t & 31, warp = t >> 5;
   int id = -2;
   if (t < p.T) {
@@ -167,8 +168,9 @@ MOE_DEVICE void stage_expand(uint8_t* st, const uint4* wb, int c, int rs, int la
 // the stages from 1 on; u's fragments stay in registers where there
 // are few, the base's rows are requested before the products.
 template <typename E, int M, int R, bool kFp16>
-MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const uint4* wb, int c0, int c1, int rank, int lane, int warp) {
-  constexpr int MT = M / 16, RS = R / 16, kStages = Smem<M, R>::kStages;
+MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R, kFp16>& s, const uint4* wb, int c0, int c1, int rank, int lane, int warp) {
+  constexpr int MT = M / 16, RS = R / 16, kStages = Smem<M, R, kFp16>::kStages;
+  constexpr int kTerms = sizeof(E) == 4 ? kAdapterTerms<kFp16> : 2;  // (of a 16-bit result: below its own rounding)
   const int g = lane >> 2, q = lane & 3, rs = (rank + 15) / 16;
   const E* base[MT][2];
   E* out[MT][2];
@@ -185,13 +187,13 @@ MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const uint4* wb, int
       mul[m][h] = kFp16 && rank > 0 ? s.row_scale[16 * m + g + 8 * h] : 1.0f;
     }
   constexpr bool kHold = MT * RS <= 4;
-  uint2 u[kHold ? MT : 1][kHold ? RS : 1][2][2];  // [.][.][hi, lo][row g, row g + 8]
+  uint2 u[kHold ? MT : 1][kHold ? RS : 1][kTerms][2];  // [.][.][term][row g, row g + 8]
 #pragma unroll
   for (int m = 0; m < (kHold ? MT : 0); ++m)
 #pragma unroll
     for (int k = 0; k < RS; ++k)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < kTerms; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           u[m][k][t][h] = *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g + 8 * h][16 * k + 4 * q]);
@@ -224,7 +226,7 @@ MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const uint4* wb, int
           if (k < rs) {
             const uint4 w0 = w[2 * k * 32], w1 = w[(2 * k + 1) * 32];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < kTerms; ++t) {
               const uint2 a0 = kHold ? u[kHold ? m : 0][kHold ? k : 0][t][0]
                                      : *reinterpret_cast<const uint2*>(&s.u[t][16 * m + g][16 * k + 4 * q]);
               const uint2 a1 = kHold ? u[kHold ? m : 0][kHold ? k : 0][t][1]
@@ -266,8 +268,8 @@ MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R>& s, const uint4* wb, int
 template <int M, int R, bool kFp16>
 __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Smem<M, R>& s = *reinterpret_cast<Smem<M, R>*>(smem_raw);
-  constexpr int MT = M / 16, NT = R / 8, kStages = Smem<M, R>::kStages, kSlots = Smem<M, R>::kSlots;
+  Smem<M, R, kFp16>& s = *reinterpret_cast<Smem<M, R, kFp16>*>(smem_raw);
+  constexpr int MT = M / 16, NT = R / 8, kStages = Smem<M, R, kFp16>::kStages, kSlots = Smem<M, R, kFp16>::kSlots;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   pdl_trigger();
   pdl_wait();
@@ -390,11 +392,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_kernel(const AdapterArgs 
         }
       }
       const int r = i / R, c = i % R;
-      uint4 hi, lo;
-      const float mul = adapter_split<R, kFp16>(v, c, rank, scale, hi, lo);
+      uint4 term[kAdapterTerms<kFp16>];
+      const float mul = adapter_split<R, kFp16>(v, c, rank, scale, term);
       if (kFp16 && c == 0) s.row_scale[r] = mul;
-      *reinterpret_cast<uint4*>(&s.u[0][r][c]) = hi;
-      *reinterpret_cast<uint4*>(&s.u[1][r][c]) = lo;
+#pragma unroll
+      for (int t = 0; t < kAdapterTerms<kFp16>; ++t) *reinterpret_cast<uint4*>(&s.u[t][r][c]) = term[t];
     }
     cluster_barrier();  // u is written, and no CTA's partial sums are read any more
   }
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kGroupThreads) adapter_group_kernel(const int3
 template <int R, bool kFp16>
 cudaError_t launch(AdapterArgs p, int num_sms, cudaStream_t st) {
   auto kern = adapter_kernel<kTileRows, R, kFp16>;
-  const int smem = sizeof(Smem<kTileRows, R>);
+  const int smem = sizeof(Smem<kTileRows, R, kFp16>);
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int most = (p.n + 1 < p.T ? p.n + 1 : p.T) + p.T / kTileRows, tiles = most < p.T ? most : p.T;

@@ -33,12 +33,17 @@ MOE_DEVICE uint4 load_x(const uint16_t* row, int c, int K) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Ranks c .. c + 7 of a row's sums as two 16-bit terms of u = scale * v (0 behind the slot's rank, where an infinite x
+// 16-bit terms that hold u: in bf16 three, whose 24 bits are all that an fp32 sum has (with two, an fp32 result of 2048 x 4096
+// and rank 16 was 2.5e-6 off the formula where fp32 products are 1.5e-7 off); in fp16 two, 22 bits of the row's largest u.
+template <bool kFp16>
+constexpr int kAdapterTerms = kFp16 ? 2 : 3;
+
+// Ranks c .. c + 7 of a row's sums as the terms of u = scale * v (0 behind the slot's rank, where an infinite x
 // makes NaN of the padding); R / 8 neighbouring lanes hold a row.  Returns what the terms were divided by: 1 in bf16;
 // in fp16 the power of two that brings the row's largest u to [1, 2), so that neither term leaves the type's range
 // (1 for a row that is zero, infinite or NaN).
 template <int R, bool kFp16>
-MOE_DEVICE float adapter_split(float (&v)[8], int c, int rank, float scale, uint4& hi, uint4& lo) {
+MOE_DEVICE float adapter_split(float (&v)[8], int c, int rank, float scale, uint4 (&term)[kAdapterTerms<kFp16>]) {
   float mul = 1.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = c + e < rank ? v[e] * scale : 0.0f;
@@ -55,23 +60,24 @@ MOE_DEVICE float adapter_split(float (&v)[8], int c, int rank, float scale, uint
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= down;
   }
-  uint32_t h[4], l[4];
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    float h0, h1;
-    if (kFp16) {
-      h[e / 2] = pack_f16x2(v[e], v[e + 1]);
-      h0 = f16_bits_to_f32(h[e / 2] & 0xffffu), h1 = f16_bits_to_f32(h[e / 2] >> 16);
-    } else {
-      h[e / 2] = cvt_bf16x2(v[e], v[e + 1]);
-      h0 = bf16_bits_to_f32(h[e / 2] & 0xffffu), h1 = bf16_bits_to_f32(h[e / 2] >> 16);
+  for (int t = 0; t < kAdapterTerms<kFp16>; ++t) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      float h0, h1;
+      if (kFp16) {
+        w[e / 2] = pack_f16x2(v[e], v[e + 1]);
+        h0 = f16_bits_to_f32(w[e / 2] & 0xffffu), h1 = f16_bits_to_f32(w[e / 2] >> 16);
+      } else {
+        w[e / 2] = cvt_bf16x2(v[e], v[e + 1]);
+        h0 = bf16_bits_to_f32(w[e / 2] & 0xffffu), h1 = bf16_bits_to_f32(w[e / 2] >> 16);
+      }
+      // (an infinity has no rest)
+      v[e] = isfinite(h0) ? v[e] - h0 : 0.0f, v[e + 1] = isfinite(h1) ? v[e + 1] - h1 : 0.0f;
     }
-    // (an infinity has no rest)
-    const float l0 = isfinite(h0) ? v[e] - h0 : 0.0f, l1 = isfinite(h1) ? v[e + 1] - h1 : 0.0f;
-    l[e / 2] = kFp16 ? pack_f16x2(l0, l1) : cvt_bf16x2(l0, l1);
+    term[t] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
   return mul;
 }
 

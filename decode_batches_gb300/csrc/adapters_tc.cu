@@ -5,9 +5,9 @@
 //           cp.async into the 128-byte-swizzled operand, A in tiles packed that way (bulk copies), a ring of 64-column
 //           stages;
 //   u       the CTAs' partial sums meet in distributed shared memory: each CTA adds up its share of the rows, scales and
-//           splits them into two 16-bit terms (adapter_split) and writes those into every CTA's MMA operand;
-//   expand  128 features at a time, over this CTA's range of N: D[rows][128] = (hi + lo) B^T, two MMAs a 16 ranks, D
-//           double buffered in TMEM; W warps add the base and write.
+//           splits them into two or three 16-bit terms (adapter_split) and writes those into every CTA's MMA operand;
+//   expand  128 features at a time, over this CTA's range of N: D[rows][128] = (sum of the terms) B^T, an MMA a term and
+//           16 ranks, D double buffered in TMEM; W warps add the base and write.
 // Bound by memory: x, base and out pass once; the weights are read once a tile, from L2, whose way to an SM is as tight
 // (64 bytes a ns and SM in either phase): so tiles are as large as still leave every SM one.  8195 rows of 4096 x 4096 in
 // 32 adapters of rank 64: 52 us, of which 12 the gather (83 MB), 23 the expand (150 MB), 6 u's way through the cluster, 9
@@ -30,31 +30,41 @@ constexpr int kStagesMax = 8;
 
 // Shared memory: the ring, then u.  During the shrink its stages run on into u's place; after it the ring's start holds
 // the partial sums, B's first tiles come behind them and the later ones, once the sums are read, also in their place.
-template <int R, int W>
+template <int R, int W, bool kFp16>
 struct Cfg {
   static constexpr int kThreads = 32 * (W + 1);      // W warps gather, add up and write, one lane issues
   static constexpr int kCtas = W == 8 ? 2 : 1;       // an SM
   static constexpr int kWBytes = R * 128;
-  static constexpr int kTerm = kRows * R * 2;        // u's hi or lo
+  static constexpr int kTerm = kRows * R * 2;        // one of u's terms
+  static constexpr int kU = kAdapterTerms<kFp16> * kTerm;
   static constexpr int kPart = kRows * R * 4;        // partial sums
   static constexpr int kBTile = kSlice * R * 2;
-  static constexpr int kRing = W == 8 ? 72 * 1024 : R <= 64 ? 160 * 1024 : 128 * 1024;
+  // (a third term takes its place from the ring, which the stages run on out of: with more shared memory in all, less L1 was
+  // left for the base's lines, 8195 fp32 rows 84 us instead of 71)
+  static constexpr int kRing = (W == 8 ? 72 : R <= 64 ? 160 : 128) * 1024 - (kU - 2 * kTerm);
   static constexpr int kBEarly = (kRing - kPart) / kBTile < 4 ? (kRing - kPart) / kBTile : 4;
   static constexpr int kBSlots = kBEarly + kPart / kBTile;
   static_assert(W == 16 || (W == 8 && R <= 64), "");
   static constexpr int kRowBytes = (R < 64 ? R : 64) * 2;  // a row of u or of a B tile within a block of 64 ranks
   static constexpr int kTail = kRows * 8 + 320;
-  static constexpr int kBytes = kRing + 2 * kTerm + kTail + 1024;
+  static constexpr int kBytes = kRing + kU + kTail + 1024;
   static constexpr int kTmemCols = 256;              // two buffers of 128; the shrink's R are the first's
   static constexpr int b_at(int slot) { return slot < kBEarly ? kPart + slot * kBTile : (slot - kBEarly) * kBTile; }
-  static_assert(kBEarly >= 2 && kBSlots <= 6, "");
+  static_assert(kBEarly >= 1 && kBSlots <= 6 && kBytes <= 227 * 1024 && kCtas * (kBytes + 1024) <= 228 * 1024, "");
   // Stages for tiles of `rows` rows (64 or 128): 6 of 16 KB or 4 of 24 at rank 64 with two CTAs an SM.
   static constexpr int stage_bytes(int rows) { return rows * 128 + kWBytes; }
   static constexpr int stages(int rows) {
-    const int n = (kRing + 2 * kTerm) / stage_bytes(rows);
+    const int n = (kRing + kU) / stage_bytes(rows);
     return n < kStagesMax ? n : kStagesMax;
   }
 };
+
+// Terms of u that the expand takes: a 16-bit result gets two, whose 2^-17 of the adapter's part lie far below the rounding
+// of result and base, 2^-9 or 2^-12 (a third costs 1 us of 52 in the 8195 rows, and 1 of 19 in 200 rows of rank 64).
+template <bool kFp16>
+MOE_DEVICE int u_terms(const AdapterArgs& p) {
+  return p.out_type == MOE_FP32 ? kAdapterTerms<kFp16> : 2;
+}
 
 // Byte offset of 16-byte piece p of row r in a tile of kRowBytes-wide rows, swizzled over the row's own width.
 template <int kRowBytes>
@@ -92,7 +102,7 @@ MOE_DEVICE void st_cluster_f32(uint32_t addr, float v) {
 // Generic writes (also to another CTA's shared memory) before the tensor core's reads.
 MOE_DEVICE void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-template <int R, int W>
+template <int R, int W, bool kFp16>
 struct Smem {
   uint8_t* ring;
   uint8_t* u;
@@ -111,8 +121,8 @@ struct Smem {
   volatile int* abort_flag;
   MOE_DEVICE explicit Smem(uint8_t* raw) {
     uint8_t* p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    ring = p, p += Cfg<R, W>::kRing;
-    u = p, p += 2 * Cfg<R, W>::kTerm;
+    ring = p, p += Cfg<R, W, kFp16>::kRing;
+    u = p, p += Cfg<R, W, kFp16>::kU;
     rows = reinterpret_cast<int*>(p), p += kRows * 4;
     row_scale = reinterpret_cast<float*>(p), p += kRows * 4;
     full = reinterpret_cast<uint64_t*>(p);
@@ -134,8 +144,8 @@ struct Turn {
 };
 
 template <int R, int W, bool kFp16>
-MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R, W>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
-  using C = Cfg<R, W>;
+MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R, W, kFp16>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
+  using C = Cfg<R, W, kFp16>;
   const uint32_t wbytes = rs * 16 * 128, idesc = kFp16 ? idesc_f16_f32(s.tile_rows, 16 * rs) : idesc_bf16_f32(s.tile_rows, 16 * rs);
   const uint64_t pol = l2_policy_evict_last();
   const int xbytes = s.tile_rows * 128, stage = C::stage_bytes(s.tile_rows), stages = C::stages(s.tile_rows);
@@ -166,9 +176,9 @@ MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R, W>& s, const ui
   mma_commit(s.d_full);
 }
 
-template <int R, int W>
-MOE_DEVICE void load_b(const AdapterArgs& p, const Smem<R, W>& s, const uint8_t* w, int j) {
-  using C = Cfg<R, W>;
+template <int R, int W, bool kFp16>
+MOE_DEVICE void load_b(const AdapterArgs& p, const Smem<R, W, kFp16>& s, const uint8_t* w, int j) {
+  using C = Cfg<R, W, kFp16>;
   const int at = j % C::kBSlots;
   mbar_arrive_expect_tx(&s.b_full[at], C::kBTile);
   bulk_load(s.ring + C::b_at(at), w + static_cast<int64_t>(j) * C::kBTile, C::kBTile, &s.b_full[at],
@@ -176,17 +186,18 @@ MOE_DEVICE void load_b(const AdapterArgs& p, const Smem<R, W>& s, const uint8_t*
 }
 
 template <int R, int W, bool kFp16>
-MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R, W>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
-  using C = Cfg<R, W>;
+MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R, W, kFp16>& s, const uint8_t* w, int rs, int n, uint32_t tmem) {
+  using C = Cfg<R, W, kFp16>;
   const uint32_t idesc = kFp16 ? idesc_f16_f32(s.tile_rows, kSlice) : idesc_bf16_f32(s.tile_rows, kSlice);
   const uint32_t u0 = smem_u32(s.u), b0 = smem_u32(s.ring);
-  for (int j = C::kBEarly; j < n && j < C::kBSlots; ++j) load_b<R, W>(p, s, w, j);  // (the partial sums' place is free now)
+  const int terms = u_terms<kFp16>(p);
+  for (int j = C::kBEarly; j < n && j < C::kBSlots; ++j) load_b<R, W, kFp16>(p, s, w, j);  // (the partial sums' place is free now)
   for (int j = 0; j < n; ++j) {
     const int at = j % C::kBSlots, buf = j & 1;
     if (!mbar_wait(&s.b_full[at], (j / C::kBSlots) & 1, s.abort_flag, p.err)) return;
     if (!mbar_wait(&s.o_empty[buf], ((j >> 1) & 1) ^ 1, s.abort_flag, p.err)) return;
     tc_fence_after();
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < terms; ++t)
       for (int k = 0; k < rs; ++k) {  // 16 ranks: 32 bytes of a row, four to a block of 64 ranks
         const uint32_t in = (k / 4) * kRows * 128 + (k % 4) * 32;
         mma_f16_ss(tmem + buf * kSlice, operand_desc<C::kRowBytes>(u0 + t * C::kTerm + in),
@@ -196,7 +207,7 @@ MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R, W>& s, const ui
     mma_commit(&s.o_full[buf]);
     if (j >= 1 && j - 1 + C::kBSlots < n) {
       if (!mbar_wait(&s.b_empty[(j - 1) % C::kBSlots], ((j - 1) / C::kBSlots) & 1, s.abort_flag, p.err)) return;
-      load_b<R, W>(p, s, w, j - 1 + C::kBSlots);
+      load_b<R, W, kFp16>(p, s, w, j - 1 + C::kBSlots);
     }
   }
 }
@@ -210,9 +221,9 @@ MOE_DEVICE void cp_async_mbar_arrive(uint64_t* bar) {
 // x's rows into the stages: eight lanes a row's 128 bytes, 32 / W rows a lane.  The copies announce themselves; a proxy
 // fence here, before each announcement, waited for every copy in flight and made the stages take turns (0.8 us each),
 // so the issuing lane has it.
-template <int R, int W>
-MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R, W>& s, int k0, int n) {
-  using C = Cfg<R, W>;
+template <int R, int W, bool kFp16>
+MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R, W, kFp16>& s, int k0, int n) {
+  using C = Cfg<R, W, kFp16>;
   const int piece = threadIdx.x & 7;
   constexpr int kPer = kRows / (4 * W);
   const uint16_t* row[kPer];
@@ -253,8 +264,8 @@ MOE_DEVICE uint32_t part_at(int row, int unit) {
   constexpr int kMask = R / 4 < 8 ? R / 4 - 1 : 7;
   return (row * (R / 4) + (unit ^ (row & kMask))) * 16;
 }
-template <int R, int W>
-MOE_DEVICE void write_part(const Smem<R, W>& s, uint32_t tmem, bool any) {
+template <int R, int W, bool kFp16>
+MOE_DEVICE void write_part(const Smem<R, W, kFp16>& s, uint32_t tmem, bool any) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = s.tile_rows / 4, row = per * (warp & 3) + lane;
   for (int c = 16 * (warp >> 2); c < R; c += 4 * W) {
     uint32_t v[16];
@@ -276,10 +287,10 @@ MOE_DEVICE void write_part(const Smem<R, W>& s, uint32_t tmem, bool any) {
 
 // u of this CTA's share of the rows, into every CTA of the cluster.
 template <int R, int W, bool kFp16>
-MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R, W>& s, float scale, int rank, int rows, int cta) {
-  using C = Cfg<R, W>;
+MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R, W, kFp16>& s, float scale, int rank, int rows, int cta) {
+  using C = Cfg<R, W, kFp16>;
   // (whole warps take part, 256 / R rows each; those past the tile's last repeat it)
-  const int share = (rows + p.cut.ctas - 1) / p.cut.ctas;
+  const int share = (rows + p.cut.ctas - 1) / p.cut.ctas, terms = u_terms<kFp16>(p);
   for (int i = threadIdx.x * 8; (i & ~255) < share * R; i += 32 * W * 8) {
     const int r = min(min(i / R, share - 1) + cta * share, rows - 1), c = i % R;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -306,13 +317,14 @@ MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R, W>& s, float scale, 
         v[e] = v[e + 4], v[e + 4] = x;
       }
     }
-    uint4 hi, lo;
-    const float mul = adapter_split<R, kFp16>(v, c, rank, scale, hi, lo);
+    uint4 term[kAdapterTerms<kFp16>];
+    const float mul = adapter_split<R, kFp16>(v, c, rank, scale, term);
     const uint32_t at = smem_u32(s.u) + (c / 64) * kRows * 128 + swizzled<C::kRowBytes>(r, c % 64 / 8);
     for (int k = 0; k < p.cut.ctas; ++k) {
       const uint32_t to = cluster_addr_u32(at, k);
-      st_cluster_v4(to, hi.x, hi.y, hi.z, hi.w);
-      st_cluster_v4(to + C::kTerm, lo.x, lo.y, lo.z, lo.w);
+#pragma unroll
+      for (int e = 0; e < kAdapterTerms<kFp16>; ++e)
+        if (e < terms) st_cluster_v4(to + e * C::kTerm, term[e].x, term[e].y, term[e].z, term[e].w);
       if (kFp16 && c == 0) st_cluster_f32(cluster_addr(&s.row_scale[r], k), mul);
     }
   }
@@ -323,7 +335,7 @@ MOE_DEVICE void share_u(const AdapterArgs& p, const Smem<R, W>& s, float scale, 
 // rows: two) before it is used: with two of 16-bit rows, 32 KB an SM, the memory's latency held the writes at 4.5 TB/s.
 // kWhole: rows are 16-byte aligned and N is a multiple of 128: no column is checked.
 template <typename E, int R, int W, bool kFp16, bool kWhole>
-MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R, W>& s, int s0, int n, uint32_t tmem) {
+MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R, W, kFp16>& s, int s0, int n, uint32_t tmem) {
   constexpr int kCols = 512 / W, kChunks = kCols / 32, kUnits = 2 * kChunks;  // of a warp in a step
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int quarter = warp & 3, part = warp >> 2, per = s.tile_rows / 4;
@@ -418,7 +430,7 @@ MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R, W>& s, int s0, int
   }
 }
 template <typename E, int R, int W, bool kFp16>
-MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R, W>& s, int s0, int n, uint32_t tmem) {
+MOE_DEVICE void write_out(const AdapterArgs& p, const Smem<R, W, kFp16>& s, int s0, int n, uint32_t tmem) {
   if (p.out_vec && p.N % kSlice == 0)
     write_out<E, R, W, kFp16, true>(p, s, s0, n, tmem);
   else
@@ -450,8 +462,8 @@ MOE_DEVICE void copy_row(const AdapterArgs& p, int64_t row, int lane) {
 // What the cluster does: a tile (its rows in s.rows), or, behind the last tile, its share of the rows without an adapter
 // (rank 0, t.rows of them from p.order[t.start], or in s.rows).  Every thread of the CTA calls it.
 // From the grouping's list:
-template <int R, int W>
-MOE_DEVICE void read_tile(const AdapterArgs& p, Smem<R, W>& s, AdapterTile& t) {
+template <int R, int W, bool kFp16>
+MOE_DEVICE void read_tile(const AdapterArgs& p, Smem<R, W, kFp16>& s, AdapterTile& t) {
   const int idx = blockIdx.x / p.cut.ctas;
   t = p.tiles[idx];  // (the list has an entry for every cluster of the grid)
   const int n = p.n_tiles[0], rest = p.n_tiles[1];
@@ -470,8 +482,8 @@ MOE_DEVICE void read_tile(const AdapterArgs& p, Smem<R, W>& s, AdapterTile& t) {
 // From the ids, by every CTA for itself: counts of all slots (no adapter counts as slot n), their tiles' scan, the slot
 // that holds the cluster's tile, and that slot's rows in order.  Beside 64 x 64 products, 300 rows: 9.8 us, with the
 // grouping's launch 12.0; 2051 rows: 13.6 and 13.4; 4096: 17.7 and 18.6, but 19.9 and 19.8 with two slots.
-template <int R, int W>
-MOE_DEVICE void count_tile(const AdapterArgs& p, Smem<R, W>& s, AdapterTile& t) {
+template <int R, int W, bool kFp16>
+MOE_DEVICE void count_tile(const AdapterArgs& p, Smem<R, W, kFp16>& s, AdapterTile& t) {
   constexpr int kCounters = 32 * W;
   int* counts = reinterpret_cast<int*>(s.ring);     // [n + 1]
   int* warp_sum = counts + kAdaptersMax + 8;        // [W]
@@ -479,7 +491,7 @@ MOE_DEVICE void count_tile(const AdapterArgs& p, Smem<R, W>& s, AdapterTile& t) 
   const int idx = blockIdx.x / p.cut.ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, most = p.cut.rows;
   const bool counter = tid < kCounters;
   s.tile_rows = most <= 64 ? 64 : kRows;
-  for (int i = tid; i <= p.n; i += Cfg<R, W>::kThreads) counts[i] = 0;
+  for (int i = tid; i <= p.n; i += Cfg<R, W, kFp16>::kThreads) counts[i] = 0;
   if (tid == 0) pick[0] = p.n, pick[1] = 0;
   if (tid < kRows) s.rows[tid] = -1;
   __syncthreads();
@@ -568,10 +580,10 @@ MOE_DEVICE void count_tile(const AdapterArgs& p, Smem<R, W>& s, AdapterTile& t) 
 }
 
 template <int R, int W, bool kFp16>
-__global__ void __launch_bounds__(Cfg<R, W>::kThreads, Cfg<R, W>::kCtas) adapter_tc_kernel(const AdapterArgs p) {
-  using C = Cfg<R, W>;
+__global__ void __launch_bounds__(Cfg<R, W, kFp16>::kThreads, Cfg<R, W, kFp16>::kCtas) adapter_tc_kernel(const AdapterArgs p) {
+  using C = Cfg<R, W, kFp16>;
   extern __shared__ uint8_t smem_raw[];
-  Smem<R, W> s(smem_raw);
+  Smem<R, W, kFp16> s(smem_raw);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStagesMax; ++i) mbar_init(&s.full[i], 32 * W + 1), mbar_init(&s.empty[i], 1);
@@ -626,17 +638,17 @@ __global__ void __launch_bounds__(Cfg<R, W>::kThreads, Cfg<R, W>::kCtas) adapter
         issue_shrink<R, W, kFp16>(p, s, wa, rs, kn, tmem);
         // the ring is free once the shrink's MMAs are done: B's first tiles, behind the partial sums' place
         if (mbar_wait(s.d_full, 0, s.abort_flag, p.err))
-          for (int j = 0; j < sn && j < C::kBEarly; ++j) load_b<R, W>(p, s, wb, j);
+          for (int j = 0; j < sn && j < C::kBEarly; ++j) load_b<R, W, kFp16>(p, s, wb, j);
       }
       __syncwarp();
       if (kn == 0 && elect_one())
-        for (int j = 0; j < sn && j < C::kBEarly; ++j) load_b<R, W>(p, s, wb, j);
+        for (int j = 0; j < sn && j < C::kBEarly; ++j) load_b<R, W, kFp16>(p, s, wb, j);
       __syncwarp();
     } else {
-      gather_x<R, W>(p, s, k0, kn);
+      gather_x<R, W, kFp16>(p, s, k0, kn);
       const bool done = kn > 0 && mbar_wait_warp(s.d_full, 0, s.abort_flag, p.err);
       tc_fence_after();
-      write_part<R, W>(s, tmem, done);
+      write_part<R, W, kFp16>(s, tmem, done);
       tc_fence_before();
     }
     cluster_barrier();
@@ -669,7 +681,7 @@ __global__ void __launch_bounds__(Cfg<R, W>::kThreads, Cfg<R, W>::kCtas) adapter
 template <int R>
 __global__ void adapter_tc_pack_kernel(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* pb, int r, int K, int N,
                                        int64_t na, int64_t nb) {
-  using C = Cfg<R, 16>;
+  using C = Cfg<R, 16, true>;
   constexpr int W = C::kRowBytes / 2;  // elements of a row
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < na + nb;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -700,7 +712,7 @@ cudaError_t pack(const uint16_t* a, const uint16_t* b, uint16_t* pa, uint16_t* p
 template <int R, int W, bool kFp16>
 cudaError_t launch_warps(const AdapterArgs& p, cudaStream_t st) {
   auto kern = adapter_tc_kernel<R, W, kFp16>;
-  using C = Cfg<R, W>;
+  using C = Cfg<R, W, kFp16>;
   cudaError_t e = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kern), C::kBytes);
   if (e != cudaSuccess) return e;
   const int clusters = adapter_clusters(p.T, p.n, p.cut, p.base != p.out);

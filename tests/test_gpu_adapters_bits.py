@@ -1,0 +1,41 @@
+"""How many bits of u = s A x an fp32 result of the adapters has, read off directly: B is the identity, so a feature is one
+element of u."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def pkg():
+    import decode_batches_gb300
+    return decode_batches_gb300
+
+
+@pytest.mark.parametrize("rank,pad_to", [(1, 16), (16, 16), (7, 32), (32, 32), (64, 64), (3, 128), (128, 128)])
+@pytest.mark.parametrize("T", [1, 40, 256, 300, 1000, 2100, 4000])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_u_keeps_its_bits(T, rank, pad_to, dt):
+    """u[j] = a0 x0 + a1 x1 with 8-bit factors whose products lie 2^-9 apart: 24 bits or so.  Sums with two terms that are
+    not zero, then one product a term of u (in bf16 three, together all 24 bits; in fp16 two, half a step of the second of
+    which is 2^-23 of the row's largest u): each of these steps keeps 24 bits of the larger operand, 2^-23 of it is lost at
+    most; u itself is exact in 64 bits."""
+    K, N = 2, 128
+    g = torch.Generator().manual_seed(T + rank)
+    draw = lambda *s: (torch.randint(128, 256, s, generator=g) / 128 * torch.where(torch.rand(s, generator=g) < 0.5, -1.0, 1.0))
+    A, x = draw(rank, K), draw(T, K)
+    A[:, 1] *= 2.0 ** -9
+    B = torch.zeros(N, rank)
+    B[torch.arange(rank), torch.arange(rank)] = 1.0
+    ad = pkg().LowRankAdapters(2, N, K, pad_to, dt)
+    ad.set(1, A.to(dt).cuda(), B.to(dt).cuda(), 2.0)
+    ad.allocate_workspace(T)
+    ids = torch.ones(T, dtype=torch.int32)
+    ids[1::7] = 0
+    u = 2.0 * (x.double() @ A.double().T)
+    u[ids == 0] = 0.0
+    got = ad.forward(x.to(dt).cuda(), ids.cuda(), out_dtype=torch.float32).double().cpu()
+    size = u.abs() if dt == torch.bfloat16 else u.abs().amax(1, keepdim=True)
+    steps = 5                                             # the shrink's sum, three products' sums, the last term's rounding
+    assert ((got[:, :rank] - u).abs() <= steps * 2.0 ** -23 * size).all()
+    assert not got[:, rank:].any()
+    assert ad.device_error() == 0
