@@ -48,7 +48,12 @@ struct Cfg {
   static constexpr int kRowBytes = (R < 64 ? R : 64) * 2;  // a row of u or of a B tile within a block of 64 ranks
   static constexpr int kTail = kRows * 8 + 320;
   static constexpr int kBytes = kRing + kU + kTail + 1024;
-  static constexpr int kTmemCols = 256;              // two buffers of 128; the shrink's R are the first's
+  // The shrink's accumulators, taken in turn by its steps: the tensor core cuts a sum's last bits at every step, always
+  // towards zero, and a quarter or an eighth of the steps leaves as little of that (an fp32 result of 8195 rows, K =
+  // 4096, two CTAs: 2.3e-6 off the formula with one, 2.9e-7 with eight, and fp32 products 2.4e-7).
+  static constexpr int kAccs = W == 8 && R == 64 || R == 128 ? 4 : 8;
+  static constexpr int kTmemCols = kAccs * R <= 256 ? 256 : 512;  // (the expand's two buffers are 256)
+  static_assert(kCtas * kTmemCols <= 512, "");
   static constexpr int b_at(int slot) { return slot < kBEarly ? kPart + slot * kBTile : (slot - kBEarly) * kBTile; }
   static_assert(kBEarly >= 1 && kBSlots <= 6 && kBytes <= 227 * 1024 && kCtas * (kBytes + 1024) <= 228 * 1024, "");
   // Stages for tiles of `rows` rows (64 or 128): 6 of 16 KB or 4 of 24 at rank 64 with two CTAs an SM.
@@ -163,7 +168,7 @@ MOE_DEVICE void issue_shrink(const AdapterArgs& p, const Smem<R, W, kFp16>& s, c
     const uint32_t at = smem_u32(s.ring + t.st * stage);
     const uint64_t xd = operand_desc<128>(at), wd = operand_desc<128>(at + xbytes);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mma_f16_ss(tmem, xd + 2 * k, wd + 2 * k, idesc, i > 0 || k > 0);
+    for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + i % C::kAccs * R, xd + 2 * k, wd + 2 * k, idesc, i >= C::kAccs || k > 0);
     mma_commit(&s.empty[t.st]);
     if (i == 0) continue;
     // the stage of the step before is about to be free: its next A tile (x is asked for by the other warps)
@@ -197,11 +202,11 @@ MOE_DEVICE void issue_expand(const AdapterArgs& p, const Smem<R, W, kFp16>& s, c
     if (!mbar_wait(&s.b_full[at], (j / C::kBSlots) & 1, s.abort_flag, p.err)) return;
     if (!mbar_wait(&s.o_empty[buf], ((j >> 1) & 1) ^ 1, s.abort_flag, p.err)) return;
     tc_fence_after();
-    for (int t = 0; t < terms; ++t)
+    for (int t = terms - 1; t >= 0; --t)  // (the small terms first: less of them is cut)
       for (int k = 0; k < rs; ++k) {  // 16 ranks: 32 bytes of a row, four to a block of 64 ranks
         const uint32_t in = (k / 4) * kRows * 128 + (k % 4) * 32;
         mma_f16_ss(tmem + buf * kSlice, operand_desc<C::kRowBytes>(u0 + t * C::kTerm + in),
-                   operand_desc<C::kRowBytes>(b0 + C::b_at(at) + in), idesc, t > 0 || k > 0);
+                   operand_desc<C::kRowBytes>(b0 + C::b_at(at) + in), idesc, t < terms - 1 || k > 0);
       }
     mma_commit(&s.b_empty[at]);
     mma_commit(&s.o_full[buf]);
@@ -257,7 +262,7 @@ MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R, W, kFp16>& s, int k
   }
 }
 
-// This CTA's partial sums from TMEM into shared memory (16-byte units swizzled by the row).  D's rows lie a quarter in each
+// This CTA's partial sums (of `accs` accumulators) from TMEM into shared memory (16-byte units swizzled by the row).  D's rows lie a quarter in each
 // warp's 32 TMEM lanes: 32, or the first 16 of them where M is 64.
 template <int R>
 MOE_DEVICE uint32_t part_at(int row, int unit) {
@@ -265,22 +270,24 @@ MOE_DEVICE uint32_t part_at(int row, int unit) {
   return (row * (R / 4) + (unit ^ (row & kMask))) * 16;
 }
 template <int R, int W, bool kFp16>
-MOE_DEVICE void write_part(const Smem<R, W, kFp16>& s, uint32_t tmem, bool any) {
+MOE_DEVICE void write_part(const Smem<R, W, kFp16>& s, uint32_t tmem, int accs) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = s.tile_rows / 4, row = per * (warp & 3) + lane;
   for (int c = 16 * (warp >> 2); c < R; c += 4 * W) {
-    uint32_t v[16];
-    if (any) {
-      __syncwarp();  // (the load is the whole warp's, and lanes without a row skipped the stores before it)
-      tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
-      tmem_wait_ld();
-    } else {
+    float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0u;
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    for (int a = 0; a < accs; ++a) {
+      uint32_t d[16];
+      __syncwarp();  // (the load is the whole warp's, and lanes without a row skipped the stores before it)
+      tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + a * R + c, d);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(d[i]);
     }
     if (lane < per) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(s.ring + part_at<R>(row, c / 4 + i)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        *reinterpret_cast<float4*>(s.ring + part_at<R>(row, c / 4 + i)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
   }
 }
@@ -648,7 +655,7 @@ __global__ void __launch_bounds__(Cfg<R, W, kFp16>::kThreads, Cfg<R, W, kFp16>::
       gather_x<R, W, kFp16>(p, s, k0, kn);
       const bool done = kn > 0 && mbar_wait_warp(s.d_full, 0, s.abort_flag, p.err);
       tc_fence_after();
-      write_part<R, W, kFp16>(s, tmem, done);
+      write_part<R, W, kFp16>(s, tmem, done ? min(kn, C::kAccs) : 0);
       tc_fence_before();
     }
     cluster_barrier();

@@ -39,3 +39,25 @@ def test_u_keeps_its_bits(T, rank, pad_to, dt):
     assert ((got[:, :rank] - u).abs() <= steps * 2.0 ** -23 * size).all()
     assert not got[:, rank:].any()
     assert ad.device_error() == 0
+
+
+@pytest.mark.parametrize("T,n,rank", [(20000, 1, 64), (20000, 1, 128), (4000, 160, 16), (2000, 160, 16)])
+def test_long_sums_of_u(T, n, rank):
+    """u = A x over K = 16384 in one CTA: 1024 steps of 16 products, of which an accumulator of the tensor core takes an
+    eighth (rank 128: a quarter).  A step cuts 2^-23 of its sum at most, towards zero, and the sum after i of m steps of
+    random signs is sqrt(i / m) of the last: 2/3 m 2^-23 of u's norm in all.  The sums of the accumulators, and of
+    u's three terms with the identity, round some 16 times more."""
+    K, N, m = 16384, 128, 256 if rank == 128 else 128
+    g = torch.Generator(device="cuda").manual_seed(T + rank)
+    rnd = lambda *s: torch.randn(s, device="cuda", generator=g)
+    ad = pkg().LowRankAdapters(n, N, K, rank)
+    A, B = rnd(rank, K).bfloat16(), torch.zeros((N, rank), device="cuda", dtype=torch.bfloat16)
+    B[torch.arange(rank), torch.arange(rank)] = 1.0
+    ad.set(n - 1, A, B)
+    ad.allocate_workspace(T)
+    x = rnd(T, K).bfloat16()
+    ids = torch.full((T,), n - 1, dtype=torch.int32, device="cuda")
+    got = ad.forward(x, ids, out_dtype=torch.float32)[:, :rank].double()
+    for rows in (slice(0, 200), slice(T - 200, T)):
+        u = x[rows].double() @ A.double().T
+        assert float((got[rows] - u).norm() / u.norm()) <= (2 * m / 3 + 16) * 2.0 ** -23
