@@ -166,7 +166,7 @@ MOE_DEVICE void stage_expand(uint8_t* st, const uint4* wb, int c, int rs, int la
 
 // The expand's loop over the warp's chunks of features.  The first kStages - 1 chunks are on their way already, in
 // the stages from 1 on; u's fragments stay in registers where there
-// are few, the base's rows are requested before the products.
+// are few, the base's rows are requested before the products.  Rank 0: the base as it is.
 template <typename E, int M, int R, bool kFp16>
 MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R, kFp16>& s, const uint4* wb, int c0, int c1, int rank, int lane, int warp) {
   constexpr int MT = M / 16, RS = R / 16, kStages = Smem<M, R, kFp16>::kStages;
@@ -249,13 +249,19 @@ MOE_DEVICE void expand(const AdapterArgs& p, Smem<M, R, kFp16>& s, const uint4* 
           b[m][h].to_f32(f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = kFp16 ? fmaf(v[i], mul[m][h], f[i]) : v[i] + f[i];
-          if (in) store8(out[m][h] + 32 * c, v);
+          if (in) {
+            if (rank > 0)  // (else the base's bits as they are: a sum would change -0 and NaN)
+              store8(out[m][h] + 32 * c, v);
+            else
+              b[m][h].store(out[m][h] + 32 * c);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (32 * c + 8 * q + i < p.N) {
-              const float f = p.base ? base[m][h][32 * c + i].f32() : 0.0f;
-              out[m][h][32 * c + i] = E::of(kFp16 ? fmaf(v[i], mul[m][h], f) : v[i] + f);
+              const E e = p.base ? base[m][h][32 * c + i] : E{};
+              const float f = e.f32();
+              out[m][h][32 * c + i] = rank == 0 ? e : E::of(kFp16 ? fmaf(v[i], mul[m][h], f) : v[i] + f);
             }
         }
       }

@@ -504,7 +504,8 @@ moe_status moe_verify_drafts(const void* target, moe_dtype dtype, int64_t ldt, c
 /*
  * Low-rank adapters of many requests beside a shared projection.  Source: the projections of "DeepSeek V4.1F Q4
  * with native DSpark MTP on M3 Ultra", Decode and DSpark paragraphs; the adapters have no counterpart on the pages.
- *   out[t] = base[t] + B_a (s_a A_a x[t]),  a = ids[t];  out[t] = base[t] where ids[t] == -1 or slot a is empty.
+ *   out[t] = base[t] + B_a (s_a A_a x[t]),  a = ids[t];  out[t] = base[t], bit for bit, where ids[t] == -1 or
+ * slot a is empty.
  * A handle holds n slots of one shape: A_a [r_a][K], B_a [N][r_a], r_a <= r_max, s_a a number.
  *   moe_adapters_create     1 <= n <= 1024, 1 <= N, K <= 2^20, 1 <= r_max <= 128; dtype (bf16 or fp16) is that of A,
  *                           B and x.  Host only.  (Slots are held padded to rank 16, 32, 64 or 128 of r_max, and twice:
