@@ -9,7 +9,7 @@ using namespace moe;
 struct moe_adapters {
   int n = 0, N = 0, K = 0, r = 0, rpad = 0;
   moe_dtype type = MOE_BF16;
-  int num_sms = 1;
+  int num_sms = 1;           // of the handle's device (before there is one: of the current at create)
   int device = -1;           // of the handle's memory, once there is any
   uint16_t* w = nullptr;     // packed weights: A of all slots, B, and both again as the tensor cores' tiles
   int32_t* rank = nullptr;   // [n]
@@ -67,6 +67,7 @@ static moe_status allocate(moe_adapters* h) {
   const int dev = current_device();
   if (h->device >= 0 && h->device != dev)
     return bad(MOE_ERR_INVALID_ARG, "the handle's memory is on another device than the current one");
+  if (h->device < 0) h->num_sms = current_sms();
   h->device = dev;
   if (!h->err) {
     LIN_TRY(cudaMalloc(&h->err, sizeof(uint32_t)));
@@ -127,6 +128,8 @@ extern "C" moe_status moe_adapters_set_workspace(moe_adapters* h, void* dev_ptr,
   if (bytes < moe_adapters_workspace_bytes(h, T_max)) return bad(MOE_ERR_WORKSPACE, "workspace too small for T_max");
   const moe_status s = allocate(h);
   if (s != MOE_OK) return s;
+  // (again: the handle's device, known now, may have more SMs than that of create)
+  if (bytes < moe_adapters_workspace_bytes(h, T_max)) return bad(MOE_ERR_WORKSPACE, "workspace too small for T_max");
   h->ws = static_cast<uint8_t*>(dev_ptr);
   h->T_max = T_max;
   return MOE_OK;
@@ -179,6 +182,8 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
 extern "C" moe_status moe_adapters_get_device_error(moe_adapters* h, uint32_t* code) {
   if (!h || !code) return bad(MOE_ERR_INVALID_ARG, "the handle and code are required");
   *code = 0;
+  if (h->device >= 0 && h->device != current_device())
+    return bad(MOE_ERR_INVALID_ARG, "the handle's memory is on another device than the current one");
   LIN_TRY(cudaDeviceSynchronize());
   if (!h->err) return MOE_OK;
   LIN_TRY(cudaMemcpy(code, h->err, sizeof(uint32_t), cudaMemcpyDeviceToHost));

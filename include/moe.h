@@ -520,6 +520,8 @@ moe_status moe_verify_drafts(const void* target, moe_dtype dtype, int64_t ldt, c
  *                           overlap.  Rows may ask for any adapters in any order.  An id outside [-1, n) sets
  *                           MOE_DEVERR_EXPERT_RANGE and counts as -1.
  *   moe_adapters_get_device_error   as moe_plan_get_device_error, for the handle's calls.
+ * The device that is current when the first slot or the workspace is set holds the handle's memory: these calls, the
+ * forward call and the error query are refused with another one current.
  * Both products accumulate in fp32; u = s_a A_a x is held as terms of the 16-bit type: three in bf16 for an fp32 result
  * (all of u's 24 bits), two for a 16-bit one (relative error 2^-16 of u), two in fp16 (2^-22 of a row's largest u); base
  * is added in fp32 and the sum rounded once.  A row's result does
