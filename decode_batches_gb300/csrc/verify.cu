@@ -164,7 +164,7 @@ MOE_DEVICE Wide operator+(Wide a, Wide b) {
   return renormalised(s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo));
 }
 MOE_DEVICE Wide operator*(float u, Wide a) {
-  const float p = u * a.hi;
+  const float p = __fmul_rn(u, a.hi);  // (rounded here: fused into the sums below, its error would count twice)
   return renormalised(p, fmaf(u, a.hi, -p) + u * a.lo);
 }
 MOE_DEVICE bool operator>(Wide a, Wide b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }

@@ -489,7 +489,8 @@ moe_status moe_combine_rows_backward(const void* grad, moe_dtype grad_dtype, int
  *   cumulative sum of r exceeds u_sample[b] * (sum of r); the last index with r > 0 if none does.  Where r sums to 0
  *   the token is drawn from that row's p, where p does too it is -1.
  * Probabilities need not sum to one.  A value that is NaN, negative or above 2^64 counts as 0; a draft outside
- * [0, V) is refused.  The products u q are exact, sums have some 48 bits.
+ * [0, V) is refused.  The products u q are exact, sums and u_sample times them have
+ * some 47 bits (where the sum is above 2^-100).
  *   tokens   int32 [R]: the accepted drafts, the drawn token, then -1, in the request's rows; rows of no request
  *            are left as they are.
  *   accepted int32 [B]: the number of accepted drafts; 0 for a request without rows; -1 (and no token is written)
