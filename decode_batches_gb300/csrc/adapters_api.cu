@@ -149,8 +149,8 @@ extern "C" moe_status moe_adapters_forward(moe_adapters* h, const void* x, int64
   if (!x || !ids || !out) return bad(MOE_ERR_INVALID_ARG, "x, ids and out are required");
   if (ldx < h->K || ldo < h->N || (base && ldb < h->N)) return bad(MOE_ERR_INVALID_ARG, "a row pitch is below the width");
   const size_t e = elem_bytes(out_dtype);
-  if (!aligned(x, 2) || !aligned(out, e) || !aligned(base, e))
-    return bad(MOE_ERR_INVALID_ARG, "x, base and out must be aligned to their elements");
+  if (!aligned(x, 2) || !aligned(ids, 4) || !aligned(out, e) || !aligned(base, e))
+    return bad(MOE_ERR_INVALID_ARG, "x, ids, base and out must be aligned to their elements");
   if (base == out && ldb != ldo) return bad(MOE_ERR_INVALID_ARG, "base and out are the same rows: their pitches must be equal");
   AdapterArgs a;
   a.x = static_cast<const uint16_t*>(x), a.ldx = ldx, a.ids = ids;

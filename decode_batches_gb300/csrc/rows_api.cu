@@ -28,6 +28,13 @@ moe_status check_tensor(const Tensor& t, int d) {
   return MOE_OK;
 }
 
+moe_status check_assignments(const int32_t* inv, const float* w, const float* dw) {
+  if (!inv) return bad(MOE_ERR_INVALID_ARG, "inv_perm is required");
+  if (!aligned(inv, 4) || !aligned(w, 4) || !aligned(dw, 4))
+    return bad(MOE_ERR_INVALID_ARG, "inv_perm, weights and dweights must be aligned to their elements");
+  return MOE_OK;
+}
+
 bool vectors(const Tensor& t, int d) { return d % 8 == 0 && rows_aligned16(t.p, t.ld, t.type, t.rows); }
 
 }  // namespace
@@ -46,7 +53,7 @@ extern "C" moe_status moe_sort_rows(const void* x, moe_dtype x_dtype, int64_t ld
   const Tensor tok{x, x_dtype, ldx, T}, rows{out, x_dtype, ldo, n_rows};
   ROWS_TRY(check_tensor(tok, d));
   ROWS_TRY(check_tensor(rows, d));
-  if (!inv_perm) return bad(MOE_ERR_INVALID_ARG, "inv_perm is required");
+  ROWS_TRY(check_assignments(inv_perm, weights, nullptr));
   RowsArgs a;
   a.tok = x, a.ld_tok = ldx, a.out = out, a.ld_out = ldo;
   a.inv = inv_perm, a.w = weights, a.n_rows = n_rows, a.T = T, a.k = k, a.d = d;
@@ -63,7 +70,7 @@ extern "C" moe_status moe_sort_rows_backward(const void* grad, moe_dtype dtype, 
   if (n_rows > 0) ROWS_TRY(check_tensor(rows, d));
   ROWS_TRY(check_tensor(out, d));
   if (dweights) ROWS_TRY(check_tensor(tok, d));
-  if (!inv_perm) return bad(MOE_ERR_INVALID_ARG, "inv_perm is required");
+  ROWS_TRY(check_assignments(inv_perm, weights, dweights));
   RowsArgs a;
   a.tok = x, a.ld_tok = ldx, a.rows = grad, a.ld_rows = ldg, a.out = dx, a.ld_out = lddx;
   a.inv = inv_perm, a.w = weights, a.dots = dweights, a.n_rows = n_rows, a.T = T, a.k = k, a.d = d;
@@ -83,7 +90,7 @@ extern "C" moe_status moe_combine_rows(const void* y, moe_dtype y_dtype, int64_t
   if (n_rows > 0) ROWS_TRY(check_tensor(rows, d));
   ROWS_TRY(check_tensor(res, d));
   if (shared) ROWS_TRY(check_tensor(add, d));
-  if (!inv_perm) return bad(MOE_ERR_INVALID_ARG, "inv_perm is required");
+  ROWS_TRY(check_assignments(inv_perm, weights, nullptr));
   RowsArgs a;
   a.rows = y, a.ld_rows = ldy, a.shared = shared, a.shared_type = shared_dtype, a.ld_shared = lds;
   a.out = out, a.ld_out = ldo, a.inv = inv_perm, a.w = weights, a.n_rows = n_rows, a.T = T, a.k = k, a.d = d;
@@ -103,7 +110,7 @@ extern "C" moe_status moe_combine_rows_backward(const void* grad, moe_dtype grad
   if (!known(y_dtype)) return bad(MOE_ERR_INVALID_ARG, "unknown element type");
   if (n_rows > 0) ROWS_TRY(check_tensor(out, d));
   if (dweights && n_rows > 0) ROWS_TRY(check_tensor(rows, d));
-  if (!inv_perm) return bad(MOE_ERR_INVALID_ARG, "inv_perm is required");
+  ROWS_TRY(check_assignments(inv_perm, weights, dweights));
   RowsArgs a;
   a.tok = grad, a.ld_tok = ldg, a.rows = y, a.ld_rows = ldy, a.out = dy, a.ld_out = lddy;
   a.inv = inv_perm, a.w = weights, a.dots = dweights, a.n_rows = n_rows, a.T = T, a.k = k, a.d = d;

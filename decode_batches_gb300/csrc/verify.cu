@@ -552,6 +552,9 @@ extern "C" moe_status moe_verify_drafts(const void* target, moe_dtype dtype, int
   if (V > (1 << 30) || B > 65535) return bad(MOE_ERR_UNSUPPORTED, "at most 2^30 tokens and 65535 requests");
   if (B == 0) return MOE_OK;
   if (!offsets || !u_sample || !accepted) return bad(MOE_ERR_INVALID_ARG, "offsets, u_sample and accepted are required");
+  if (!aligned(drafts, 4) || !aligned(offsets, 4) || !aligned(u, 4) || !aligned(u_sample, 4) || !aligned(tokens, 4) ||
+      !aligned(accepted, 4))
+    return bad(MOE_ERR_INVALID_ARG, "drafts, offsets, u, u_sample, tokens and accepted must be aligned to their elements");
   if (R > 0) {
     if (!target || !drafts || !u || !tokens)
       return bad(MOE_ERR_INVALID_ARG, "target, drafts, u and tokens are required");
