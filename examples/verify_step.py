@@ -73,18 +73,19 @@ class CombineRows(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         y, inv, gates = ctx.saved_tensors
-        dy, dgates = combine_rows_backward(grad.contiguous(), inv, gates, y)
+        # (rows that no entry names, those of dropped assignments, have no gradient)
+        dy, dgates = combine_rows_backward(grad.contiguous(), inv, gates, y, out=torch.zeros_like(y))
         return dy, None, dgates
 
 
 def own_experts(plan, x, ids, gates, weights):
-    """out[t] = sum_j gates[t, j] tanh(x[t] weights[e]), e = ids[t, j] (each token's ids distinct): any expert function may
-    stand in its place."""
+    """out[t] = sum_j gates[t, j] tanh(x[t] weights[e]), e = ids[t, j]: any expert function may stand in its place.  An id
+    outside [0, E) and one that a token has already contribute nothing; their rows lie behind the last expert's."""
     _, offsets, _, inv = plan.permute(ids)
     inv = inv.view(ids.shape)
     rows = SortRows.apply(x, inv)
-    parts = torch.tensor_split(rows, offsets[1:-1].tolist())
-    y = torch.cat([torch.tanh(p @ w) for p, w in zip(parts, weights)])
+    *parts, dropped = torch.tensor_split(rows, offsets[1:].tolist())
+    y = torch.cat([torch.tanh(p @ w) for p, w in zip(parts, weights)] + [torch.zeros_like(dropped)])
     return CombineRows.apply(y, inv, gates)
 
 
