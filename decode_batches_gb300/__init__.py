@@ -314,11 +314,21 @@ def _outside(out: torch.Tensor, *inputs):
             raise ValueError("an output overlaps an input")
 
 
+def _lost_gradient(call: str):
+    """A call whose result has no gradient of its own, given tensors that want one: refused rather than detached."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{call} does not record its gradient: call it under torch.no_grad(), or in a torch.autograd.Function "
+                         f"whose backward calls {call}_backward")
+
+
 def sort_rows(x: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Tensor] = None,
               out: Optional[torch.Tensor] = None, stream=None):
     """Token rows x [T][d] (bf16, fp16 or fp32, any row pitch) in expert order: out[inv[t, j]] = weights[t, j] x[t]
     (moe_sort_rows).  inv int32 [T][k] is ``MoePlan.permute``'s, viewed as (T, k); -1: dropped.  out [rows][d] of
-    x's type (default T * k rows) keeps the rows that no entry names; a new one's are undefined."""
+    x's type (default T * k rows) keeps the rows that no entry names; a new one's are undefined.  Tensors that require
+    a gradient are refused while gradients are recorded: ``sort_rows_backward`` computes it."""
+    if x.requires_grad or (weights is not None and weights.requires_grad):
+        _lost_gradient("sort_rows")
     if stream is not None:
         with torch.cuda.stream(stream):
             return sort_rows(x, inv, weights, out)
@@ -365,7 +375,10 @@ def sort_rows_backward(grad: torch.Tensor, inv: torch.Tensor, weights: Optional[
 def combine_rows(y: torch.Tensor, inv: torch.Tensor, weights: Optional[torch.Tensor] = None,
                  shared: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, out_dtype=None, stream=None):
     """Rows y [rows][d] in expert order back to the tokens: out[t] = sum_j weights[t, j] y[inv[t, j]] + shared[t]
-    (moe_combine_rows), in out_dtype (default y's).  y, shared and out: bf16, fp16 or fp32 each, any row pitch."""
+    (moe_combine_rows), in out_dtype (default y's).  y, shared and out: bf16, fp16 or fp32 each, any row pitch.  Tensors
+    that require a gradient are refused while gradients are recorded: ``combine_rows_backward`` computes it."""
+    if y.requires_grad or (weights is not None and weights.requires_grad) or (shared is not None and shared.requires_grad):
+        _lost_gradient("combine_rows")
     if stream is not None:
         with torch.cuda.stream(stream):
             return combine_rows(y, inv, weights, shared, out, out_dtype)
