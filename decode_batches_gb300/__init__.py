@@ -624,6 +624,7 @@ class LowRankAdapters:
         return int(self.lib.moe_adapters_workspace_bytes(self._h, T_max))
 
     def set_workspace(self, buf: torch.Tensor, T_max: int):
+        _here(buf)
         _check(self.lib.moe_adapters_set_workspace(self._h, _dev(buf, "workspace"), buf.numel() * buf.element_size(), T_max))
         self._ws = buf
         self.T_max = T_max

@@ -64,3 +64,24 @@ def test_calls_with_another_device_current(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, (r.returncode, r.stderr)
+
+
+def test_a_workspace_on_another_device_is_refused(monkeypatch):
+    import pytest
+    import torch
+
+    import decode_batches_gb300 as p
+
+    class Elsewhere:                       # a buffer as a second device would have it
+        device, is_cuda, dtype = "cuda:1", True, torch.uint8
+        get_device = staticmethod(lambda: 1)
+        is_contiguous = staticmethod(lambda: True)
+        data_ptr = staticmethod(lambda: 1 << 20)
+        numel = staticmethod(lambda: 1 << 20)
+        element_size = staticmethod(lambda: 1)
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    ad = p.LowRankAdapters(4, 64, 96, 16)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        ad.set_workspace(Elsewhere(), 100)
+    assert ad.T_max == 0
