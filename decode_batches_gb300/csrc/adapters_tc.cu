@@ -746,11 +746,15 @@ cudaError_t launch_adapter_tc_pack(const uint16_t* a, const uint16_t* b, uint16_
   }
 }
 
-// Up to 3500 rows two CTAs of 8 warps run on an SM, whose waits fill each other, above one of 16 with a deep ring (rank 64,
-// 4096 x 4096; 4096 rows: 39.4 and 36.7 us, 2051: 25.6 and 27.4, 20000: 116 and 96).  CTAs that share a tile: a power of
-// two that should leave all tiles running at once.  How many there will be is unknown here: a slot that has rows has a
-// tile at least, and loses part of one.  (8195 rows in 32 slots, one of 16 warps: 52 us with 2 CTAs a tile and 60 with 1
-// where 64 tiles come out, 67 and 60 where 80 do.)
+// Up to 3500 rows two CTAs of 8 warps run on an SM, whose waits fill each other, above one of 16 with a deep ring.  Both, us,
+// two CTAs first, in 8 slots (in 64), a tenth of the rows without an adapter:
+//     rows               1500                     3500                     5000                     8000
+//     rank 64, 4096x4096 25.2 34.7 (33.9 37.9)    36.2 36.0 (48.4 39.6)    54.1 42.5 (57.1 47.2)    59.6 47.1 (91.6 60.1)
+//     rank 16, 2048x4096 19.0 27.2 (22.5 27.8)    25.4 34.1 (34.4 30.2)    36.5 37.6 (37.4 38.0)    42.3 40.3 (58.4 48.4)
+//     rank 16, 1024x1024 14.0 19.7 (14.6 16.1)    15.5 21.6 (17.6 17.8)    18.8 19.0 (18.9 20.3)    20.5 20.1 (26.2 23.1)
+// CTAs that share a tile: a power of two that should leave all tiles running at once.  How many there will be is unknown here:
+// a slot that has rows has a tile at least, and loses part of one.  (8195 rows in 32 slots, one of 16 warps: 52 us with 2 CTAs
+// a tile and 60 with 1 where 64 tiles come out, 67 and 60 where 80 do.)
 AdapterCut adapter_cut(int T, int n, int rpad, int num_sms) {
   const int used = n < T ? n : T;
   AdapterCut c;

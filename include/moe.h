@@ -512,8 +512,9 @@ moe_status moe_verify_drafts(const void* target, moe_dtype dtype, int64_t ldt, c
  *                           B and x.  Host only.  (Slots are held padded to rank 16, 32, 64 or 128 of r_max, and twice:
  *                           as small and as large steps read them.)
  *   moe_adapters_set        contiguous A and B (device) copied into slot `slot` of the handle's memory in the kernel's
- *                           layout; r = 0 empties the slot.  Synchronous (waits for the device); other slots' contents
- *                           are kept, so that adapters come and go while the handle serves.
+ *                           layout; r = 0 empties the slot.  Synchronous: waits for the whole device before and after, so
+ *                           that queued calls finish with the old contents (not while a stream is being captured).  Other
+ *                           slots keep theirs.
  *   ..._workspace_bytes / set_workspace   caller-owned memory for grouping up to T_max rows, 256-byte aligned; one call
  *                           at a time uses it (order them on a stream).
  *   moe_adapters_forward    x [T][K] (pitch ldx), ids int32 [T], base [T][N] (pitch ldb; NULL: zero) and out [T][N]
