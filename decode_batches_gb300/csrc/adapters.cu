@@ -14,9 +14,9 @@
 // barriers, 4.8 us for one row (rank 16, 4096 x 4096) of which a launch is 2; 48 rows of 35 adapters of rank 64 16.5 us,
 // 2.2 TB/s of weights.
 //
-// u is split in 16-bit terms, three in bf16 (all of its 24 bits) and two in fp16 (2^-22 of a row's largest), since
-// one term's 2^-8 would dominate the result.  In fp16 a row's u is first brought to [1, 2) by a power of two, so
-// that neither term leaves the type's range.
+// u is split in 16-bit terms, three in bf16 (all of its 24 bits; a 16-bit result takes the first two, 2^-16 of u) and
+// two in fp16 (2^-22 of a row's largest), since one term's 2^-8 would dominate the result.  In fp16 a row's u is first
+// brought to [1, 2) by a power of two, so that neither term leaves the type's range.
 #include "adapters.cuh"
 #include "adapters_split.cuh"
 #include "cluster.cuh"

@@ -262,8 +262,8 @@ MOE_DEVICE void gather_x(const AdapterArgs& p, const Smem<R, W, kFp16>& s, int k
   }
 }
 
-// This CTA's partial sums (of `accs` accumulators) from TMEM into shared memory (16-byte units swizzled by the row).  D's rows lie a quarter in each
-// warp's 32 TMEM lanes: 32, or the first 16 of them where M is 64.
+// This CTA's partial sums (of `accs` accumulators) from TMEM into shared memory (16-byte units swizzled by the row).  D's
+// rows lie a quarter in each warp's 32 TMEM lanes: 32, or the first 16 of them where M is 64.
 template <int R>
 MOE_DEVICE uint32_t part_at(int row, int unit) {
   constexpr int kMask = R / 4 < 8 ? R / 4 - 1 : 7;
