@@ -15,8 +15,8 @@
 // 2.2 TB/s of weights.
 //
 // u is split in 16-bit terms, three in bf16 (all of its 24 bits; a 16-bit result takes the first two, 2^-16 of u) and
-// two in fp16 (2^-22 of a row's largest), since one term's 2^-8 would dominate the result.  In fp16 a row's u is first
-// brought to [1, 2) by a power of two, so that neither term leaves the type's range.
+// two in fp16 (22 bits), since one term's 2^-8 would dominate the result.  In fp16 a row's u is first brought to the upper
+// end of the type's range by a power of two, so that neither term leaves it.
 #include "adapters.cuh"
 #include "adapters_split.cuh"
 #include "cluster.cuh"

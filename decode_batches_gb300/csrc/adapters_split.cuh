@@ -34,14 +34,15 @@ MOE_DEVICE uint4 load_x(const uint16_t* row, int c, int K) {
 }
 
 // 16-bit terms that hold u: in bf16 three, whose 24 bits are all that an fp32 sum has (with two, an fp32 result of 2048 x 4096
-// and rank 16 was 2.5e-6 off the formula where fp32 products are 1.5e-7 off); in fp16 two, 22 bits of the row's largest u.
+// and rank 16 was 2.5e-6 off the formula where fp32 products are 1.5e-7 off); in fp16 two, 22 bits.
 template <bool kFp16>
 constexpr int kAdapterTerms = kFp16 ? 2 : 3;
 
 // Ranks c .. c + 7 of a row's sums as the terms of u = scale * v (0 behind the slot's rank, where an infinite x
 // makes NaN of the padding); R / 8 neighbouring lanes hold a row.  Returns what the terms were divided by: 1 in bf16;
-// in fp16 the power of two that brings the row's largest u to [1, 2), so that neither term leaves the type's range
-// (1 for a row that is zero, infinite or NaN).
+// in fp16 the power of two that brings the row's largest u to [2^14, 2^15): neither term leaves the type's range, and a u
+// keeps its 22 bits down to 2^-17 of the largest (with the largest in [1, 2), one 2^-10 below it had 14 left).
+// (1 for a row that is zero, infinite or NaN.)
 template <int R, bool kFp16>
 MOE_DEVICE float adapter_split(float (&v)[8], int c, int rank, float scale, uint4 (&term)[kAdapterTerms<kFp16>]) {
   float mul = 1.0f;
@@ -54,7 +55,7 @@ MOE_DEVICE float adapter_split(float (&v)[8], int c, int rank, float scale, uint
 #pragma unroll
     for (int o = 1; o < R / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     const int ex = static_cast<int>(__float_as_uint(big) >> 23) - 127;  // big in [2^ex, 2^(ex + 1))
-    const int e2 = ex == -127 || ex == 128 ? 0 : max(-126, min(126, ex));
+    const int e2 = ex == -127 || ex == 128 ? 0 : max(-126, ex - 14);
     mul = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
     const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
 #pragma unroll

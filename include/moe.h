@@ -525,9 +525,9 @@ moe_status moe_verify_drafts(const void* target, moe_dtype dtype, int64_t ldt, c
  * The device that is current when the first slot or the workspace is set holds the handle's memory: these calls, the
  * forward call and the error query are refused with another one current.
  * Both products accumulate in fp32; u = s_a A_a x is held as terms of the 16-bit type: three in bf16 for an fp32 result
- * (all of u's 24 bits), two for a 16-bit one (relative error 2^-16 of u), two in fp16 (2^-22 of a row's largest u); base
- * is added in fp32 and the sum rounded once.  A row's result does
- * not depend on its place or on the other rows; steps of another T may split the sums otherwise.  T_max <= 2^26.
+ * (all of u's 24 bits), two for a 16-bit one (relative error 2^-16 of u), two in fp16 (2^-22 of u, or 2^-39 of the row's
+ * largest where that is more); base is added in fp32 and the sum rounded once.  A row's result does not depend on its
+ * place or on the other rows; steps of another T may split the sums otherwise.  T_max <= 2^26.
  * The forward call only enqueues work; a NULL or not-ready handle, T < 0 or T > T_max, a pitch below the width or an
  * unknown type is an error before any launch.
  */

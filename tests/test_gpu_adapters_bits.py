@@ -61,3 +61,26 @@ def test_long_sums_of_u(T, n, rank):
     for rows in (slice(0, 200), slice(T - 200, T)):
         u = x[rows].double() @ A.double().T
         assert float((got[rows] - u).norm() / u.norm()) <= (2 * m / 3 + 16) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("rank,T", [(16, 1), (16, 300), (64, 40), (64, 2100), (128, 600), (32, 4000)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+def test_small_u_beside_large_ones(T, rank, dt):
+    """The u of a row lie up to 2^15 apart: each keeps its own bits, as many steps as above from exact."""
+    K, N = 2, 128
+    g = torch.Generator().manual_seed(T + rank)
+    draw = lambda *s: (torch.randint(128, 256, s, generator=g) / 128 * torch.where(torch.rand(s, generator=g) < 0.5, -1.0, 1.0))
+    A, x = draw(rank, K), draw(T, K)
+    A *= 2.0 ** (8 - torch.arange(rank) % 16)[:, None]
+    A[:, 1] *= 2.0 ** -9
+    assert torch.equal(A.to(dt).float(), A) and torch.equal(x.to(dt).float(), x)
+    B = torch.zeros(N, rank)
+    B[torch.arange(rank), torch.arange(rank)] = 1.0
+    for scale in (1.0, 2.0 ** 40, 2.0 ** -60):
+        ad = pkg().LowRankAdapters(1, N, K, rank, dt)
+        ad.set(0, A.to(dt).cuda(), B.to(dt).cuda(), scale)
+        ad.allocate_workspace(T)
+        u = scale * (x.double() @ A.double().T)
+        got = ad.forward(x.to(dt).cuda(), torch.zeros(T, dtype=torch.int32).cuda(), out_dtype=torch.float32).double().cpu()
+        assert ((got[:, :rank] - u).abs() <= 5 * 2.0 ** -23 * u.abs()).all()
+        assert not got[:, rank:].any()
